@@ -85,6 +85,10 @@ typedef enum {
                               this call's sizes (the call planned for itself; outputs are
                               valid), or the plan's lengths differ from cache_seqlens (a stale
                               plan: outputs and appends are unspecified) */
+#define PKV_ERR_POOL 32    /* pkv_table_update: too few free pages for a row, or a pool whose
+                              header is not one */
+#define PKV_ERR_TREE 64    /* a drafted tree whose parents are not earlier nodes, or an accepted
+                              path that does not rise */
 
 /* Geometry of one K or V page pool (both share it).  page_size is a power of
  * two in [1, 256]; head_dim is 64, 128 or 256; num_pages >= 2 (page 0 is the
@@ -432,6 +436,190 @@ PKV_API pkv_status pkv_mixed_attn(const pkv_cache_desc *desc, void *k_cache, voi
                                   int32_t batch, int32_t num_q_heads, int32_t total_q, int32_t max_qlen,
                                   int32_t decode_max_qlen, float softmax_scale, void *out, float *lse,
                                   void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/* ---------------------------------------------------------------------
+ * Block tables that follow request lengths on the device.
+ * The device counterpart of pkv_pool_* / pkv_table_*: "flex_attention + paged
+ * KV + CUDA graphs vs vLLM", "What each option did" (PageTable.reserve) and
+ * "mini-infer系统实战-06 True PagedAttention", section 5 (no host round trip
+ * inside a step).  A captured step can so grow, shrink and release its rows.
+ * --------------------------------------------------------------------- */
+
+/*
+ * pkv_device_pool_bytes / pkv_device_pool_init -- a pool of the pages
+ * 1 .. num_pages-1 in device memory (page 0 is never handed out).  It is an
+ * int32 array: word 0 the ring index of the next page handed out, word 1 the
+ * number of free pages, words 2 .. 15 reserved (zero between calls), then a
+ * ring of num_pages - 1 page ids.  Pages are handed out from the ring's head
+ * and come back at its tail: first in, first out.  After the init every page
+ * is free and they are handed out in ascending order; a caller that wants
+ * another order writes the ring itself.  pkv_device_pool_bytes returns 0 if
+ * num_pages < 2.
+ */
+PKV_API size_t pkv_device_pool_bytes(int32_t num_pages);
+PKV_API pkv_status pkv_device_pool_init(void *pool, size_t pool_bytes, int32_t num_pages, void *stream);
+
+/*
+ * pkv_table_update -- makes every row's block table cover the tokens it is
+ * about to hold, and tells where its new tokens go.  Row b holds
+ * cache_seqlens[b] tokens and gets n_b = new_tokens[b] more: it needs
+ * ceil((cache_seqlens[b] + n_b) / page_size) blocks (none if it is inactive,
+ * cache_seqlens[b] < 0; its n_b then counts as 0).  Blocks past that go back
+ * to the pool and their entries become 0; missing ones are taken from it.
+ *
+ *  pool              device pool (pkv_device_pool_init), modified.
+ *  page_size         a power of two in [1, 256].
+ *  block_table       device int32 [batch, max_blocks], modified.
+ *  held_blocks       device int32 [batch], modified: blocks row b holds now
+ *                    (0 for a fresh row).
+ *  cache_seqlens     device int32 [batch].
+ *  new_tokens        device int32 [batch], or NULL for 0.
+ *  indptr            device int32 [batch + 1] or NULL: exclusive prefix sum of
+ *                    n_b (a qo_indptr / append_indptr), 0 for a failing row.
+ *  slot_map          device int64 [max_tokens] or NULL: for token t of the
+ *                    ragged batch, page * page_size + place in the page.
+ *  positions         device int32 [max_tokens] or NULL: cache_seqlens[b] + i.
+ *                    Both get -1 behind the last token.
+ * Pages are taken in row order, those of a row in block order, and returned
+ * in the same order; a page returned by a call is handed out from the next
+ * call on.  A row fails when it would exceed max_blocks (PKV_ERR_OVERFLOW),
+ * when n_b < 0 or its tokens would end past max_tokens (PKV_ERR_QLEN; with
+ * slot_map or positions only), when the pages it and the rows before it need
+ * are more than are free (PKV_ERR_POOL) or when held_blocks[b] is outside
+ * [0, max_blocks] (PKV_ERR_PAGE): its blocks stay as they are and it gets no
+ * token.  A page id outside [1, num_pages) found in the ring or in an entry
+ * being returned sets PKV_ERR_PAGE (the entry becomes 0, its slots -1; a bad
+ * entry being returned goes into the ring as 0).  A
+ * pool whose header is out of range, or that would get back more pages than
+ * it lent, sets PKV_ERR_POOL and nothing changes (indptr all 0).
+ * batch 0 .. 1024.  One kernel on `stream`; calls that share a pool, a table
+ * or a held_blocks must not run concurrently.
+ */
+PKV_API pkv_status pkv_table_update(void *pool, int32_t num_pages, int32_t page_size, int32_t *block_table,
+                                    int32_t max_blocks, int32_t *held_blocks, const int32_t *cache_seqlens,
+                                    const int32_t *new_tokens, int32_t batch, int32_t *indptr, int64_t *slot_map,
+                                    int32_t *positions, int32_t max_tokens, int32_t *err_flag, void *stream);
+
+/* ---------------------------------------------------------------------
+ * Speculative decoding with a tree of drafted tokens per row.  Row b drafts
+ * n_b = qo_indptr[b+1] - qo_indptr[b] nodes (at most max_nodes <= 256) on top
+ * of its L_b = cache_seqlens[b] cached tokens; node i sits at cache position
+ * L_b + i whatever its depth.  A step: pkv_tree_build (masks, positions for
+ * the rotary embedding), pkv_tree_attn in every layer, pkv_tree_accept on the
+ * target model's choices, pkv_tree_commit (the accepted tokens' K/V move to
+ * the front), pkv_table_update.
+ * Source: "flex_attention + paged KV + CUDA graphs vs vLLM", "Why this works"
+ * (an attention mask over physical pages) and "What broke correctness" (a row
+ * whose mask leaves nothing must not give NaN); the paged cache of
+ * "mini-infer系统实战-06 True PagedAttention", section 1.
+ *
+ * Row fates shared by the tree calls: n_b = 0 writes nothing per node; a node
+ * range that is reversed or leaves [0, total_q) sets PKV_ERR_QLEN and writes
+ * nothing per node (overlapping ranges: unspecified values); n_b > max_nodes
+ * sets PKV_ERR_QLEN.
+ * --------------------------------------------------------------------- */
+
+/*
+ * pkv_tree_build -- ancestor masks and positions of drafted trees.
+ *  parents           device int32 [total_q]: node i's parent within its row,
+ *                    -1 (the node continues the cached tokens) or an earlier
+ *                    node (< i).
+ *  tree_mask         device int32 [total_q, mask_words], mask_words >=
+ *                    ceil(max_nodes / 32), at most 8: bit j of word j / 32 of
+ *                    node i is set iff j is i or one of its ancestors.
+ *  positions         device int32 [total_q] or NULL: L_b + depth of node i (0
+ *                    for a root).
+ * A row that is inactive, too long (PKV_ERR_QLEN) or whose parents are not
+ * earlier nodes (PKV_ERR_TREE) gets empty masks and positions -1.
+ * batch >= 0; one kernel.
+ */
+PKV_API pkv_status pkv_tree_build(const int32_t *parents, const int32_t *qo_indptr, const int32_t *cache_seqlens,
+                                  int32_t batch, int32_t total_q, int32_t max_nodes, int32_t *tree_mask,
+                                  int32_t mask_words, int32_t *positions, int32_t *err_flag, void *stream);
+
+/*
+ * pkv_tree_workspace_size -- bytes of device workspace pkv_tree_attn needs (0
+ * on invalid or unsupported arguments).  It needs no initialisation; calls
+ * that share a workspace must not run concurrently.
+ */
+PKV_API size_t pkv_tree_workspace_size(int32_t batch, int32_t total_q, int32_t max_blocks, int32_t num_q_heads,
+                                       int32_t max_nodes, const pkv_cache_desc *desc);
+
+/*
+ * pkv_tree_attn -- append every row's drafted tokens, then attend: node i of
+ * row b sees the L_b cached keys and drafted key j of its row iff bit j of its
+ * mask is set (bits at and past n_b are ignored; any mask is allowed, not only
+ * a tree's).
+ *
+ *  q                 device bf16 [total_q, num_q_heads, head_dim].
+ *  k_new, v_new      device bf16 [total_q, num_kv_heads, head_dim], written at
+ *                    positions L_b .. L_b + n_b - 1 as pkv_append does; or
+ *                    both NULL when they are cached there already.
+ *  cache_seqlens     L_b, WITHOUT the drafted tokens in either case.
+ *  tree_mask         device int32 [total_q, mask_words], mask_words in
+ *                    [ceil(max_nodes / 32), 8].
+ *  max_nodes         1 .. 256; a longer row appends nothing and gets
+ *                    PKV_ERR_QLEN, out = 0, lse = -inf.
+ *  out, lse          as pkv_mixed_attn.  A node that sees no key gives out = 0,
+ *                    lse = -inf.
+ *  batch             0 .. 1024; total_q * num_q_heads < 2^31; at most 128
+ *                    query heads per kv head; page_size at least 8.
+ * K/V of a drafted token reach only the nodes that see it, whatever they hold
+ * (infinities and NaN included).  Other row fates as pkv_mixed_attn:
+ * inactive; PKV_ERR_OVERFLOW when L_b + n_b exceeds max_blocks * page_size;
+ * PKV_ERR_PAGE for a bad page among the first ceil((L_b + n_b) / page_size).
+ */
+PKV_API pkv_status pkv_tree_attn(const pkv_cache_desc *desc, void *k_cache, void *v_cache, const void *q,
+                                 const void *k_new, const void *v_new, const int32_t *qo_indptr,
+                                 const int32_t *tree_mask, int32_t mask_words, const int32_t *block_table,
+                                 int32_t max_blocks, const int32_t *cache_seqlens, int32_t batch, int32_t num_q_heads,
+                                 int32_t total_q, int32_t max_nodes, float softmax_scale, void *out, float *lse,
+                                 void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/*
+ * pkv_tree_accept -- the path of drafted tokens that the target model chose
+ * itself: from the cached tokens on, the lowest-numbered child whose drafted
+ * token equals the target's choice at its parent, as long as there is one.
+ *  draft_tokens      device int32 [total_q].
+ *  target_tokens     device int32 [total_q]: the target's choice after node i.
+ *  root_targets      device int32 [batch]: the target's choice after the
+ *                    cached tokens; NULL: the first node without a parent is
+ *                    accepted unseen (it is the last step's token).
+ *  path              device int32 [batch, max_path]: accepted nodes in order,
+ *                    -1 behind them; at most max_path (>= 1) are accepted.
+ *  path_len          device int32 [batch].
+ *  next_token        device int32 [batch] or NULL: the target's choice after
+ *                    the last accepted node (root_targets[b], or -1 without
+ *                    it, if none is).
+ *  seqlens_out       device int32 [batch] or NULL: L_b + path_len[b].  It may
+ *                    be cache_seqlens itself if pkv_tree_commit is given the
+ *                    lengths before.
+ * A row that is inactive, malformed, too long or whose parents are not earlier
+ * nodes (PKV_ERR_TREE) gets path_len 0, next_token -1 and seqlens_out L_b.
+ */
+PKV_API pkv_status pkv_tree_accept(const int32_t *parents, const int32_t *draft_tokens, const int32_t *target_tokens,
+                                   const int32_t *root_targets, const int32_t *qo_indptr,
+                                   const int32_t *cache_seqlens, int32_t batch, int32_t total_q, int32_t max_nodes,
+                                   int32_t *path, int32_t max_path, int32_t *path_len, int32_t *next_token,
+                                   int32_t *seqlens_out, int32_t *err_flag, void *stream);
+
+/*
+ * pkv_tree_commit -- the accepted tokens' K/V move from position L_b + path[i]
+ * to L_b + i (bit copies) in num_layers pools that share one block table.
+ *  k_caches, v_caches  host arrays of num_layers (1 .. 128) device pools, all
+ *                    distinct.
+ *  path, path_len    as pkv_tree_accept writes them; max_path 1 .. 256.
+ *  cache_seqlens     L_b: the lengths before the accepted tokens.
+ * Inactive rows move nothing.  A row moves nothing and sets a bit when its
+ * path_len is outside [0, max_path] or its path does not rise from >= 0
+ * (PKV_ERR_TREE), when a position passes max_blocks * page_size
+ * (PKV_ERR_OVERFLOW) or a page it reads or writes is outside [1, num_pages)
+ * (PKV_ERR_PAGE).  One kernel.
+ */
+PKV_API pkv_status pkv_tree_commit(const pkv_cache_desc *desc, int32_t num_layers, void *const *k_caches,
+                                   void *const *v_caches, const int32_t *path, int32_t max_path,
+                                   const int32_t *path_len, const int32_t *block_table, int32_t max_blocks,
+                                   const int32_t *cache_seqlens, int32_t batch, int32_t *err_flag, void *stream);
 
 /* ---------------------------------------------------------------------
  * Host page-pool and block-table helpers (no device memory involved).

@@ -8,11 +8,13 @@ binding (``api``) and the seeded synthetic workload generators
 from .api import (  # noqa: F401
     HND,
     DecodeStep,
+    LayerCaches,
     NHD,
     PagePool,
     PkvError,
     cache_desc,
     decode_workspace,
+    device_pool,
     default_decode_max_qlen,
     mixed_workspace,
     pkv_append,
@@ -24,6 +26,13 @@ from .api import (  # noqa: F401
     pkv_pool_bytes,
     pkv_prefill_attn,
     pkv_prefill_workspace_size,
+    pkv_table_update,
+    pkv_tree_accept,
+    pkv_tree_attn,
+    pkv_tree_build,
+    pkv_tree_commit,
+    pkv_tree_workspace_size,
     prefill_workspace,
     pkv_validate_host,
+    tree_workspace,
 )

@@ -49,6 +49,15 @@ SIGNATURES = {
     "pkv_mixed_workspace_size": (SIZE, [I32, I32, I32, I32, I32, I32, DESC_P]),
     "pkv_mixed_attn": (I32, [DESC_P, P, P, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32, ctypes.c_float, P, P, P,
                              SIZE, P, P]),
+    "pkv_device_pool_bytes": (SIZE, [I32]),
+    "pkv_device_pool_init": (I32, [P, SIZE, I32, P]),
+    "pkv_table_update": (I32, [P, I32, I32, P, I32, P, P, P, I32, P, P, P, I32, P, P]),
+    "pkv_tree_build": (I32, [P, P, P, I32, I32, I32, P, I32, P, P, P]),
+    "pkv_tree_workspace_size": (SIZE, [I32, I32, I32, I32, I32, DESC_P]),
+    "pkv_tree_attn": (I32, [DESC_P, P, P, P, P, P, P, P, I32, P, I32, P, I32, I32, I32, I32, ctypes.c_float, P, P, P,
+                            SIZE, P, P]),
+    "pkv_tree_accept": (I32, [P, P, P, P, P, P, I32, I32, I32, P, I32, P, P, P, P, P]),
+    "pkv_tree_commit": (I32, [DESC_P, I32, P, P, P, I32, P, P, I32, P, I32, P, P]),
     "pkv_pool_create": (P, [I32]),
     "pkv_pool_destroy": (None, [P]),
     "pkv_pool_alloc": (I32, [P, I32, I32P]),

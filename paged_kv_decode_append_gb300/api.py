@@ -21,7 +21,7 @@ DECODE_OVERLAP_PROLOGUE = 1  # pkv_decode_attn_ex flags (see include/pkv.h)
 DECODE_EARLY_KV = 2
 DECODE_MAKE_PLAN = 4
 DECODE_USE_PLAN = 8
-ERR_PAGE, ERR_OVERFLOW, ERR_TIMEOUT, ERR_QLEN, ERR_PLAN = 1, 2, 4, 8, 16
+ERR_PAGE, ERR_OVERFLOW, ERR_TIMEOUT, ERR_QLEN, ERR_PLAN, ERR_POOL, ERR_TREE = 1, 2, 4, 8, 16, 32, 64
 
 
 class PkvError(RuntimeError):
@@ -296,6 +296,220 @@ def pkv_mixed_attn(k_cache, v_cache, q, k_new, v_new, qo_indptr, block_table, ca
         _ptr(err_flag), _stream(q.device))
     _check(st, "pkv_mixed_attn")
     return out
+
+
+POOL_HEADER = 16  # int32 words before the ring of a device pool
+
+
+def _shape(t, want, name):
+    if t is not None and tuple(t.shape) != tuple(want):
+        raise ValueError(f"{name}: expected shape {tuple(want)}, got {tuple(t.shape)}")
+
+
+def _one_device(*tensors):
+    """The device of the call's tensors, made sure to be the current one (the
+    library launches on the current device)."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors on different devices")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{dev}, which is not the current device")
+    return dev
+
+
+def device_pool(num_pages: int, device="cuda") -> torch.Tensor:
+    """A pool of pages ``1 .. num_pages - 1`` in device memory
+    (``pkv_device_pool_init``), as an int32 tensor; every page is free."""
+    n = int(_lib.load().pkv_device_pool_bytes(num_pages))
+    if n == 0:
+        raise PkvError(EINVAL, "pkv_device_pool_bytes")
+    pool = torch.empty(n // 4, dtype=torch.int32, device=device)
+    _one_device(pool)
+    _check(_lib.load().pkv_device_pool_init(_ptr(pool), n, num_pages, _stream(pool.device)), "pkv_device_pool_init")
+    return pool
+
+
+def pkv_table_update(pool, block_table, held_blocks, cache_seqlens, new_tokens, page_size: int, indptr=None,
+                     slot_map=None, positions=None, err_flag=None) -> None:
+    """Makes every row's ``block_table`` entry list cover ``cache_seqlens[b] +
+    new_tokens[b]`` tokens (none for an inactive row) from the device ``pool``,
+    and writes the new tokens' ``indptr`` ``[B + 1]``, ``slot_map`` (int64) and
+    ``positions`` ``[max_tokens]`` where given."""
+    for t, n in ((pool, "pool"), (block_table, "block_table"), (held_blocks, "held_blocks"),
+                 (cache_seqlens, "cache_seqlens"), (new_tokens, "new_tokens"), (indptr, "indptr"),
+                 (positions, "positions"), (err_flag, "err_flag")):
+        _i32(t, n)
+    if slot_map is not None and (slot_map.dtype != torch.int64 or not slot_map.is_contiguous()):
+        raise ValueError("slot_map: expected a contiguous int64 tensor")
+    _one_device(pool, block_table, held_blocks, cache_seqlens, new_tokens, indptr, slot_map, positions, err_flag)
+    B, width = block_table.shape
+    for t, n in ((held_blocks, "held_blocks"), (cache_seqlens, "cache_seqlens"), (new_tokens, "new_tokens")):
+        _shape(t, (B,), n)
+    _shape(indptr, (B + 1,), "indptr")
+    tokens = 0
+    if slot_map is not None or positions is not None:
+        tokens = (slot_map if slot_map is not None else positions).numel()
+        _shape(slot_map, (tokens,), "slot_map")
+        _shape(positions, (tokens,), "positions")
+    st = _lib.load().pkv_table_update(_ptr(pool), pool.numel() - POOL_HEADER + 1, page_size, _ptr(block_table), width,
+                                      _ptr(held_blocks), _ptr(cache_seqlens), _ptr(new_tokens), B, _ptr(indptr),
+                                      _ptr(slot_map), _ptr(positions), tokens, _ptr(err_flag), _stream(pool.device))
+    _check(st, "pkv_table_update")
+
+
+def pkv_tree_build(parents, qo_indptr, cache_seqlens, max_nodes: int, mask=None, positions=None, err_flag=None):
+    """Ancestor masks (int32 words, bit j of node i: j is i or an ancestor)
+    and positions ``cache_seqlens[b] + depth`` of drafted trees; ``parents``
+    ``[total_q]`` holds the parent's index within the row, or -1.  Returns
+    ``(mask, positions)``."""
+    for t, n in ((parents, "parents"), (qo_indptr, "qo_indptr"), (cache_seqlens, "cache_seqlens"), (mask, "mask"),
+                 (positions, "positions"), (err_flag, "err_flag")):
+        _i32(t, n)
+    T, B = parents.shape[0], cache_seqlens.shape[0]
+    if mask is None:
+        mask = torch.empty(T, (max_nodes + 31) // 32, dtype=torch.int32, device=parents.device)
+    if positions is None:
+        positions = torch.empty(T, dtype=torch.int32, device=parents.device)
+    _one_device(parents, qo_indptr, cache_seqlens, mask, positions, err_flag)
+    _shape(qo_indptr, (B + 1,), "qo_indptr")
+    _shape(mask, (T, mask.shape[-1]), "mask")
+    _shape(positions, (T,), "positions")
+    st = _lib.load().pkv_tree_build(_ptr(parents), _ptr(qo_indptr), _ptr(cache_seqlens), B, T, max_nodes, _ptr(mask),
+                                    mask.shape[1], _ptr(positions), _ptr(err_flag), _stream(parents.device))
+    _check(st, "pkv_tree_build")
+    return mask, positions
+
+
+def pkv_tree_workspace_size(batch: int, total_q: int, max_blocks: int, num_q_heads: int, max_nodes: int,
+                            desc: CacheDesc) -> int:
+    return int(_lib.load().pkv_tree_workspace_size(batch, total_q, max_blocks, num_q_heads, max_nodes,
+                                                   ctypes.byref(desc)))
+
+
+def tree_workspace(batch: int, total_q: int, max_blocks: int, num_q_heads: int, max_nodes: int, desc: CacheDesc,
+                   device) -> torch.Tensor:
+    """A workspace for pkv_tree_attn (needs no initialisation)."""
+    n = pkv_tree_workspace_size(batch, total_q, max_blocks, num_q_heads, max_nodes, desc)
+    if n == 0:
+        raise PkvError(EUNSUPPORTED, "pkv_tree_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def pkv_tree_attn(k_cache, v_cache, q, k_new, v_new, qo_indptr, tree_mask, block_table, cache_seqlens,
+                  softmax_scale: float, max_nodes: int, out=None, lse=None, workspace=None, err_flag=None,
+                  layout: int = NHD) -> torch.Tensor:
+    """Append of every row's drafted tokens (``k_new``/``v_new`` ``[total_q,
+    Hkv, D]``, or both None when cached already), then attention of every node
+    over its row's ``cache_seqlens[b]`` cached keys and the drafted ones whose
+    bit ``tree_mask`` ``[total_q, words]`` sets.  Returns ``out`` ``[total_q,
+    Hq, D]`` bf16."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (q, "q"), (k_new, "k_new"), (v_new, "v_new"),
+                 (out, "out")):
+        _bf16(t, n)
+    for t, n in ((qo_indptr, "qo_indptr"), (tree_mask, "tree_mask"), (block_table, "block_table"),
+                 (cache_seqlens, "cache_seqlens"), (err_flag, "err_flag")):
+        _i32(t, n)
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse: expected contiguous float32")
+    desc = cache_desc(k_cache, layout)
+    T, Hq, D = q.shape
+    B, width = block_table.shape
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        workspace = tree_workspace(B, T, width, Hq, max_nodes, desc, q.device)
+    _one_device(q, k_cache, v_cache, k_new, v_new, qo_indptr, tree_mask, block_table, cache_seqlens, out, lse,
+                workspace, err_flag)
+    _shape(v_cache, k_cache.shape, "v_cache")
+    _shape(q, (T, Hq, desc.head_dim), "q")
+    _shape(k_new, (T, desc.num_kv_heads, D), "k_new")
+    _shape(v_new, (T, desc.num_kv_heads, D), "v_new")
+    _shape(out, q.shape, "out")
+    _shape(lse, (T, Hq), "lse")
+    _shape(qo_indptr, (B + 1,), "qo_indptr")
+    _shape(cache_seqlens, (B,), "cache_seqlens")
+    _shape(tree_mask, (T, tree_mask.shape[-1]), "tree_mask")
+    st = _lib.load().pkv_tree_attn(
+        ctypes.byref(desc), _ptr(k_cache), _ptr(v_cache), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(qo_indptr),
+        _ptr(tree_mask), tree_mask.shape[1], _ptr(block_table), width, _ptr(cache_seqlens), B, Hq, T, int(max_nodes),
+        float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(err_flag),
+        _stream(q.device))
+    _check(st, "pkv_tree_attn")
+    return out
+
+
+def pkv_tree_accept(parents, draft_tokens, target_tokens, root_targets, qo_indptr, cache_seqlens, max_nodes: int,
+                    path=None, path_len=None, next_token=None, seqlens_out=None, err_flag=None):
+    """The path of drafted tokens that the target model chose itself.  Returns
+    ``(path [B, max_path], path_len [B], next_token [B], seqlens_out [B])``;
+    ``root_targets`` None accepts each row's first root unseen."""
+    for t, n in ((parents, "parents"), (draft_tokens, "draft_tokens"), (target_tokens, "target_tokens"),
+                 (root_targets, "root_targets"), (qo_indptr, "qo_indptr"), (cache_seqlens, "cache_seqlens"),
+                 (path, "path"), (path_len, "path_len"), (next_token, "next_token"), (seqlens_out, "seqlens_out"),
+                 (err_flag, "err_flag")):
+        _i32(t, n)
+    T, B, dev = parents.shape[0], cache_seqlens.shape[0], parents.device
+    if path is None:
+        path = torch.empty(B, max_nodes, dtype=torch.int32, device=dev)
+    if path_len is None:
+        path_len = torch.empty(B, dtype=torch.int32, device=dev)
+    if next_token is None:
+        next_token = torch.empty(B, dtype=torch.int32, device=dev)
+    if seqlens_out is None:
+        seqlens_out = torch.empty(B, dtype=torch.int32, device=dev)
+    _one_device(parents, draft_tokens, target_tokens, root_targets, qo_indptr, cache_seqlens, path, path_len,
+                next_token, seqlens_out, err_flag)
+    _shape(draft_tokens, (T,), "draft_tokens")
+    _shape(target_tokens, (T,), "target_tokens")
+    _shape(qo_indptr, (B + 1,), "qo_indptr")
+    _shape(path, (B, path.shape[-1]), "path")
+    for t, n in ((root_targets, "root_targets"), (path_len, "path_len"), (next_token, "next_token"),
+                 (seqlens_out, "seqlens_out")):
+        _shape(t, (B,), n)
+    st = _lib.load().pkv_tree_accept(_ptr(parents), _ptr(draft_tokens), _ptr(target_tokens), _ptr(root_targets),
+                                     _ptr(qo_indptr), _ptr(cache_seqlens), B, T, max_nodes, _ptr(path), path.shape[1],
+                                     _ptr(path_len), _ptr(next_token), _ptr(seqlens_out), _ptr(err_flag), _stream(dev))
+    _check(st, "pkv_tree_accept")
+    return path, path_len, next_token, seqlens_out
+
+
+class LayerCaches:
+    """The K and V pools of a model's layers, which share one block table, as
+    :func:`pkv_tree_commit` takes them (keeps the tensors alive)."""
+
+    def __init__(self, k_caches, v_caches, layout: int = NHD):
+        if len(k_caches) != len(v_caches) or len(k_caches) < 1:
+            raise ValueError("one k and one v cache per layer")
+        for t in (*k_caches, *v_caches):
+            _bf16(t, "caches")
+            _shape(t, k_caches[0].shape, "caches")
+            if t.device != k_caches[0].device:
+                raise ValueError("caches on different devices")
+        self._keep = (list(k_caches), list(v_caches))
+        arr = ctypes.c_void_p * len(k_caches)
+        self.k_ptrs, self.v_ptrs = (arr(*[t.data_ptr() for t in lst]) for lst in self._keep)
+        self.num_layers = len(k_caches)
+        self.desc = cache_desc(k_caches[0], layout)
+        self.device = k_caches[0].device
+
+
+def pkv_tree_commit(layers: LayerCaches, path, path_len, block_table, cache_seqlens, err_flag=None) -> None:
+    """Moves the K/V of each row's accepted nodes ``path[b, :path_len[b]]``
+    from position ``cache_seqlens[b] + path[b, i]`` to ``cache_seqlens[b] +
+    i`` in every layer (``cache_seqlens`` without the accepted tokens)."""
+    for t, n in ((path, "path"), (path_len, "path_len"), (block_table, "block_table"),
+                 (cache_seqlens, "cache_seqlens"), (err_flag, "err_flag")):
+        _i32(t, n)
+    B, width = block_table.shape
+    _one_device(layers._keep[0][0], path, path_len, block_table, cache_seqlens, err_flag)
+    _shape(path, (B, path.shape[-1]), "path")
+    _shape(path_len, (B,), "path_len")
+    _shape(cache_seqlens, (B,), "cache_seqlens")
+    st = _lib.load().pkv_tree_commit(ctypes.byref(layers.desc), layers.num_layers, layers.k_ptrs, layers.v_ptrs,
+                                     _ptr(path), path.shape[1], _ptr(path_len), _ptr(block_table), width,
+                                     _ptr(cache_seqlens), B, _ptr(err_flag), _stream(layers.device))
+    _check(st, "pkv_tree_commit")
 
 
 def pkv_pool_bytes(desc: CacheDesc) -> int:

@@ -25,27 +25,6 @@ int log2_exact(int x)
     return s;
 }
 
-// Geometry checks shared by every entry point.
-pkv_status check_desc(const pkv_cache_desc *d)
-{
-    if (d == nullptr)
-        return PKV_EINVAL;
-    if (d->num_pages < 2 || d->num_kv_heads < 1 || d->page_size < 1 || d->head_dim < 1)
-        return PKV_EINVAL;
-    if (d->layout != PKV_NHD && d->layout != PKV_HND)
-        return PKV_EINVAL;
-    if (log2_exact(d->page_size) < 0 || d->page_size > 256)
-        return PKV_EUNSUPPORTED;
-    if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256)
-        return PKV_EUNSUPPORTED;
-    // TMA coordinates are int32: the token (NHD) or page-head (HND) axis must fit.
-    const int64_t rows = d->layout == PKV_NHD ? (int64_t)d->num_pages * d->page_size
-                                              : (int64_t)d->num_pages * d->num_kv_heads;
-    if (rows > INT32_MAX)
-        return PKV_EUNSUPPORTED;
-    return PKV_OK;
-}
-
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -72,6 +51,27 @@ int current_device()
 constexpr int kMaxDevices = 64;
 
 } // namespace
+
+// Geometry checks shared by every entry point.
+pkv_status check_desc(const pkv_cache_desc *d)
+{
+    if (d == nullptr)
+        return PKV_EINVAL;
+    if (d->num_pages < 2 || d->num_kv_heads < 1 || d->page_size < 1 || d->head_dim < 1)
+        return PKV_EINVAL;
+    if (d->layout != PKV_NHD && d->layout != PKV_HND)
+        return PKV_EINVAL;
+    if (log2_exact(d->page_size) < 0 || d->page_size > 256)
+        return PKV_EUNSUPPORTED;
+    if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256)
+        return PKV_EUNSUPPORTED;
+    // TMA coordinates are int32: the token (NHD) or page-head (HND) axis must fit.
+    const int64_t rows = d->layout == PKV_NHD ? (int64_t)d->num_pages * d->page_size
+                                              : (int64_t)d->num_pages * d->num_kv_heads;
+    if (rows > INT32_MAX)
+        return PKV_EUNSUPPORTED;
+    return PKV_OK;
+}
 
 int sm_count(int device)
 {
@@ -590,6 +590,84 @@ pkv_status pkv_mixed_attn(const pkv_cache_desc *desc, void *k_cache, void *v_cac
             return PKV_ECUDA;
     }
     return PKV_OK;
+}
+
+size_t pkv_tree_workspace_size(int32_t batch, int32_t total_q, int32_t max_blocks, int32_t num_q_heads,
+                               int32_t max_nodes, const pkv_cache_desc *desc)
+{
+    TreeShape shape;
+    if (tree_shape(batch, total_q, max_blocks, num_q_heads, max_nodes, desc, &shape) != PKV_OK)
+        return 0;
+    return shape.bytes;
+}
+
+pkv_status pkv_tree_attn(const pkv_cache_desc *desc, void *k_cache, void *v_cache, const void *q, const void *k_new,
+                         const void *v_new, const int32_t *qo_indptr, const int32_t *tree_mask, int32_t mask_words,
+                         const int32_t *block_table, int32_t max_blocks, const int32_t *cache_seqlens, int32_t batch,
+                         int32_t num_q_heads, int32_t total_q, int32_t max_nodes, float softmax_scale, void *out,
+                         float *lse, void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream)
+{
+    TreeShape shape;
+    const pkv_status st = tree_shape(batch, total_q, max_blocks, num_q_heads, max_nodes, desc, &shape);
+    if (st != PKV_OK)
+        return st;
+    if (!isfinite(softmax_scale) || (k_new == nullptr) != (v_new == nullptr) || mask_words * 32 < max_nodes)
+        return PKV_EINVAL;
+    if (mask_words > kTreeMaxNodes / 32)
+        return PKV_EUNSUPPORTED;
+    if (batch == 0 || total_q == 0)
+        return PKV_OK;
+    if (k_cache == nullptr || v_cache == nullptr || q == nullptr || out == nullptr || qo_indptr == nullptr ||
+        tree_mask == nullptr || block_table == nullptr || cache_seqlens == nullptr)
+        return PKV_EINVAL;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(q) || !aligned16(out) ||
+        (k_new != nullptr && (!aligned16(k_new) || !aligned16(v_new))))
+        return PKV_EINVAL;
+    if (workspace == nullptr || workspace_bytes < shape.bytes || !aligned16(workspace))
+        return PKV_EWORKSPACE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (k_new != nullptr) {
+        AppendArgs a;
+        a.desc = *desc;
+        a.page_shift = log2_exact(desc->page_size);
+        a.k_cache = k_cache;
+        a.v_cache = v_cache;
+        a.k_new = k_new;
+        a.v_new = v_new;
+        a.num_tokens = total_q;
+        a.append_indptr = qo_indptr;
+        a.block_table = block_table;
+        a.max_blocks = max_blocks;
+        a.cache_seqlens = cache_seqlens;
+        a.batch = batch;
+        a.err_flag = err_flag;
+        a.max_count = max_nodes;
+        if (launch_append(a, s) != cudaSuccess)
+            return PKV_ECUDA;
+    }
+    TreeArgs t;
+    t.desc = *desc;
+    t.batch = batch;
+    t.num_q_heads = num_q_heads;
+    t.total_q = total_q;
+    t.max_blocks = max_blocks;
+    t.max_nodes = max_nodes;
+    t.mask_words = mask_words;
+    t.q_scale = softmax_scale * 1.4426950408889634f;
+    t.qo_indptr = qo_indptr;
+    t.tree_mask = tree_mask;
+    t.block_table = block_table;
+    t.cache_seqlens = cache_seqlens;
+    t.k_cache = k_cache;
+    t.v_cache = v_cache;
+    t.q = q;
+    t.out = out;
+    t.lse = lse;
+    t.workspace = workspace;
+    t.err_flag = err_flag;
+    t.shape = shape;
+    t.after_append = k_new != nullptr;
+    return launch_tree_attn(t, s) == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
 } // extern "C"

@@ -153,6 +153,9 @@ CUresult encode_group_map(CUtensorMap *map, const pkv_cache_desc &d, void *base,
 
 int sm_count(int device);
 
+// Geometry checks shared by every entry point.
+pkv_status check_desc(const pkv_cache_desc *d);
+
 // ---------------------------------------------------------------- prefill
 
 // Largest batch one prefill call plans for (the plan lives in shared memory).
@@ -214,5 +217,39 @@ int prefill_box_tokens(int page_size);
 // The K and V tensor maps the prefill kernel for this head_dim reads.
 bool encode_prefill_maps(const pkv_cache_desc &d, const void *k_cache, const void *v_cache, PrefillMaps *maps);
 
+// ------------------------------------------------------------------- tree
+
+constexpr int kTreeMaxNodes = 256; // drafted tokens of a row
+constexpr int kMaxTreeBatch = 1024;
+
+struct TreeShape {
+    int group; // num_q_heads / num_kv_heads
+    size_t bytes;
+};
+
+// Every size check of pkv_tree_attn; fills `s` on PKV_OK.
+pkv_status tree_shape(int batch, int total_q, int max_blocks, int num_q_heads, int max_nodes,
+                      const pkv_cache_desc *desc, TreeShape *s);
+
+struct TreeArgs {
+    pkv_cache_desc desc;
+    int batch, num_q_heads, total_q, max_blocks, max_nodes, mask_words;
+    float q_scale; // softmax_scale * log2(e)
+    const int32_t *qo_indptr;
+    const int32_t *tree_mask;
+    const int32_t *block_table;
+    const int32_t *cache_seqlens; // without the drafted tokens
+    const void *k_cache;
+    const void *v_cache;
+    const void *q;
+    void *out;
+    float *lse;
+    void *workspace;
+    int32_t *err_flag;
+    TreeShape shape;
+    bool after_append; // this call's append kernel precedes on the stream
+};
+
+cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t stream);
 
 } // namespace pkv
