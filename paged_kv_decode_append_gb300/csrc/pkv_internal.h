@@ -223,7 +223,10 @@ constexpr int kTreeMaxNodes = 256; // drafted tokens of a row
 constexpr int kMaxTreeBatch = 1024;
 
 struct TreeShape {
-    int group; // num_q_heads / num_kv_heads
+    int group;     // num_q_heads / num_kv_heads
+    int q_tile;    // nodes of a work unit: 128 MMA rows
+    int slot_rows; // rows of a partial result
+    size_t off_ml, off_o; // partial results in the workspace, after the CTAs' records
     size_t bytes;
 };
 
@@ -251,5 +254,12 @@ struct TreeArgs {
 };
 
 cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t stream);
+
+// K and V maps (encode_group_map, boxes of min(page_size, 64) tokens) and a map
+// of q [total_q, num_q_heads, head_dim] with boxes of box_nodes nodes x one kv
+// head's query heads x 64 columns (128-byte swizzle).
+bool encode_tree_maps(const pkv_cache_desc &desc, const void *k_cache, const void *v_cache, const void *q,
+                      int num_q_heads, int total_q, int group, int box_nodes, CUtensorMap *k, CUtensorMap *v,
+                      CUtensorMap *qm);
 
 } // namespace pkv

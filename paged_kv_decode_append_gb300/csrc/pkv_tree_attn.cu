@@ -1,124 +1,1124 @@
 // pkv_tree_attn.cu -- attention of a tree of drafted tokens over the paged
-// cache: node i of row b attends the row's L_b cached keys and drafted key j
-// iff bit j of its mask is set (include/pkv.h).
+// cache, on the 5th-generation tensor cores (tcgen05, TMEM accumulators).
+//
+// What it computes.  Node i of row b attends the row's L_b cached keys and
+// drafted key j (position L_b + j) iff bit j of its mask is set
+// (include/pkv.h): S = Q K^T, p = exp2(S scale log2(e) - m), O = p V / sum p.
+//
+// What bounds it.  A unit is (row, kv head, up to 128 (node, head) pairs): one
+// MMA row tile, so a K/V byte is read once for all of them.  Per 128 keys at
+// head_dim 128 a unit reads 64 KB, 1.45 us of an SM's share of the measured
+// HBM rate, and needs 24 MMAs of 128 x 128 x 16 (8 for S, 16 for P V, whose P
+// is kept as two bf16 parts), about 0.8 us: memory bounds it up to 128 pairs
+// whatever their number, the tensor pipe beyond (the next unit finds the same
+// K/V in L2).
+//
+// How (one persistent CTA per SM):
+//  - The units are laid end to end as a line of positions (kStartCost for the
+//    fixed cost of a unit, then its 64-token blocks) and every CTA takes an
+//    equal range, so a long row is shared by many CTAs.  Each CTA finds its
+//    range itself from the row arrays: no plan kernel, no host readback.
+//  - A unit inside one CTA's range is finished there.  The others leave (m, l)
+//    and O in the workspace, fp32, and a second kernel joins them in range
+//    order (results do not depend on timing).  A CTA has at most two such
+//    slices: the one it starts in and the one it ends in.
+//  - Warps: 0 loads K, 2 loads V, each with TMA into a ring of its own (one
+//    lane per box, a box per page piece); 3 loads Q (TMA); 1 owns TMEM and one
+//    thread of it issues the MMAs; 4-7 and 8-11 are two softmax groups that take
+//    alternate tiles, one thread per MMA row.  While one group is at tile t the
+//    tensor pipe runs S of tile t + 1 and P V of tile t - 1.
+//  - The groups share one O and one running maximum: (m, l) of a row go from
+//    group to group through shared memory, m as soon as a tile's maximum is
+//    known, so the other group is hardly ever held up.  m moves only when a
+//    score exceeds it by more than 2^8 (then O is rescaled); the weights are
+//    taken as 2^(s - m - 8) <= 1, so a large value cannot overflow before the
+//    division.
+//  - P replaces S in TMEM as bf16 hi + lo parts (16 significant bits; 8 alone
+//    leave errors of 2^-9 of the row's scale in small outputs).
+//  - Tiles with drafted keys take their visibility as four 32-bit words per
+//    row, shifted out of the node's mask.  V of drafted tokens is looked
+//    through in shared memory: an infinity or NaN there is replaced by 0 for
+//    the MMA (0 * inf would reach nodes that do not see it) and added in the
+//    epilogue to the nodes that do.
+#include <cuda_bf16.h>
 #include <math.h>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "pkv_tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
-struct TreeParams {
-    const __nv_bfloat16 *q, *k, *v;
+constexpr int kTaRows = 128;      // M of every MMA
+constexpr int kTaBlock = 64;      // tokens per position of the work line
+constexpr int kStartCost = 2;     // positions that a unit costs before its first block
+constexpr int kMinBlocks = 2;     // a unit is not cut nearer than this to its ends
+constexpr int kMinRange = 6;      // positions that are worth a CTA of their own
+constexpr int kTaMaxCtas = 160;   // persistent CTAs the workspace has room for
+constexpr int kTaKWarp = 0, kTaMmaWarp = 1, kTaVWarp = 2, kTaQWarp = 3, kTaSoftmaxWarp = 4;
+constexpr int kTaThreads = 384;
+constexpr int kFlags = 16;        // slices whose flags are kept: more than the loads run ahead of the epilogue
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kLn2 = 0.693147180559945309f;
+
+// Record of a CTA's shared slices (combine kernel).
+constexpr int kHeadValid = 1, kHeadEnd = 2, kTail = 4, kHeadBad = 8, kTailBad = 16;
+
+template <int D> struct TaCfg {
+    static constexpr int kTile = D == 256 ? 64 : 128;             // tokens per step
+    static constexpr uint32_t kItemBytes = kTile * D * 2;         // K or V of a step
+    static constexpr int kKStages = D == 64 ? 6 : D == 128 ? 3 : 2;
+    static constexpr int kVStages = D == 64 ? 6 : 3;
+    static constexpr uint32_t kGroupStride = 8 * D * 2;           // 8 token rows, all of head_dim
+    static constexpr uint32_t kQBytes = kTaRows * D * 2;          // [D / 64][128 rows][128 B], swizzled
+    static constexpr uint32_t kQBlock = kTaRows * 128;
+    static constexpr uint32_t kOffK = 0;
+    static constexpr uint32_t kOffV = kOffK + kKStages * kItemBytes;
+    static constexpr uint32_t kOffQ = kOffV + kVStages * kItemBytes;
+    static constexpr uint32_t kOffBar = kOffQ + kQBytes;
+    static constexpr uint32_t kOffChain = kOffBar + 1024;         // m [128], l [128]
+    static constexpr uint32_t kSmem = kOffChain + 1024 + 1024;    // + alignment slack
+    static constexpr int kOBufs = D == 256 ? 1 : 2;
+    static constexpr uint32_t kColS = kOBufs * D;                 // two S buffers of kTile columns
+    static constexpr uint32_t kTmemCols = 512;
+    static_assert(kSmem <= 232448, "shared memory");
+    static_assert(kColS + 2 * kTile <= kTmemCols, "TMEM columns");
+};
+
+struct TaBars {
+    uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+    uint64_t m_set[2][4], l_set[2][4]; // by softmax group and TMEM lane quarter
+    uint64_t drain;
+    int32_t bad[kFlags];       // a page of the slice is out of range
+    int32_t nonfinite[kFlags]; // V of a drafted token holds an infinity or NaN
+    uint32_t tmem_base;
+    int32_t abort;
+};
+static_assert(sizeof(TaBars) <= 1024, "barrier block");
+
+struct TaParams {
     const int32_t *indptr, *mask, *table, *seqlens;
+    const __nv_bfloat16 *v_cache;
     __nv_bfloat16 *out;
     float *lse;
     int32_t *err_flag;
-    int batch, num_q_heads, num_kv_heads, total_q, max_blocks, max_nodes, words;
-    int page_shift, num_pages, layout;
+    int4 *records;     // [CTA]
+    float2 *part_ml;   // [2 * CTA][slot_rows]
+    float *part_o;     // [2 * CTA][slot_rows][D]
+    int batch, num_q_heads, num_kv_heads, group, total_q, max_blocks, max_nodes, words;
+    int page_shift, box_shift, num_pages, layout;
+    int q_tile;        // nodes per unit
+    int slot_rows;
+    uint32_t q_box_bytes;
     float q_scale;
+    int pdl;
+    bool wide;         // out is 32-byte aligned
 };
 
-constexpr int kTreeWarps = 4;
-constexpr float kLn2 = 0.693147180559945309f;
+struct TaMaps {
+    CUtensorMap k, v, q;
+};
 
-// One CTA per (node, query head), its warps on every kTreeWarps-th key: dot
-// product over the lanes, online softmax per warp, merged in shared memory.
-template <int D>
-__global__ void __launch_bounds__(kTreeWarps * 32) tree_attn_kernel(const TreeParams p)
+// ---------------------------------------------------------------- work line
+
+struct TaRow {
+    int first;  // token of node 0
+    int nodes;
+    int len;    // cached tokens
+    int blocks; // 64-token blocks of keys; 0: the row's output is zeroed
+    int tiles;  // units per kv head
+    int err;
+};
+
+// Row b's part in the call (see include/pkv.h); tiles = 0 when it owns no node.
+__device__ __forceinline__ TaRow ta_row(const TaParams &p, int b)
 {
-    constexpr int kPer = D / 32;
-    __shared__ float s_m[kTreeWarps], s_l[kTreeWarps], s_o[kTreeWarps][D];
-    const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int lo = 0, hi = p.batch - 1; // last row whose range starts at or before t
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.indptr[mid] <= t)
-            lo = mid;
-        else
-            hi = mid - 1;
+    TaRow r;
+    r.first = p.indptr[b];
+    const int64_t n = (int64_t)p.indptr[b + 1] - r.first;
+    r.len = p.seqlens[b];
+    r.err = 0;
+    r.blocks = 0;
+    r.nodes = 0;
+    r.tiles = 0;
+    if (r.first < 0 || n < 0 || n > (int64_t)p.total_q - r.first) {
+        r.err = PKV_ERR_QLEN;
+        return r;
     }
-    const int b = lo, first = p.indptr[b];
-    const int64_t n = (int64_t)p.indptr[b + 1] - first;
-    if (first < 0 || n < 0 || n > (int64_t)p.total_q - first) {
-        if (threadIdx.x == 0)
-            set_error(p.err_flag, PKV_ERR_QLEN);
-        return;
-    }
-    if (t < first || t >= first + n)
-        return;
-    const int L = p.seqlens[b];
-    const int64_t keys = (int64_t)L + n;
-    const int32_t *row = p.table + (int64_t)b * p.max_blocks;
-    int err = 0;
-    bool zero = L < 0;
-    if (!zero && n > p.max_nodes)
-        err = PKV_ERR_QLEN;
-    else if (!zero && keys > ((int64_t)p.max_blocks << p.page_shift))
-        err = PKV_ERR_OVERFLOW;
-    else if (!zero) {
-        int bad = 0;
-        for (int64_t k = threadIdx.x; (k << p.page_shift) < keys; k += kTreeWarps * 32)
-            bad |= row[k] < 1 || row[k] >= p.num_pages;
-        if (__syncthreads_or(bad))
-            err = PKV_ERR_PAGE;
-    }
+    r.nodes = (int)n;
+    r.tiles = (r.nodes + p.q_tile - 1) / p.q_tile;
+    const int64_t keys = (int64_t)r.len + n;
     if (n > p.max_nodes)
-        err = PKV_ERR_QLEN;
-    if (threadIdx.x == 0)
-        set_error(p.err_flag, err);
-    zero |= err != 0;
-    const int g = h / (p.num_q_heads / p.num_kv_heads);
-    const __nv_bfloat16 *q = p.q + ((int64_t)t * p.num_q_heads + h) * D;
-    float x[kPer], o[kPer], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        x[e] = __bfloat162float(q[e * 32 + lane]) * p.q_scale;
-        o[e] = 0.f;
+        r.err = PKV_ERR_QLEN;
+    else if (r.len >= 0 && keys > (int64_t)p.max_blocks << p.page_shift)
+        r.err = PKV_ERR_OVERFLOW;
+    else if (r.len >= 0 && n > 0)
+        r.blocks = (int)((keys + kTaBlock - 1) / kTaBlock);
+    if (n == 0)
+        r.err = 0;
+    return r;
+}
+
+// Block at which a cut `x` positions into a unit of `blocks` blocks falls.
+__device__ __forceinline__ int ta_cut(int64_t x, int blocks)
+{
+    const int64_t k = x - kStartCost;
+    if (k < kMinBlocks)
+        return 0;
+    return blocks - k < kMinBlocks ? blocks : (int)k;
+}
+
+// The slices of one CTA's range, in order.  Every role walks them by itself.
+struct TaSlices {
+    TaRow row;
+    int b, unit;        // row, unit within the row
+    int64_t off, left;  // position within the unit, positions left
+    bool fresh;         // `row` is to be read
+    // the current slice
+    int g, rt;          // kv head, row tile
+    int tok0, tok1;     // its tokens (equal: a unit whose output is zeroed)
+    bool begins, ends;
+
+    __device__ __forceinline__ bool next(const TaParams &p)
+    {
+        while (left > 0) {
+            if (fresh) {
+                row = ta_row(p, b);
+                fresh = false;
+            }
+            const int units = row.tiles * p.num_kv_heads;
+            if (unit >= units) {
+                ++b;
+                unit = 0;
+                off = 0;
+                fresh = true;
+                continue;
+            }
+            const int64_t size = kStartCost + row.blocks, take = min(size - off, left);
+            const int a = ta_cut(off, row.blocks), z = off + take >= size ? row.blocks : ta_cut(off + take, row.blocks);
+            const bool at_start = off == 0;
+            const int u = unit;
+            left -= take;
+            off += take;
+            if (off >= size) {
+                ++unit;
+                off = 0;
+            }
+            if (row.blocks == 0 ? !at_start : a >= z)
+                continue;
+            // units of a row: row tiles of a kv head next to one another (their K/V stay in L2)
+            g = u / row.tiles;
+            rt = u - g * row.tiles;
+            begins = a == 0;
+            ends = z == row.blocks;
+            tok0 = a * kTaBlock;
+            tok1 = min(z * kTaBlock, row.blocks == 0 ? 0 : row.len + row.nodes);
+            return true;
+        }
+        return false;
     }
-    for (int64_t k = warp; !zero && k < keys; k += kTreeWarps) {
-        const int j = (int)(k - L);
-        if (j >= 0 && !((uint32_t)p.mask[(int64_t)t * p.words + (j >> 5)] >> (j & 31) & 1u))
+    // MMA rows in use
+    __device__ __forceinline__ int rows(const TaParams &p) const
+    {
+        return min(p.q_tile, row.nodes - rt * p.q_tile) * p.group;
+    }
+};
+
+// The tiles of those slices, one after the other.
+template <int D> struct TaTiles {
+    TaSlices s;
+    int j;  // tile within the slice
+    int nt; // tiles of the slice
+    int gt; // tiles before this one
+    int live; // slices with tiles before this one
+
+    __device__ __forceinline__ void start(const TaSlices &from)
+    {
+        s = from;
+        j = nt = 0;
+        gt = live = -1;
+    }
+    __device__ __forceinline__ bool next(const TaParams &p)
+    {
+        ++j;
+        while (j >= nt) {
+            if (!s.next(p))
+                return false;
+            j = 0;
+            nt = (s.tok1 - s.tok0 + TaCfg<D>::kTile - 1) / TaCfg<D>::kTile;
+        }
+        ++gt;
+        live += j == 0;
+        return true;
+    }
+    __device__ __forceinline__ int tok() const { return s.tok0 + j * TaCfg<D>::kTile; }
+    __device__ __forceinline__ int tokens() const { return min(TaCfg<D>::kTile, s.tok1 - tok()); }
+    __device__ __forceinline__ bool last() const { return j == nt - 1; }
+};
+
+// ---------------------------------------------------------------- waits
+
+__device__ __noinline__ bool ta_wait_slow(uint64_t *bar, uint32_t parity, TaBars &bars, int32_t *err_flag)
+{
+    const uint64_t start = globaltimer_ns();
+    volatile int32_t *abort = &bars.abort;
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity))
+                return true;
+        if (*abort != 0)
+            return false;
+        if (globaltimer_ns() - start > kWaitLimitNs) {
+            *abort = 1;
+            set_error(err_flag, PKV_ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// Bounded wait for the phase of the given parity; gives up when another role has.
+__device__ __forceinline__ bool ta_wait(uint64_t *bar, uint32_t parity, TaBars &bars, int32_t *err_flag)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    return ta_wait_slow(bar, parity, bars, err_flag);
+}
+// The same for a whole warp: all lanes get the same answer.
+__device__ __forceinline__ bool ta_wait_all(uint64_t *bar, uint32_t parity, TaBars &bars, int32_t *err_flag)
+{
+    return __all_sync(0xffffffffu, ta_wait(bar, parity, bars, err_flag));
+}
+
+// ---------------------------------------------------------------- loads
+
+// One warp loads all K (or all V) tiles of the CTA, one box per lane: boxes of
+// min(page, 64) tokens, at most kTile / 8 = 16.  A page id outside the pool
+// loads nothing and marks the slice.
+template <int D>
+__device__ void ta_load_kv(const TaParams &p, const CUtensorMap *map, uint8_t *ring, uint64_t *full, uint64_t *empty,
+                           int stages, int32_t *flags, bool is_k, const TaSlices &from, TaBars &bars, int lane)
+{
+    using C = TaCfg<D>;
+    const int bsh = p.box_shift, BT = 1 << bsh, boxes = C::kTile >> bsh;
+    const uint32_t box_bytes = (uint32_t)BT * D * 2;
+    const bool nhd = p.layout == PKV_NHD;
+    // Lane i holds the page of box i of the tile.
+    auto page_of = [&](const TaTiles<D> &t) {
+        const int tok = t.tok() + (lane << bsh);
+        int id = 0;
+        if (lane < boxes && tok < t.s.tok1)
+            id = p.table[(int64_t)t.s.b * p.max_blocks + (tok >> p.page_shift)];
+        return id;
+    };
+    TaTiles<D> t, ahead;
+    t.start(from);
+    bool more = t.next(p);
+    int id = more ? page_of(t) : 0;
+    int slot = 0, issued = 0;
+    uint32_t round = 0; // times the ring has been filled
+    while (more) {
+        ahead = t;
+        const bool ahead_more = ahead.next(p);
+        const int id_ahead = ahead_more ? page_of(ahead) : 0;
+        if (t.j == 0 && lane == 0) // a new slice: its flag starts clear
+            *(volatile int32_t *)&flags[t.live % kFlags] = 0;
+        if (round > 0 && !ta_wait_all(&empty[slot], (round - 1) & 1, bars, p.err_flag))
+            break;
+        const int tok = t.tok() + (lane << bsh);
+        const bool want = lane < boxes && tok < t.s.tok1;
+        const bool good = want && id >= 1 && id < p.num_pages;
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, good));
+        const bool bad = __any_sync(0xffffffffu, want && !good);
+        if (lane == 0) {
+            if (bad && is_k)
+                *(volatile int32_t *)&flags[t.live % kFlags] = 1;
+            mbar_arrive_expect_tx(&full[slot], n * box_bytes);
+        }
+        __syncwarp();
+        if (good) {
+            const int in_page = tok & ((1 << p.page_shift) - 1);
+            const int c3 = nhd ? ((id << p.page_shift) + in_page) >> 3 : in_page >> 3;
+            const int c4 = nhd ? t.s.g : id * p.num_kv_heads + t.s.g;
+            tma_load_5d_plain(ring + slot * C::kItemBytes + lane * box_bytes, map, 0, 0, 0, c3, c4, &full[slot]);
+        }
+        ++issued;
+        if (++slot == stages) {
+            slot = 0;
+            ++round;
+        }
+        t = ahead;
+        id = id_ahead;
+        more = ahead_more;
+    }
+    // Copies still in flight (a role gave up): they land before the CTA ends.
+    for (int k = issued > stages ? issued - stages : 0; k < issued; ++k)
+        mbar_wait(&full[k % stages], (uint32_t)(k / stages) & 1);
+}
+
+// Q of every slice: [node][head] rows of 64-column blocks.
+template <int D>
+__device__ void ta_load_q(const TaParams &p, const CUtensorMap *map, uint8_t *q_smem, const TaSlices &from, TaBars &bars)
+{
+    using C = TaCfg<D>;
+    TaSlices s = from;
+    uint32_t uc = 0;
+    while (s.next(p)) {
+        if (s.tok0 >= s.tok1)
             continue;
-        const int64_t page = row[k >> p.page_shift], slot = k & ((1 << p.page_shift) - 1);
+        if (uc > 0 && !ta_wait(&bars.q_empty, (uc - 1) & 1, bars, p.err_flag))
+            break;
+        mbar_arrive_expect_tx(&bars.q_full, p.q_box_bytes * (D / 64));
+        for (int c = 0; c < D / 64; ++c)
+            tma_load_3d_plain(q_smem + c * C::kQBlock, map, c * 64, s.g * p.group, s.row.first + s.rt * p.q_tile,
+                              &bars.q_full);
+        ++uc;
+    }
+    if (uc > 0)
+        mbar_wait(&bars.q_full, (uc - 1) & 1);
+}
+
+// ---------------------------------------------------------------- MMA
+
+template <int D>
+__device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t tmem, const TaSlices &from)
+{
+    using C = TaCfg<D>;
+    constexpr uint32_t kIdescS = tc_idesc_bf16(kTaRows, C::kTile, false, false);
+    constexpr uint32_t kIdescO = tc_idesc_bf16(kTaRows, D, false, true);
+    const uint32_t k_base = smem_addr(smem + C::kOffK), v_base = smem_addr(smem + C::kOffV);
+    const uint64_t qd = tc_sw128_desc(smem_addr(smem + C::kOffQ), 16, 1024);
+    TaTiles<D> t;
+    t.start(from);
+    bool issued = false, more = t.next(p);
+    uint32_t units = 0;         // slices whose S has begun
+    int prev = -1;              // tile whose P V is due
+    int prev_tokens = 0;
+    bool prev_first = false;
+    uint32_t prev_unit = 0;
+    while (more || prev >= 0) {
+        if (more) { // S of this tile
+            const int slot = t.gt % C::kKStages;
+            if (t.j == 0) {
+                if (!ta_wait(&bars.q_full, units & 1, bars, p.err_flag))
+                    break;
+                ++units;
+            }
+            if (!ta_wait(&bars.k_full[slot], (uint32_t)(t.gt / C::kKStages) & 1, bars, p.err_flag))
+                break;
+            tc_fence_after();
+            issued = true;
+            const uint32_t d = tmem + C::kColS + (uint32_t)(t.gt & 1) * C::kTile;
+            const uint64_t kd = tc_sw128_desc(k_base + slot * C::kItemBytes, 16, C::kGroupStride);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                tc_mma_bf16(d, qd + (uint64_t)(((kk >> 2) * C::kQBlock + (kk & 3) * 32) >> 4),
+                            kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), kIdescS, kk > 0 ? 1u : 0u);
+            tc_commit(&bars.s_full[t.gt & 1]);
+            tc_commit(&bars.k_empty[slot]);
+            if (t.last())
+                tc_commit(&bars.q_empty);
+        }
+        if (prev >= 0) { // O += P V of the tile before
+            const int slot = prev % C::kVStages;
+            const uint32_t ob = C::kOBufs == 1 ? 0 : prev_unit & 1, use = C::kOBufs == 1 ? prev_unit : prev_unit >> 1;
+            if (!ta_wait(&bars.p_full[prev & 1], (uint32_t)(prev >> 1) & 1, bars, p.err_flag))
+                break;
+            if (prev_first && use > 0 && !ta_wait(&bars.o_free[ob], (use - 1) & 1, bars, p.err_flag))
+                break;
+            if (!ta_wait(&bars.v_full[slot], (uint32_t)(prev / C::kVStages) & 1, bars, p.err_flag))
+                break;
+            tc_fence_after();
+            const uint32_t pt = tmem + C::kColS + (uint32_t)(prev & 1) * C::kTile, o = tmem + ob * D;
+            const uint64_t vd = tc_sw128_desc(v_base + slot * C::kItemBytes, 1024, C::kGroupStride);
+            const int steps = (prev_tokens + 15) >> 4; // 16 keys each
+            for (int k = 0; k < steps; ++k) {
+                const uint32_t a = pt + 32 * (k >> 1) + 8 * (k & 1); // hi part; the lo part 16 columns on
+                const uint64_t b = vd + (uint64_t)((2 * k * C::kGroupStride) >> 4);
+                tc_mma_bf16_ts(o, a, b, kIdescO, !prev_first || k > 0 ? 1u : 0u);
+                tc_mma_bf16_ts(o, a + 16, b, kIdescO, 1u);
+            }
+            tc_commit(&bars.o_done[prev & 1]);
+            tc_commit(&bars.v_empty[slot]);
+            prev = -1;
+        }
+        if (more) {
+            prev = t.gt;
+            prev_tokens = t.tokens();
+            prev_first = t.j == 0;
+            prev_unit = units - 1;
+            more = t.next(p);
+        }
+    }
+    if (issued) {
+        tc_commit(&bars.drain);
+        mbar_wait(&bars.drain, 0);
+    }
+}
+
+// ---------------------------------------------------------------- softmax
+
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr)
+                 : "memory");
+}
+// Waits for the loads issued before; the registers pass through it, so that
+// nothing is computed from them earlier.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+__device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Which of the 32 keys from drafted index j0 on (negative: cached) a node
+// sees: cached ones all, drafted ones by its mask, none at and past `nodes`.
+__device__ __forceinline__ uint32_t ta_seen(const TaParams &p, const int32_t *mask, int nodes, int j0)
+{
+    auto word = [&](int w) { // drafted keys 32 w .. 32 w + 31
+        if (w < 0)
+            return 0xffffffffu;
+        if (w * 32 >= nodes)
+            return 0u;
+        const uint32_t x = (uint32_t)mask[w];
+        return nodes - w * 32 >= 32 ? x : x & ((1u << (nodes - w * 32)) - 1u);
+    };
+    const int w = j0 >> 5, sh = j0 & 31;
+    return sh == 0 ? word(w) : __funnelshift_r(word(w), word(w + 1), sh);
+}
+
+// 32 bytes to global memory; one store where the address allows it (`wide`).
+__device__ __forceinline__ void store32(void *dst, const uint32_t *w, bool wide)
+{
+    if (!wide) {
+        static_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        return;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ bool bf16_nonfinite(uint32_t half)
+{
+    return (half & 0x7f80u) == 0x7f80u;
+}
+
+// V rows of a tile in shared memory: rows r0 .. r1 - 1 (past the keys, up to a
+// multiple of 16) become 0; rows d0 .. r0 - 1 (drafted tokens) are looked
+// through and lose their infinities and NaN.  Returns whether there were any.
+template <int D>
+__device__ bool ta_clean_v(uint8_t *vb, int d0, int r0, int r1, int thread)
+{
+    using C = TaCfg<D>;
+    constexpr int kPieces = D / 8; // 16-byte pieces of a row
+    bool found = false;
+    for (int i = thread; i < (r1 - d0) * kPieces; i += kTaRows) {
+        const int row = d0 + i / kPieces, piece = i % kPieces;
+        uint4 *at = reinterpret_cast<uint4 *>(vb + (row >> 3) * C::kGroupStride + (piece >> 3) * 1024 + (row & 7) * 128 +
+                                              (piece & 7) * 16);
+        if (row >= r0) {
+            *at = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+        }
+        uint4 x = *at;
+        bool hit = false;
+        uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (bf16_nonfinite(w[k])) {
+                w[k] &= 0xffff0000u;
+                hit = true;
+            }
+            if (bf16_nonfinite(w[k] >> 16)) {
+                w[k] &= 0xffffu;
+                hit = true;
+            }
+        }
+        if (hit) {
+            *at = x;
+            found = true;
+        }
+    }
+    return found;
+}
+
+// What the infinities and NaN of drafted tokens j0 .. j1 - 1 add to column
+// `col` of a node that sees those in `mask` (rare; read again from the cache).
+template <int D>
+__device__ __noinline__ float ta_nonfinite(const TaParams &p, int b, int len, int g, const int32_t *mask, int j0, int j1,
+                                           int col)
+{
+    float sum = 0.f;
+    for (int j = j0; j < j1; ++j) {
+        if (!((uint32_t)mask[j >> 5] >> (j & 31) & 1u))
+            continue;
+        const int tok = len + j;
+        const int64_t page = p.table[(int64_t)b * p.max_blocks + (tok >> p.page_shift)];
+        if (page < 1 || page >= p.num_pages)
+            continue;
+        const int64_t slot = tok & ((1 << p.page_shift) - 1);
         const int64_t at = p.layout == PKV_NHD ? (((page << p.page_shift) + slot) * p.num_kv_heads + g) * D
                                                : (((page * p.num_kv_heads + g) << p.page_shift) + slot) * D;
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e)
-            s += x[e] * __bfloat162float(p.k[at + e * 32 + lane]);
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, w);
-        const float top = fmaxf(m, s), scale = exp2f(m - top), e2 = exp2f(s - top);
-        m = top;
-        l = l * scale + e2;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e)
-            o[e] = o[e] * scale + e2 * __bfloat162float(p.v[at + e * 32 + lane]);
+        const uint32_t v = reinterpret_cast<const uint16_t *>(p.v_cache)[at + col];
+        if (bf16_nonfinite(v))
+            sum += __uint_as_float(v << 16);
     }
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-    }
+    return sum;
+}
+
+// One of the two softmax groups (group gi takes the tiles of parity gi); thread
+// = MMA row.  Both groups finish every slice, half of O's columns each.
+template <int D>
+__device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t tmem, const TaSlices &from, int warp,
+                           int lane)
+{
+    using C = TaCfg<D>;
+    constexpr int kChunks = C::kTile / 32;
+    const int gi = (warp - kTaSoftmaxWarp) >> 2;
+    const int quarter = warp & 3; // TMEM lanes this warp may access
+    const int r = quarter * 32 + lane;
+    const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16);
+    float *m_chain = reinterpret_cast<float *>(smem + C::kOffChain), *l_chain = m_chain + kTaRows;
+    const float qs = p.q_scale, qse = qs > 0.f ? qs : 1.f;
+    const int node_in_tile = r / p.group, head_in_group = r - node_in_tile * p.group;
+    int gt = 0;         // tiles before this slice
+    uint32_t units = 0; // slices with tiles before this one
+    int record = 0;
+    int4 tail = make_int4(0, 0, 0, 0);
+
+    TaSlices s = from;
+    while (s.next(p)) {
+        const int rows = s.rows(p);
+        const bool live = r < rows, warp_live = quarter * 32 < rows;
+        const int node = s.rt * p.q_tile + node_in_tile;
+        const int64_t token = (int64_t)s.row.first + node;
+        const int64_t out_row = token * p.num_q_heads + s.g * p.group + head_in_group;
+        if (s.tok0 >= s.tok1) { // a row that is inactive or in error: zeros
+            if (s.g == 0 && s.rt == 0 && r == 0 && gi == 0)
+                set_error(p.err_flag, s.row.err);
+            if (live) {
+                const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                for (int c = gi * (D / 2); c < (gi + 1) * (D / 2); c += 16)
+                    store32(p.out + out_row * D + c, zero, p.wide);
+                if (gi == 0 && p.lse != nullptr)
+                    p.lse[out_row] = -INFINITY;
+            }
+            continue;
+        }
+        const int32_t *mask = p.mask + (live ? token : (int64_t)s.row.first) * p.words;
+        const int nt = (s.tok1 - s.tok0 + C::kTile - 1) / C::kTile;
+        float m = -INFINITY, l = 0.f;
+        for (int j = (gt + gi) & 1; j < nt; j += 2) { // gt + j has parity gi
+            const int tile = gt + j;
+            const int tok = s.tok0 + j * C::kTile, tokens = min(C::kTile, s.tok1 - tok);
+            if (!ta_wait_all(&bars.s_full[gi], (uint32_t)(tile >> 1) & 1, bars, p.err_flag))
+                return;
+            tc_fence_after();
+            const uint32_t s_col = t_row + C::kColS + (uint32_t)gi * C::kTile;
+            // which keys the node sees, where some are drafted or past the slice's end
+            const bool masked = tok + C::kTile > s.row.len || tokens < C::kTile;
+            uint32_t seen[kChunks];
+            if (masked) {
 #pragma unroll
-    for (int e = 0; e < kPer; ++e)
-        s_o[warp][e * 32 + lane] = o[e];
+                for (int c = 0; c < kChunks; ++c) {
+                    const int end = tokens - 32 * c;
+                    seen[c] = ta_seen(p, mask, s.row.nodes, tok + 32 * c - s.row.len) &
+                              (end >= 32 ? 0xffffffffu : end <= 0 ? 0u : (1u << end) - 1u);
+                }
+            }
+            // scores of chunk c; a positive scale is folded into the exponent
+            auto finish = [&](int c, uint32_t (&x)[32]) {
+                if (!(qs > 0.f)) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = __float_as_uint(__uint_as_float(x[i]) * qs);
+                }
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = seen[c] >> i & 1u ? x[i] : 0xff800000u;
+                }
+            };
+            float mx = -INFINITY;
+            if (warp_live) {
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < kChunks; c += 2) {
+                    uint32_t x[2][32];
+                    tmem_ld32_issue(s_col + 32 * c, x[0]);
+                    tmem_ld32_issue(s_col + 32 * c + 32, x[1]);
+                    tmem_ld_wait(x[0]);
+                    tmem_ld_wait(x[1]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        finish(c + h, x[h]);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[h][i]));
+                    }
+                }
+                mx = live ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qse : -INFINITY;
+            }
+            // the row's maximum so far comes from the other group, which had the tile before
+            float before = -INFINITY;
+            if (j > 0) {
+                if (!ta_wait_all(&bars.m_set[1 - gi][quarter], (uint32_t)((tile - 1) >> 1) & 1, bars, p.err_flag))
+                    return;
+                before = m_chain[r];
+            }
+            const bool grow = mx > before + kRescaleLog2;
+            m = grow ? mx : before;
+            m_chain[r] = m;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars.m_set[gi][quarter]);
+            const float alpha = grow ? ex2_approx(before - m) : 1.f; // 0 on the first tile
+            float2 sum2 = make_float2(0.f, 0.f);
+            if (warp_live) {
+                const float m_ref = m == -INFINITY ? 0.f : m + kRescaleLog2;
+                const float2 q2 = make_float2(qse, qse), nm2 = make_float2(-m_ref, -m_ref);
+                uint32_t x[2][32];
+                tmem_ld32_issue(s_col, x[0]);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    uint32_t (&y)[32] = x[c & 1];
+                    tmem_ld_wait(y);
+                    if (c + 1 < kChunks)
+                        tmem_ld32_issue(s_col + 32 * c + 32, x[(c + 1) & 1]);
+                    finish(c, y);
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 a = ffma2(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), q2,
+                                               nm2);
+                        const float2 w = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+                        sum2 = __fadd2_rn(sum2, w);
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(w.x, w.y);
+                        const float2 hf = __bfloat1622float2(h);
+                        const float2 d = __fadd2_rn(w, make_float2(-hf.x, -hf.y));
+                        const __nv_bfloat162 lw = __floats2bfloat162_rn(d.x, d.y);
+                        hi[e] = *reinterpret_cast<const uint32_t *>(&h);
+                        lo[e] = *reinterpret_cast<const uint32_t *>(&lw);
+                    }
+                    tmem_st16_issue(s_col + 32 * c, hi);
+                    tmem_st16_issue(s_col + 32 * c + 16, lo);
+                }
+                tmem_st_wait();
+            }
+            // O holds this slice's sum only after its first P V
+            const uint32_t o_col = t_row + (C::kOBufs == 1 ? 0u : (units & 1) * D);
+            const bool rescale = grow && before != -INFINITY;
+            if (__any_sync(0xffffffffu, rescale)) {
+                if (!ta_wait_all(&bars.o_done[(tile - 1) & 1], (uint32_t)((tile - 1) >> 1) & 1, bars, p.err_flag))
+                    return;
+                tc_fence_after();
+                const float a = rescale ? alpha : 1.f;
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o_col + c, o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+                    tmem_st32(o_col + c, o);
+                }
+            }
+            if (tok + tokens > s.row.len || (tokens & 15) != 0) {
+                const int slot = tile % C::kVStages;
+                if (!ta_wait_all(&bars.v_full[slot], (uint32_t)(tile / C::kVStages) & 1, bars, p.err_flag))
+                    return;
+                const int d0 = min(tokens, max(0, s.row.len - tok));
+                if (ta_clean_v<D>(smem + C::kOffV + slot * C::kItemBytes, d0, tokens, (tokens + 15) & ~15, r))
+                    *(volatile int32_t *)&bars.nonfinite[units % kFlags] = 1;
+                fence_proxy_async_smem(); // before the MMA's reads
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars.p_full[gi]);
+            // the row's sum, when the other group has added its tile
+            if (j > 0) {
+                if (!ta_wait_all(&bars.l_set[1 - gi][quarter], (uint32_t)((tile - 1) >> 1) & 1, bars, p.err_flag))
+                    return;
+                l = l_chain[r];
+            }
+            l = l * alpha + (sum2.x + sum2.y);
+            l_chain[r] = l;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars.l_set[gi][quarter]);
+        }
+        const int end = gt + nt - 1; // the slice's last tile
+        if ((end & 1) != gi) {
+            if (!ta_wait_all(&bars.l_set[1 - gi][quarter], (uint32_t)(end >> 1) & 1, bars, p.err_flag))
+                return;
+            m = m_chain[r]; // not written again before this group's next tile
+            l = l_chain[r];
+        }
+        if (!ta_wait_all(&bars.o_done[end & 1], (uint32_t)(end >> 1) & 1, bars, p.err_flag))
+            return;
+        tc_fence_after();
+        const bool bad = *(volatile int32_t *)&bars.bad[units % kFlags] != 0;
+        const bool nonfinite = *(volatile int32_t *)&bars.nonfinite[units % kFlags] != 0;
+        const uint32_t o_col = t_row + (C::kOBufs == 1 ? 0u : (units & 1) * D);
+        const bool whole = s.begins && s.ends;
+        const int64_t part = (int64_t)(2 * blockIdx.x + (s.begins ? 1 : 0)) * p.slot_rows + r;
+        const float inv = whole && l > 0.f ? 1.f / l : l != l ? l : 0.f;
+        for (int c = gi * (D / 2); warp_live && c < (gi + 1) * (D / 2); c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_col + c, o);
+            if (nonfinite && live) {
+                const int j0 = max(0, s.tok0 - s.row.len), j1 = min(s.row.nodes, s.tok1 - s.row.len);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    o[e] = __float_as_uint(__uint_as_float(o[e]) +
+                                           ta_nonfinite<D>(p, s.b, s.row.len, s.g, mask, j0, j1, c + e));
+            }
+            if (!live)
+                continue;
+            if (whole) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv,
+                                                                   __uint_as_float(o[2 * e + 1]) * inv);
+                    w[e] = bad || l == 0.f ? 0u : *reinterpret_cast<const uint32_t *>(&h);
+                }
+                store32(p.out + out_row * D + c, w, p.wide);
+                store32(p.out + out_row * D + c + 16, w + 8, p.wide);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                    store32(p.part_o + part * D + c + e, o + e, true);
+            }
+        }
+        if (live && gi == 0) {
+            if (!whole)
+                p.part_ml[part] = make_float2(m, l);
+            else if (p.lse != nullptr)
+                p.lse[out_row] = bad || l == 0.f ? -INFINITY : (m + kRescaleLog2 + log2f(l)) * kLn2;
+        }
+        if (r == 0 && gi == 0) {
+            if (bad)
+                set_error(p.err_flag, PKV_ERR_PAGE);
+            if (!s.begins)
+                record |= kHeadValid | (s.ends ? kHeadEnd : 0) | (bad ? kHeadBad : 0);
+            else if (!s.ends) {
+                record |= kTail | (bad ? kTailBad : 0);
+                tail = make_int4(0, s.row.first + s.rt * p.q_tile, s.g, rows);
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&bars.o_free[C::kOBufs == 1 ? 0 : units & 1]);
+        gt += nt;
+        ++units;
+    }
+    if (r == 0 && gi == 0) {
+        tail.x = record;
+        p.records[blockIdx.x] = tail;
+    }
+}
+
+// ---------------------------------------------------------------- kernel
+
+// Positions of row b on the work line.
+__device__ __forceinline__ int64_t ta_positions(const TaParams &p, const TaRow &r)
+{
+    return (int64_t)r.tiles * p.num_kv_heads * (kStartCost + r.blocks);
+}
+
+// This CTA's range: prefix sum of the rows' positions (in `scratch`), equal parts, and the row and unit its part starts in.
+__device__ void ta_start(const TaParams &p, int64_t *scratch, TaSlices *out)
+{
+    int64_t *s_warp = scratch + kMaxTreeBatch + 1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.batch + kTaThreads - 1) / kTaThreads; // consecutive rows of a thread
+    int64_t sum = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b < p.batch) {
+            const TaRow r = ta_row(p, b);
+            sum += ta_positions(p, r);
+            if (blockIdx.x == 0 && r.tiles == 0)
+                set_error(p.err_flag, r.err); // no unit reports it
+        }
+    }
+    int64_t x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    if (lane == 31)
+        s_warp[warp] = x;
     __syncthreads();
-    float top = -INFINITY, total = 0.f;
-    for (int w = 0; w < kTreeWarps; ++w)
-        top = fmaxf(top, s_m[w]);
-    for (int w = 0; w < kTreeWarps; ++w)
-        total += s_m[w] == -INFINITY ? 0.f : s_l[w] * exp2f(s_m[w] - top);
-    for (int c = threadIdx.x; c < D; c += kTreeWarps * 32) {
-        float sum = 0.f;
-        for (int w = 0; w < kTreeWarps; ++w)
-            sum += s_m[w] == -INFINITY ? 0.f : s_o[w][c] * exp2f(s_m[w] - top);
-        p.out[((int64_t)t * p.num_q_heads + h) * D + c] = __float2bfloat16_rn(total == 0.f ? 0.f : sum / total);
+    int64_t total = 0;
+    for (int w = 0; w < kTaThreads / 32; ++w) {
+        x += w < warp ? s_warp[w] : 0;
+        total += s_warp[w];
     }
-    if (threadIdx.x == 0 && p.lse != nullptr)
-        p.lse[(int64_t)t * p.num_q_heads + h] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+    x -= sum;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b < p.batch) {
+            scratch[b] = x;
+            x += ta_positions(p, ta_row(p, b));
+        }
+    }
+    __syncthreads();
+    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kMinRange));
+    const int c = blockIdx.x;
+    const int64_t lo = c < ctas ? total * c / ctas : total, hi = c < ctas ? total * (c + 1) / ctas : total;
+    out->left = hi - lo;
+    out->fresh = true;
+    out->b = 0;
+    out->unit = 0;
+    out->off = 0;
+    if (hi > lo) {
+        int a = 0, z = p.batch - 1; // last row that starts at or before lo
+        while (a < z) {
+            const int mid = (a + z + 1) >> 1;
+            if (scratch[mid] <= lo)
+                a = mid;
+            else
+                z = mid - 1;
+        }
+        const TaRow r = ta_row(p, a);
+        const int64_t size = kStartCost + r.blocks, in_row = lo - scratch[a];
+        out->b = a;
+        out->unit = (int)(in_row / size);
+        out->off = in_row - out->unit * size;
+    }
+    __syncthreads(); // the scratch is overwritten by the first copies
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTaThreads, 1)
+    tree_attn_kernel(const __grid_constant__ TaParams p, const __grid_constant__ TaMaps maps)
+{
+    using C = TaCfg<D>;
+    extern __shared__ unsigned char ta_smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ta_smem_raw) + 1023) & ~uintptr_t(1023));
+    TaBars &bars = *reinterpret_cast<TaBars *>(smem + C::kOffBar);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); // the combine kernel waits for this grid
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kKStages; ++i) {
+            mbar_init(&bars.k_full[i], 1);
+            mbar_init(&bars.k_empty[i], 1);
+        }
+        for (int i = 0; i < C::kVStages; ++i) {
+            mbar_init(&bars.v_full[i], 1);
+            mbar_init(&bars.v_empty[i], 1);
+        }
+        mbar_init(&bars.q_full, 1);
+        mbar_init(&bars.q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.p_full[i], 4); // the warps of the tile's group
+            mbar_init(&bars.o_done[i], 1);
+            mbar_init(&bars.o_free[i], 8); // the warps of both groups
+            for (int w = 0; w < 4; ++w) {
+                mbar_init(&bars.m_set[i][w], 1);
+                mbar_init(&bars.l_set[i][w], 1);
+            }
+        }
+        mbar_init(&bars.drain, 1);
+        bars.abort = 0;
+        mbar_init_fence();
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.v);
+        prefetch_tensormap(&maps.q);
+    }
+    if (warp == kTaMmaWarp) {
+        tmem_alloc(&bars.tmem_base, C::kTmemCols);
+        tmem_relinquish();
+    }
+    // The row arrays are read before the append of this call has finished: it
+    // does not write them, and everything before it has.
+    TaSlices from;
+    ta_start(p, reinterpret_cast<int64_t *>(smem + C::kOffK), &from);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (p.pdl)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    fence_proxy_async_smem(); // the scratch's reads and writes before the copies over it
+    const uint32_t tmem = bars.tmem_base;
+    if (threadIdx.x == kTaSoftmaxWarp * 32) // the thread that writes it at the end
+        p.records[blockIdx.x] = make_int4(0, 0, 0, 0);
+
+    if (warp == kTaKWarp)
+        ta_load_kv<D>(p, &maps.k, smem + C::kOffK, bars.k_full, bars.k_empty, C::kKStages, bars.bad, true, from, bars,
+                      lane);
+    else if (warp == kTaVWarp)
+        ta_load_kv<D>(p, &maps.v, smem + C::kOffV, bars.v_full, bars.v_empty, C::kVStages, bars.nonfinite, false, from,
+                      bars, lane);
+    else if (warp == kTaQWarp) {
+        if (lane == 0)
+            ta_load_q<D>(p, &maps.q, smem + C::kOffQ, from, bars);
+        __syncwarp();
+    } else if (warp == kTaMmaWarp) {
+        if (lane == 0)
+            ta_mma<D>(p, smem, bars, tmem, from);
+        __syncwarp();
+    } else
+        ta_softmax<D>(p, smem, bars, tmem, from, warp, lane);
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kTaMmaWarp)
+        tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// ---------------------------------------------------------------- combine
+
+constexpr int kCombineThreads = 128;
+constexpr int kCombineParts = 8; // blocks per shared unit
+
+// Joins the slices of the unit that CTA blockIdx.x began and did not end: out =
+// sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, over the CTAs after it up to
+// the one that ended it, in that order.  D / 8 threads per MMA row.
+template <int D>
+__global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __grid_constant__ TaParams p, int ctas)
+{
+    __shared__ int s_slot[kTaMaxCtas + 1];
+    __shared__ int s_n, s_bad;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c0 = blockIdx.x, tid = threadIdx.x;
+    const int4 rec = p.records[c0];
+    if (!(rec.x & kTail))
+        return;
+    if (tid < 32) {
+        int n = 1;
+        int bad = rec.x & kTailBad;
+        if (tid == 0)
+            s_slot[0] = 2 * c0 + 1;
+        for (int base = c0 + 1; base < ctas; base += 32) {
+            const int flags = base + tid < ctas ? p.records[base + tid].x : 0;
+            const uint32_t ends = __ballot_sync(0xffffffffu, flags & kHeadEnd);
+            const int stop = ends != 0 ? __ffs(ends) - 1 : 31;
+            const bool mine = tid <= stop && (flags & kHeadValid);
+            const uint32_t valid = __ballot_sync(0xffffffffu, mine);
+            bad |= __any_sync(0xffffffffu, mine && (flags & kHeadBad));
+            if (mine)
+                s_slot[n + __popc(valid & ((1u << tid) - 1u))] = 2 * (base + tid);
+            n += __popc(valid);
+            if (ends != 0)
+                break;
+        }
+        if (tid == 0) {
+            s_n = n;
+            s_bad = bad;
+        }
+    }
+    __syncthreads();
+    const int n = s_n;
+    constexpr int kPerRow = D / 8;
+    const int col = tid % kPerRow * 8;
+    for (int row = blockIdx.y * (kCombineThreads / kPerRow) + tid / kPerRow; row < rec.w;
+         row += kCombineParts * (kCombineThreads / kPerRow)) {
+        float m = -INFINITY;
+        for (int i = 0; i < n; ++i)
+            m = fmaxf(m, p.part_ml[(int64_t)s_slot[i] * p.slot_rows + row].x);
+        float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const int64_t at = (int64_t)s_slot[i] * p.slot_rows + row;
+            const float2 ml = p.part_ml[at];
+            const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+            const float4 a = *reinterpret_cast<const float4 *>(p.part_o + at * D + col);
+            const float4 b = *reinterpret_cast<const float4 *>(p.part_o + at * D + col + 4);
+            if (ml.x == -INFINITY) // nothing seen there: its O is all zeros (or no sum at all)
+                continue;
+            l += w * ml.y;
+            o[0] += w * a.x, o[1] += w * a.y, o[2] += w * a.z, o[3] += w * a.w;
+            o[4] += w * b.x, o[5] += w * b.y, o[6] += w * b.z, o[7] += w * b.w;
+        }
+        const bool zero = s_bad != 0 || l == 0.f;
+        const float inv = 1.f / l;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
+            w[e] = zero ? 0u : *reinterpret_cast<const uint32_t *>(&h);
+        }
+        const int64_t out_row = ((int64_t)rec.y + row / p.group) * p.num_q_heads + rec.z * p.group + row % p.group;
+        *reinterpret_cast<uint4 *>(p.out + out_row * D + col) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (col == 0 && p.lse != nullptr)
+            p.lse[out_row] = zero ? -INFINITY : (m + kRescaleLog2 + log2f(l)) * kLn2;
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+struct TaEntry {
+    int D;
+    const void *attn, *combine;
+    uint32_t smem;
+};
+
+const TaEntry kTaTable[] = {
+    {64, reinterpret_cast<const void *>(&tree_attn_kernel<64>), reinterpret_cast<const void *>(&tree_combine_kernel<64>),
+     TaCfg<64>::kSmem},
+    {128, reinterpret_cast<const void *>(&tree_attn_kernel<128>),
+     reinterpret_cast<const void *>(&tree_combine_kernel<128>), TaCfg<128>::kSmem},
+    {256, reinterpret_cast<const void *>(&tree_attn_kernel<256>),
+     reinterpret_cast<const void *>(&tree_combine_kernel<256>), TaCfg<256>::kSmem},
+};
+
+const TaEntry *ta_find(int D)
+{
+    for (const TaEntry &e : kTaTable)
+        if (e.D == D)
+            return &e;
+    return nullptr;
+}
+
+// Once per device: the kernel's shared memory.
+bool ta_ready(int device, const TaEntry *e)
+{
+    constexpr int kDevices = 64;
+    static bool done[kDevices][3] = {};
+    if (device < 0 || device >= kDevices)
+        return false;
+    bool &slot = done[device][e - kTaTable];
+    if (!slot)
+        slot = cudaFuncSetAttribute(e->attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)e->smem) == cudaSuccess;
+    return slot;
 }
 
 } // namespace
@@ -133,29 +1133,42 @@ pkv_status tree_shape(int batch, int total_q, int max_blocks, int num_q_heads, i
         num_q_heads % desc->num_kv_heads != 0)
         return PKV_EINVAL;
     s->group = num_q_heads / desc->num_kv_heads;
-    if (batch > kMaxTreeBatch || max_nodes > kTreeMaxNodes || desc->page_size < 8 || s->group > 128 ||
+    if (batch > kMaxTreeBatch || max_nodes > kTreeMaxNodes || desc->page_size < 8 || s->group > kTaRows ||
         (int64_t)total_q * num_q_heads >= ((int64_t)1 << 31))
         return PKV_EUNSUPPORTED;
-    s->bytes = 256;
+    s->q_tile = kTaRows / s->group;
+    s->slot_rows = (s->q_tile < max_nodes ? s->q_tile : max_nodes) * s->group;
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    s->off_ml = up(kTaMaxCtas * sizeof(int4));
+    s->off_o = s->off_ml + up((size_t)2 * kTaMaxCtas * s->slot_rows * sizeof(float2));
+    s->bytes = 256 + s->off_o + up((size_t)2 * kTaMaxCtas * s->slot_rows * desc->head_dim * sizeof(float));
     return PKV_OK;
 }
 
 cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t stream)
 {
-    TreeParams p;
-    p.q = static_cast<const __nv_bfloat16 *>(a.q);
-    p.k = static_cast<const __nv_bfloat16 *>(a.k_cache);
-    p.v = static_cast<const __nv_bfloat16 *>(a.v_cache);
+    const TaEntry *e = ta_find(a.desc.head_dim);
+    int dev = 0;
+    if (e == nullptr || cudaGetDevice(&dev) != cudaSuccess || !ta_ready(dev, e))
+        return cudaErrorInvalidValue;
+    unsigned char *ws =
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(a.workspace) + 255) & ~uintptr_t(255));
+    TaParams p;
     p.indptr = a.qo_indptr;
     p.mask = a.tree_mask;
     p.table = a.block_table;
     p.seqlens = a.cache_seqlens;
+    p.v_cache = static_cast<const __nv_bfloat16 *>(a.v_cache);
     p.out = static_cast<__nv_bfloat16 *>(a.out);
     p.lse = a.lse;
     p.err_flag = a.err_flag;
+    p.records = reinterpret_cast<int4 *>(ws);
+    p.part_ml = reinterpret_cast<float2 *>(ws + a.shape.off_ml);
+    p.part_o = reinterpret_cast<float *>(ws + a.shape.off_o);
     p.batch = a.batch;
     p.num_q_heads = a.num_q_heads;
     p.num_kv_heads = a.desc.num_kv_heads;
+    p.group = a.shape.group;
     p.total_q = a.total_q;
     p.max_blocks = a.max_blocks;
     p.max_nodes = a.max_nodes;
@@ -163,17 +1176,43 @@ cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t stream)
     p.page_shift = 0;
     while ((1 << p.page_shift) < a.desc.page_size)
         ++p.page_shift;
+    p.box_shift = p.page_shift < 6 ? p.page_shift : 6;
     p.num_pages = a.desc.num_pages;
     p.layout = a.desc.layout;
+    p.q_tile = a.shape.q_tile;
+    p.slot_rows = a.shape.slot_rows;
     p.q_scale = a.q_scale;
-    const dim3 grid(a.total_q, a.num_q_heads);
-    if (a.desc.head_dim == 64)
-        tree_attn_kernel<64><<<grid, kTreeWarps * 32, 0, stream>>>(p);
-    else if (a.desc.head_dim == 128)
-        tree_attn_kernel<128><<<grid, kTreeWarps * 32, 0, stream>>>(p);
-    else
-        tree_attn_kernel<256><<<grid, kTreeWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    p.pdl = a.after_append ? 1 : 0;
+    p.wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+    const int box_nodes = a.shape.slot_rows / a.shape.group < a.total_q ? a.shape.slot_rows / a.shape.group : a.total_q;
+    p.q_box_bytes = (uint32_t)box_nodes * a.shape.group * 128;
+    TaMaps m;
+    if (!encode_tree_maps(a.desc, a.k_cache, a.v_cache, a.q, a.num_q_heads, a.total_q, a.shape.group, box_nodes, &m.k,
+                          &m.v, &m.q))
+        return cudaErrorInvalidValue;
+
+    const int grid = sm_count(dev) < kTaMaxCtas ? sm_count(dev) : kTaMaxCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kTaThreads);
+    cfg.dynamicSmemBytes = e->smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.pdl ? 1 : 0;
+    void *args[] = {&p, &m};
+    cudaError_t err = cudaLaunchKernelExC(&cfg, e->attn, args);
+    if (err != cudaSuccess)
+        return err;
+    int ctas = grid;
+    cfg.gridDim = dim3(grid, kCombineParts);
+    cfg.blockDim = dim3(kCombineThreads);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    void *combine_args[] = {&p, &ctas};
+    return cudaLaunchKernelExC(&cfg, e->combine, combine_args);
 }
 
 } // namespace pkv
