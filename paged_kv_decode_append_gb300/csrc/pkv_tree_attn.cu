@@ -460,31 +460,6 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
 
 // ---------------------------------------------------------------- softmax
 
-__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                 : "r"(taddr)
-                 : "memory");
-}
-// Waits for the loads issued before; the registers pass through it, so that
-// nothing is computed from them earlier.
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
-}
-
 __device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t (&r)[16])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -644,47 +619,35 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                 return;
             tc_fence_after();
             const uint32_t s_col = t_row + C::kColS + (uint32_t)gi * C::kTile;
-            // which keys the node sees, where some are drafted or past the slice's end
+            // Tiles with drafted keys or past the slice's end, and scales that cannot
+            // be folded into the exponent: S is rewritten once, so that the
+            // passes below are the same short loops for every tile.
             const bool masked = tok + C::kTile > s.row.len || tokens < C::kTile;
-            uint32_t seen[kChunks];
-            if (masked) {
-#pragma unroll
+            if (warp_live && (masked || !(qs > 0.f))) {
+                const float by = qs > 0.f ? 1.f : qs;
+#pragma unroll 1
                 for (int c = 0; c < kChunks; ++c) {
                     const int end = tokens - 32 * c;
-                    seen[c] = ta_seen(p, mask, s.row.nodes, tok + 32 * c - s.row.len) &
-                              (end >= 32 ? 0xffffffffu : end <= 0 ? 0u : (1u << end) - 1u);
+                    const uint32_t seen = ta_seen(p, mask, s.row.nodes, tok + 32 * c - s.row.len) &
+                                          (end >= 32 ? 0xffffffffu : end <= 0 ? 0u : (1u << end) - 1u);
+                    uint32_t x[32];
+                    tmem_ld32(s_col + 32 * c, x);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = seen >> i & 1u ? __float_as_uint(__uint_as_float(x[i]) * by) : 0xff800000u;
+                    tmem_st32(s_col + 32 * c, x);
                 }
             }
-            // scores of chunk c; a positive scale is folded into the exponent
-            auto finish = [&](int c, uint32_t (&x)[32]) {
-                if (!(qs > 0.f)) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        x[i] = __float_as_uint(__uint_as_float(x[i]) * qs);
-                }
-                if (masked) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        x[i] = seen[c] >> i & 1u ? x[i] : 0xff800000u;
-                }
-            };
             float mx = -INFINITY;
             if (warp_live) {
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                for (int c = 0; c < kChunks; ++c) {
+                    uint32_t x[32];
+                    tmem_ld32(s_col + 32 * c, x);
 #pragma unroll
-                for (int c = 0; c < kChunks; c += 2) {
-                    uint32_t x[2][32];
-                    tmem_ld32_issue(s_col + 32 * c, x[0]);
-                    tmem_ld32_issue(s_col + 32 * c + 32, x[1]);
-                    tmem_ld_wait(x[0]);
-                    tmem_ld_wait(x[1]);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        finish(c + h, x[h]);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[h][i]));
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[i]));
                 }
                 mx = live ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qse : -INFINITY;
             }
@@ -706,15 +669,10 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
             if (warp_live) {
                 const float m_ref = m == -INFINITY ? 0.f : m + kRescaleLog2;
                 const float2 q2 = make_float2(qse, qse), nm2 = make_float2(-m_ref, -m_ref);
-                uint32_t x[2][32];
-                tmem_ld32_issue(s_col, x[0]);
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < kChunks; ++c) {
-                    uint32_t (&y)[32] = x[c & 1];
-                    tmem_ld_wait(y);
-                    if (c + 1 < kChunks)
-                        tmem_ld32_issue(s_col + 32 * c + 32, x[(c + 1) & 1]);
-                    finish(c, y);
+                    uint32_t y[32];
+                    tmem_ld32(s_col + 32 * c, y);
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -723,8 +681,7 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                         const float2 w = make_float2(ex2_approx(a.x), ex2_approx(a.y));
                         sum2 = __fadd2_rn(sum2, w);
                         const __nv_bfloat162 h = __floats2bfloat162_rn(w.x, w.y);
-                        const float2 hf = __bfloat1622float2(h);
-                        const float2 d = __fadd2_rn(w, make_float2(-hf.x, -hf.y));
+                        const float2 d = ffma2(__bfloat1622float2(h), make_float2(-1.f, -1.f), w);
                         const __nv_bfloat162 lw = __floats2bfloat162_rn(d.x, d.y);
                         hi[e] = *reinterpret_cast<const uint32_t *>(&h);
                         lo[e] = *reinterpret_cast<const uint32_t *>(&lw);
@@ -742,6 +699,7 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                     return;
                 tc_fence_after();
                 const float a = rescale ? alpha : 1.f;
+#pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     tmem_ld32(o_col + c, o);
@@ -792,6 +750,7 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
         const bool whole = s.begins && s.ends;
         const int64_t part = (int64_t)(2 * blockIdx.x + (s.begins ? 1 : 0)) * p.slot_rows + r;
         const float inv = whole && l > 0.f ? 1.f / l : l != l ? l : 0.f;
+#pragma unroll 1
         for (int c = gi * (D / 2); warp_live && c < (gi + 1) * (D / 2); c += 32) {
             uint32_t o[32];
             tmem_ld32(o_col + c, o);
