@@ -22,8 +22,8 @@
 //    and O in the workspace, fp32, and a second kernel joins them in range
 //    order (results do not depend on timing).  A CTA has at most two such
 //    slices: the one it starts in and the one it ends in.
-//  - Warps: 0 loads K, 2 loads V, each with TMA into a ring of its own (one
-//    lane per box, a box per page piece); 3 loads Q (TMA); 1 owns TMEM and one
+//  - Warps: 0 loads Q and K, 2 loads V, with TMA, K and V into a ring each (one
+//    lane per box, a box per page piece); 3 looks V through; 1 owns TMEM and one
 //    thread of it issues the MMAs; 4-7 and 8-11 are two softmax groups that take
 //    alternate tiles, one thread per MMA row.  While one group is at tile t the
 //    tensor pipe runs S of tile t + 1 and P V of tile t - 1.
@@ -37,7 +37,7 @@
 //    leave errors of 2^-9 of the row's scale in small outputs).
 //  - Tiles with drafted keys take their visibility as four 32-bit words per
 //    row, shifted out of the node's mask.  V of drafted tokens is looked
-//    through in shared memory: an infinity or NaN there is replaced by 0 for
+//    through in shared memory before the MMAs read it: an infinity or NaN there is replaced by 0 for
 //    the MMA (0 * inf would reach nodes that do not see it) and added in the
 //    epilogue to the nodes that do.
 #include <cuda_bf16.h>
@@ -56,7 +56,7 @@ constexpr int kStartCost = 2;     // positions that a unit costs before its firs
 constexpr int kMinBlocks = 2;     // a unit is not cut nearer than this to its ends
 constexpr int kMinRange = 6;      // positions that are worth a CTA of their own
 constexpr int kTaMaxCtas = 160;   // persistent CTAs the workspace has room for
-constexpr int kTaKWarp = 0, kTaMmaWarp = 1, kTaVWarp = 2, kTaQWarp = 3, kTaSoftmaxWarp = 4;
+constexpr int kTaKWarp = 0, kTaMmaWarp = 1, kTaVWarp = 2, kTaCheckWarp = 3, kTaSoftmaxWarp = 4;
 constexpr int kTaThreads = 384;
 constexpr int kFlags = 16;        // slices whose flags are kept: more than the loads run ahead of the epilogue
 constexpr float kRescaleLog2 = 8.0f;
@@ -87,8 +87,8 @@ template <int D> struct TaCfg {
 };
 
 struct TaBars {
-    uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
-    uint64_t q_full, q_empty;
+    uint64_t k_full[6], k_empty[6], v_full[6], v_ready[6], v_empty[6];
+    uint64_t q_full;
     uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
     uint64_t m_set[2][4], l_set[2][4]; // by softmax group and TMEM lane quarter
     uint64_t drain;
@@ -256,7 +256,6 @@ template <int D> struct TaTiles {
     }
     __device__ __forceinline__ int tok() const { return s.tok0 + j * TaCfg<D>::kTile; }
     __device__ __forceinline__ int tokens() const { return min(TaCfg<D>::kTile, s.tok1 - tok()); }
-    __device__ __forceinline__ bool last() const { return j == nt - 1; }
 };
 
 // ---------------------------------------------------------------- waits
@@ -294,16 +293,33 @@ __device__ __forceinline__ bool ta_wait_all(uint64_t *bar, uint32_t parity, TaBa
 
 // ---------------------------------------------------------------- loads
 
+// The Q rows of a slice: [node][head], a 64-column block at a time.
+template <int D>
+__device__ __forceinline__ void ta_load_q(const TaParams &p, const CUtensorMap *map, uint8_t *q_smem, const TaSlices &s,
+                                          TaBars &bars)
+{
+    mbar_arrive_expect_tx(&bars.q_full, p.q_box_bytes * (D / 64));
+    for (int c = 0; c < D / 64; ++c)
+        tma_load_3d_plain(q_smem + c * TaCfg<D>::kQBlock, map, c * 64, s.g * p.group, s.row.first + s.rt * p.q_tile,
+                          &bars.q_full);
+}
+
 // One warp loads all K (or all V) tiles of the CTA, one box per lane: boxes of
 // min(page, 64) tokens, at most kTile / 8 = 16.  A page id outside the pool
-// loads nothing and marks the slice.
-template <int D>
-__device__ void ta_load_kv(const TaParams &p, const CUtensorMap *map, uint8_t *ring, uint64_t *full, uint64_t *empty,
-                           int stages, int32_t *flags, bool is_k, const TaSlices &from, TaBars &bars, int lane)
+// loads nothing and marks the slice.  The K warp also loads Q: the slot of
+// tile T + kKStages - 1 is free when S of tile T - 1 is done, which is when a
+// slice that begins with tile T may have the Q buffer.
+template <int D, bool IS_K>
+__device__ void ta_load(const TaParams &p, const TaMaps &maps, uint8_t *smem, TaBars &bars, const TaSlices &from,
+                        int lane)
 {
     using C = TaCfg<D>;
-    const int bsh = p.box_shift, BT = 1 << bsh, boxes = C::kTile >> bsh;
-    const uint32_t box_bytes = (uint32_t)BT * D * 2;
+    constexpr int kStages = IS_K ? C::kKStages : C::kVStages;
+    const CUtensorMap *map = IS_K ? &maps.k : &maps.v;
+    uint8_t *ring = smem + (IS_K ? C::kOffK : C::kOffV);
+    uint64_t *full = IS_K ? bars.k_full : bars.v_full, *empty = IS_K ? bars.k_empty : bars.v_empty;
+    const int bsh = p.box_shift, boxes = C::kTile >> bsh;
+    const uint32_t box_bytes = (uint32_t)(1 << bsh) * D * 2;
     const bool nhd = p.layout == PKV_NHD;
     // Lane i holds the page of box i of the tile.
     auto page_of = [&](const TaTiles<D> &t) {
@@ -313,74 +329,155 @@ __device__ void ta_load_kv(const TaParams &p, const CUtensorMap *map, uint8_t *r
             id = p.table[(int64_t)t.s.b * p.max_blocks + (tok >> p.page_shift)];
         return id;
     };
-    TaTiles<D> t, ahead;
+    TaTiles<D> t, ahead, behind; // the next tile's pages are read one ahead; Q comes kStages - 1 behind
     t.start(from);
     bool more = t.next(p);
     int id = more ? page_of(t) : 0;
-    int slot = 0, issued = 0;
+    if (IS_K) {
+        behind = t;
+        if (more && lane == 0)
+            ta_load_q<D>(p, &maps.q, smem + C::kOffQ, t.s, bars);
+    }
+    int slot = 0, issued = 0, q_issued = IS_K && more ? 1 : 0;
     uint32_t round = 0; // times the ring has been filled
-    while (more) {
-        ahead = t;
-        const bool ahead_more = ahead.next(p);
-        const int id_ahead = ahead_more ? page_of(ahead) : 0;
-        if (t.j == 0 && lane == 0) // a new slice: its flag starts clear
-            *(volatile int32_t *)&flags[t.live % kFlags] = 0;
+    for (int x = 0;; ++x) {
+        if (!more && (!IS_K || x >= issued + kStages - 1))
+            break;
         if (round > 0 && !ta_wait_all(&empty[slot], (round - 1) & 1, bars, p.err_flag))
             break;
-        const int tok = t.tok() + (lane << bsh);
-        const bool want = lane < boxes && tok < t.s.tok1;
-        const bool good = want && id >= 1 && id < p.num_pages;
-        const uint32_t n = __popc(__ballot_sync(0xffffffffu, good));
-        const bool bad = __any_sync(0xffffffffu, want && !good);
-        if (lane == 0) {
-            if (bad && is_k)
-                *(volatile int32_t *)&flags[t.live % kFlags] = 1;
-            mbar_arrive_expect_tx(&full[slot], n * box_bytes);
+        if (more) {
+            ahead = t;
+            const bool ahead_more = ahead.next(p);
+            const int id_ahead = ahead_more ? page_of(ahead) : 0;
+            const int tok = t.tok() + (lane << bsh);
+            const bool want = lane < boxes && tok < t.s.tok1;
+            const bool good = want && id >= 1 && id < p.num_pages;
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, good));
+            const bool bad = __any_sync(0xffffffffu, want && !good);
+            if (lane == 0) {
+                if (IS_K && (bad || t.j == 0))
+                    *(volatile int32_t *)&bars.bad[t.live % kFlags] = bad; // a later clean tile leaves the mark
+                mbar_arrive_expect_tx(&full[slot], n * box_bytes);
+            }
+            __syncwarp();
+            if (good) {
+                const int in_page = tok & ((1 << p.page_shift) - 1);
+                const int c3 = nhd ? ((id << p.page_shift) + in_page) >> 3 : in_page >> 3;
+                const int c4 = nhd ? t.s.g : id * p.num_kv_heads + t.s.g;
+                tma_load_5d_plain(ring + slot * C::kItemBytes + lane * box_bytes, map, 0, 0, 0, c3, c4, &full[slot]);
+            }
+            ++issued;
+            t = ahead;
+            id = id_ahead;
+            more = ahead_more;
         }
-        __syncwarp();
-        if (good) {
-            const int in_page = tok & ((1 << p.page_shift) - 1);
-            const int c3 = nhd ? ((id << p.page_shift) + in_page) >> 3 : in_page >> 3;
-            const int c4 = nhd ? t.s.g : id * p.num_kv_heads + t.s.g;
-            tma_load_5d_plain(ring + slot * C::kItemBytes + lane * box_bytes, map, 0, 0, 0, c3, c4, &full[slot]);
+        if (IS_K && x > kStages - 1) {
+            behind.next(p);
+            if (behind.j == 0) {
+                if (lane == 0)
+                    ta_load_q<D>(p, &maps.q, smem + C::kOffQ, behind.s, bars);
+                ++q_issued;
+            }
         }
-        ++issued;
-        if (++slot == stages) {
+        if (++slot == kStages) {
             slot = 0;
             ++round;
         }
-        t = ahead;
-        id = id_ahead;
-        more = ahead_more;
     }
     // Copies still in flight (a role gave up): they land before the CTA ends.
-    for (int k = issued > stages ? issued - stages : 0; k < issued; ++k)
-        mbar_wait(&full[k % stages], (uint32_t)(k / stages) & 1);
+    for (int k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
+        mbar_wait(&full[k % kStages], (uint32_t)(k / kStages) & 1);
+    if (q_issued > 0)
+        mbar_wait(&bars.q_full, (uint32_t)(q_issued - 1) & 1);
 }
 
-// Q of every slice: [node][head] rows of 64-column blocks.
+__device__ __forceinline__ bool bf16_nonfinite(uint32_t half)
+{
+    return (half & 0x7f80u) == 0x7f80u;
+}
+
+// One warp looks V through before the MMAs read it.  Of a tile with drafted
+// tokens it replaces their infinities and NaN by 0 (and marks the slice); rows
+// past the keys, up to the multiple of 16 that the MMAs read, become 0.
 template <int D>
-__device__ void ta_load_q(const TaParams &p, const CUtensorMap *map, uint8_t *q_smem, const TaSlices &from, TaBars &bars)
+__device__ void ta_check_v(const TaParams &p, uint8_t *smem, TaBars &bars, const TaSlices &from, int lane)
 {
     using C = TaCfg<D>;
-    TaSlices s = from;
-    uint32_t uc = 0;
-    while (s.next(p)) {
-        if (s.tok0 >= s.tok1)
-            continue;
-        if (uc > 0 && !ta_wait(&bars.q_empty, (uc - 1) & 1, bars, p.err_flag))
-            break;
-        mbar_arrive_expect_tx(&bars.q_full, p.q_box_bytes * (D / 64));
-        for (int c = 0; c < D / 64; ++c)
-            tma_load_3d_plain(q_smem + c * C::kQBlock, map, c * 64, s.g * p.group, s.row.first + s.rt * p.q_tile,
-                              &bars.q_full);
-        ++uc;
+    constexpr int kPieces = D / 8; // 16-byte pieces of a row
+    TaTiles<D> t;
+    t.start(from);
+    while (t.next(p)) {
+        const int slot = t.gt % C::kVStages, tokens = t.tokens();
+        const uint32_t parity = (uint32_t)(t.gt / C::kVStages) & 1;
+        if (t.j == 0 && lane == 0)
+            *(volatile int32_t *)&bars.nonfinite[t.live % kFlags] = 0;
+        if (!ta_wait_all(&bars.v_full[slot], parity, bars, p.err_flag))
+            return;
+        const int d0 = min(tokens, max(0, t.s.row.len - t.tok())), r1 = (tokens + 15) & ~15;
+        if (d0 < r1) {
+            uint8_t *vb = smem + C::kOffV + slot * C::kItemBytes;
+            bool found = false;
+#pragma unroll 4
+            for (int i = d0 * kPieces + lane; i < r1 * kPieces; i += 32) {
+                const int row = i / kPieces, piece = i % kPieces;
+                uint4 *at = reinterpret_cast<uint4 *>(vb + (row >> 3) * C::kGroupStride + (piece >> 3) * 1024 +
+                                                      (row & 7) * 128 + (piece & 7) * 16);
+                uint4 x = *at;
+                uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+                bool hit = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const bool lo = bf16_nonfinite(w[k]), hi = bf16_nonfinite(w[k] >> 16);
+                    w[k] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0xffffu : 0xffffffffu);
+                    hit |= lo || hi;
+                }
+                const bool past = row >= tokens;
+                if (past)
+                    x = make_uint4(0u, 0u, 0u, 0u);
+                if (hit || past)
+                    *at = x;
+                found |= hit && !past;
+            }
+            if (found)
+                *(volatile int32_t *)&bars.nonfinite[t.live % kFlags] = 1;
+            fence_proxy_async_smem(); // before the MMAs' reads
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&bars.v_ready[slot]);
     }
-    if (uc > 0)
-        mbar_wait(&bars.q_full, (uc - 1) & 1);
 }
 
 // ---------------------------------------------------------------- MMA
+
+// The MMA warp runs as a whole, so that descriptors stay in uniform registers;
+// one elected thread (always the same) issues.
+__device__ __forceinline__ void ta_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred e, p;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+__device__ __forceinline__ void ta_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred e, p;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+__device__ __forceinline__ void ta_commit(uint64_t *bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+                     smem_addr(bar))
+                 : "memory");
+}
 
 template <int D>
 __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t tmem, const TaSlices &from)
@@ -402,11 +499,11 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
         if (more) { // S of this tile
             const int slot = t.gt % C::kKStages;
             if (t.j == 0) {
-                if (!ta_wait(&bars.q_full, units & 1, bars, p.err_flag))
+                if (!ta_wait_all(&bars.q_full, units & 1, bars, p.err_flag))
                     break;
                 ++units;
             }
-            if (!ta_wait(&bars.k_full[slot], (uint32_t)(t.gt / C::kKStages) & 1, bars, p.err_flag))
+            if (!ta_wait_all(&bars.k_full[slot], (uint32_t)(t.gt / C::kKStages) & 1, bars, p.err_flag))
                 break;
             tc_fence_after();
             issued = true;
@@ -414,21 +511,19 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
             const uint64_t kd = tc_sw128_desc(k_base + slot * C::kItemBytes, 16, C::kGroupStride);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-                tc_mma_bf16(d, qd + (uint64_t)(((kk >> 2) * C::kQBlock + (kk & 3) * 32) >> 4),
+                ta_mma_ss(d, qd + (uint64_t)(((kk >> 2) * C::kQBlock + (kk & 3) * 32) >> 4),
                             kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), kIdescS, kk > 0 ? 1u : 0u);
-            tc_commit(&bars.s_full[t.gt & 1]);
-            tc_commit(&bars.k_empty[slot]);
-            if (t.last())
-                tc_commit(&bars.q_empty);
+            ta_commit(&bars.s_full[t.gt & 1]);
+            ta_commit(&bars.k_empty[slot]);
         }
         if (prev >= 0) { // O += P V of the tile before
             const int slot = prev % C::kVStages;
             const uint32_t ob = C::kOBufs == 1 ? 0 : prev_unit & 1, use = C::kOBufs == 1 ? prev_unit : prev_unit >> 1;
-            if (!ta_wait(&bars.p_full[prev & 1], (uint32_t)(prev >> 1) & 1, bars, p.err_flag))
+            if (!ta_wait_all(&bars.p_full[prev & 1], (uint32_t)(prev >> 1) & 1, bars, p.err_flag))
                 break;
-            if (prev_first && use > 0 && !ta_wait(&bars.o_free[ob], (use - 1) & 1, bars, p.err_flag))
+            if (prev_first && use > 0 && !ta_wait_all(&bars.o_free[ob], (use - 1) & 1, bars, p.err_flag))
                 break;
-            if (!ta_wait(&bars.v_full[slot], (uint32_t)(prev / C::kVStages) & 1, bars, p.err_flag))
+            if (!ta_wait_all(&bars.v_ready[slot], (uint32_t)(prev / C::kVStages) & 1, bars, p.err_flag))
                 break;
             tc_fence_after();
             const uint32_t pt = tmem + C::kColS + (uint32_t)(prev & 1) * C::kTile, o = tmem + ob * D;
@@ -437,11 +532,11 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
             for (int k = 0; k < steps; ++k) {
                 const uint32_t a = pt + 32 * (k >> 1) + 8 * (k & 1); // hi part; the lo part 16 columns on
                 const uint64_t b = vd + (uint64_t)((2 * k * C::kGroupStride) >> 4);
-                tc_mma_bf16_ts(o, a, b, kIdescO, !prev_first || k > 0 ? 1u : 0u);
-                tc_mma_bf16_ts(o, a + 16, b, kIdescO, 1u);
+                ta_mma_ts(o, a, b, kIdescO, !prev_first || k > 0 ? 1u : 0u);
+                ta_mma_ts(o, a + 16, b, kIdescO, 1u);
             }
-            tc_commit(&bars.o_done[prev & 1]);
-            tc_commit(&bars.v_empty[slot]);
+            ta_commit(&bars.o_done[prev & 1]);
+            ta_commit(&bars.v_empty[slot]);
             prev = -1;
         }
         if (more) {
@@ -453,7 +548,7 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
         }
     }
     if (issued) {
-        tc_commit(&bars.drain);
+        ta_commit(&bars.drain);
         mbar_wait(&bars.drain, 0);
     }
 }
@@ -473,20 +568,17 @@ __device__ __forceinline__ void tmem_st_wait()
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Which of the 32 keys from drafted index j0 on (negative: cached) a node
-// sees: cached ones all, drafted ones by its mask, none at and past `nodes`.
-__device__ __forceinline__ uint32_t ta_seen(const TaParams &p, const int32_t *mask, int nodes, int j0)
+// Which of the drafted keys 32 w .. 32 w + 31 a node sees (w < 0: cached
+// keys, all of them; none at and past `nodes`).
+__device__ __forceinline__ uint32_t ta_mask_word(const int32_t *mask, int nodes, int w)
 {
-    auto word = [&](int w) { // drafted keys 32 w .. 32 w + 31
-        if (w < 0)
-            return 0xffffffffu;
-        if (w * 32 >= nodes)
-            return 0u;
-        const uint32_t x = (uint32_t)mask[w];
-        return nodes - w * 32 >= 32 ? x : x & ((1u << (nodes - w * 32)) - 1u);
-    };
-    const int w = j0 >> 5, sh = j0 & 31;
-    return sh == 0 ? word(w) : __funnelshift_r(word(w), word(w + 1), sh);
+    if (w < 0)
+        return 0xffffffffu;
+    const int rest = nodes - w * 32;
+    if (rest <= 0)
+        return 0u;
+    const uint32_t x = (uint32_t)mask[w];
+    return rest >= 32 ? x : x & ((1u << rest) - 1u);
 }
 
 // 32 bytes to global memory; one store where the address allows it (`wide`).
@@ -500,50 +592,6 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t *w, bool wide)
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                  "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
-}
-
-__device__ __forceinline__ bool bf16_nonfinite(uint32_t half)
-{
-    return (half & 0x7f80u) == 0x7f80u;
-}
-
-// V rows of a tile in shared memory: rows r0 .. r1 - 1 (past the keys, up to a
-// multiple of 16) become 0; rows d0 .. r0 - 1 (drafted tokens) are looked
-// through and lose their infinities and NaN.  Returns whether there were any.
-template <int D>
-__device__ bool ta_clean_v(uint8_t *vb, int d0, int r0, int r1, int thread)
-{
-    using C = TaCfg<D>;
-    constexpr int kPieces = D / 8; // 16-byte pieces of a row
-    bool found = false;
-    for (int i = thread; i < (r1 - d0) * kPieces; i += kTaRows) {
-        const int row = d0 + i / kPieces, piece = i % kPieces;
-        uint4 *at = reinterpret_cast<uint4 *>(vb + (row >> 3) * C::kGroupStride + (piece >> 3) * 1024 + (row & 7) * 128 +
-                                              (piece & 7) * 16);
-        if (row >= r0) {
-            *at = make_uint4(0u, 0u, 0u, 0u);
-            continue;
-        }
-        uint4 x = *at;
-        bool hit = false;
-        uint32_t *w = reinterpret_cast<uint32_t *>(&x);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (bf16_nonfinite(w[k])) {
-                w[k] &= 0xffff0000u;
-                hit = true;
-            }
-            if (bf16_nonfinite(w[k] >> 16)) {
-                w[k] &= 0xffffu;
-                hit = true;
-            }
-        }
-        if (hit) {
-            *at = x;
-            found = true;
-        }
-    }
-    return found;
 }
 
 // What the infinities and NaN of drafted tokens j0 .. j1 - 1 add to column
@@ -615,6 +663,15 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
         for (int j = (gt + gi) & 1; j < nt; j += 2) { // gt + j has parity gi
             const int tile = gt + j;
             const int tok = s.tok0 + j * C::kTile, tokens = min(C::kTile, s.tok1 - tok);
+            // tiles with drafted keys or past the slice's end: the node's mask words
+            const bool masked = tok + C::kTile > s.row.len || tokens < C::kTile;
+            uint32_t words[kChunks + 1];
+            if (masked) {
+                const int w0 = (tok - s.row.len) >> 5;
+#pragma unroll
+                for (int c = 0; c <= kChunks; ++c)
+                    words[c] = ta_mask_word(mask, s.row.nodes, w0 + c);
+            }
             if (!ta_wait_all(&bars.s_full[gi], (uint32_t)(tile >> 1) & 1, bars, p.err_flag))
                 return;
             tc_fence_after();
@@ -622,14 +679,19 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
             // Tiles with drafted keys or past the slice's end, and scales that cannot
             // be folded into the exponent: S is rewritten once, so that the
             // passes below are the same short loops for every tile.
-            const bool masked = tok + C::kTile > s.row.len || tokens < C::kTile;
             if (warp_live && (masked || !(qs > 0.f))) {
                 const float by = qs > 0.f ? 1.f : qs;
+                const int shift = (tok - s.row.len) & 31;
 #pragma unroll 1
                 for (int c = 0; c < kChunks; ++c) {
                     const int end = tokens - 32 * c;
-                    const uint32_t seen = ta_seen(p, mask, s.row.nodes, tok + 32 * c - s.row.len) &
-                                          (end >= 32 ? 0xffffffffu : end <= 0 ? 0u : (1u << end) - 1u);
+                    uint32_t seen = end >= 32 ? 0xffffffffu : end <= 0 ? 0u : (1u << end) - 1u;
+                    if (masked) {
+                        seen &= __funnelshift_r(words[0], words[1], shift);
+#pragma unroll
+                        for (int w = 0; w < kChunks; ++w)
+                            words[w] = words[w + 1];
+                    }
                     uint32_t x[32];
                     tmem_ld32(s_col + 32 * c, x);
 #pragma unroll
@@ -708,15 +770,6 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                         o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
                     tmem_st32(o_col + c, o);
                 }
-            }
-            if (tok + tokens > s.row.len || (tokens & 15) != 0) {
-                const int slot = tile % C::kVStages;
-                if (!ta_wait_all(&bars.v_full[slot], (uint32_t)(tile / C::kVStages) & 1, bars, p.err_flag))
-                    return;
-                const int d0 = min(tokens, max(0, s.row.len - tok));
-                if (ta_clean_v<D>(smem + C::kOffV + slot * C::kItemBytes, d0, tokens, (tokens + 15) & ~15, r))
-                    *(volatile int32_t *)&bars.nonfinite[units % kFlags] = 1;
-                fence_proxy_async_smem(); // before the MMA's reads
             }
             tc_fence_before();
             __syncwarp();
@@ -900,10 +953,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
         for (int i = 0; i < C::kVStages; ++i) {
             mbar_init(&bars.v_full[i], 1);
+            mbar_init(&bars.v_ready[i], 1);
             mbar_init(&bars.v_empty[i], 1);
         }
         mbar_init(&bars.q_full, 1);
-        mbar_init(&bars.q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
             mbar_init(&bars.p_full[i], 4); // the warps of the tile's group
@@ -940,20 +993,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         p.records[blockIdx.x] = make_int4(0, 0, 0, 0);
 
     if (warp == kTaKWarp)
-        ta_load_kv<D>(p, &maps.k, smem + C::kOffK, bars.k_full, bars.k_empty, C::kKStages, bars.bad, true, from, bars,
-                      lane);
+        ta_load<D, true>(p, maps, smem, bars, from, lane);
     else if (warp == kTaVWarp)
-        ta_load_kv<D>(p, &maps.v, smem + C::kOffV, bars.v_full, bars.v_empty, C::kVStages, bars.nonfinite, false, from,
-                      bars, lane);
-    else if (warp == kTaQWarp) {
-        if (lane == 0)
-            ta_load_q<D>(p, &maps.q, smem + C::kOffQ, from, bars);
-        __syncwarp();
-    } else if (warp == kTaMmaWarp) {
-        if (lane == 0)
-            ta_mma<D>(p, smem, bars, tmem, from);
-        __syncwarp();
-    } else
+        ta_load<D, false>(p, maps, smem, bars, from, lane);
+    else if (warp == kTaCheckWarp)
+        ta_check_v<D>(p, smem, bars, from, lane);
+    else if (warp == kTaMmaWarp)
+        ta_mma<D>(p, smem, bars, tmem, from);
+    else
         ta_softmax<D>(p, smem, bars, tmem, from, warp, lane);
 
     tc_fence_before();
