@@ -13,6 +13,10 @@
 // whatever their number, the tensor pipe beyond (the next unit finds the same
 // K/V in L2).
 //
+// The roles' code is kept short (one walk of the range, loops not unrolled
+// beyond 32 columns): at 120 KB a sixth of the instruction fetches missed the
+// SM's instruction cache and a tile took half again as long.
+//
 // How (one persistent CTA per SM):
 //  - The units are laid end to end as a line of positions (kStartCost for the
 //    fixed cost of a unit, then its 64-token blocks) and every CTA takes an
@@ -22,8 +26,9 @@
 //    and O in the workspace, fp32, and a second kernel joins them in range
 //    order (results do not depend on timing).  A CTA has at most two such
 //    slices: the one it starts in and the one it ends in.
-//  - Warps: 0 loads Q and K, 2 loads V, with TMA, K and V into a ring each (one
-//    lane per box, a box per page piece); 3 looks V through; 1 owns TMEM and one
+//  - Warps: 3 walks the CTA's range, hands its slices to the others through a
+//    ring and looks V through; 0 loads Q and K, 2 loads V, with TMA, K and V into
+//    a ring each (one lane per box, a box per page piece); 1 owns TMEM and one
 //    thread of it issues the MMAs; 4-7 and 8-11 are two softmax groups that take
 //    alternate tiles, one thread per MMA row.  While one group is at tile t the
 //    tensor pipe runs S of tile t + 1 and P V of tile t - 1.
@@ -56,9 +61,10 @@ constexpr int kStartCost = 2;     // positions that a unit costs before its firs
 constexpr int kMinBlocks = 2;     // a unit is not cut nearer than this to its ends
 constexpr int kMinRange = 6;      // positions that are worth a CTA of their own
 constexpr int kTaMaxCtas = 160;   // persistent CTAs the workspace has room for
-constexpr int kTaKWarp = 0, kTaMmaWarp = 1, kTaVWarp = 2, kTaCheckWarp = 3, kTaSoftmaxWarp = 4;
+constexpr int kTaKWarp = 0, kTaMmaWarp = 1, kTaVWarp = 2, kTaWalkWarp = 3, kTaSoftmaxWarp = 4;
 constexpr int kTaThreads = 384;
-constexpr int kFlags = 16;        // slices whose flags are kept: more than the loads run ahead of the epilogue
+constexpr int kSlices = 8;        // slices handed out and not yet done with
+constexpr int kReaders = 12;      // warps that read them
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.693147180559945309f;
 
@@ -86,14 +92,27 @@ template <int D> struct TaCfg {
     static_assert(kColS + 2 * kTile <= kTmemCols, "TMEM columns");
 };
 
+// What the roles need to know of a slice.
+struct TaSlice {
+    int32_t b, g;          // row, kv head
+    int32_t first;         // token of the row's node 0
+    int32_t node0, nodes;  // first node of the unit, nodes of the row
+    int32_t len;           // cached tokens
+    int32_t tok0, tok1;    // the slice's tokens
+    int32_t flags;         // kBegins, kEnds, kOver
+};
+constexpr int kBegins = 1, kEnds = 2, kOver = 4; // it starts / ends the unit; no more slices
+
 struct TaBars {
     uint64_t k_full[6], k_empty[6], v_full[6], v_ready[6], v_empty[6];
     uint64_t q_full;
     uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
     uint64_t m_set[2][4], l_set[2][4]; // by softmax group and TMEM lane quarter
+    uint64_t slice_full[kSlices], slice_empty[kSlices];
     uint64_t drain;
-    int32_t bad[kFlags];       // a page of the slice is out of range
-    int32_t nonfinite[kFlags]; // V of a drafted token holds an infinity or NaN
+    TaSlice slice[kSlices];
+    uint8_t bad[kSlices];       // a page of the slice is out of range
+    uint8_t nonfinite[kSlices]; // V of a drafted token holds an infinity or NaN
     uint32_t tmem_base;
     int32_t abort;
 };
@@ -171,93 +190,6 @@ __device__ __forceinline__ int ta_cut(int64_t x, int blocks)
     return blocks - k < kMinBlocks ? blocks : (int)k;
 }
 
-// The slices of one CTA's range, in order.  Every role walks them by itself.
-struct TaSlices {
-    TaRow row;
-    int b, unit;        // row, unit within the row
-    int64_t off, left;  // position within the unit, positions left
-    bool fresh;         // `row` is to be read
-    // the current slice
-    int g, rt;          // kv head, row tile
-    int tok0, tok1;     // its tokens (equal: a unit whose output is zeroed)
-    bool begins, ends;
-
-    __device__ __forceinline__ bool next(const TaParams &p)
-    {
-        while (left > 0) {
-            if (fresh) {
-                row = ta_row(p, b);
-                fresh = false;
-            }
-            const int units = row.tiles * p.num_kv_heads;
-            if (unit >= units) {
-                ++b;
-                unit = 0;
-                off = 0;
-                fresh = true;
-                continue;
-            }
-            const int64_t size = kStartCost + row.blocks, take = min(size - off, left);
-            const int a = ta_cut(off, row.blocks), z = off + take >= size ? row.blocks : ta_cut(off + take, row.blocks);
-            const bool at_start = off == 0;
-            const int u = unit;
-            left -= take;
-            off += take;
-            if (off >= size) {
-                ++unit;
-                off = 0;
-            }
-            if (row.blocks == 0 ? !at_start : a >= z)
-                continue;
-            // units of a row: row tiles of a kv head next to one another (their K/V stay in L2)
-            g = u / row.tiles;
-            rt = u - g * row.tiles;
-            begins = a == 0;
-            ends = z == row.blocks;
-            tok0 = a * kTaBlock;
-            tok1 = min(z * kTaBlock, row.blocks == 0 ? 0 : row.len + row.nodes);
-            return true;
-        }
-        return false;
-    }
-    // MMA rows in use
-    __device__ __forceinline__ int rows(const TaParams &p) const
-    {
-        return min(p.q_tile, row.nodes - rt * p.q_tile) * p.group;
-    }
-};
-
-// The tiles of those slices, one after the other.
-template <int D> struct TaTiles {
-    TaSlices s;
-    int j;  // tile within the slice
-    int nt; // tiles of the slice
-    int gt; // tiles before this one
-    int live; // slices with tiles before this one
-
-    __device__ __forceinline__ void start(const TaSlices &from)
-    {
-        s = from;
-        j = nt = 0;
-        gt = live = -1;
-    }
-    __device__ __forceinline__ bool next(const TaParams &p)
-    {
-        ++j;
-        while (j >= nt) {
-            if (!s.next(p))
-                return false;
-            j = 0;
-            nt = (s.tok1 - s.tok0 + TaCfg<D>::kTile - 1) / TaCfg<D>::kTile;
-        }
-        ++gt;
-        live += j == 0;
-        return true;
-    }
-    __device__ __forceinline__ int tok() const { return s.tok0 + j * TaCfg<D>::kTile; }
-    __device__ __forceinline__ int tokens() const { return min(TaCfg<D>::kTile, s.tok1 - tok()); }
-};
-
 // ---------------------------------------------------------------- waits
 
 __device__ __noinline__ bool ta_wait_slow(uint64_t *bar, uint32_t parity, TaBars &bars, int32_t *err_flag)
@@ -291,18 +223,157 @@ __device__ __forceinline__ bool ta_wait_all(uint64_t *bar, uint32_t parity, TaBa
     return __all_sync(0xffffffffu, ta_wait(bar, parity, bars, err_flag));
 }
 
-// ---------------------------------------------------------------- loads
+// ---------------------------------------------------------------- slices
 
-// The Q rows of a slice: [node][head], a 64-column block at a time.
+// Where a CTA's range starts, and its length in positions.
+struct TaStart {
+    int b, unit;       // row, unit within the row
+    int64_t off, left; // position within the unit, positions of the range
+};
+
+// Zeros and -inf for a unit of a row that is inactive or in error.  A whole warp.
 template <int D>
-__device__ __forceinline__ void ta_load_q(const TaParams &p, const CUtensorMap *map, uint8_t *q_smem, const TaSlices &s,
-                                          TaBars &bars)
+__device__ void ta_zero_unit(const TaParams &p, const TaRow &row, int g, int node0, int lane)
 {
-    mbar_arrive_expect_tx(&bars.q_full, p.q_box_bytes * (D / 64));
-    for (int c = 0; c < D / 64; ++c)
-        tma_load_3d_plain(q_smem + c * TaCfg<D>::kQBlock, map, c * 64, s.g * p.group, s.row.first + s.rt * p.q_tile,
-                          &bars.q_full);
+    const int rows = min(p.q_tile, row.nodes - node0) * p.group;
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r) {
+        const int64_t at = ((int64_t)row.first + node0 + r / p.group) * p.num_q_heads + g * p.group + r % p.group;
+        if (lane < D / 8)
+            *reinterpret_cast<uint4 *>(p.out + at * D + lane * 8) = make_uint4(0u, 0u, 0u, 0u);
+        if (lane == 0 && p.lse != nullptr)
+            p.lse[at] = -INFINITY;
+    }
 }
+
+// Cuts a CTA's range into slices, in order; units without keys to read are
+// finished here.  A whole warp.
+template <int D> struct TaWalk {
+    TaStart at;
+    TaRow row;
+    int n; // slices handed out
+    bool over;
+
+    __device__ __forceinline__ void start(const TaParams &p, const TaStart &from)
+    {
+        at = from;
+        row = ta_row(p, at.b);
+        n = 0;
+        over = false;
+    }
+    // Hands out the next slice (its slot is free).
+    __device__ __forceinline__ void publish(const TaParams &p, TaBars &bars, int lane)
+    {
+        TaSlice s;
+        s.flags = kOver;
+#pragma unroll 1
+        while (at.left > 0) {
+            if (at.unit >= row.tiles * p.num_kv_heads) {
+                ++at.b;
+                at.unit = 0;
+                at.off = 0;
+                row = ta_row(p, at.b);
+                continue;
+            }
+            const int64_t size = kStartCost + row.blocks, take = min(size - at.off, at.left);
+            const bool at_start = at.off == 0, at_end = at.off + take >= size;
+            const int a = ta_cut(at.off, row.blocks), z = at_end ? row.blocks : ta_cut(at.off + take, row.blocks);
+            const int unit = at.unit;
+            at.left -= take;
+            at.off += take;
+            if (at_end) {
+                ++at.unit;
+                at.off = 0;
+            }
+            if (row.blocks > 0 && a >= z)
+                continue;
+            // units of a row: row tiles of a kv head next to one another (their K/V stay in L2)
+            const int g = unit / row.tiles, node0 = (unit - g * row.tiles) * p.q_tile;
+            if (row.blocks == 0) {
+                if (at_start) {
+                    if (unit == 0 && lane == 0)
+                        set_error(p.err_flag, row.err);
+                    ta_zero_unit<D>(p, row, g, node0, lane);
+                }
+                continue;
+            }
+            s.b = at.b;
+            s.g = g;
+            s.first = row.first;
+            s.node0 = node0;
+            s.nodes = row.nodes;
+            s.len = row.len;
+            s.tok0 = a * kTaBlock;
+            s.tok1 = min(z * kTaBlock, row.len + row.nodes);
+            s.flags = (a == 0 ? kBegins : 0) | (z == row.blocks ? kEnds : 0);
+            break;
+        }
+        const int slot = n % kSlices;
+        if (lane == 0) {
+            bars.slice[slot] = s;
+            bars.bad[slot] = bars.nonfinite[slot] = 0;
+            mbar_arrive(&bars.slice_full[slot]);
+        }
+        over = (s.flags & kOver) != 0;
+        ++n;
+    }
+};
+
+// The n-th slice; a role that gave up sees the end.
+__device__ __forceinline__ TaSlice ta_slice(const TaParams &p, TaBars &bars, int n)
+{
+    TaSlice s;
+    if (ta_wait_all(&bars.slice_full[n % kSlices], (uint32_t)(n / kSlices) & 1, bars, p.err_flag))
+        s = bars.slice[n % kSlices];
+    else
+        s.flags = kOver;
+    return s;
+}
+__device__ __forceinline__ void ta_slice_done(TaBars &bars, int n, int lane)
+{
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(&bars.slice_empty[n % kSlices]);
+}
+
+// The tiles of the slices, one after the other, for a warp that looks at one
+// slice at a time.
+template <int D> struct TaTiles {
+    TaSlice s;
+    int n;    // index of the slice
+    int tok;  // first token of the tile
+    int gt;   // tiles before this one
+
+    __device__ __forceinline__ void start()
+    {
+        n = gt = -1;
+        tok = s.tok1 = 0;
+    }
+    __device__ __forceinline__ bool next(const TaParams &p, TaBars &bars, int lane, bool done = true)
+    {
+        tok += TaCfg<D>::kTile;
+        ++gt;
+        if (tok < s.tok1)
+            return true;
+        if (n >= 0 && done)
+            ta_slice_done(bars, n, lane);
+        s = ta_slice(p, bars, ++n);
+        tok = s.tok0;
+        return !(s.flags & kOver);
+    }
+    __device__ __forceinline__ bool first() const { return tok == s.tok0; }
+    __device__ __forceinline__ int tokens() const { return min(TaCfg<D>::kTile, s.tok1 - tok); }
+};
+
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+// ---------------------------------------------------------------- loads
 
 // One warp loads all K (or all V) tiles of the CTA, one box per lane: boxes of
 // min(page, 64) tokens, at most kTile / 8 = 16.  A page id outside the pool
@@ -310,8 +381,7 @@ __device__ __forceinline__ void ta_load_q(const TaParams &p, const CUtensorMap *
 // tile T + kKStages - 1 is free when S of tile T - 1 is done, which is when a
 // slice that begins with tile T may have the Q buffer.
 template <int D, bool IS_K>
-__device__ void ta_load(const TaParams &p, const TaMaps &maps, uint8_t *smem, TaBars &bars, const TaSlices &from,
-                        int lane)
+__device__ void ta_load(const TaParams &p, const TaMaps &maps, uint8_t *smem, TaBars &bars, int lane)
 {
     using C = TaCfg<D>;
     constexpr int kStages = IS_K ? C::kKStages : C::kVStages;
@@ -321,44 +391,32 @@ __device__ void ta_load(const TaParams &p, const TaMaps &maps, uint8_t *smem, Ta
     const int bsh = p.box_shift, boxes = C::kTile >> bsh;
     const uint32_t box_bytes = (uint32_t)(1 << bsh) * D * 2;
     const bool nhd = p.layout == PKV_NHD;
-    // Lane i holds the page of box i of the tile.
-    auto page_of = [&](const TaTiles<D> &t) {
-        const int tok = t.tok() + (lane << bsh);
-        int id = 0;
-        if (lane < boxes && tok < t.s.tok1)
-            id = p.table[(int64_t)t.s.b * p.max_blocks + (tok >> p.page_shift)];
-        return id;
-    };
-    TaTiles<D> t, ahead, behind; // the next tile's pages are read one ahead; Q comes kStages - 1 behind
-    t.start(from);
-    bool more = t.next(p);
-    int id = more ? page_of(t) : 0;
-    if (IS_K) {
-        behind = t;
-        if (more && lane == 0)
-            ta_load_q<D>(p, &maps.q, smem + C::kOffQ, t.s, bars);
-    }
-    int slot = 0, issued = 0, q_issued = IS_K && more ? 1 : 0;
+    TaTiles<D> t;
+    t.start();
+    int q_slice = 0, q_tile0 = 0; // next slice whose Q is due, its first tile
+    int slot = 0, issued = 0, issued_slices = 0;
     uint32_t round = 0; // times the ring has been filled
+    bool more = true;
+    int id = 0; // this lane's page of the coming tile
+#pragma unroll 1
     for (int x = 0;; ++x) {
+        more = more && t.next(p, bars, lane, !IS_K);
         if (!more && (!IS_K || x >= issued + kStages - 1))
             break;
+        const int tok = t.tok + (lane << bsh);
+        const bool want = more && lane < boxes && tok < t.s.tok1;
+        const int32_t *row = p.table + (int64_t)t.s.b * p.max_blocks;
+        if (more && (t.first() || x == 0))
+            id = want ? row[tok >> p.page_shift] : 0;
         if (round > 0 && !ta_wait_all(&empty[slot], (round - 1) & 1, bars, p.err_flag))
             break;
         if (more) {
-            ahead = t;
-            const bool ahead_more = ahead.next(p);
-            const int id_ahead = ahead_more ? page_of(ahead) : 0;
-            const int tok = t.tok() + (lane << bsh);
-            const bool want = lane < boxes && tok < t.s.tok1;
             const bool good = want && id >= 1 && id < p.num_pages;
             const uint32_t n = __popc(__ballot_sync(0xffffffffu, good));
-            const bool bad = __any_sync(0xffffffffu, want && !good);
-            if (lane == 0) {
-                if (IS_K && (bad || t.j == 0))
-                    *(volatile int32_t *)&bars.bad[t.live % kFlags] = bad; // a later clean tile leaves the mark
+            if (__any_sync(0xffffffffu, want && !good) && IS_K && lane == 0)
+                *(volatile uint8_t *)&bars.bad[t.n % kSlices] = 1;
+            if (lane == 0)
                 mbar_arrive_expect_tx(&full[slot], n * box_bytes);
-            }
             __syncwarp();
             if (good) {
                 const int in_page = tok & ((1 << p.page_shift) - 1);
@@ -367,16 +425,25 @@ __device__ void ta_load(const TaParams &p, const TaMaps &maps, uint8_t *smem, Ta
                 tma_load_5d_plain(ring + slot * C::kItemBytes + lane * box_bytes, map, 0, 0, 0, c3, c4, &full[slot]);
             }
             ++issued;
-            t = ahead;
-            id = id_ahead;
-            more = ahead_more;
+            issued_slices = t.n + 1;
+            const int then = tok + C::kTile; // the pages of the slice's next tile, a step ahead
+            id = lane < boxes && then < t.s.tok1 ? row[then >> p.page_shift] : 0;
         }
-        if (IS_K && x > kStages - 1) {
-            behind.next(p);
-            if (behind.j == 0) {
+        if (IS_K) {
+            if (more && t.first() && x > 0 && lane < D / 64) // a slice's Q into L2 before its buffer is free
+                tma_prefetch_3d(&maps.q, lane * 64, t.s.g * p.group, t.s.first + t.s.node0);
+            // Q: of the first slice at once, of the others kStages - 1 tiles on
+            if (q_slice < issued_slices && (q_slice == 0 || x >= q_tile0 + kStages - 1)) {
+                const TaSlice s = bars.slice[q_slice % kSlices];
                 if (lane == 0)
-                    ta_load_q<D>(p, &maps.q, smem + C::kOffQ, behind.s, bars);
-                ++q_issued;
+                    mbar_arrive_expect_tx(&bars.q_full, p.q_box_bytes * (D / 64));
+                __syncwarp();
+                if (lane < D / 64)
+                    tma_load_3d_plain(smem + C::kOffQ + lane * C::kQBlock, &maps.q, lane * 64, s.g * p.group,
+                                      s.first + s.node0, &bars.q_full);
+                q_tile0 += (s.tok1 - s.tok0 + C::kTile - 1) / C::kTile;
+                ta_slice_done(bars, q_slice, lane);
+                ++q_slice;
             }
         }
         if (++slot == kStages) {
@@ -385,10 +452,11 @@ __device__ void ta_load(const TaParams &p, const TaMaps &maps, uint8_t *smem, Ta
         }
     }
     // Copies still in flight (a role gave up): they land before the CTA ends.
+#pragma unroll 1
     for (int k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
         mbar_wait(&full[k % kStages], (uint32_t)(k / kStages) & 1);
-    if (q_issued > 0)
-        mbar_wait(&bars.q_full, (uint32_t)(q_issued - 1) & 1);
+    if (q_slice > 0)
+        mbar_wait(&bars.q_full, (uint32_t)(q_slice - 1) & 1);
 }
 
 __device__ __forceinline__ bool bf16_nonfinite(uint32_t half)
@@ -396,28 +464,50 @@ __device__ __forceinline__ bool bf16_nonfinite(uint32_t half)
     return (half & 0x7f80u) == 0x7f80u;
 }
 
-// One warp looks V through before the MMAs read it.  Of a tile with drafted
-// tokens it replaces their infinities and NaN by 0 (and marks the slice); rows
-// past the keys, up to the multiple of 16 that the MMAs read, become 0.
+// One warp hands out the slices, as far ahead as there is room, and looks V
+// through before the MMAs read it.  Of a tile with drafted tokens it replaces
+// their infinities and NaN by 0 (and marks the slice); rows past the keys, up
+// to the multiple of 16 that the MMAs read, become 0.
 template <int D>
-__device__ void ta_check_v(const TaParams &p, uint8_t *smem, TaBars &bars, const TaSlices &from, int lane)
+__device__ void ta_walk(const TaParams &p, uint8_t *smem, TaBars &bars, const TaStart &from, int lane)
 {
     using C = TaCfg<D>;
     constexpr int kPieces = D / 8; // 16-byte pieces of a row
-    TaTiles<D> t;
-    t.start(from);
-    while (t.next(p)) {
-        const int slot = t.gt % C::kVStages, tokens = t.tokens();
-        const uint32_t parity = (uint32_t)(t.gt / C::kVStages) & 1;
-        if (t.j == 0 && lane == 0)
-            *(volatile int32_t *)&bars.nonfinite[t.live % kFlags] = 0;
-        if (!ta_wait_all(&bars.v_full[slot], parity, bars, p.err_flag))
+    TaWalk<D> walk;
+    walk.start(p, from);
+    int n = 0, v_slot = 0; // the slice at hand
+    uint32_t v_par = 0;
+    TaSlice s;
+    s.tok1 = s.len = 0;
+    int tok = 0;
+#pragma unroll 1
+    for (;;) {
+#pragma unroll 1
+        while (!walk.over) {
+            uint64_t *empty = &bars.slice_empty[walk.n % kSlices];
+            const uint32_t parity = (uint32_t)(walk.n / kSlices - 1) & 1;
+            if (walk.n >= kSlices && !__all_sync(0xffffffffu, mbar_test_wait(empty, parity))) {
+                if (walk.n > n)
+                    break;
+                if (!ta_wait_all(empty, parity, bars, p.err_flag))
+                    return;
+            }
+            walk.publish(p, bars, lane);
+        }
+        if (tok >= s.tok1) {
+            s = ta_slice(p, bars, n);
+            if (s.flags & kOver)
+                return;
+            tok = s.tok0;
+        }
+        if (!ta_wait_all(&bars.v_full[v_slot], v_par, bars, p.err_flag))
             return;
-        const int d0 = min(tokens, max(0, t.s.row.len - t.tok())), r1 = (tokens + 15) & ~15;
+        const int tokens = min(C::kTile, s.tok1 - tok);
+        const int d0 = min(tokens, max(0, s.len - tok)), r1 = (tokens + 15) & ~15;
         if (d0 < r1) {
-            uint8_t *vb = smem + C::kOffV + slot * C::kItemBytes;
+            uint8_t *vb = smem + C::kOffV + v_slot * C::kItemBytes;
             bool found = false;
-#pragma unroll 4
+#pragma unroll 2
             for (int i = d0 * kPieces + lane; i < r1 * kPieces; i += 32) {
                 const int row = i / kPieces, piece = i % kPieces;
                 uint4 *at = reinterpret_cast<uint4 *>(vb + (row >> 3) * C::kGroupStride + (piece >> 3) * 1024 +
@@ -439,12 +529,19 @@ __device__ void ta_check_v(const TaParams &p, uint8_t *smem, TaBars &bars, const
                 found |= hit && !past;
             }
             if (found)
-                *(volatile int32_t *)&bars.nonfinite[t.live % kFlags] = 1;
+                *(volatile uint8_t *)&bars.nonfinite[n % kSlices] = 1;
             fence_proxy_async_smem(); // before the MMAs' reads
         }
         __syncwarp();
         if (lane == 0)
-            mbar_arrive(&bars.v_ready[slot]);
+            mbar_arrive(&bars.v_ready[v_slot]);
+        if (++v_slot == C::kVStages) {
+            v_slot = 0;
+            v_par ^= 1;
+        }
+        tok += C::kTile;
+        if (tok >= s.tok1)
+            ta_slice_done(bars, n++, lane);
     }
 }
 
@@ -480,71 +577,83 @@ __device__ __forceinline__ void ta_commit(uint64_t *bar)
 }
 
 template <int D>
-__device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t tmem, const TaSlices &from)
+__device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t tmem, int lane)
 {
     using C = TaCfg<D>;
     constexpr uint32_t kIdescS = tc_idesc_bf16(kTaRows, C::kTile, false, false);
     constexpr uint32_t kIdescO = tc_idesc_bf16(kTaRows, D, false, true);
-    const uint32_t k_base = smem_addr(smem + C::kOffK), v_base = smem_addr(smem + C::kOffV);
-    const uint64_t qd = tc_sw128_desc(smem_addr(smem + C::kOffQ), 16, 1024);
+    const uint64_t kd0 = tc_sw128_desc(smem_addr(smem + C::kOffK), 16, C::kGroupStride);
+    const uint64_t vd0 = tc_sw128_desc(smem_addr(smem + C::kOffV), 1024, C::kGroupStride);
+    const uint64_t qd0 = tc_sw128_desc(smem_addr(smem + C::kOffQ), 16, 1024);
     TaTiles<D> t;
-    t.start(from);
-    bool issued = false, more = t.next(p);
-    uint32_t units = 0;         // slices whose S has begun
-    int prev = -1;              // tile whose P V is due
-    int prev_tokens = 0;
+    t.start();
+    bool issued = false, more = t.next(p, bars, lane);
+    int prev = -1; // tile whose P V is due
+    int prev_tokens = 0, prev_unit = 0;
     bool prev_first = false;
-    uint32_t prev_unit = 0;
+    int k_slot = 0, v_slot = 0;
+    uint32_t k_par = 0, v_par = 0;
+#pragma unroll 1
     while (more || prev >= 0) {
-        if (more) { // S of this tile
-            const int slot = t.gt % C::kKStages;
-            if (t.j == 0) {
-                if (!ta_wait_all(&bars.q_full, units & 1, bars, p.err_flag))
-                    break;
-                ++units;
-            }
-            if (!ta_wait_all(&bars.k_full[slot], (uint32_t)(t.gt / C::kKStages) & 1, bars, p.err_flag))
+        if (more) { // S of the next tile
+            if ((t.first() && !ta_wait_all(&bars.q_full, (uint32_t)t.n & 1, bars, p.err_flag)) ||
+                !ta_wait_all(&bars.k_full[k_slot], k_par, bars, p.err_flag))
                 break;
             tc_fence_after();
             issued = true;
             const uint32_t d = tmem + C::kColS + (uint32_t)(t.gt & 1) * C::kTile;
-            const uint64_t kd = tc_sw128_desc(k_base + slot * C::kItemBytes, 16, C::kGroupStride);
+            const uint64_t kd = kd0 + (uint64_t)(k_slot * C::kItemBytes >> 4);
+#pragma unroll 1
+            for (int blk = 0; blk < D / 64; ++blk)
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                ta_mma_ss(d, qd + (uint64_t)(((kk >> 2) * C::kQBlock + (kk & 3) * 32) >> 4),
-                            kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), kIdescS, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < 4; ++kk)
+                    ta_mma_ss(d, qd0 + (uint64_t)((blk * C::kQBlock + kk * 32) >> 4),
+                              kd + (uint64_t)((blk * 1024 + kk * 32) >> 4), kIdescS, blk + kk > 0 ? 1u : 0u);
             ta_commit(&bars.s_full[t.gt & 1]);
-            ta_commit(&bars.k_empty[slot]);
+            ta_commit(&bars.k_empty[k_slot]);
+            if (++k_slot == C::kKStages) {
+                k_slot = 0;
+                k_par ^= 1;
+            }
         }
-        if (prev >= 0) { // O += P V of the tile before
-            const int slot = prev % C::kVStages;
-            const uint32_t ob = C::kOBufs == 1 ? 0 : prev_unit & 1, use = C::kOBufs == 1 ? prev_unit : prev_unit >> 1;
-            if (!ta_wait_all(&bars.p_full[prev & 1], (uint32_t)(prev >> 1) & 1, bars, p.err_flag))
-                break;
-            if (prev_first && use > 0 && !ta_wait_all(&bars.o_free[ob], (use - 1) & 1, bars, p.err_flag))
-                break;
-            if (!ta_wait_all(&bars.v_ready[slot], (uint32_t)(prev / C::kVStages) & 1, bars, p.err_flag))
+        if (prev >= 0) { // O += P V of the one before
+            const uint32_t ob = C::kOBufs == 1 ? 0 : prev_unit & 1;
+            const uint32_t use = C::kOBufs == 1 ? prev_unit : prev_unit >> 1;
+            if ((prev_first && use > 0 && !ta_wait_all(&bars.o_free[ob], (use - 1) & 1, bars, p.err_flag)) ||
+                !ta_wait_all(&bars.v_ready[v_slot], v_par, bars, p.err_flag) ||
+                !ta_wait_all(&bars.p_full[prev & 1], (uint32_t)(prev >> 1) & 1, bars, p.err_flag))
                 break;
             tc_fence_after();
-            const uint32_t pt = tmem + C::kColS + (uint32_t)(prev & 1) * C::kTile, o = tmem + ob * D;
-            const uint64_t vd = tc_sw128_desc(v_base + slot * C::kItemBytes, 1024, C::kGroupStride);
-            const int steps = (prev_tokens + 15) >> 4; // 16 keys each
-            for (int k = 0; k < steps; ++k) {
-                const uint32_t a = pt + 32 * (k >> 1) + 8 * (k & 1); // hi part; the lo part 16 columns on
-                const uint64_t b = vd + (uint64_t)((2 * k * C::kGroupStride) >> 4);
-                ta_mma_ts(o, a, b, kIdescO, !prev_first || k > 0 ? 1u : 0u);
-                ta_mma_ts(o, a + 16, b, kIdescO, 1u);
+            const uint32_t o = tmem + ob * D;
+            uint32_t a = tmem + C::kColS + (uint32_t)(prev & 1) * C::kTile;
+            uint64_t vd = vd0 + (uint64_t)(v_slot * C::kItemBytes >> 4);
+            // 16 keys a step: P's hi parts, then the lo parts 16 columns on
+#pragma unroll 1
+            for (int k = 0; k < prev_tokens; k += 32) {
+                ta_mma_ts(o, a, vd, kIdescO, !prev_first || k > 0 ? 1u : 0u);
+                ta_mma_ts(o, a + 16, vd, kIdescO, 1u);
+                vd += (uint64_t)(2 * C::kGroupStride >> 4);
+                if (k + 16 < prev_tokens) {
+                    ta_mma_ts(o, a + 8, vd, kIdescO, 1u);
+                    ta_mma_ts(o, a + 24, vd, kIdescO, 1u);
+                }
+                vd += (uint64_t)(2 * C::kGroupStride >> 4);
+                a += 32;
             }
             ta_commit(&bars.o_done[prev & 1]);
-            ta_commit(&bars.v_empty[slot]);
-            prev = -1;
+            ta_commit(&bars.v_empty[v_slot]);
+            if (++v_slot == C::kVStages) {
+                v_slot = 0;
+                v_par ^= 1;
+            }
         }
+        prev = -1;
         if (more) {
             prev = t.gt;
             prev_tokens = t.tokens();
-            prev_first = t.j == 0;
-            prev_unit = units - 1;
-            more = t.next(p);
+            prev_first = t.first();
+            prev_unit = t.n;
+            more = t.next(p, bars, lane);
         }
     }
     if (issued) {
@@ -594,35 +703,46 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t *w, bool wide)
                  : "memory");
 }
 
-// What the infinities and NaN of drafted tokens j0 .. j1 - 1 add to column
-// `col` of a node that sees those in `mask` (rare; read again from the cache).
+// Adds to columns c0 .. c1 - 1 of a node's O the infinities and NaN that the
+// drafted tokens j0 .. j1 - 1 it sees hold there (rare; read again from the
+// cache).  A whole warp; lanes with `live` false change nothing.
 template <int D>
-__device__ __noinline__ float ta_nonfinite(const TaParams &p, int b, int len, int g, const int32_t *mask, int j0, int j1,
-                                           int col)
+__device__ __noinline__ void ta_add_nonfinite(const TaParams &p, int b, int len, int g, const int32_t *mask, int j0, int j1,
+                                              bool live, uint32_t o_col, int c0, int c1)
 {
-    float sum = 0.f;
-    for (int j = j0; j < j1; ++j) {
-        if (!((uint32_t)mask[j >> 5] >> (j & 31) & 1u))
-            continue;
-        const int tok = len + j;
-        const int64_t page = p.table[(int64_t)b * p.max_blocks + (tok >> p.page_shift)];
-        if (page < 1 || page >= p.num_pages)
-            continue;
-        const int64_t slot = tok & ((1 << p.page_shift) - 1);
-        const int64_t at = p.layout == PKV_NHD ? (((page << p.page_shift) + slot) * p.num_kv_heads + g) * D
-                                               : (((page * p.num_kv_heads + g) << p.page_shift) + slot) * D;
-        const uint32_t v = reinterpret_cast<const uint16_t *>(p.v_cache)[at + col];
-        if (bf16_nonfinite(v))
-            sum += __uint_as_float(v << 16);
+    for (int c = c0; c < c1; ++c) {
+        float sum = 0.f;
+        for (int j = j0; j < j1; ++j) {
+            if (!live || !((uint32_t)mask[j >> 5] >> (j & 31) & 1u))
+                continue;
+            const int tok = len + j;
+            const int64_t page = p.table[(int64_t)b * p.max_blocks + (tok >> p.page_shift)];
+            if (page < 1 || page >= p.num_pages)
+                continue;
+            const int64_t slot = tok & ((1 << p.page_shift) - 1);
+            const int64_t at = p.layout == PKV_NHD ? (((page << p.page_shift) + slot) * p.num_kv_heads + g) * D
+                                                   : (((page * p.num_kv_heads + g) << p.page_shift) + slot) * D;
+            const uint32_t v = reinterpret_cast<const uint16_t *>(p.v_cache)[at + c];
+            if (bf16_nonfinite(v))
+                sum += __uint_as_float(v << 16);
+        }
+        __syncwarp();
+        uint32_t x;
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                     : "=r"(x)
+                     : "r"(o_col + c)
+                     : "memory");
+        x = __float_as_uint(__uint_as_float(x) + sum);
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(o_col + c),
+                     "r"(x)
+                     : "memory");
     }
-    return sum;
 }
 
 // One of the two softmax groups (group gi takes the tiles of parity gi); thread
 // = MMA row.  Both groups finish every slice, half of O's columns each.
 template <int D>
-__device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t tmem, const TaSlices &from, int warp,
-                           int lane)
+__device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t tmem, int warp, int lane)
 {
     using C = TaCfg<D>;
     constexpr int kChunks = C::kTile / 32;
@@ -634,43 +754,33 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
     const float qs = p.q_scale, qse = qs > 0.f ? qs : 1.f;
     const int node_in_tile = r / p.group, head_in_group = r - node_in_tile * p.group;
     int gt = 0;         // tiles before this slice
-    uint32_t units = 0; // slices with tiles before this one
     int record = 0;
     int4 tail = make_int4(0, 0, 0, 0);
 
-    TaSlices s = from;
-    while (s.next(p)) {
-        const int rows = s.rows(p);
+#pragma unroll 1
+    for (int n = 0;; ++n) {
+        const TaSlice s = ta_slice(p, bars, n);
+        if (s.flags & kOver)
+            break;
+        const int rows = min(p.q_tile, s.nodes - s.node0) * p.group; // MMA rows in use
         const bool live = r < rows, warp_live = quarter * 32 < rows;
-        const int node = s.rt * p.q_tile + node_in_tile;
-        const int64_t token = (int64_t)s.row.first + node;
+        const int64_t token = (int64_t)s.first + s.node0 + node_in_tile;
         const int64_t out_row = token * p.num_q_heads + s.g * p.group + head_in_group;
-        if (s.tok0 >= s.tok1) { // a row that is inactive or in error: zeros
-            if (s.g == 0 && s.rt == 0 && r == 0 && gi == 0)
-                set_error(p.err_flag, s.row.err);
-            if (live) {
-                const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-                for (int c = gi * (D / 2); c < (gi + 1) * (D / 2); c += 16)
-                    store32(p.out + out_row * D + c, zero, p.wide);
-                if (gi == 0 && p.lse != nullptr)
-                    p.lse[out_row] = -INFINITY;
-            }
-            continue;
-        }
-        const int32_t *mask = p.mask + (live ? token : (int64_t)s.row.first) * p.words;
+        const int32_t *mask = p.mask + (live ? token : (int64_t)s.first) * p.words;
         const int nt = (s.tok1 - s.tok0 + C::kTile - 1) / C::kTile;
         float m = -INFINITY, l = 0.f;
+#pragma unroll 1
         for (int j = (gt + gi) & 1; j < nt; j += 2) { // gt + j has parity gi
             const int tile = gt + j;
             const int tok = s.tok0 + j * C::kTile, tokens = min(C::kTile, s.tok1 - tok);
             // tiles with drafted keys or past the slice's end: the node's mask words
-            const bool masked = tok + C::kTile > s.row.len || tokens < C::kTile;
+            const bool masked = tok + C::kTile > s.len || tokens < C::kTile;
             uint32_t words[kChunks + 1];
             if (masked) {
-                const int w0 = (tok - s.row.len) >> 5;
+                const int w0 = (tok - s.len) >> 5;
 #pragma unroll
                 for (int c = 0; c <= kChunks; ++c)
-                    words[c] = ta_mask_word(mask, s.row.nodes, w0 + c);
+                    words[c] = ta_mask_word(mask, s.nodes, w0 + c);
             }
             if (!ta_wait_all(&bars.s_full[gi], (uint32_t)(tile >> 1) & 1, bars, p.err_flag))
                 return;
@@ -681,7 +791,7 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
             // passes below are the same short loops for every tile.
             if (warp_live && (masked || !(qs > 0.f))) {
                 const float by = qs > 0.f ? 1.f : qs;
-                const int shift = (tok - s.row.len) & 31;
+                const int shift = (tok - s.len) & 31;
 #pragma unroll 1
                 for (int c = 0; c < kChunks; ++c) {
                     const int end = tokens - 32 * c;
@@ -754,7 +864,7 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                 tmem_st_wait();
             }
             // O holds this slice's sum only after its first P V
-            const uint32_t o_col = t_row + (C::kOBufs == 1 ? 0u : (units & 1) * D);
+            const uint32_t o_col = t_row + (C::kOBufs == 1 ? 0u : (n & 1) * D);
             const bool rescale = grow && before != -INFINITY;
             if (__any_sync(0xffffffffu, rescale)) {
                 if (!ta_wait_all(&bars.o_done[(tile - 1) & 1], (uint32_t)((tile - 1) >> 1) & 1, bars, p.err_flag))
@@ -797,23 +907,19 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
         if (!ta_wait_all(&bars.o_done[end & 1], (uint32_t)(end >> 1) & 1, bars, p.err_flag))
             return;
         tc_fence_after();
-        const bool bad = *(volatile int32_t *)&bars.bad[units % kFlags] != 0;
-        const bool nonfinite = *(volatile int32_t *)&bars.nonfinite[units % kFlags] != 0;
-        const uint32_t o_col = t_row + (C::kOBufs == 1 ? 0u : (units & 1) * D);
-        const bool whole = s.begins && s.ends;
-        const int64_t part = (int64_t)(2 * blockIdx.x + (s.begins ? 1 : 0)) * p.slot_rows + r;
+        const bool bad = *(volatile uint8_t *)&bars.bad[n % kSlices] != 0;
+        const bool nonfinite = *(volatile uint8_t *)&bars.nonfinite[n % kSlices] != 0;
+        const uint32_t o_col = t_row + (C::kOBufs == 1 ? 0u : (n & 1) * D);
+        const bool begins = s.flags & kBegins, ends = s.flags & kEnds, whole = begins && ends;
+        const int64_t part = (int64_t)(2 * blockIdx.x + (begins ? 1 : 0)) * p.slot_rows + r;
         const float inv = whole && l > 0.f ? 1.f / l : l != l ? l : 0.f;
+        if (nonfinite && warp_live)
+            ta_add_nonfinite<D>(p, s.b, s.len, s.g, mask, max(0, s.tok0 - s.len), min(s.nodes, s.tok1 - s.len), live, o_col,
+                                gi * (D / 2), (gi + 1) * (D / 2));
 #pragma unroll 1
         for (int c = gi * (D / 2); warp_live && c < (gi + 1) * (D / 2); c += 32) {
             uint32_t o[32];
             tmem_ld32(o_col + c, o);
-            if (nonfinite && live) {
-                const int j0 = max(0, s.tok0 - s.row.len), j1 = min(s.row.nodes, s.tok1 - s.row.len);
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    o[e] = __float_as_uint(__uint_as_float(o[e]) +
-                                           ta_nonfinite<D>(p, s.b, s.row.len, s.g, mask, j0, j1, c + e));
-            }
             if (!live)
                 continue;
             if (whole) {
@@ -841,19 +947,19 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
         if (r == 0 && gi == 0) {
             if (bad)
                 set_error(p.err_flag, PKV_ERR_PAGE);
-            if (!s.begins)
-                record |= kHeadValid | (s.ends ? kHeadEnd : 0) | (bad ? kHeadBad : 0);
-            else if (!s.ends) {
+            if (!begins)
+                record |= kHeadValid | (ends ? kHeadEnd : 0) | (bad ? kHeadBad : 0);
+            else if (!ends) {
                 record |= kTail | (bad ? kTailBad : 0);
-                tail = make_int4(0, s.row.first + s.rt * p.q_tile, s.g, rows);
+                tail = make_int4(0, s.first + s.node0, s.g, rows);
             }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0)
-            mbar_arrive(&bars.o_free[C::kOBufs == 1 ? 0 : units & 1]);
+            mbar_arrive(&bars.o_free[C::kOBufs == 1 ? 0 : n & 1]);
+        ta_slice_done(bars, n, lane);
         gt += nt;
-        ++units;
     }
     if (r == 0 && gi == 0) {
         tail.x = record;
@@ -870,7 +976,7 @@ __device__ __forceinline__ int64_t ta_positions(const TaParams &p, const TaRow &
 }
 
 // This CTA's range: prefix sum of the rows' positions (in `scratch`), equal parts, and the row and unit its part starts in.
-__device__ void ta_start(const TaParams &p, int64_t *scratch, TaSlices *out)
+__device__ void ta_start(const TaParams &p, int64_t *scratch, TaStart *out)
 {
     int64_t *s_warp = scratch + kMaxTreeBatch + 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -913,7 +1019,6 @@ __device__ void ta_start(const TaParams &p, int64_t *scratch, TaSlices *out)
     const int c = blockIdx.x;
     const int64_t lo = c < ctas ? total * c / ctas : total, hi = c < ctas ? total * (c + 1) / ctas : total;
     out->left = hi - lo;
-    out->fresh = true;
     out->b = 0;
     out->unit = 0;
     out->off = 0;
@@ -967,6 +1072,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 mbar_init(&bars.l_set[i][w], 1);
             }
         }
+        for (int i = 0; i < kSlices; ++i) {
+            mbar_init(&bars.slice_full[i], 1);
+            mbar_init(&bars.slice_empty[i], kReaders);
+        }
         mbar_init(&bars.drain, 1);
         bars.abort = 0;
         mbar_init_fence();
@@ -980,7 +1089,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
     // The row arrays are read before the append of this call has finished: it
     // does not write them, and everything before it has.
-    TaSlices from;
+    TaStart from;
     ta_start(p, reinterpret_cast<int64_t *>(smem + C::kOffK), &from);
     tc_fence_before();
     __syncthreads();
@@ -992,16 +1101,16 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     if (threadIdx.x == kTaSoftmaxWarp * 32) // the thread that writes it at the end
         p.records[blockIdx.x] = make_int4(0, 0, 0, 0);
 
-    if (warp == kTaKWarp)
-        ta_load<D, true>(p, maps, smem, bars, from, lane);
+    if (warp == kTaWalkWarp)
+        ta_walk<D>(p, smem, bars, from, lane);
+    else if (warp == kTaKWarp)
+        ta_load<D, true>(p, maps, smem, bars, lane);
     else if (warp == kTaVWarp)
-        ta_load<D, false>(p, maps, smem, bars, from, lane);
-    else if (warp == kTaCheckWarp)
-        ta_check_v<D>(p, smem, bars, from, lane);
+        ta_load<D, false>(p, maps, smem, bars, lane);
     else if (warp == kTaMmaWarp)
-        ta_mma<D>(p, smem, bars, tmem, from);
+        ta_mma<D>(p, smem, bars, tmem, lane);
     else
-        ta_softmax<D>(p, smem, bars, tmem, from, warp, lane);
+        ta_softmax<D>(p, smem, bars, tmem, warp, lane);
 
     tc_fence_before();
     __syncthreads();
