@@ -226,7 +226,7 @@ struct TreeShape {
     int group;     // num_q_heads / num_kv_heads
     int q_tile;    // nodes of a work unit: 128 MMA rows
     int slot_rows; // rows of a partial result
-    size_t off_ml, off_o; // partial results in the workspace, after the CTAs' records
+    size_t off_rows, off_ml, off_o; // workspace: rows' (m, l) and partial results, after the CTAs' records
     size_t bytes;
 };
 

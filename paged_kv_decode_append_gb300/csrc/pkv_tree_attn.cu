@@ -29,15 +29,14 @@
 //  - Warps: 3 walks the CTA's range, hands its slices to the others through a
 //    ring and looks V through; 0 loads Q and K, 2 loads V, with TMA, K and V into
 //    a ring each (one lane per box, a box per page piece); 1 owns TMEM and one
-//    thread of it issues the MMAs; 4-7 and 8-11 are two softmax groups that take
-//    alternate tiles, one thread per MMA row.  While one group is at tile t the
-//    tensor pipe runs S of tile t + 1 and P V of tile t - 1.
-//  - The groups share one O and one running maximum: (m, l) of a row go from
-//    group to group through shared memory, m as soon as a tile's maximum is
-//    known, so the other group is hardly ever held up.  m moves only when a
-//    score exceeds it by more than 2^8 (then O is rescaled); the weights are
-//    taken as 2^(s - m - 8) <= 1, so a large value cannot overflow before the
-//    division.
+//    thread of it issues the MMAs; 4-7 and 8-11 run the softmax, two threads per
+//    MMA row on half of a tile's columns each (they exchange their maxima); 12-15
+//    finish slices, so that the softmax goes on with the next one meanwhile.
+//    While the softmax is at tile t the tensor pipe runs S of tile t + 1 and P V
+//    of tile t - 1.
+//  - The running maximum m moves only when a score exceeds it by more than 2^8
+//    (then O is rescaled); the weights are taken as 2^(s - m - 8) <= 1, so a
+//    large value cannot overflow before the division.
 //  - P replaces S in TMEM as bf16 hi + lo parts (16 significant bits; 8 alone
 //    leave errors of 2^-9 of the row's scale in small outputs).
 //  - Tiles with drafted keys take their visibility as four 32-bit words per
@@ -61,10 +60,11 @@ constexpr int kStartCost = 2;     // positions that a unit costs before its firs
 constexpr int kMinBlocks = 2;     // a unit is not cut nearer than this to its ends
 constexpr int kMinRange = 6;      // positions that are worth a CTA of their own
 constexpr int kTaMaxCtas = 160;   // persistent CTAs the workspace has room for
-constexpr int kTaKWarp = 0, kTaMmaWarp = 1, kTaVWarp = 2, kTaWalkWarp = 3, kTaSoftmaxWarp = 4;
-constexpr int kTaThreads = 384;
+constexpr int kTaKWarp = 0, kTaMmaWarp = 1, kTaVWarp = 2, kTaWalkWarp = 3, kTaSoftmaxWarp = 4,
+              kTaEndWarp = 12;
+constexpr int kTaThreads = 512;
 constexpr int kSlices = 8;        // slices handed out and not yet done with
-constexpr int kReaders = 12;      // warps that read them
+constexpr int kReaders = 16;      // warps that read them
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.693147180559945309f;
 
@@ -83,8 +83,8 @@ template <int D> struct TaCfg {
     static constexpr uint32_t kOffV = kOffK + kKStages * kItemBytes;
     static constexpr uint32_t kOffQ = kOffV + kVStages * kItemBytes;
     static constexpr uint32_t kOffBar = kOffQ + kQBytes;
-    static constexpr uint32_t kOffChain = kOffBar + 1024;         // m [128], l [128]
-    static constexpr uint32_t kSmem = kOffChain + 1024 + 1024;    // + alignment slack
+    static constexpr uint32_t kOffMax = kOffBar + 1024;           // maxima, [tile parity][half][128 rows]
+    static constexpr uint32_t kSmem = kOffMax + 2048;
     static constexpr int kOBufs = D == 256 ? 1 : 2;
     static constexpr uint32_t kColS = kOBufs * D;                 // two S buffers of kTile columns
     static constexpr uint32_t kTmemCols = 512;
@@ -107,7 +107,9 @@ struct TaBars {
     uint64_t k_full[6], k_empty[6], v_full[6], v_ready[6], v_empty[6];
     uint64_t q_full;
     uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
-    uint64_t m_set[2][4], l_set[2][4]; // by softmax group and TMEM lane quarter
+    uint64_t o_last[2];       // O of a slice (by its parity) is complete
+    uint64_t ml_full[2], ml_free[2]; // (m, l) of a slice written / read
+    uint64_t pair[4];         // the two softmax warps of each TMEM lane quarter
     uint64_t slice_full[kSlices], slice_empty[kSlices];
     uint64_t drain;
     TaSlice slice[kSlices];
@@ -125,6 +127,7 @@ struct TaParams {
     float *lse;
     int32_t *err_flag;
     int4 *records;     // [CTA]
+    float2 *row_ml;    // [CTA][slice parity][half][128 rows]: from the softmax to the finishing warps
     float2 *part_ml;   // [2 * CTA][slot_rows]
     float *part_o;     // [2 * CTA][slot_rows][D]
     int batch, num_q_heads, num_kv_heads, group, total_q, max_blocks, max_nodes, words;
@@ -590,7 +593,7 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
     bool issued = false, more = t.next(p, bars, lane);
     int prev = -1; // tile whose P V is due
     int prev_tokens = 0, prev_unit = 0;
-    bool prev_first = false;
+    bool prev_first = false, prev_last = false;
     int k_slot = 0, v_slot = 0;
     uint32_t k_par = 0, v_par = 0;
 #pragma unroll 1
@@ -642,6 +645,8 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
             }
             ta_commit(&bars.o_done[prev & 1]);
             ta_commit(&bars.v_empty[v_slot]);
+            if (prev_last)
+                ta_commit(&bars.o_last[prev_unit & 1]);
             if (++v_slot == C::kVStages) {
                 v_slot = 0;
                 v_par ^= 1;
@@ -652,6 +657,7 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
             prev = t.gt;
             prev_tokens = t.tokens();
             prev_first = t.first();
+            prev_last = t.tok + C::kTile >= t.s.tok1;
             prev_unit = t.n;
             more = t.next(p, bars, lane);
         }
@@ -739,79 +745,76 @@ __device__ __noinline__ void ta_add_nonfinite(const TaParams &p, int b, int len,
     }
 }
 
-// One of the two softmax groups (group gi takes the tiles of parity gi); thread
-// = MMA row.  Both groups finish every slice, half of O's columns each.
+// The softmax: two threads per MMA row, each on half of a tile's columns and
+// (where O is rescaled) half of O's.
 template <int D>
 __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t tmem, int warp, int lane)
 {
     using C = TaCfg<D>;
-    constexpr int kChunks = C::kTile / 32;
-    const int gi = (warp - kTaSoftmaxWarp) >> 2;
+    constexpr int kChunks = C::kTile / 64;      // 32-column chunks of this thread
+    const int half = (warp - kTaSoftmaxWarp) >> 2;
     const int quarter = warp & 3; // TMEM lanes this warp may access
     const int r = quarter * 32 + lane;
     const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16);
-    float *m_chain = reinterpret_cast<float *>(smem + C::kOffChain), *l_chain = m_chain + kTaRows;
+    float *maxima = reinterpret_cast<float *>(smem + C::kOffMax);
     const float qs = p.q_scale, qse = qs > 0.f ? qs : 1.f;
-    const int node_in_tile = r / p.group, head_in_group = r - node_in_tile * p.group;
-    int gt = 0;         // tiles before this slice
-    int record = 0;
-    int4 tail = make_int4(0, 0, 0, 0);
+    const int node_in_tile = r / p.group;
+    int gt = 0;          // tiles before this one
+    uint32_t meetings = 0; // of the two warps of this quarter
 
 #pragma unroll 1
     for (int n = 0;; ++n) {
         const TaSlice s = ta_slice(p, bars, n);
         if (s.flags & kOver)
-            break;
+            return;
         const int rows = min(p.q_tile, s.nodes - s.node0) * p.group; // MMA rows in use
         const bool live = r < rows, warp_live = quarter * 32 < rows;
-        const int64_t token = (int64_t)s.first + s.node0 + node_in_tile;
-        const int64_t out_row = token * p.num_q_heads + s.g * p.group + head_in_group;
-        const int32_t *mask = p.mask + (live ? token : (int64_t)s.first) * p.words;
-        const int nt = (s.tok1 - s.tok0 + C::kTile - 1) / C::kTile;
-        float m = -INFINITY, l = 0.f;
+        const int32_t *mask = p.mask + ((int64_t)s.first + (live ? s.node0 + node_in_tile : 0)) * p.words;
+        const uint32_t o_col = t_row + (C::kOBufs == 1 ? 0u : (n & 1) * D);
+        float m = -INFINITY, l = 0.f; // l: this half's part of the row's sum
 #pragma unroll 1
-        for (int j = (gt + gi) & 1; j < nt; j += 2) { // gt + j has parity gi
-            const int tile = gt + j;
-            const int tok = s.tok0 + j * C::kTile, tokens = min(C::kTile, s.tok1 - tok);
+        for (int tok = s.tok0; tok < s.tok1; tok += C::kTile, ++gt) {
+            const int tok_h = tok + half * (C::kTile / 2), tokens = s.tok1 - tok_h; // this half's keys
             // tiles with drafted keys or past the slice's end: the node's mask words
-            const bool masked = tok + C::kTile > s.len || tokens < C::kTile;
+            const bool masked = tok + C::kTile > s.len || tok + C::kTile > s.tok1;
             uint32_t words[kChunks + 1];
-            if (masked) {
-                const int w0 = (tok - s.len) >> 5;
+            if (masked && warp_live) {
+                const int w0 = (tok_h - s.len) >> 5;
 #pragma unroll
                 for (int c = 0; c <= kChunks; ++c)
                     words[c] = ta_mask_word(mask, s.nodes, w0 + c);
             }
-            if (!ta_wait_all(&bars.s_full[gi], (uint32_t)(tile >> 1) & 1, bars, p.err_flag))
+            if (!ta_wait_all(&bars.s_full[gt & 1], (uint32_t)(gt >> 1) & 1, bars, p.err_flag))
                 return;
             tc_fence_after();
-            const uint32_t s_col = t_row + C::kColS + (uint32_t)gi * C::kTile;
-            // Tiles with drafted keys or past the slice's end, and scales that cannot
-            // be folded into the exponent: S is rewritten once, so that the
-            // passes below are the same short loops for every tile.
-            if (warp_live && (masked || !(qs > 0.f))) {
-                const float by = qs > 0.f ? 1.f : qs;
-                const int shift = (tok - s.len) & 31;
-#pragma unroll 1
-                for (int c = 0; c < kChunks; ++c) {
-                    const int end = tokens - 32 * c;
-                    uint32_t seen = end >= 32 ? 0xffffffffu : end <= 0 ? 0u : (1u << end) - 1u;
-                    if (masked) {
-                        seen &= __funnelshift_r(words[0], words[1], shift);
-#pragma unroll
-                        for (int w = 0; w < kChunks; ++w)
-                            words[w] = words[w + 1];
-                    }
-                    uint32_t x[32];
-                    tmem_ld32(s_col + 32 * c, x);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        x[i] = seen >> i & 1u ? __float_as_uint(__uint_as_float(x[i]) * by) : 0xff800000u;
-                    tmem_st32(s_col + 32 * c, x);
-                }
-            }
-            float mx = -INFINITY;
+            const uint32_t s_col = t_row + C::kColS + (uint32_t)(gt & 1) * C::kTile + half * (C::kTile / 2);
+            float alpha = 1.f;
+            bool rescale = false;
             if (warp_live) {
+                // Tiles with drafted keys or past the slice's end, and scales that
+                // cannot be folded into the exponent: S is rewritten once, so that
+                // the passes below are the same short loops for every tile.
+                if (masked || !(qs > 0.f)) {
+                    const float by = qs > 0.f ? 1.f : qs;
+                    const int shift = (tok_h - s.len) & 31;
+#pragma unroll 1
+                    for (int c = 0; c < kChunks; ++c) {
+                        const int end = tokens - 32 * c;
+                        uint32_t seen = end >= 32 ? 0xffffffffu : end <= 0 ? 0u : (1u << end) - 1u;
+                        if (masked) {
+                            seen &= __funnelshift_r(words[0], words[1], shift);
+#pragma unroll
+                            for (int w = 0; w < kChunks; ++w)
+                                words[w] = words[w + 1];
+                        }
+                        uint32_t x[32];
+                        tmem_ld32(s_col + 32 * c, x);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            x[i] = seen >> i & 1u ? __float_as_uint(__uint_as_float(x[i]) * by) : 0xff800000u;
+                        tmem_st32(s_col + 32 * c, x);
+                    }
+                }
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
                 for (int c = 0; c < kChunks; ++c) {
@@ -821,24 +824,23 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                     for (int i = 0; i < 32; ++i)
                         m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[i]));
                 }
-                mx = live ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qse : -INFINITY;
-            }
-            // the row's maximum so far comes from the other group, which had the tile before
-            float before = -INFINITY;
-            if (j > 0) {
-                if (!ta_wait_all(&bars.m_set[1 - gi][quarter], (uint32_t)((tile - 1) >> 1) & 1, bars, p.err_flag))
+                float mx = live ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qse : -INFINITY;
+                // the row's maximum over both halves
+                float *at = maxima + (meetings & 1) * (2 * kTaRows) + r;
+                at[half * kTaRows] = mx;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bars.pair[quarter]);
+                if (!ta_wait_all(&bars.pair[quarter], meetings & 1, bars, p.err_flag))
                     return;
-                before = m_chain[r];
-            }
-            const bool grow = mx > before + kRescaleLog2;
-            m = grow ? mx : before;
-            m_chain[r] = m;
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bars.m_set[gi][quarter]);
-            const float alpha = grow ? ex2_approx(before - m) : 1.f; // 0 on the first tile
-            float2 sum2 = make_float2(0.f, 0.f);
-            if (warp_live) {
+                ++meetings;
+                mx = fmaxf(mx, at[(1 - half) * kTaRows]);
+                if (mx > m + kRescaleLog2) {
+                    rescale = m != -INFINITY; // before the slice's first P V there is no O
+                    alpha = ex2_approx(m - mx);
+                    m = mx;
+                }
+                float2 sum2 = make_float2(0.f, 0.f);
                 const float m_ref = m == -INFINITY ? 0.f : m + kRescaleLog2;
                 const float2 q2 = make_float2(qse, qse), nm2 = make_float2(-m_ref, -m_ref);
 #pragma unroll 1
@@ -862,17 +864,15 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                     tmem_st16_issue(s_col + 32 * c + 16, lo);
                 }
                 tmem_st_wait();
+                l = l * alpha + (sum2.x + sum2.y);
             }
-            // O holds this slice's sum only after its first P V
-            const uint32_t o_col = t_row + (C::kOBufs == 1 ? 0u : (n & 1) * D);
-            const bool rescale = grow && before != -INFINITY;
             if (__any_sync(0xffffffffu, rescale)) {
-                if (!ta_wait_all(&bars.o_done[(tile - 1) & 1], (uint32_t)((tile - 1) >> 1) & 1, bars, p.err_flag))
+                if (!ta_wait_all(&bars.o_done[(gt - 1) & 1], (uint32_t)((gt - 1) >> 1) & 1, bars, p.err_flag))
                     return;
                 tc_fence_after();
                 const float a = rescale ? alpha : 1.f;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
                     uint32_t o[32];
                     tmem_ld32(o_col + c, o);
 #pragma unroll
@@ -884,27 +884,58 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&bars.p_full[gi]);
-            // the row's sum, when the other group has added its tile
-            if (j > 0) {
-                if (!ta_wait_all(&bars.l_set[1 - gi][quarter], (uint32_t)((tile - 1) >> 1) & 1, bars, p.err_flag))
-                    return;
-                l = l_chain[r];
-            }
-            l = l * alpha + (sum2.x + sum2.y);
-            l_chain[r] = l;
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bars.l_set[gi][quarter]);
+                mbar_arrive(&bars.p_full[gt & 1]);
         }
-        const int end = gt + nt - 1; // the slice's last tile
-        if ((end & 1) != gi) {
-            if (!ta_wait_all(&bars.l_set[1 - gi][quarter], (uint32_t)(end >> 1) & 1, bars, p.err_flag))
-                return;
-            m = m_chain[r]; // not written again before this group's next tile
-            l = l_chain[r];
-        }
-        if (!ta_wait_all(&bars.o_done[end & 1], (uint32_t)(end >> 1) & 1, bars, p.err_flag))
+        // (m, l) to the warps that finish the slice
+        if (n >= 2 && !ta_wait_all(&bars.ml_free[n & 1], (uint32_t)(n / 2 - 1) & 1, bars, p.err_flag))
+            return;
+        p.row_ml[((int64_t)blockIdx.x * 4 + (n & 1) * 2 + half) * kTaRows + r] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&bars.ml_full[n & 1]);
+        ta_slice_done(bars, n, lane);
+    }
+}
+
+// A value another warp of this CTA has written (never from an earlier load).
+__device__ __forceinline__ float2 load_fresh(const float2 *at)
+{
+    float2 v;
+    asm volatile("ld.volatile.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(at) : "memory");
+    return v;
+}
+
+// Finishes the slices, one thread per MMA row: O / l to out where the slice is a
+// whole unit, else O and (m, l) to the workspace.
+template <int D>
+__device__ void ta_finish(const TaParams &p, TaBars &bars, uint32_t tmem, int warp, int lane)
+{
+    using C = TaCfg<D>;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16);
+    const int node_in_tile = r / p.group, head_in_group = r - node_in_tile * p.group;
+    int record = 0;
+    int4 tail = make_int4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int n = 0;; ++n) {
+        const TaSlice s = ta_slice(p, bars, n);
+        if (s.flags & kOver)
+            break;
+        const int rows = min(p.q_tile, s.nodes - s.node0) * p.group;
+        const bool live = r < rows, warp_live = quarter * 32 < rows;
+        const int64_t token = (int64_t)s.first + (live ? s.node0 + node_in_tile : 0);
+        const int64_t out_row = token * p.num_q_heads + s.g * p.group + head_in_group;
+        const uint32_t parity = (uint32_t)(n >> 1) & 1;
+        if (!ta_wait_all(&bars.ml_full[n & 1], parity, bars, p.err_flag))
+            return;
+        const float2 *ml = p.row_ml + ((int64_t)blockIdx.x * 4 + (n & 1) * 2) * kTaRows + r;
+        const float2 a = load_fresh(ml), b = load_fresh(ml + kTaRows);
+        const float m = a.x, l = a.y + b.y;
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&bars.ml_free[n & 1]);
+        if (!ta_wait_all(&bars.o_last[n & 1], parity, bars, p.err_flag))
             return;
         tc_fence_after();
         const bool bad = *(volatile uint8_t *)&bars.bad[n % kSlices] != 0;
@@ -912,12 +943,13 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
         const uint32_t o_col = t_row + (C::kOBufs == 1 ? 0u : (n & 1) * D);
         const bool begins = s.flags & kBegins, ends = s.flags & kEnds, whole = begins && ends;
         const int64_t part = (int64_t)(2 * blockIdx.x + (begins ? 1 : 0)) * p.slot_rows + r;
-        const float inv = whole && l > 0.f ? 1.f / l : l != l ? l : 0.f;
+        const bool zero = bad || l == 0.f;
+        const float inv = 1.f / l;
         if (nonfinite && warp_live)
-            ta_add_nonfinite<D>(p, s.b, s.len, s.g, mask, max(0, s.tok0 - s.len), min(s.nodes, s.tok1 - s.len), live, o_col,
-                                gi * (D / 2), (gi + 1) * (D / 2));
+            ta_add_nonfinite<D>(p, s.b, s.len, s.g, p.mask + token * p.words, max(0, s.tok0 - s.len),
+                                min(s.nodes, s.tok1 - s.len), live, o_col, 0, D);
 #pragma unroll 1
-        for (int c = gi * (D / 2); warp_live && c < (gi + 1) * (D / 2); c += 32) {
+        for (int c = 0; warp_live && c < D; c += 32) {
             uint32_t o[32];
             tmem_ld32(o_col + c, o);
             if (!live)
@@ -928,7 +960,7 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                 for (int e = 0; e < 16; ++e) {
                     const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv,
                                                                    __uint_as_float(o[2 * e + 1]) * inv);
-                    w[e] = bad || l == 0.f ? 0u : *reinterpret_cast<const uint32_t *>(&h);
+                    w[e] = zero ? 0u : *reinterpret_cast<const uint32_t *>(&h);
                 }
                 store32(p.out + out_row * D + c, w, p.wide);
                 store32(p.out + out_row * D + c + 16, w + 8, p.wide);
@@ -938,13 +970,17 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                     store32(p.part_o + part * D + c + e, o + e, true);
             }
         }
-        if (live && gi == 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&bars.o_free[C::kOBufs == 1 ? 0 : n & 1]);
+        if (live) {
             if (!whole)
                 p.part_ml[part] = make_float2(m, l);
             else if (p.lse != nullptr)
-                p.lse[out_row] = bad || l == 0.f ? -INFINITY : (m + kRescaleLog2 + log2f(l)) * kLn2;
+                p.lse[out_row] = zero ? -INFINITY : (m + kRescaleLog2 + log2f(l)) * kLn2;
         }
-        if (r == 0 && gi == 0) {
+        if (r == 0) {
             if (bad)
                 set_error(p.err_flag, PKV_ERR_PAGE);
             if (!begins)
@@ -954,14 +990,9 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                 tail = make_int4(0, s.first + s.node0, s.g, rows);
             }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&bars.o_free[C::kOBufs == 1 ? 0 : n & 1]);
         ta_slice_done(bars, n, lane);
-        gt += nt;
     }
-    if (r == 0 && gi == 0) {
+    if (r == 0) {
         tail.x = record;
         p.records[blockIdx.x] = tail;
     }
@@ -1045,8 +1076,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     tree_attn_kernel(const __grid_constant__ TaParams p, const __grid_constant__ TaMaps maps)
 {
     using C = TaCfg<D>;
-    extern __shared__ unsigned char ta_smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ta_smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) unsigned char ta_smem_raw[];
+    uint8_t *smem = ta_smem_raw;
+    if ((smem_addr(smem) & 1023u) != 0) { // the swizzled tiles need it; dynamic shared memory starts so
+        set_error(p.err_flag, PKV_ERR_TIMEOUT);
+        return;
+    }
     TaBars &bars = *reinterpret_cast<TaBars *>(smem + C::kOffBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -1064,14 +1099,15 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         mbar_init(&bars.q_full, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[i], 4); // the warps of the tile's group
+            mbar_init(&bars.p_full[i], 8); // the softmax warps
             mbar_init(&bars.o_done[i], 1);
-            mbar_init(&bars.o_free[i], 8); // the warps of both groups
-            for (int w = 0; w < 4; ++w) {
-                mbar_init(&bars.m_set[i][w], 1);
-                mbar_init(&bars.l_set[i][w], 1);
-            }
+            mbar_init(&bars.o_last[i], 1);
+            mbar_init(&bars.o_free[i], 4); // the finishing warps
+            mbar_init(&bars.ml_full[i], 8);
+            mbar_init(&bars.ml_free[i], 4);
         }
+        for (int i = 0; i < 4; ++i)
+            mbar_init(&bars.pair[i], 2);
         for (int i = 0; i < kSlices; ++i) {
             mbar_init(&bars.slice_full[i], 1);
             mbar_init(&bars.slice_empty[i], kReaders);
@@ -1098,7 +1134,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         asm volatile("griddepcontrol.wait;" ::: "memory");
     fence_proxy_async_smem(); // the scratch's reads and writes before the copies over it
     const uint32_t tmem = bars.tmem_base;
-    if (threadIdx.x == kTaSoftmaxWarp * 32) // the thread that writes it at the end
+    if (threadIdx.x == kTaEndWarp * 32) // the thread that writes it at the end
         p.records[blockIdx.x] = make_int4(0, 0, 0, 0);
 
     if (warp == kTaWalkWarp)
@@ -1109,8 +1145,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         ta_load<D, false>(p, maps, smem, bars, lane);
     else if (warp == kTaMmaWarp)
         ta_mma<D>(p, smem, bars, tmem, lane);
-    else
+    else if (warp < kTaEndWarp)
         ta_softmax<D>(p, smem, bars, tmem, warp, lane);
+    else
+        ta_finish<D>(p, bars, tmem, warp, lane);
 
     tc_fence_before();
     __syncthreads();
@@ -1254,7 +1292,8 @@ pkv_status tree_shape(int batch, int total_q, int max_blocks, int num_q_heads, i
     s->q_tile = kTaRows / s->group;
     s->slot_rows = (s->q_tile < max_nodes ? s->q_tile : max_nodes) * s->group;
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-    s->off_ml = up(kTaMaxCtas * sizeof(int4));
+    s->off_rows = up(kTaMaxCtas * sizeof(int4));
+    s->off_ml = s->off_rows + up((size_t)kTaMaxCtas * 4 * kTaRows * sizeof(float2));
     s->off_o = s->off_ml + up((size_t)2 * kTaMaxCtas * s->slot_rows * sizeof(float2));
     s->bytes = 256 + s->off_o + up((size_t)2 * kTaMaxCtas * s->slot_rows * desc->head_dim * sizeof(float));
     return PKV_OK;
@@ -1278,6 +1317,7 @@ cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t stream)
     p.lse = a.lse;
     p.err_flag = a.err_flag;
     p.records = reinterpret_cast<int4 *>(ws);
+    p.row_ml = reinterpret_cast<float2 *>(ws + a.shape.off_rows);
     p.part_ml = reinterpret_cast<float2 *>(ws + a.shape.off_ml);
     p.part_o = reinterpret_cast<float *>(ws + a.shape.off_o);
     p.batch = a.batch;
