@@ -137,6 +137,7 @@ struct TaParams {
     uint32_t q_box_bytes;
     float q_scale;
     int pdl;
+    uint32_t k65536;
     bool wide;         // out is 32-byte aligned
 };
 
@@ -155,13 +156,23 @@ struct TaRow {
     int err;
 };
 
-// Row b's part in the call (see include/pkv.h); tiles = 0 when it owns no node.
-__device__ __forceinline__ TaRow ta_row(const TaParams &p, int b)
+// What a row's part in the call is made from.
+struct TaRaw {
+    int first, end, len;
+};
+__device__ __forceinline__ TaRaw ta_raw(const TaParams &p, int b)
+{
+    b = min(b, p.batch - 1);
+    return {p.indptr[b], p.indptr[b + 1], p.seqlens[b]};
+}
+
+// A row's part in the call (see include/pkv.h); tiles = 0 when it owns no node.
+__device__ __forceinline__ TaRow ta_row(const TaParams &p, const TaRaw &raw)
 {
     TaRow r;
-    r.first = p.indptr[b];
-    const int64_t n = (int64_t)p.indptr[b + 1] - r.first;
-    r.len = p.seqlens[b];
+    r.first = raw.first;
+    const int64_t n = (int64_t)raw.end - r.first;
+    r.len = raw.len;
     r.err = 0;
     r.blocks = 0;
     r.nodes = 0;
@@ -254,13 +265,15 @@ __device__ void ta_zero_unit(const TaParams &p, const TaRow &row, int g, int nod
 template <int D> struct TaWalk {
     TaStart at;
     TaRow row;
+    TaRaw then; // the next row, read ahead
     int n; // slices handed out
     bool over;
 
     __device__ __forceinline__ void start(const TaParams &p, const TaStart &from)
     {
         at = from;
-        row = ta_row(p, at.b);
+        row = ta_row(p, ta_raw(p, at.b));
+        then = ta_raw(p, at.b + 1);
         n = 0;
         over = false;
     }
@@ -275,7 +288,8 @@ template <int D> struct TaWalk {
                 ++at.b;
                 at.unit = 0;
                 at.off = 0;
-                row = ta_row(p, at.b);
+                row = ta_row(p, then);
+                then = ta_raw(p, at.b + 1);
                 continue;
             }
             const int64_t size = kStartCost + row.blocks, take = min(size - at.off, at.left);
@@ -467,6 +481,14 @@ __device__ __forceinline__ bool bf16_nonfinite(uint32_t half)
     return (half & 0x7f80u) == 0x7f80u;
 }
 
+// The i-th 16-byte piece of a V tile in shared memory, row by row (D / 8 pieces
+// a row; which piece of the row it is, the swizzle decides).
+template <int D> __device__ __forceinline__ uint8_t *ta_v_piece(uint8_t *vb, int i)
+{
+    const int row = i / (D / 8), piece = i % (D / 8);
+    return vb + (row >> 3) * TaCfg<D>::kGroupStride + (piece >> 3) * 1024 + (row & 7) * 128 + (piece & 7) * 16;
+}
+
 // One warp hands out the slices, as far ahead as there is room, and looks V
 // through before the MMAs read it.  Of a tile with drafted tokens it replaces
 // their infinities and NaN by 0 (and marks the slice); rows past the keys, up
@@ -509,30 +531,31 @@ __device__ void ta_walk(const TaParams &p, uint8_t *smem, TaBars &bars, const Ta
         const int d0 = min(tokens, max(0, s.len - tok)), r1 = (tokens + 15) & ~15;
         if (d0 < r1) {
             uint8_t *vb = smem + C::kOffV + v_slot * C::kItemBytes;
-            bool found = false;
-#pragma unroll 2
-            for (int i = d0 * kPieces + lane; i < r1 * kPieces; i += 32) {
-                const int row = i / kPieces, piece = i % kPieces;
-                uint4 *at = reinterpret_cast<uint4 *>(vb + (row >> 3) * C::kGroupStride + (piece >> 3) * 1024 +
-                                                      (row & 7) * 128 + (piece & 7) * 16);
-                uint4 x = *at;
-                uint32_t *w = reinterpret_cast<uint32_t *>(&x);
-                bool hit = false;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const bool lo = bf16_nonfinite(w[k]), hi = bf16_nonfinite(w[k] >> 16);
-                    w[k] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0xffffu : 0xffffffffu);
-                    hit |= lo || hi;
-                }
-                const bool past = row >= tokens;
-                if (past)
-                    x = make_uint4(0u, 0u, 0u, 0u);
-                if (hit || past)
-                    *at = x;
-                found |= hit && !past;
+            // any infinity or NaN: 0 * x is NaN, and stays in the sum
+            __nv_bfloat162 sum = __floats2bfloat162_rn(0.f, 0.f);
+            const __nv_bfloat162 zero = sum;
+#pragma unroll 4
+            for (int i = d0 * kPieces + lane; i < tokens * kPieces; i += 32) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(ta_v_piece<D>(vb, i));
+                sum = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&x.x), zero, sum);
+                sum = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&x.y), zero, sum);
+                sum = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&x.z), zero, sum);
+                sum = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&x.w), zero, sum);
             }
-            if (found)
-                *(volatile uint8_t *)&bars.nonfinite[n % kSlices] = 1;
+            if (__any_sync(0xffffffffu, __hisnan(sum.x) || __hisnan(sum.y))) {
+#pragma unroll 1
+                for (int i = d0 * kPieces + lane; i < tokens * kPieces; i += 32) {
+                    uint32_t *w = reinterpret_cast<uint32_t *>(ta_v_piece<D>(vb, i));
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k)
+                        w[k] &= (bf16_nonfinite(w[k]) ? 0xffff0000u : 0xffffffffu) &
+                                (bf16_nonfinite(w[k] >> 16) ? 0xffffu : 0xffffffffu);
+                }
+                if (lane == 0)
+                    *(volatile uint8_t *)&bars.nonfinite[n % kSlices] = 1;
+            }
+            for (int i = tokens * kPieces + lane; i < r1 * kPieces; i += 32)
+                *reinterpret_cast<uint4 *>(ta_v_piece<D>(vb, i)) = make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem(); // before the MMAs' reads
         }
         __syncwarp();
@@ -678,6 +701,13 @@ __device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t (
                  "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
 }
+// Three-input maximum (one instruction).
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ void tmem_st_wait()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -815,16 +845,16 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                         tmem_st32(s_col + 32 * c, x);
                     }
                 }
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float m2[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
                 for (int c = 0; c < kChunks; ++c) {
                     uint32_t x[32];
                     tmem_ld32(s_col + 32 * c, x);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[i]));
+                    for (int i = 0; i < 32; i += 2)
+                        m2[i >> 1 & 1] = max3(m2[i >> 1 & 1], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
                 }
-                float mx = live ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qse : -INFINITY;
+                float mx = live ? fmaxf(m2[0], m2[1]) * qse : -INFINITY;
                 // the row's maximum over both halves
                 float *at = maxima + (meetings & 1) * (2 * kTaRows) + r;
                 at[half * kTaRows] = mx;
@@ -855,7 +885,10 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                         const float2 w = make_float2(ex2_approx(a.x), ex2_approx(a.y));
                         sum2 = __fadd2_rn(sum2, w);
                         const __nv_bfloat162 h = __floats2bfloat162_rn(w.x, w.y);
-                        const float2 d = ffma2(__bfloat1622float2(h), make_float2(-1.f, -1.f), w);
+                        const uint32_t hw = *reinterpret_cast<const uint32_t *>(&h);
+                        uint32_t h0;
+                        asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(h0) : "r"(hw), "r"(p.k65536), "r"(0));
+                        const float2 d = ffma2(make_float2(__uint_as_float(h0), __uint_as_float(hw & 0xffff0000u)), make_float2(-1.f, -1.f), w);
                         const __nv_bfloat162 lw = __floats2bfloat162_rn(d.x, d.y);
                         hi[e] = *reinterpret_cast<const uint32_t *>(&h);
                         lo[e] = *reinterpret_cast<const uint32_t *>(&lw);
@@ -1016,7 +1049,7 @@ __device__ void ta_start(const TaParams &p, int64_t *scratch, TaStart *out)
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
         if (b < p.batch) {
-            const TaRow r = ta_row(p, b);
+            const TaRow r = ta_row(p, ta_raw(p, b));
             sum += ta_positions(p, r);
             if (blockIdx.x == 0 && r.tiles == 0)
                 set_error(p.err_flag, r.err); // no unit reports it
@@ -1042,7 +1075,7 @@ __device__ void ta_start(const TaParams &p, int64_t *scratch, TaStart *out)
         const int b = tid * per + i;
         if (b < p.batch) {
             scratch[b] = x;
-            x += ta_positions(p, ta_row(p, b));
+            x += ta_positions(p, ta_row(p, ta_raw(p, b)));
         }
     }
     __syncthreads();
@@ -1062,7 +1095,7 @@ __device__ void ta_start(const TaParams &p, int64_t *scratch, TaStart *out)
             else
                 z = mid - 1;
         }
-        const TaRow r = ta_row(p, a);
+        const TaRow r = ta_row(p, ta_raw(p, a));
         const int64_t size = kStartCost + r.blocks, in_row = lo - scratch[a];
         out->b = a;
         out->unit = (int)(in_row / size);
@@ -1338,6 +1371,7 @@ cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t stream)
     p.slot_rows = a.shape.slot_rows;
     p.q_scale = a.q_scale;
     p.pdl = a.after_append ? 1 : 0;
+    p.k65536 = 65536u;
     p.wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     const int box_nodes = a.shape.slot_rows / a.shape.group < a.total_q ? a.shape.slot_rows / a.shape.group : a.total_q;
     p.q_box_bytes = (uint32_t)box_nodes * a.shape.group * 128;
