@@ -81,6 +81,8 @@ def load(build_if_missing: bool = True):
     than its sources.  Raises if it cannot be built or loaded: there is no
     fallback implementation."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if build_if_missing and not _build.up_to_date():

@@ -300,22 +300,38 @@ def pkv_mixed_attn(k_cache, v_cache, q, k_new, v_new, qo_indptr, block_table, ca
 
 POOL_HEADER = 16  # int32 words before the ring of a device pool
 
-
-def _shape(t, want, name):
-    if t is not None and tuple(t.shape) != tuple(want):
-        raise ValueError(f"{name}: expected shape {tuple(want)}, got {tuple(t.shape)}")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _one_device(*tensors):
-    """The device of the call's tensors, made sure to be the current one (the
-    library launches on the current device)."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors on different devices")
+def _stream_of(dev: int) -> int:
+    """The current stream of device ``dev`` as an integer."""
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _at(dev: int, name: str, t, dtype, *shape):
+    """Address of ``t`` (None for None) once it is a contiguous tensor of
+    ``dtype`` and ``shape`` (if given) on CUDA device ``dev``."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor on cuda:{dev}")
+    if shape and t.shape != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _device_of(t, name: str) -> int:
+    """The device a call runs on: its first tensor's, which has to be the
+    current one (the library launches on the current device)."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor")
     if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors on cuda:{dev}, which is not the current device")
+        raise ValueError(f"{name} is on cuda:{dev}, which is not the current device")
     return dev
+
+
+_I32, _I64, _BF16, _F32, _U8 = torch.int32, torch.int64, torch.bfloat16, torch.float32, torch.uint8
 
 
 def device_pool(num_pages: int, device="cuda") -> torch.Tensor:
@@ -325,8 +341,8 @@ def device_pool(num_pages: int, device="cuda") -> torch.Tensor:
     if n == 0:
         raise PkvError(EINVAL, "pkv_device_pool_bytes")
     pool = torch.empty(n // 4, dtype=torch.int32, device=device)
-    _one_device(pool)
-    _check(_lib.load().pkv_device_pool_init(_ptr(pool), n, num_pages, _stream(pool.device)), "pkv_device_pool_init")
+    dev = _device_of(pool, "pool")
+    _check(_lib.load().pkv_device_pool_init(pool.data_ptr(), n, num_pages, _stream_of(dev)), "pkv_device_pool_init")
     return pool
 
 
@@ -336,26 +352,21 @@ def pkv_table_update(pool, block_table, held_blocks, cache_seqlens, new_tokens, 
     new_tokens[b]`` tokens (none for an inactive row) from the device ``pool``,
     and writes the new tokens' ``indptr`` ``[B + 1]``, ``slot_map`` (int64) and
     ``positions`` ``[max_tokens]`` where given."""
-    for t, n in ((pool, "pool"), (block_table, "block_table"), (held_blocks, "held_blocks"),
-                 (cache_seqlens, "cache_seqlens"), (new_tokens, "new_tokens"), (indptr, "indptr"),
-                 (positions, "positions"), (err_flag, "err_flag")):
-        _i32(t, n)
-    if slot_map is not None and (slot_map.dtype != torch.int64 or not slot_map.is_contiguous()):
-        raise ValueError("slot_map: expected a contiguous int64 tensor")
-    _one_device(pool, block_table, held_blocks, cache_seqlens, new_tokens, indptr, slot_map, positions, err_flag)
+    dev = _device_of(pool, "pool")
     B, width = block_table.shape
-    for t, n in ((held_blocks, "held_blocks"), (cache_seqlens, "cache_seqlens"), (new_tokens, "new_tokens")):
-        _shape(t, (B,), n)
-    _shape(indptr, (B + 1,), "indptr")
     tokens = 0
-    if slot_map is not None or positions is not None:
-        tokens = (slot_map if slot_map is not None else positions).numel()
-        _shape(slot_map, (tokens,), "slot_map")
-        _shape(positions, (tokens,), "positions")
-    st = _lib.load().pkv_table_update(_ptr(pool), pool.numel() - POOL_HEADER + 1, page_size, _ptr(block_table), width,
-                                      _ptr(held_blocks), _ptr(cache_seqlens), _ptr(new_tokens), B, _ptr(indptr),
-                                      _ptr(slot_map), _ptr(positions), tokens, _ptr(err_flag), _stream(pool.device))
-    _check(st, "pkv_table_update")
+    if slot_map is not None:
+        tokens = slot_map.numel()
+    elif positions is not None:
+        tokens = positions.numel()
+    st = _lib.load().pkv_table_update(
+        _at(dev, "pool", pool, _I32), pool.numel() - POOL_HEADER + 1, page_size,
+        _at(dev, "block_table", block_table, _I32), width, _at(dev, "held_blocks", held_blocks, _I32, B),
+        _at(dev, "cache_seqlens", cache_seqlens, _I32, B), _at(dev, "new_tokens", new_tokens, _I32, B), B,
+        _at(dev, "indptr", indptr, _I32, B + 1), _at(dev, "slot_map", slot_map, _I64, tokens),
+        _at(dev, "positions", positions, _I32, tokens), tokens, _at(dev, "err_flag", err_flag, _I32), _stream_of(dev))
+    if st:
+        _check(st, "pkv_table_update")
 
 
 def pkv_tree_build(parents, qo_indptr, cache_seqlens, max_nodes: int, mask=None, positions=None, err_flag=None):
@@ -363,21 +374,19 @@ def pkv_tree_build(parents, qo_indptr, cache_seqlens, max_nodes: int, mask=None,
     and positions ``cache_seqlens[b] + depth`` of drafted trees; ``parents``
     ``[total_q]`` holds the parent's index within the row, or -1.  Returns
     ``(mask, positions)``."""
-    for t, n in ((parents, "parents"), (qo_indptr, "qo_indptr"), (cache_seqlens, "cache_seqlens"), (mask, "mask"),
-                 (positions, "positions"), (err_flag, "err_flag")):
-        _i32(t, n)
-    T, B = parents.shape[0], cache_seqlens.shape[0]
+    dev = _device_of(parents, "parents")
+    T, B = parents.numel(), cache_seqlens.numel()
     if mask is None:
         mask = torch.empty(T, (max_nodes + 31) // 32, dtype=torch.int32, device=parents.device)
     if positions is None:
         positions = torch.empty(T, dtype=torch.int32, device=parents.device)
-    _one_device(parents, qo_indptr, cache_seqlens, mask, positions, err_flag)
-    _shape(qo_indptr, (B + 1,), "qo_indptr")
-    _shape(mask, (T, mask.shape[-1]), "mask")
-    _shape(positions, (T,), "positions")
-    st = _lib.load().pkv_tree_build(_ptr(parents), _ptr(qo_indptr), _ptr(cache_seqlens), B, T, max_nodes, _ptr(mask),
-                                    mask.shape[1], _ptr(positions), _ptr(err_flag), _stream(parents.device))
-    _check(st, "pkv_tree_build")
+    words = mask.size(-1)
+    st = _lib.load().pkv_tree_build(
+        _at(dev, "parents", parents, _I32, T), _at(dev, "qo_indptr", qo_indptr, _I32, B + 1),
+        _at(dev, "cache_seqlens", cache_seqlens, _I32, B), B, T, max_nodes, _at(dev, "mask", mask, _I32, T, words), words,
+        _at(dev, "positions", positions, _I32, T), _at(dev, "err_flag", err_flag, _I32), _stream_of(dev))
+    if st:
+        _check(st, "pkv_tree_build")
     return mask, positions
 
 
@@ -404,38 +413,27 @@ def pkv_tree_attn(k_cache, v_cache, q, k_new, v_new, qo_indptr, tree_mask, block
     over its row's ``cache_seqlens[b]`` cached keys and the drafted ones whose
     bit ``tree_mask`` ``[total_q, words]`` sets.  Returns ``out`` ``[total_q,
     Hq, D]`` bf16."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (q, "q"), (k_new, "k_new"), (v_new, "v_new"),
-                 (out, "out")):
-        _bf16(t, n)
-    for t, n in ((qo_indptr, "qo_indptr"), (tree_mask, "tree_mask"), (block_table, "block_table"),
-                 (cache_seqlens, "cache_seqlens"), (err_flag, "err_flag")):
-        _i32(t, n)
-    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous()):
-        raise ValueError("lse: expected contiguous float32")
+    dev = _device_of(q, "q")
     desc = cache_desc(k_cache, layout)
     T, Hq, D = q.shape
     B, width = block_table.shape
+    words = tree_mask.size(-1)
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
         workspace = tree_workspace(B, T, width, Hq, max_nodes, desc, q.device)
-    _one_device(q, k_cache, v_cache, k_new, v_new, qo_indptr, tree_mask, block_table, cache_seqlens, out, lse,
-                workspace, err_flag)
-    _shape(v_cache, k_cache.shape, "v_cache")
-    _shape(q, (T, Hq, desc.head_dim), "q")
-    _shape(k_new, (T, desc.num_kv_heads, D), "k_new")
-    _shape(v_new, (T, desc.num_kv_heads, D), "v_new")
-    _shape(out, q.shape, "out")
-    _shape(lse, (T, Hq), "lse")
-    _shape(qo_indptr, (B + 1,), "qo_indptr")
-    _shape(cache_seqlens, (B,), "cache_seqlens")
-    _shape(tree_mask, (T, tree_mask.shape[-1]), "tree_mask")
+    if D != desc.head_dim:
+        raise ValueError("q: head_dim differs from the cache's")
+    K = desc.num_kv_heads
     st = _lib.load().pkv_tree_attn(
-        ctypes.byref(desc), _ptr(k_cache), _ptr(v_cache), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(qo_indptr),
-        _ptr(tree_mask), tree_mask.shape[1], _ptr(block_table), width, _ptr(cache_seqlens), B, Hq, T, int(max_nodes),
-        float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(err_flag),
-        _stream(q.device))
-    _check(st, "pkv_tree_attn")
+        ctypes.byref(desc), _at(dev, "k_cache", k_cache, _BF16), _at(dev, "v_cache", v_cache, _BF16, *k_cache.shape),
+        _at(dev, "q", q, _BF16), _at(dev, "k_new", k_new, _BF16, T, K, D), _at(dev, "v_new", v_new, _BF16, T, K, D),
+        _at(dev, "qo_indptr", qo_indptr, _I32, B + 1), _at(dev, "tree_mask", tree_mask, _I32, T, words), words,
+        _at(dev, "block_table", block_table, _I32), width, _at(dev, "cache_seqlens", cache_seqlens, _I32, B), B, Hq, T,
+        max_nodes, softmax_scale, _at(dev, "out", out, _BF16, T, Hq, D), _at(dev, "lse", lse, _F32, T, Hq),
+        _at(dev, "workspace", workspace, _U8), workspace.numel(), _at(dev, "err_flag", err_flag, _I32), _stream_of(dev))
+    if st:
+        _check(st, "pkv_tree_attn")
     return out
 
 
@@ -444,33 +442,26 @@ def pkv_tree_accept(parents, draft_tokens, target_tokens, root_targets, qo_indpt
     """The path of drafted tokens that the target model chose itself.  Returns
     ``(path [B, max_path], path_len [B], next_token [B], seqlens_out [B])``;
     ``root_targets`` None accepts each row's first root unseen."""
-    for t, n in ((parents, "parents"), (draft_tokens, "draft_tokens"), (target_tokens, "target_tokens"),
-                 (root_targets, "root_targets"), (qo_indptr, "qo_indptr"), (cache_seqlens, "cache_seqlens"),
-                 (path, "path"), (path_len, "path_len"), (next_token, "next_token"), (seqlens_out, "seqlens_out"),
-                 (err_flag, "err_flag")):
-        _i32(t, n)
-    T, B, dev = parents.shape[0], cache_seqlens.shape[0], parents.device
+    dev = _device_of(parents, "parents")
+    T, B = parents.numel(), cache_seqlens.numel()
     if path is None:
-        path = torch.empty(B, max_nodes, dtype=torch.int32, device=dev)
+        path = torch.empty(B, max_nodes, dtype=torch.int32, device=parents.device)
     if path_len is None:
-        path_len = torch.empty(B, dtype=torch.int32, device=dev)
+        path_len = torch.empty(B, dtype=torch.int32, device=parents.device)
     if next_token is None:
-        next_token = torch.empty(B, dtype=torch.int32, device=dev)
+        next_token = torch.empty(B, dtype=torch.int32, device=parents.device)
     if seqlens_out is None:
-        seqlens_out = torch.empty(B, dtype=torch.int32, device=dev)
-    _one_device(parents, draft_tokens, target_tokens, root_targets, qo_indptr, cache_seqlens, path, path_len,
-                next_token, seqlens_out, err_flag)
-    _shape(draft_tokens, (T,), "draft_tokens")
-    _shape(target_tokens, (T,), "target_tokens")
-    _shape(qo_indptr, (B + 1,), "qo_indptr")
-    _shape(path, (B, path.shape[-1]), "path")
-    for t, n in ((root_targets, "root_targets"), (path_len, "path_len"), (next_token, "next_token"),
-                 (seqlens_out, "seqlens_out")):
-        _shape(t, (B,), n)
-    st = _lib.load().pkv_tree_accept(_ptr(parents), _ptr(draft_tokens), _ptr(target_tokens), _ptr(root_targets),
-                                     _ptr(qo_indptr), _ptr(cache_seqlens), B, T, max_nodes, _ptr(path), path.shape[1],
-                                     _ptr(path_len), _ptr(next_token), _ptr(seqlens_out), _ptr(err_flag), _stream(dev))
-    _check(st, "pkv_tree_accept")
+        seqlens_out = torch.empty(B, dtype=torch.int32, device=parents.device)
+    width = path.size(-1)
+    st = _lib.load().pkv_tree_accept(
+        _at(dev, "parents", parents, _I32, T), _at(dev, "draft_tokens", draft_tokens, _I32, T),
+        _at(dev, "target_tokens", target_tokens, _I32, T), _at(dev, "root_targets", root_targets, _I32, B),
+        _at(dev, "qo_indptr", qo_indptr, _I32, B + 1), _at(dev, "cache_seqlens", cache_seqlens, _I32, B), B, T, max_nodes,
+        _at(dev, "path", path, _I32, B, width), width, _at(dev, "path_len", path_len, _I32, B),
+        _at(dev, "next_token", next_token, _I32, B), _at(dev, "seqlens_out", seqlens_out, _I32, B),
+        _at(dev, "err_flag", err_flag, _I32), _stream_of(dev))
+    if st:
+        _check(st, "pkv_tree_accept")
     return path, path_len, next_token, seqlens_out
 
 
@@ -481,35 +472,32 @@ class LayerCaches:
     def __init__(self, k_caches, v_caches, layout: int = NHD):
         if len(k_caches) != len(v_caches) or len(k_caches) < 1:
             raise ValueError("one k and one v cache per layer")
-        for t in (*k_caches, *v_caches):
-            _bf16(t, "caches")
-            _shape(t, k_caches[0].shape, "caches")
-            if t.device != k_caches[0].device:
-                raise ValueError("caches on different devices")
+        self.device = _device_of(k_caches[0], "k_caches")
         self._keep = (list(k_caches), list(v_caches))
+        shape = k_caches[0].shape
         arr = ctypes.c_void_p * len(k_caches)
-        self.k_ptrs, self.v_ptrs = (arr(*[t.data_ptr() for t in lst]) for lst in self._keep)
+        self.k_ptrs, self.v_ptrs = (arr(*[_at(self.device, "caches", t, _BF16, *shape) for t in side])
+                                    for side in self._keep)
         self.num_layers = len(k_caches)
         self.desc = cache_desc(k_caches[0], layout)
-        self.device = k_caches[0].device
 
 
 def pkv_tree_commit(layers: LayerCaches, path, path_len, block_table, cache_seqlens, err_flag=None) -> None:
     """Moves the K/V of each row's accepted nodes ``path[b, :path_len[b]]``
     from position ``cache_seqlens[b] + path[b, i]`` to ``cache_seqlens[b] +
     i`` in every layer (``cache_seqlens`` without the accepted tokens)."""
-    for t, n in ((path, "path"), (path_len, "path_len"), (block_table, "block_table"),
-                 (cache_seqlens, "cache_seqlens"), (err_flag, "err_flag")):
-        _i32(t, n)
+    dev = _device_of(path, "path")
+    if dev != layers.device:
+        raise ValueError("path and caches on different devices")
     B, width = block_table.shape
-    _one_device(layers._keep[0][0], path, path_len, block_table, cache_seqlens, err_flag)
-    _shape(path, (B, path.shape[-1]), "path")
-    _shape(path_len, (B,), "path_len")
-    _shape(cache_seqlens, (B,), "cache_seqlens")
-    st = _lib.load().pkv_tree_commit(ctypes.byref(layers.desc), layers.num_layers, layers.k_ptrs, layers.v_ptrs,
-                                     _ptr(path), path.shape[1], _ptr(path_len), _ptr(block_table), width,
-                                     _ptr(cache_seqlens), B, _ptr(err_flag), _stream(layers.device))
-    _check(st, "pkv_tree_commit")
+    steps = path.size(-1)
+    st = _lib.load().pkv_tree_commit(
+        ctypes.byref(layers.desc), layers.num_layers, layers.k_ptrs, layers.v_ptrs,
+        _at(dev, "path", path, _I32, B, steps), steps, _at(dev, "path_len", path_len, _I32, B),
+        _at(dev, "block_table", block_table, _I32), width, _at(dev, "cache_seqlens", cache_seqlens, _I32, B), B,
+        _at(dev, "err_flag", err_flag, _I32), _stream_of(dev))
+    if st:
+        _check(st, "pkv_tree_commit")
 
 
 def pkv_pool_bytes(desc: CacheDesc) -> int:

@@ -162,7 +162,7 @@ struct TaRaw {
 };
 __device__ __forceinline__ TaRaw ta_raw(const TaParams &p, int b)
 {
-    b = min(b, p.batch - 1);
+    b = max(0, min(b, p.batch - 1));
     return {p.indptr[b], p.indptr[b + 1], p.seqlens[b]};
 }
 
@@ -241,8 +241,9 @@ __device__ __forceinline__ bool ta_wait_all(uint64_t *bar, uint32_t parity, TaBa
 
 // Where a CTA's range starts, and its length in positions.
 struct TaStart {
-    int b, unit;       // row, unit within the row
     int64_t off, left; // position within the unit, positions of the range
+    int b, unit;       // row, unit within the row
+    TaRow row;
 };
 
 // Zeros and -inf for a unit of a row that is inactive or in error.  A whole warp.
@@ -272,7 +273,7 @@ template <int D> struct TaWalk {
     __device__ __forceinline__ void start(const TaParams &p, const TaStart &from)
     {
         at = from;
-        row = ta_row(p, ta_raw(p, at.b));
+        row = at.row;
         then = ta_raw(p, at.b + 1);
         n = 0;
         over = false;
@@ -420,6 +421,8 @@ __device__ void ta_load(const TaParams &p, const TaMaps &maps, uint8_t *smem, Ta
         more = more && t.next(p, bars, lane, !IS_K);
         if (!more && (!IS_K || x >= issued + kStages - 1))
             break;
+        if (more && p.pdl && t.tok + C::kTile > t.s.len) // drafted tokens: this call's append has put them there
+            asm volatile("griddepcontrol.wait;" ::: "memory");
         const int tok = t.tok + (lane << bsh);
         const bool want = more && lane < boxes && tok < t.s.tok1;
         const int32_t *row = p.table + (int64_t)t.s.b * p.max_blocks;
@@ -1039,21 +1042,26 @@ __device__ __forceinline__ int64_t ta_positions(const TaParams &p, const TaRow &
     return (int64_t)r.tiles * p.num_kv_heads * (kStartCost + r.blocks);
 }
 
-// This CTA's range: prefix sum of the rows' positions (in `scratch`), equal parts, and the row and unit its part starts in.
-__device__ void ta_start(const TaParams &p, int64_t *scratch, TaStart *out)
+// This CTA's range, an equal part of all rows' positions: prefix sum over the
+// rows (a few consecutive ones per thread), and the thread whose rows the range
+// starts in says where.  `scratch`: kTaThreads / 32 sums, then a TaStart.
+__device__ TaStart ta_start(const TaParams &p, int64_t *scratch)
 {
-    int64_t *s_warp = scratch + kMaxTreeBatch + 1;
+    constexpr int kPer = (kMaxTreeBatch + kTaThreads - 1) / kTaThreads;
+    TaStart *found = reinterpret_cast<TaStart *>(scratch + kTaThreads / 32);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.batch + kTaThreads - 1) / kTaThreads; // consecutive rows of a thread
+    TaRow row[kPer];
     int64_t sum = 0;
-    for (int i = 0; i < per; ++i) {
-        const int b = tid * per + i;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int b = tid * kPer + i;
+        row[i].tiles = row[i].blocks = 0;
         if (b < p.batch) {
-            const TaRow r = ta_row(p, ta_raw(p, b));
-            sum += ta_positions(p, r);
-            if (blockIdx.x == 0 && r.tiles == 0)
-                set_error(p.err_flag, r.err); // no unit reports it
+            row[i] = ta_row(p, ta_raw(p, b));
+            if (blockIdx.x == 0 && row[i].tiles == 0)
+                set_error(p.err_flag, row[i].err); // no unit reports it
         }
+        sum += ta_positions(p, row[i]);
     }
     int64_t x = sum;
 #pragma unroll
@@ -1063,45 +1071,45 @@ __device__ void ta_start(const TaParams &p, int64_t *scratch, TaStart *out)
             x += y;
     }
     if (lane == 31)
-        s_warp[warp] = x;
+        scratch[warp] = x;
+    if (tid == 0) { // an empty range, at row 0
+        found->off = found->left = 0;
+        found->b = found->unit = 0;
+        found->row = row[0];
+    }
     __syncthreads();
     int64_t total = 0;
+#pragma unroll
     for (int w = 0; w < kTaThreads / 32; ++w) {
-        x += w < warp ? s_warp[w] : 0;
-        total += s_warp[w];
+        const int64_t v = scratch[w];
+        x += w < warp ? v : 0;
+        total += v;
     }
     x -= sum;
-    for (int i = 0; i < per; ++i) {
-        const int b = tid * per + i;
-        if (b < p.batch) {
-            scratch[b] = x;
-            x += ta_positions(p, ta_row(p, ta_raw(p, b)));
+    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kMinRange));
+    const int c = blockIdx.x;
+    if (c < ctas) {
+        // as the quotient and remainder of total / ctas, with small numbers
+        const int64_t q = total / ctas, rest = total - q * ctas;
+        const int64_t lo = q * c + rest * c / ctas, hi = q * (c + 1) + rest * (c + 1) / ctas;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int64_t positions = ta_positions(p, row[i]), in_row = lo - x;
+            if (hi > lo && in_row >= 0 && in_row < positions) {
+                const int size = kStartCost + row[i].blocks;
+                TaStart at;
+                at.b = tid * kPer + i;
+                at.unit = (int)(in_row / size);
+                at.off = in_row - (int64_t)at.unit * size;
+                at.left = hi - lo;
+                at.row = row[i];
+                *found = at;
+            }
+            x += positions;
         }
     }
     __syncthreads();
-    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kMinRange));
-    const int c = blockIdx.x;
-    const int64_t lo = c < ctas ? total * c / ctas : total, hi = c < ctas ? total * (c + 1) / ctas : total;
-    out->left = hi - lo;
-    out->b = 0;
-    out->unit = 0;
-    out->off = 0;
-    if (hi > lo) {
-        int a = 0, z = p.batch - 1; // last row that starts at or before lo
-        while (a < z) {
-            const int mid = (a + z + 1) >> 1;
-            if (scratch[mid] <= lo)
-                a = mid;
-            else
-                z = mid - 1;
-        }
-        const TaRow r = ta_row(p, ta_raw(p, a));
-        const int64_t size = kStartCost + r.blocks, in_row = lo - scratch[a];
-        out->b = a;
-        out->unit = (int)(in_row / size);
-        out->off = in_row - out->unit * size;
-    }
-    __syncthreads(); // the scratch is overwritten by the first copies
+    return *found;
 }
 
 template <int D>
@@ -1156,15 +1164,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         tmem_alloc(&bars.tmem_base, C::kTmemCols);
         tmem_relinquish();
     }
-    // The row arrays are read before the append of this call has finished: it
-    // does not write them, and everything before it has.
-    TaStart from;
-    ta_start(p, reinterpret_cast<int64_t *>(smem + C::kOffK), &from);
+    // With an append before it this kernel starts beside that: everything earlier
+    // is complete, and only K/V at and past a row's length wait for it.
+    const TaStart from = ta_start(p, reinterpret_cast<int64_t *>(smem + C::kOffK));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (p.pdl)
-        asm volatile("griddepcontrol.wait;" ::: "memory");
     fence_proxy_async_smem(); // the scratch's reads and writes before the copies over it
     const uint32_t tmem = bars.tmem_base;
     if (threadIdx.x == kTaEndWarp * 32) // the thread that writes it at the end
@@ -1183,6 +1188,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     else
         ta_finish<D>(p, bars, tmem, warp, lane);
 
+    if (p.pdl && warp == kTaKWarp) // this grid ends after the append, whether it read its tokens or not
+        asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1192,81 +1199,92 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 
 // ---------------------------------------------------------------- combine
 
-constexpr int kCombineThreads = 128;
-constexpr int kCombineParts = 8; // blocks per shared unit
+constexpr int kCombineThreads = 256;
 
 // Joins the slices of the unit that CTA blockIdx.x began and did not end: out =
 // sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, over the CTAs after it up to
-// the one that ended it, in that order.  D / 8 threads per MMA row.
+// the one that ended it, in that order.  D / 8 threads per MMA row; gridDim.y
+// blocks take one row per thread, so that all of a thread's loads are under way
+// at once: what bounds this kernel is the chain record, (m, l) and O.
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __grid_constant__ TaParams p, int ctas)
 {
-    __shared__ int s_slot[kTaMaxCtas + 1];
-    __shared__ int s_n, s_bad;
+    const int c0 = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+    constexpr int kPerRow = D / 8;
+    const int col = tid % kPerRow * 8, row = blockIdx.y * (kCombineThreads / kPerRow) + tid / kPerRow;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c0 = blockIdx.x, tid = threadIdx.x;
     const int4 rec = p.records[c0];
+    int flags = c0 + 1 + lane < ctas ? p.records[c0 + 1 + lane].x : 0; // of the 32 CTAs after it
     if (!(rec.x & kTail))
         return;
-    if (tid < 32) {
-        int n = 1;
-        int bad = rec.x & kTailBad;
-        if (tid == 0)
-            s_slot[0] = 2 * c0 + 1;
-        for (int base = c0 + 1; base < ctas; base += 32) {
-            const int flags = base + tid < ctas ? p.records[base + tid].x : 0;
-            const uint32_t ends = __ballot_sync(0xffffffffu, flags & kHeadEnd);
-            const int stop = ends != 0 ? __ffs(ends) - 1 : 31;
-            const bool mine = tid <= stop && (flags & kHeadValid);
-            const uint32_t valid = __ballot_sync(0xffffffffu, mine);
-            bad |= __any_sync(0xffffffffu, mine && (flags & kHeadBad));
-            if (mine)
-                s_slot[n + __popc(valid & ((1u << tid) - 1u))] = 2 * (base + tid);
-            n += __popc(valid);
-            if (ends != 0)
-                break;
-        }
-        if (tid == 0) {
-            s_n = n;
-            s_bad = bad;
-        }
-    }
-    __syncthreads();
-    const int n = s_n;
-    constexpr int kPerRow = D / 8;
-    const int col = tid % kPerRow * 8;
-    for (int row = blockIdx.y * (kCombineThreads / kPerRow) + tid / kPerRow; row < rec.w;
-         row += kCombineParts * (kCombineThreads / kPerRow)) {
-        float m = -INFINITY;
-        for (int i = 0; i < n; ++i)
-            m = fmaxf(m, p.part_ml[(int64_t)s_slot[i] * p.slot_rows + row].x);
-        float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const int64_t at = (int64_t)s_slot[i] * p.slot_rows + row;
-            const float2 ml = p.part_ml[at];
-            const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-            const float4 a = *reinterpret_cast<const float4 *>(p.part_o + at * D + col);
-            const float4 b = *reinterpret_cast<const float4 *>(p.part_o + at * D + col + 4);
-            if (ml.x == -INFINITY) // nothing seen there: its O is all zeros (or no sum at all)
-                continue;
-            l += w * ml.y;
-            o[0] += w * a.x, o[1] += w * a.y, o[2] += w * a.z, o[3] += w * a.w;
-            o[4] += w * b.x, o[5] += w * b.y, o[6] += w * b.z, o[7] += w * b.w;
-        }
-        const bool zero = s_bad != 0 || l == 0.f;
-        const float inv = 1.f / l;
-        uint32_t w[4];
+    const int64_t at_row = min(row, rec.w - 1); // (whole warps go on: they vote)
+    float m = -INFINITY, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    int bad = rec.x & kTailBad;
+    constexpr int kAtOnce = 4;
+    int slot[kAtOnce] = {2 * c0 + 1, -1, -1, -1}, n = 1; // slices found and not yet added
+#pragma unroll 1
+    for (int c = c0 + 1;; c += 32) {
+        const uint32_t ends = __ballot_sync(0xffffffffu, flags & kHeadEnd);
+        const int stop = ends != 0 ? __ffs(ends) - 1 : 31;
+        const bool mine = lane <= stop && (flags & kHeadValid);
+        bad |= __any_sync(0xffffffffu, mine && (flags & kHeadBad));
+        uint32_t valid = __ballot_sync(0xffffffffu, mine);
+        const bool over = ends != 0 || c + 32 >= ctas;
+        if (!over)
+            flags = c + 32 + lane < ctas ? p.records[c + 32 + lane].x : 0;
+#pragma unroll 1
+        while (valid != 0 || (over && n > 0)) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
-            w[e] = zero ? 0u : *reinterpret_cast<const uint32_t *>(&h);
+            for (int i = 0; i < kAtOnce; ++i)
+                if (i >= n && valid != 0) {
+                    slot[i] = 2 * (c + __ffs(valid) - 1);
+                    valid &= valid - 1;
+                    n = i + 1;
+                }
+            if (n < kAtOnce && !over)
+                break;
+            float2 ml[kAtOnce];
+            float4 y[kAtOnce][2];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int64_t at = (int64_t)(i < n ? slot[i] : slot[0]) * p.slot_rows + at_row;
+                ml[i] = p.part_ml[at];
+                y[i][0] = *reinterpret_cast<const float4 *>(p.part_o + at * D + col);
+                y[i][1] = *reinterpret_cast<const float4 *>(p.part_o + at * D + col + 4);
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                if (i >= n || ml[i].x == -INFINITY) // (nothing is seen there)
+                    continue;
+                const float top = fmaxf(m, ml[i].x);
+                const float w0 = m == -INFINITY ? 0.f : ex2_approx(m - top), w1 = ex2_approx(ml[i].x - top);
+                m = top;
+                l = l * w0 + ml[i].y * w1;
+                const float x[8] = {y[i][0].x, y[i][0].y, y[i][0].z, y[i][0].w,
+                                    y[i][1].x, y[i][1].y, y[i][1].z, y[i][1].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    o[e] = o[e] * w0 + x[e] * w1;
+            }
+            n = 0;
         }
-        const int64_t out_row = ((int64_t)rec.y + row / p.group) * p.num_q_heads + rec.z * p.group + row % p.group;
-        *reinterpret_cast<uint4 *>(p.out + out_row * D + col) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (col == 0 && p.lse != nullptr)
-            p.lse[out_row] = zero ? -INFINITY : (m + kRescaleLog2 + log2f(l)) * kLn2;
+        if (over)
+            break;
     }
+    if (row >= rec.w)
+        return;
+    const bool zero = bad != 0 || l == 0.f;
+    const float inv = 1.f / l;
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
+        w[e] = zero ? 0u : *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const int64_t out_row = ((int64_t)rec.y + row / p.group) * p.num_q_heads + rec.z * p.group + row % p.group;
+    *reinterpret_cast<uint4 *>(p.out + out_row * D + col) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (col == 0 && p.lse != nullptr)
+        p.lse[out_row] = zero ? -INFINITY : (m + kRescaleLog2 + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- host side
@@ -1396,7 +1414,8 @@ cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t stream)
     if (err != cudaSuccess)
         return err;
     int ctas = grid;
-    cfg.gridDim = dim3(grid, kCombineParts);
+    const int rows_a_block = kCombineThreads / (a.desc.head_dim / 8);
+    cfg.gridDim = dim3(grid, (a.shape.slot_rows + rows_a_block - 1) / rows_a_block);
     cfg.blockDim = dim3(kCombineThreads);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
