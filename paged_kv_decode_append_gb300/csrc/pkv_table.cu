@@ -14,7 +14,7 @@
 // never meet and every block and token can be done by any thread.
 //
 // How.  The prefix sums are over at most 1024 rows: every CTA does them again
-// in shared memory (one row per thread, one warp-shuffle scan each) instead of
+// in shared memory (one row per thread, one scan for all three) instead of
 // waiting for another, then the CTAs share out the warps' pieces of blocks and
 // tokens.  The CTA that finishes last (a ticket in the pool's header; it never
 // waits) writes what the others still read: held_blocks and the header.
@@ -27,8 +27,8 @@ namespace {
 constexpr int kPoolHeader = 16; // int32 words before the ring
 constexpr int kTableThreads = 1024;
 constexpr int kTableMaxBatch = kTableThreads; // one row per thread
-constexpr int kTablePiece = 128;              // tokens a warp lays out at a time
-constexpr int kTableTokensPerCta = 4096;
+constexpr int kTablePiece = 64;               // tokens a warp lays out at a time
+constexpr int kTableTokensPerCta = 1024;
 
 struct TableParams {
     int32_t *pool;
@@ -44,29 +44,39 @@ struct TableParams {
     int page_shift, max_blocks, batch, max_tokens;
 };
 
-// Inclusive prefix sum over the block's threads; *total gets the sum.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_t *total)
+// Inclusive prefix sums over the block's threads of K values at once; total
+// gets the sums.
+template <int K> __device__ __forceinline__ void block_scan(int64_t (&v)[K], int64_t (*s_warp)[32], int64_t (&total)[K])
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (int)blockDim.x >> 5;
-    int64_t x = v;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o)
-            x += y;
-    }
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, v[k], o);
+            if (lane >= o)
+                v[k] += y;
+        }
     if (lane == 31)
-        s_warp[warp] = x;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            s_warp[k][warp] = v[k];
     __syncthreads();
-    int64_t before = 0, sum = 0;
-    for (int w = 0; w < warps; ++w) {
-        const int64_t t = s_warp[w];
-        before += w < warp ? t : 0;
-        sum += t;
+    // every warp adds the warps' sums up again, one per lane
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        int64_t x = lane < warps ? s_warp[k][lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o)
+                x += y;
+        }
+        total[k] = __shfl_sync(0xffffffffu, x, 31);
+        const int64_t before = __shfl_sync(0xffffffffu, x, warp > 0 ? warp - 1 : 0);
+        v[k] += warp > 0 ? before : 0;
     }
     __syncthreads();
-    *total = sum;
-    return before + x;
 }
 
 // The last row r in [lo, n) with first[r] <= t (first is non-decreasing).
@@ -85,7 +95,7 @@ __device__ __forceinline__ int row_of(const int *first, int lo, int n, int t)
 
 __global__ void __launch_bounds__(kTableThreads) table_update_kernel(const TableParams p)
 {
-    __shared__ int64_t s_warp[32];
+    __shared__ int64_t s_warp[3][32];
     __shared__ int s_take[kTableMaxBatch + 1], s_give[kTableMaxBatch + 1], s_tok[kTableMaxBatch + 1];
     __shared__ int s_len[kTableMaxBatch], s_held[kTableMaxBatch], s_want[kTableMaxBatch];
     __shared__ int s_last;
@@ -113,47 +123,52 @@ __global__ void __launch_bounds__(kTableThreads) table_update_kernel(const Table
         if (!ok)
             n = 0;
     }
-    int64_t total = 0;
+    // 2. one prefix sum over the rows for tokens, pages taken and pages returned;
+    // where the list or the pool is too short, again without the rows that fail
     const bool lists_tokens = p.slot_map != nullptr || p.positions != nullptr;
-    if (lists_tokens) {
-        const int64_t end = block_scan(n, s_warp, &total);
-        if (n > 0 && end > p.max_tokens) {
+    int64_t take = 0, give = 0, sum[3], total[3];
+    auto pages = [&] {
+        take = ok && want > held ? want - held : 0;
+        give = ok && held > want ? held - want : 0;
+    };
+    auto scan = [&] {
+        sum[0] = n;
+        sum[1] = take;
+        sum[2] = give;
+        block_scan<3>(sum, s_warp, total);
+    };
+    pages();
+    scan();
+    if (lists_tokens && total[0] > p.max_tokens) {
+        if (n > 0 && sum[0] > p.max_tokens) {
             err |= PKV_ERR_QLEN;
             ok = false;
+            n = 0;
         }
+        pages();
+        scan();
     }
-    // 2. pages: the rows are served in order as long as the free ones last
-    int64_t take = ok && want > held ? want - held : 0;
-    const int64_t give = ok && held > want ? held - want : 0;
-    const int64_t took = block_scan(take, s_warp, &total);
-    if (take > 0 && took > count) {
-        err |= PKV_ERR_POOL;
-        ok = false;
+    const bool pool_ok = head >= 0 && head < p.cap && count >= 0 && count <= p.cap && total[2] <= p.cap - count;
+    if (!pool_ok || total[1] > count) { // the rows are served in order as long as the free pages last
+        if (!pool_ok)
+            err |= tid == 0 ? PKV_ERR_POOL : 0;
+        else if (take > 0 && sum[1] > count)
+            err |= PKV_ERR_POOL;
+        if (!pool_ok || (take > 0 && sum[1] > count)) {
+            ok = false;
+            n = 0;
+        }
+        pages();
+        scan();
     }
-    int64_t given_total = 0;
-    const int64_t given = block_scan(give, s_warp, &given_total);
-    const bool pool_ok = head >= 0 && head < p.cap && count >= 0 && count <= p.cap && given_total <= p.cap - count;
-    if (!pool_ok) {
-        ok = false;
-        err |= tid == 0 ? PKV_ERR_POOL : 0;
-    }
-    if (!ok) {
-        n = 0;
-        take = 0;
-    }
-    int64_t tok_total = 0, take_total = 0;
-    const int64_t tok_end = block_scan(n, s_warp, &tok_total);
-    // (rows that failed for want of pages come behind every row that got some)
-    block_scan(take, s_warp, &take_total);
-    if (!pool_ok)
-        given_total = 0;
+    const int64_t take_total = total[1], given_total = total[2];
     if (tid < p.batch) {
         s_len[tid] = len;
         s_held[tid] = held;
         s_want[tid] = ok ? (int)want : held;
-        s_take[tid] = (int)min(took - take, take_total); // take = 0 behind the rows that were served
-        s_give[tid] = (int)(given - give);
-        s_tok[tid] = (int)min(tok_end - n, (int64_t)INT32_MAX);
+        s_take[tid] = (int)(sum[1] - take);
+        s_give[tid] = (int)(sum[2] - give);
+        s_tok[tid] = (int)min(sum[0] - n, (int64_t)INT32_MAX);
         if (blockIdx.x == 0) {
             if (p.indptr != nullptr)
                 p.indptr[tid] = s_tok[tid];
@@ -163,7 +178,7 @@ __global__ void __launch_bounds__(kTableThreads) table_update_kernel(const Table
     if (tid == 0) {
         s_take[p.batch] = (int)take_total;
         s_give[p.batch] = (int)given_total;
-        s_tok[p.batch] = (int)min(tok_total, (int64_t)INT32_MAX);
+        s_tok[p.batch] = (int)min(total[0], (int64_t)INT32_MAX);
         if (blockIdx.x == 0 && p.indptr != nullptr)
             p.indptr[p.batch] = s_tok[p.batch];
     }
