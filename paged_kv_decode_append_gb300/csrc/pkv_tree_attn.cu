@@ -614,9 +614,17 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
     const uint64_t kd0 = tc_sw128_desc(smem_addr(smem + C::kOffK), 16, C::kGroupStride);
     const uint64_t vd0 = tc_sw128_desc(smem_addr(smem + C::kOffV), 1024, C::kGroupStride);
     const uint64_t qd0 = tc_sw128_desc(smem_addr(smem + C::kOffQ), 16, 1024);
-    TaTiles<D> t;
-    t.start();
-    bool issued = false, more = t.next(p, bars, lane);
+    // The walk over tiles in warp-uniform registers (a value that one lane read is
+    // uniform to the compiler): TMEM addresses and descriptors then need no move
+    // into uniform registers at every MMA.
+    int n = 0, tok = 0, tok0 = 0, tok1 = 0, gt = 0;
+    auto open = [&] { // slice n
+        const TaSlice s = ta_slice(p, bars, n);
+        tok = tok0 = __shfl_sync(0xffffffffu, s.tok0, 0);
+        tok1 = __shfl_sync(0xffffffffu, s.tok1, 0);
+        return !__shfl_sync(0xffffffffu, s.flags & kOver, 0);
+    };
+    bool issued = false, more = open();
     int prev = -1; // tile whose P V is due
     int prev_tokens = 0, prev_unit = 0;
     bool prev_first = false, prev_last = false;
@@ -625,12 +633,12 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
 #pragma unroll 1
     while (more || prev >= 0) {
         if (more) { // S of the next tile
-            if ((t.first() && !ta_wait_all(&bars.q_full, (uint32_t)t.n & 1, bars, p.err_flag)) ||
+            if (((tok == tok0) && !ta_wait_all(&bars.q_full, (uint32_t)n & 1, bars, p.err_flag)) ||
                 !ta_wait_all(&bars.k_full[k_slot], k_par, bars, p.err_flag))
                 break;
             tc_fence_after();
             issued = true;
-            const uint32_t d = tmem + C::kColS + (uint32_t)(t.gt & 1) * C::kTile;
+            const uint32_t d = tmem + C::kColS + (uint32_t)(gt & 1) * C::kTile;
             const uint64_t kd = kd0 + (uint64_t)(k_slot * C::kItemBytes >> 4);
 #pragma unroll 1
             for (int blk = 0; blk < D / 64; ++blk)
@@ -638,7 +646,7 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
                 for (int kk = 0; kk < 4; ++kk)
                     ta_mma_ss(d, qd0 + (uint64_t)((blk * C::kQBlock + kk * 32) >> 4),
                               kd + (uint64_t)((blk * 1024 + kk * 32) >> 4), kIdescS, blk + kk > 0 ? 1u : 0u);
-            ta_commit(&bars.s_full[t.gt & 1]);
+            ta_commit(&bars.s_full[gt & 1]);
             ta_commit(&bars.k_empty[k_slot]);
             if (++k_slot == C::kKStages) {
                 k_slot = 0;
@@ -680,12 +688,17 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
         }
         prev = -1;
         if (more) {
-            prev = t.gt;
-            prev_tokens = t.tokens();
-            prev_first = t.first();
-            prev_last = t.tok + C::kTile >= t.s.tok1;
-            prev_unit = t.n;
-            more = t.next(p, bars, lane);
+            prev = gt;
+            prev_tokens = min(C::kTile, tok1 - tok);
+            prev_first = (tok == tok0);
+            prev_last = tok + C::kTile >= tok1;
+            prev_unit = n;
+            ++gt;
+            tok += C::kTile;
+            if (tok >= tok1) {
+                ta_slice_done(bars, n++, lane);
+                more = open();
+            }
         }
     }
     if (issued) {
@@ -1042,6 +1055,13 @@ __device__ __forceinline__ int64_t ta_positions(const TaParams &p, const TaRow &
     return (int64_t)r.tiles * p.num_kv_heads * (kStartCost + r.blocks);
 }
 
+// a / b for a >= 0, b > 0: 64-bit division only where it is needed (it is long,
+// and this is the start of every CTA).
+__device__ __forceinline__ int64_t ta_div(int64_t a, int64_t b)
+{
+    return a >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // This CTA's range, an equal part of all rows' positions: prefix sum over the
 // rows (a few consecutive ones per thread), and the thread whose rows the range
 // starts in says where.  `scratch`: kTaThreads / 32 sums, then a TaStart.
@@ -1086,12 +1106,13 @@ __device__ TaStart ta_start(const TaParams &p, int64_t *scratch)
         total += v;
     }
     x -= sum;
-    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kMinRange));
+    const int64_t ctas = total >= (int64_t)gridDim.x * kMinRange ? gridDim.x : max(1, (int)total / kMinRange);
     const int c = blockIdx.x;
     if (c < ctas) {
         // as the quotient and remainder of total / ctas, with small numbers
-        const int64_t q = total / ctas, rest = total - q * ctas;
-        const int64_t lo = q * c + rest * c / ctas, hi = q * (c + 1) + rest * (c + 1) / ctas;
+        const int64_t q = ta_div(total, ctas);
+        const int rest = (int)(total - q * ctas); // (below 160: products with c stay small)
+        const int64_t lo = q * c + rest * c / (int)ctas, hi = q * (c + 1) + rest * (c + 1) / (int)ctas;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int64_t positions = ta_positions(p, row[i]), in_row = lo - x;
@@ -1099,7 +1120,7 @@ __device__ TaStart ta_start(const TaParams &p, int64_t *scratch)
                 const int size = kStartCost + row[i].blocks;
                 TaStart at;
                 at.b = tid * kPer + i;
-                at.unit = (int)(in_row / size);
+                at.unit = (int)ta_div(in_row, size);
                 at.off = in_row - (int64_t)at.unit * size;
                 at.left = hi - lo;
                 at.row = row[i];
@@ -1124,7 +1145,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         return;
     }
     TaBars &bars = *reinterpret_cast<TaBars *>(smem + C::kOffBar);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); // the combine kernel waits for this grid
     if (threadIdx.x == 0) {
@@ -1171,7 +1192,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     __syncthreads();
     tc_fence_after();
     fence_proxy_async_smem(); // the scratch's reads and writes before the copies over it
-    const uint32_t tmem = bars.tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem_base, 0);
     if (threadIdx.x == kTaEndWarp * 32) // the thread that writes it at the end
         p.records[blockIdx.x] = make_int4(0, 0, 0, 0);
 
