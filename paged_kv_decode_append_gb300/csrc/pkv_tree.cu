@@ -188,10 +188,12 @@ struct CommitParams {
 // One CTA per (row, layer).  The path rises (path[i] >= i), so a token's
 // destination is never the source of a later one; each thread owns 16-byte
 // pieces of a token's K or V, loads up to kCommitAhead tokens' pieces and then
-// stores them, in path order.
+// stores them, in path order.  The tokens that lie right already are the first
+// ones (path[i] = i from some i on never again), and are skipped.
 __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const __grid_constant__ CommitParams p)
 {
     __shared__ int64_t s_src[kTreeNodes], s_dst[kTreeNodes]; // elements, head 0
+    __shared__ int s_stay; // first tokens that lie right
     const int b = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x;
     const int L = p.seqlens[b], n = p.path_len[b];
     if (L < 0 || n == 0)
@@ -199,6 +201,9 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const __gri
     int err = 0;
     if (n < 0 || n > p.max_path)
         err = PKV_ERR_TREE;
+    if (tid == 0)
+        s_stay = 0;
+    __syncthreads();
     const int P = 1 << p.page_shift;
     const int32_t *path = p.path + (int64_t)b * p.max_path;
     const int32_t *row = p.table + (int64_t)b * p.max_blocks;
@@ -223,6 +228,8 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const __gri
                 err = PKV_ERR_PAGE;
                 continue;
             }
+            if (node == i)
+                atomicMax(&s_stay, i + 1);
             s_src[i] = element(page_from, (int)(from & (P - 1)));
             s_dst[i] = element(page_to, (int)(to & (P - 1)));
         }
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const __gri
         __nv_bfloat16 *pool = static_cast<__nv_bfloat16 *>(c < pieces ? p.k[layer] : p.v[layer]);
         const int x = c < pieces ? c : c - pieces;
         pool += x / per_head * head_step + x % per_head * 8;
-        for (int i0 = 0; i0 < n; i0 += kCommitAhead) {
+        for (int i0 = s_stay; i0 < n; i0 += kCommitAhead) {
             uint4 piece[kCommitAhead];
 #pragma unroll
             for (int k = 0; k < kCommitAhead; ++k)
