@@ -40,18 +40,22 @@ struct BuildParams {
     const int32_t *parents, *indptr, *seqlens;
     int32_t *mask, *positions, *err_flag;
     int total_q, max_nodes, words;
+    bool whole; // mask rows in 16-byte pieces
 };
 
 // One CTA per row, one thread per node.  mask_i = bit i | mask_parent(i), by
 // pointer doubling: each round ors in the mask of the node one hop up and
-// doubles the hop, so a tree of depth d takes ceil(log2 d) rounds.
+// doubles the hop, so a tree of depth d takes ceil(log2 d) rounds.  A node's
+// ancestors come before it, so warps 0 .. 3 have nothing in words 4 .. 7; a node
+// that has reached its root no longer reads or writes.  A row of s_mask is 12
+// words: any 8 consecutive rows' 16-byte pieces lie in different banks.
 __global__ void __launch_bounds__(kTreeNodes) tree_build_kernel(const BuildParams p)
 {
-    __shared__ uint32_t s_mask[kTreeNodes][kTreeWords + 1]; // padded against bank conflicts
+    __shared__ uint4 s_mask[kTreeNodes][3]; // (two are used)
     __shared__ int s_up[kTreeNodes];
     const TreeRow r = tree_row(p.indptr, p.seqlens, blockIdx.x, p.total_q, p.max_nodes);
     const int i = threadIdx.x;
-    const bool mine = r.ok && i < r.nodes;
+    const bool mine = r.ok && i < r.nodes, high = i >= 128;
     int up = -1;
     if (mine)
         up = p.parents[r.first + i];
@@ -59,48 +63,57 @@ __global__ void __launch_bounds__(kTreeNodes) tree_build_kernel(const BuildParam
     if (i == 0)
         set_error(p.err_flag, r.err | (bad ? PKV_ERR_TREE : 0));
     const bool ok = r.ok && !bad;
-    uint32_t m[kTreeWords];
-#pragma unroll
-    for (int w = 0; w < kTreeWords; ++w)
-        m[w] = mine && ok && (i >> 5) == w ? 1u << (i & 31) : 0u;
-    if (ok) {
-        for (;;) {
-            if (i < r.nodes) {
-#pragma unroll
-                for (int w = 0; w < kTreeWords; ++w)
-                    if (w < p.words)
-                        s_mask[i][w] = m[w];
-                s_up[i] = up;
+    if (!ok) {
+        const int64_t words = (int64_t)r.nodes * p.words;
+        for (int64_t k = i; k < words; k += blockDim.x)
+            p.mask[(int64_t)r.first * p.words + k] = 0;
+        if (p.positions != nullptr)
+            for (int64_t k = i; k < r.nodes; k += blockDim.x)
+                p.positions[r.first + k] = -1;
+        return;
+    }
+    const uint32_t bit = 1u << (i & 31);
+    auto own = [&](int w) { return (i >> 5) == w ? bit : 0u; };
+    uint4 lo = make_uint4(own(0), own(1), own(2), own(3)), hi = make_uint4(own(4), own(5), own(6), own(7));
+    s_mask[i][0] = lo;
+    s_mask[i][1] = hi;
+    s_up[i] = up;
+    while (__syncthreads_or(up >= 0)) {
+        const bool more = up >= 0;
+        if (more) {
+            const uint4 x = s_mask[up][0];
+            lo = make_uint4(lo.x | x.x, lo.y | x.y, lo.z | x.z, lo.w | x.w);
+            if (high) {
+                const uint4 y = s_mask[up][1];
+                hi = make_uint4(hi.x | y.x, hi.y | y.y, hi.z | y.z, hi.w | y.w);
             }
-            if (!__syncthreads_or(mine && up >= 0))
-                break;
-            if (mine && up >= 0) {
-#pragma unroll
-                for (int w = 0; w < kTreeWords; ++w)
-                    if (w < p.words)
-                        m[w] |= s_mask[up][w];
-                up = s_up[up];
-            }
-            __syncthreads();
+            up = s_up[up];
+        }
+        __syncthreads();
+        if (more) {
+            s_mask[i][0] = lo;
+            if (high)
+                s_mask[i][1] = hi;
+            s_up[i] = up;
         }
     }
-    if (p.positions != nullptr && i < r.nodes) {
-        int depth = -1;
-#pragma unroll
-        for (int w = 0; w < kTreeWords; ++w)
-            depth += __popc(m[w]);
-        p.positions[r.first + i] = ok ? r.len + depth : -1;
-    }
-    // rows of masks, consecutive threads on consecutive words
-    const int total = r.nodes * p.words;
-    for (int k = i; k < total; k += blockDim.x) {
-        const int node = k / p.words;
-        p.mask[(int64_t)r.first * p.words + k] = ok ? (int32_t)s_mask[node][k - node * p.words] : 0;
-    }
-    // a row of more than max_nodes: its nodes past the CTA's threads
+    if (i >= r.nodes)
+        return;
     if (p.positions != nullptr)
-        for (int k = i + blockDim.x; k < r.nodes; k += blockDim.x)
-            p.positions[r.first + k] = -1;
+        p.positions[r.first + i] = r.len - 1 + __popc(lo.x) + __popc(lo.y) + __popc(lo.z) + __popc(lo.w) +
+                                   __popc(hi.x) + __popc(hi.y) + __popc(hi.z) + __popc(hi.w);
+    int32_t *out = p.mask + ((int64_t)r.first + i) * p.words;
+    if (p.whole) { // rows of 4 or 8 aligned words
+        *reinterpret_cast<uint4 *>(out) = lo;
+        if (p.words == 8)
+            *reinterpret_cast<uint4 *>(out + 4) = hi;
+        return;
+    }
+    const uint32_t m[kTreeWords] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int w = 0; w < kTreeWords; ++w)
+        if (w < p.words)
+            out[w] = (int32_t)m[w];
 }
 
 // ---------------------------------------------------------------- acceptance
@@ -293,6 +306,7 @@ pkv_status pkv_tree_build(const int32_t *parents, const int32_t *qo_indptr, cons
     p.total_q = total_q;
     p.max_nodes = max_nodes;
     p.words = mask_words;
+    p.whole = mask_words % 4 == 0 && (reinterpret_cast<uintptr_t>(tree_mask) & 15u) == 0;
     const int threads = (max_nodes + 31) / 32 * 32;
     tree_build_kernel<<<batch, threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ECUDA;

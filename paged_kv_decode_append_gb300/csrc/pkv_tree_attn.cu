@@ -7,11 +7,19 @@
 //
 // What bounds it.  A unit is (row, kv head, up to 128 (node, head) pairs): one
 // MMA row tile, so a K/V byte is read once for all of them.  Per 128 keys at
-// head_dim 128 a unit reads 64 KB, 1.45 us of an SM's share of the measured
-// HBM rate, and needs 24 MMAs of 128 x 128 x 16 (8 for S, 16 for P V, whose P
-// is kept as two bf16 parts), about 0.8 us: memory bounds it up to 128 pairs
-// whatever their number, the tensor pipe beyond (the next unit finds the same
-// K/V in L2).
+// head_dim 128 a unit reads 64 KB, 1.45 us of an SM's share of the measured HBM
+// rate, and needs 24 MMAs of 128 x 128 x 16 (8 for S, 16 for P V, whose P is
+// kept as two bf16 parts), 0.8 us at the tensor peak.  Measured (stamps of the
+// SM clock): a step takes 1.56 us, the MMA warp busy throughout -- S 0.25, P V
+// 0.74 (46 ns an MMA against 33 at the peak, its A operand coming from TMEM
+// beside the softmax's loads), commits 0.13, the rest waits between them.  So
+// the issue of MMAs bounds long rows, and memory is near: 64 uneven rows of 64
+// nodes with 4 heads a kv head (two row tiles, the second finds K/V in L2)
+// take 168.7 us = 541 TFLOP/s, 2.9 TB/s of algorithmic bytes, and the counters
+// show the tensor pipe active 43 % of the cycles, issue slots 39 %.  Short calls
+// are bound by latency: 16 trees over 4-6 thousand tokens take 37 us, of which
+// the start of the CTAs is 3, the append 3, the tail and the combine kernel 6;
+// one node over 15 tokens takes 11.5 us for its three kernels.
 //
 // The roles' code is kept short (one walk of the range, loops not unrolled
 // beyond 32 columns): at 120 KB a sixth of the instruction fetches missed the
@@ -39,11 +47,15 @@
 //    large value cannot overflow before the division.
 //  - P replaces S in TMEM as bf16 hi + lo parts (16 significant bits; 8 alone
 //    leave errors of 2^-9 of the row's scale in small outputs).
-//  - Tiles with drafted keys take their visibility as four 32-bit words per
-//    row, shifted out of the node's mask.  V of drafted tokens is looked
-//    through in shared memory before the MMAs read it: an infinity or NaN there is replaced by 0 for
-//    the MMA (0 * inf would reach nodes that do not see it) and added in the
-//    epilogue to the nodes that do.
+//  - Tiles with drafted keys take their visibility as 32-bit words, shifted
+//    out of the node's mask.  V of drafted tokens is looked through in shared
+//    memory before the MMAs read it: an infinity or NaN there is replaced by 0
+//    for the MMA (0 * inf would reach nodes that do not see it) and added in
+//    the epilogue to the nodes that do.
+//  - Cutting the line: kStartCost 1 .. 4 and kMinRange 4 .. 16 were measured on
+//    short, long, even and uneven batches; 2 and 6 are within 1 % of the best
+//    everywhere (kMinRange 12: 16 trees 5 % slower; a minimum that grows with
+//    the rows in use: head_dim 256 43 -> 55 us).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -137,7 +149,7 @@ struct TaParams {
     uint32_t q_box_bytes;
     float q_scale;
     int pdl;
-    uint32_t k65536;
+    uint32_t k65536;   // 65536: a shift by 16 as a multiplication, in the FMA pipe beside the busy ALU
     bool wide;         // out is 32-byte aligned
 };
 
@@ -904,7 +916,8 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                         const uint32_t hw = *reinterpret_cast<const uint32_t *>(&h);
                         uint32_t h0;
                         asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(h0) : "r"(hw), "r"(p.k65536), "r"(0));
-                        const float2 d = ffma2(make_float2(__uint_as_float(h0), __uint_as_float(hw & 0xffff0000u)), make_float2(-1.f, -1.f), w);
+                        const float2 d = ffma2(make_float2(__uint_as_float(h0), __uint_as_float(hw & 0xffff0000u)),
+                                               make_float2(-1.f, -1.f), w); // exact
                         const __nv_bfloat162 lw = __floats2bfloat162_rn(d.x, d.y);
                         hi[e] = *reinterpret_cast<const uint32_t *>(&h);
                         lo[e] = *reinterpret_cast<const uint32_t *>(&lw);
@@ -994,9 +1007,12 @@ __device__ void ta_finish(const TaParams &p, TaBars &bars, uint32_t tmem, int wa
         const int64_t part = (int64_t)(2 * blockIdx.x + (begins ? 1 : 0)) * p.slot_rows + r;
         const bool zero = bad || l == 0.f;
         const float inv = 1.f / l;
-        if (nonfinite && warp_live)
+        if (nonfinite && warp_live) {
+            if (p.pdl) // V is read from the cache again, where this call's append puts it
+                asm volatile("griddepcontrol.wait;" ::: "memory");
             ta_add_nonfinite<D>(p, s.b, s.len, s.g, p.mask + token * p.words, max(0, s.tok0 - s.len),
                                 min(s.nodes, s.tok1 - s.len), live, o_col, 0, D);
+        }
 #pragma unroll 1
         for (int c = 0; warp_live && c < D; c += 32) {
             uint32_t o[32];
@@ -1226,7 +1242,9 @@ constexpr int kCombineThreads = 256;
 // sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, over the CTAs after it up to
 // the one that ended it, in that order.  D / 8 threads per MMA row; gridDim.y
 // blocks take one row per thread, so that all of a thread's loads are under way
-// at once: what bounds this kernel is the chain record, (m, l) and O.
+// at once: what bounds this kernel is the chain record, (m, l) and O (4.5 us
+// from its start to its end with 16 trees of 64 nodes, where 70 KB a unit are
+// joined from about 5 slices; 7 when a block took 16 rows).
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __grid_constant__ TaParams p, int ctas)
 {

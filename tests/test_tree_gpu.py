@@ -435,6 +435,23 @@ def test_build_matches_the_walk(max_nodes, words):
     assert int(err.item()) == 0
 
 
+@pytest.mark.parametrize("max_nodes,words", [(70, 3), (64, 4), (130, 5), (3, 6), (200, 7), (256, 8), (129, 8)])
+def test_build_writes_mask_rows_of_any_width_and_alignment(max_nodes, words):
+    rng = np.random.default_rng(words)
+    counts = rng.integers(0, max_nodes + 1, 9)
+    counts[0] = max_nodes
+    parents = ref.random_parents(rng, counts)
+    indptr = np.concatenate([[0], np.cumsum(counts)])
+    T = int(indptr[-1])
+    want = ref.pack([ref.ancestor_bits(p) for p in parents], words)
+    for at in (0, 1, 2, 4):
+        room = torch.full((T * words + 8,), 7, dtype=torch.int32, device=DEV)
+        mask = room[at:at + T * words].view(T, words)
+        pkv.pkv_tree_build(i32(np.concatenate(parents)), i32(indptr), i32(np.zeros(9)), max_nodes, mask=mask)
+        assert np.array_equal(mask.cpu().numpy(), want)
+        assert (room[:at] == 7).all() and (room[at + T * words:] == 7).all()
+
+
 def test_build_and_accept_refuse_what_is_no_tree():
     parents = [[-1, 0, 1], [-1, 1], [-2], [0], [-1, 0, 2, 0], [-1]]
     indptr = np.concatenate([[0], np.cumsum([len(p) for p in parents])])
