@@ -482,7 +482,8 @@ PKV_API pkv_status pkv_device_pool_init(void *pool, size_t pool_bytes, int32_t n
  *                    Both get -1 behind the last token.
  * Pages are taken in row order, those of a row in block order, and returned
  * in the same order; a page returned by a call is handed out from the next
- * call on.  A row fails when it would exceed max_blocks (PKV_ERR_OVERFLOW),
+ * call on.  A row fails when it would exceed max_blocks or 2^31 - 1 tokens
+ * (PKV_ERR_OVERFLOW),
  * when n_b < 0 or its tokens would end past max_tokens (PKV_ERR_QLEN; with
  * slot_map or positions only), when the pages it and the rows before it need
  * are more than are free (PKV_ERR_POOL) or when held_blocks[b] is outside
@@ -566,8 +567,8 @@ PKV_API size_t pkv_tree_workspace_size(int32_t batch, int32_t total_q, int32_t m
  *                    query heads per kv head; page_size at least 8.
  * K/V of a drafted token reach only the nodes that see it, whatever they hold
  * (infinities and NaN included).  Other row fates as pkv_mixed_attn:
- * inactive; PKV_ERR_OVERFLOW when L_b + n_b exceeds max_blocks * page_size;
- * PKV_ERR_PAGE for a bad page among the first ceil((L_b + n_b) / page_size).
+ * inactive; PKV_ERR_OVERFLOW when L_b + n_b exceeds max_blocks * page_size or
+ * 2^31 - 256; PKV_ERR_PAGE for a bad page among the first ceil((L_b + n_b) / page_size).
  */
 PKV_API pkv_status pkv_tree_attn(const pkv_cache_desc *desc, void *k_cache, void *v_cache, const void *q,
                                  const void *k_new, const void *v_new, const int32_t *qo_indptr,

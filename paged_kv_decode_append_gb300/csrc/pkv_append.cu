@@ -23,6 +23,7 @@ struct AParams {
     const int32_t *seqlens;
     int32_t *err_flag;
     int num_tokens, batch, max_blocks, page_size, page_shift, num_pages, num_kv_heads, head_dim, layout;
+    int64_t max_len; // rows longer than this overflow
     int max_count; // rows appending more tokens than this append nothing
     int pdl_wait;  // launched as a programmatic dependent: wait for the preceding grid before exiting
 };
@@ -62,7 +63,7 @@ __device__ __forceinline__ void append_token(const AParams &p)
     // validate the row's destination range [L, L + count)
     const int32_t *bt_row = p.block_table + (int64_t)b * p.max_blocks;
     int err = 0;
-    if ((int64_t)L + count > (int64_t)p.max_blocks * p.page_size) {
+    if ((int64_t)L + count > p.max_len) {
         err = PKV_ERR_OVERFLOW;
     } else {
         const int blk0 = L >> p.page_shift, blk1 = (L + count - 1) >> p.page_shift;
@@ -135,6 +136,9 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t stream)
     p.head_dim = a.desc.head_dim;
     p.layout = a.desc.layout;
     p.max_count = a.max_count;
+    p.max_len = (int64_t)a.max_blocks * a.desc.page_size;
+    if (p.max_len > a.max_len)
+        p.max_len = a.max_len;
     p.pdl_wait = a.overlap_prior ? 1 : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.num_tokens);

@@ -121,6 +121,7 @@ struct AppendArgs {
     int batch;
     int32_t *err_flag;
     int max_count = 0x7fffffff; // rows appending more tokens than this append nothing
+    int64_t max_len = 0x7fffffff; // rows of more tokens than this overflow, whatever their table holds
     // Launch as a programmatic dependent of the preceding kernel: the two may
     // run side by side, so that kernel must not write what the append reads
     // or writes (k_new, v_new, the cache, indptr, cache_seqlens, block_table);
@@ -221,6 +222,7 @@ bool encode_prefill_maps(const pkv_cache_desc &d, const void *k_cache, const voi
 
 constexpr int kTreeMaxNodes = 256; // drafted tokens of a row
 constexpr int kMaxTreeBatch = 1024;
+constexpr int kTreeMaxKeys = 0x7fffff00; // keys of a row, cached and drafted (token arithmetic is 32-bit)
 
 struct TreeShape {
     int group;     // num_q_heads / num_kv_heads

@@ -48,7 +48,11 @@ struct BuildParams {
 // doubles the hop, so a tree of depth d takes ceil(log2 d) rounds.  A node's
 // ancestors come before it, so warps 0 .. 3 have nothing in words 4 .. 7; a node
 // that has reached its root no longer reads or writes.  A row of s_mask is 12
-// words: any 8 consecutive rows' 16-byte pieces lie in different banks.
+// words: any 8 consecutive rows' 16-byte pieces lie in different banks.  Bound
+// by shared memory (the masks of random parents) and by the chain of loads
+// before it: 1024 rows of 129 .. 256 nodes, 7.9 MB, take 5.3 us (8.0 with the
+// masks word by word and every node in every round; 6.1 with rows of 8 words
+// written word by word, as other widths are), a few rows 2.0: the launch.
 __global__ void __launch_bounds__(kTreeNodes) tree_build_kernel(const BuildParams p)
 {
     __shared__ uint4 s_mask[kTreeNodes][3]; // (two are used)
@@ -97,23 +101,23 @@ __global__ void __launch_bounds__(kTreeNodes) tree_build_kernel(const BuildParam
             s_up[i] = up;
         }
     }
-    if (i >= r.nodes)
-        return;
-    if (p.positions != nullptr)
+    if (p.positions != nullptr && i < r.nodes)
         p.positions[r.first + i] = r.len - 1 + __popc(lo.x) + __popc(lo.y) + __popc(lo.z) + __popc(lo.w) +
                                    __popc(hi.x) + __popc(hi.y) + __popc(hi.z) + __popc(hi.w);
-    int32_t *out = p.mask + ((int64_t)r.first + i) * p.words;
     if (p.whole) { // rows of 4 or 8 aligned words
-        *reinterpret_cast<uint4 *>(out) = lo;
-        if (p.words == 8)
-            *reinterpret_cast<uint4 *>(out + 4) = hi;
+        int32_t *out = p.mask + ((int64_t)r.first + i) * p.words;
+        if (i < r.nodes) {
+            *reinterpret_cast<uint4 *>(out) = lo;
+            if (p.words == 8)
+                *reinterpret_cast<uint4 *>(out + 4) = hi;
+        }
         return;
     }
-    const uint32_t m[kTreeWords] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-    for (int w = 0; w < kTreeWords; ++w)
-        if (w < p.words)
-            out[w] = (int32_t)m[w];
+    // others: a warp's rows lie one after the other, consecutive lanes on consecutive words
+    const int node0 = i & ~31, end = min(32, r.nodes - node0) * p.words;
+    const uint32_t *rows = reinterpret_cast<const uint32_t *>(s_mask[node0]);
+    for (int k = i & 31; k < end; k += 32)
+        p.mask[((int64_t)r.first + node0) * p.words + k] = (int32_t)rows[k / p.words * 12 + k % p.words];
 }
 
 // ---------------------------------------------------------------- acceptance
@@ -128,7 +132,9 @@ constexpr int kAcceptWarps = 4;
 
 // One warp per row; each lane keeps the parents of nodes lane, lane + 32, ...
 // and whether the node's drafted token is what the target chose at its parent.
-// A step down the path is one ballot per 32 nodes.
+// A step down the path is one ballot per 32 nodes.  Bound by the chain of four
+// loads (range, parent, the parent's choice) and the ballots: 1024 rows of up to
+// 129 nodes take 5.0 us, a few rows 2.8.
 __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const AcceptParams p)
 {
     const int b = (int)blockIdx.x * kAcceptWarps + ((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -188,7 +194,7 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Ac
 // ---------------------------------------------------------------- commit
 
 constexpr int kMaxLayers = 128;
-constexpr int kCommitThreads = 128;
+constexpr int kCommitThreads = 256;
 constexpr int kCommitAhead = 8; // tokens in flight per thread
 
 struct CommitParams {
@@ -202,7 +208,10 @@ struct CommitParams {
 // destination is never the source of a later one; each thread owns 16-byte
 // pieces of a token's K or V, loads up to kCommitAhead tokens' pieces and then
 // stores them, in path order.  The tokens that lie right already are the first
-// ones (path[i] = i from some i on never again), and are skipped.
+// ones (path[i] = i from some i on never again), and are skipped.  Bound by
+// memory: 36 layers x 64 rows of 8 heads of 128 (75 MB read and written, with
+// the tokens that stay) take 15.1 us, 4.9 TB/s, a small call 2.5.  Measured: 4
+// tokens ahead 15.7 and 16 16.5 us; 128 threads 15.5, 512 20.2.
 __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const __grid_constant__ CommitParams p)
 {
     __shared__ int64_t s_src[kTreeNodes], s_dst[kTreeNodes]; // elements, head 0

@@ -198,7 +198,7 @@ __device__ __forceinline__ TaRow ta_row(const TaParams &p, const TaRaw &raw)
     const int64_t keys = (int64_t)r.len + n;
     if (n > p.max_nodes)
         r.err = PKV_ERR_QLEN;
-    else if (r.len >= 0 && keys > (int64_t)p.max_blocks << p.page_shift)
+    else if (r.len >= 0 && keys > min((int64_t)p.max_blocks << p.page_shift, (int64_t)kTreeMaxKeys))
         r.err = PKV_ERR_OVERFLOW;
     else if (r.len >= 0 && n > 0)
         r.blocks = (int)((keys + kTaBlock - 1) / kTaBlock);

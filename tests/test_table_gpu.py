@@ -164,6 +164,24 @@ def test_broken_state_is_reported():
     assert slots.tolist() == [-1, -1, 35, 36]
 
 
+def test_rows_past_the_tokens_that_32_bits_count():
+    P, wide = 256, 2 ** 23 + 1
+    pool = pkv.device_pool(10)
+    table = torch.zeros(2, wide, dtype=torch.int32, device=DEV)
+    for L in (2 ** 31 - 3, 2 ** 31 - 1):
+        held, err = i32([2 ** 23 - 1, 0]), torch.zeros(1, dtype=torch.int32, device=DEV)
+        indptr, was = i32([9, 9, 9]), pool[HEAD:].clone()
+        slots, pos = torch.zeros(8, dtype=torch.int64, device=DEV), torch.zeros(8, dtype=torch.int32, device=DEV)
+        pool[:2] = i32([0, 9])
+        table[1] = 0
+        pkv.pkv_table_update(pool, table, held, i32([L, 3]), i32([5, 2]), P, indptr=indptr, slot_map=slots,
+                             positions=pos, err_flag=err)
+        assert int(err.item()) == pkv.api.ERR_OVERFLOW and indptr.tolist() == [0, 0, 2]
+        assert held.tolist() == [2 ** 23 - 1, 1] and not table[0].any() and int(table[1, 0]) == 1
+        assert slots.tolist() == [P + 3, P + 4] + [-1] * 6 and pos.tolist() == [3, 4] + [-1] * 6
+        assert torch.equal(pool[HEAD:], was)
+
+
 def test_captured_updates_advance_the_pool():
     pair = Pair(300, 16, 8, 16, seed=3)
     lens, new = i32(np.zeros(16)), i32(np.zeros(16))

@@ -411,6 +411,30 @@ def test_offsets_past_32_bits():
     assert torch.equal(at(lo), new[1]) and torch.equal(at(lo + 1), new[17])
 
 
+def test_rows_past_the_tokens_that_32_bits_count():
+    """A table of more than 2^31 tokens: the row overflows, its neighbour is served."""
+    P, H, D = 256, 1, 64
+    case = wl.mixed_step(52, [5, 6], [30, 40], 4, H, D, P, wl.NHD, device=DEV)
+    seen = trees(case, 4)
+    table = np.full((2, 2 ** 23 + 1), case.block_table[0, 0], np.int32)
+    table[1, :case.max_blocks] = case.block_table[1]
+    case.block_table = table
+    for L in (2 ** 31 - 260, 2 ** 31 - 3):
+        case.cache_seqlens[0] = L
+        k, v = case.k_cache.clone(), case.v_cache.clone()
+        before = k[int(table[0, 0])].clone()
+        call = (k, v, case.q, case.k_new, case.v_new, i32(case.qo_indptr), i32(ref.pack(seen, 1)), i32(table),
+                i32(case.cache_seqlens), case.softmax_scale, 6)
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        lse = torch.zeros(11, 4, device=DEV)
+        out = pkv.pkv_tree_attn(*call, lse=lse, err_flag=err)
+        assert int(err.item()) == pkv.api.ERR_OVERFLOW
+        assert (out[:5] == 0).all() and torch.isneginf(lse[:5]).all()
+        assert torch.equal(k[int(table[0, 0])].view(torch.int16), before.view(torch.int16))
+        want, _, tol = ref.attention(case, seen, rows=[1])
+        assert (np.abs(out[5:].double().cpu().numpy() - want[5:]) <= tol[5:]).all()
+
+
 # ------------------------------------------------------------------- masks
 
 
