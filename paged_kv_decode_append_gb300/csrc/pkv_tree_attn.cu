@@ -17,9 +17,10 @@
 // nodes with 4 heads a kv head (two row tiles, the second finds K/V in L2)
 // take 168.7 us = 541 TFLOP/s, 2.9 TB/s of algorithmic bytes, and the counters
 // show the tensor pipe active 43 % of the cycles, issue slots 39 %.  Short calls
-// are bound by latency: 16 trees over 4-6 thousand tokens take 37 us, of which
-// the start of the CTAs is 3, the append 3, the tail and the combine kernel 6;
-// one node over 15 tokens takes 11.5 us for its three kernels.
+// are bound by latency: 32 rows of 512 .. 1024 tokens with trees of 16 nodes
+// take 37 us, of which the start of the CTAs is 3, the append 3, the tail and
+// the combine kernel 6; one node over 64 tokens takes 11.5 us for its three
+// kernels.
 //
 // The roles' code is kept short (one walk of the range, loops not unrolled
 // beyond 32 columns): at 120 KB a sixth of the instruction fetches missed the
@@ -116,9 +117,11 @@ struct TaSlice {
 constexpr int kBegins = 1, kEnds = 2, kOver = 4; // it starts / ends the unit; no more slices
 
 struct TaBars {
-    uint64_t k_full[6], k_empty[6], v_full[6], v_ready[6], v_empty[6];
+    uint64_t k_full[6], v_full[6], v_ready[6];
+    uint64_t s_full[6];       // S of the tile in K slot i is complete: K is free, too
+    uint64_t o_done[6];       // P V of the tile in V slot i is complete: V is free, too
     uint64_t q_full;
-    uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+    uint64_t p_full[2], o_free[2];
     uint64_t o_last[2];       // O of a slice (by its parity) is complete
     uint64_t ml_full[2], ml_free[2]; // (m, l) of a slice written / read
     uint64_t pair[4];         // the two softmax warps of each TMEM lane quarter
@@ -242,6 +245,13 @@ __device__ __forceinline__ bool ta_wait(uint64_t *bar, uint32_t parity, TaBars &
     if (mbar_try_wait(bar, parity))
         return true;
     return ta_wait_slow(bar, parity, bars, err_flag);
+}
+// Two phases at once, odd lanes on the second; all lanes of the warp get the same answer.
+__device__ __forceinline__ bool ta_wait_both(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1,
+                                             TaBars &bars, int32_t *err_flag)
+{
+    const bool odd = threadIdx.x & 1;
+    return __all_sync(0xffffffffu, ta_wait(odd ? bar1 : bar0, odd ? parity1 : parity0, bars, err_flag));
 }
 // The same for a whole warp: all lanes get the same answer.
 __device__ __forceinline__ bool ta_wait_all(uint64_t *bar, uint32_t parity, TaBars &bars, int32_t *err_flag)
@@ -417,7 +427,7 @@ __device__ void ta_load(const TaParams &p, const TaMaps &maps, uint8_t *smem, Ta
     constexpr int kStages = IS_K ? C::kKStages : C::kVStages;
     const CUtensorMap *map = IS_K ? &maps.k : &maps.v;
     uint8_t *ring = smem + (IS_K ? C::kOffK : C::kOffV);
-    uint64_t *full = IS_K ? bars.k_full : bars.v_full, *empty = IS_K ? bars.k_empty : bars.v_empty;
+    uint64_t *full = IS_K ? bars.k_full : bars.v_full, *empty = IS_K ? bars.s_full : bars.o_done;
     const int bsh = p.box_shift, boxes = C::kTile >> bsh;
     const uint32_t box_bytes = (uint32_t)(1 << bsh) * D * 2;
     const bool nhd = p.layout == PKV_NHD;
@@ -590,22 +600,54 @@ __device__ void ta_walk(const TaParams &p, uint8_t *smem, TaBars &bars, const Ta
 
 // The MMA warp runs as a whole, so that descriptors stay in uniform registers;
 // one elected thread (always the same) issues.
-__device__ __forceinline__ void ta_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+// Four MMAs of 64 values of the inner dimension: A and B 32 bytes on each time.
+__device__ __forceinline__ void ta_mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile("{\n\t.reg .pred e, p;\n\t"
+    asm volatile("{\n\t.reg .pred e, p, t;\n\t"
+                 ".reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
                  "elect.sync _|e, 0xffffffff;\n\t"
                  "setp.ne.b32 p, %4, 0;\n\t"
-                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "setp.eq.b32 t, 0, 0;\n\t"
+                 "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+                 "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
                  "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
-__device__ __forceinline__ void ta_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+// The MMAs of 16 keys: P's hi parts, then the lo parts 16 columns on.
+__device__ __forceinline__ void ta_mma_pv(uint32_t o, uint32_t a, uint64_t v, uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile("{\n\t.reg .pred e, p;\n\t"
+    asm volatile("{\n\t.reg .pred e, p, t;\n\t"
+                 ".reg .b32 a1;\n\t"
                  "elect.sync _|e, 0xffffffff;\n\t"
                  "setp.ne.b32 p, %4, 0;\n\t"
-                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 "setp.eq.b32 t, 0, 0;\n\t"
+                 "add.u32 a1, %1, 16;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], %2, %3, t;\n\t}" ::"r"(o),
+                 "r"(a), "l"(v), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+// The MMAs of 32 keys; V is 16 keys on after the first two.
+template <uint32_t STEP>
+__device__ __forceinline__ void ta_mma_pv2(uint32_t o, uint32_t a, uint64_t v, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred e, p, t;\n\t"
+                 ".reg .b32 a1, a2, a3;\n\t"
+                 ".reg .b64 v1;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "setp.eq.b32 t, 0, 0;\n\t"
+                 "add.u32 a1, %1, 16;\n\tadd.u32 a2, %1, 8;\n\tadd.u32 a3, %1, 24;\n\t"
+                 "add.s64 v1, %2, %5;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], %2, %3, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], v1, %3, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], v1, %3, t;\n\t}" ::"r"(o),
+                 "r"(a), "l"(v), "r"(idesc), "r"(accumulate), "n"(STEP)
                  : "memory");
 }
 __device__ __forceinline__ void ta_commit(uint64_t *bar)
@@ -654,12 +696,9 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
             const uint64_t kd = kd0 + (uint64_t)(k_slot * C::kItemBytes >> 4);
 #pragma unroll 1
             for (int blk = 0; blk < D / 64; ++blk)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    ta_mma_ss(d, qd0 + (uint64_t)((blk * C::kQBlock + kk * 32) >> 4),
-                              kd + (uint64_t)((blk * 1024 + kk * 32) >> 4), kIdescS, blk + kk > 0 ? 1u : 0u);
-            ta_commit(&bars.s_full[gt & 1]);
-            ta_commit(&bars.k_empty[k_slot]);
+                ta_mma_ss4(d, qd0 + (uint64_t)(blk * C::kQBlock >> 4), kd + (uint64_t)(blk * 1024 >> 4), kIdescS,
+                           blk > 0 ? 1u : 0u);
+            ta_commit(&bars.s_full[k_slot]);
             if (++k_slot == C::kKStages) {
                 k_slot = 0;
                 k_par ^= 1;
@@ -669,28 +708,24 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
             const uint32_t ob = C::kOBufs == 1 ? 0 : prev_unit & 1;
             const uint32_t use = C::kOBufs == 1 ? prev_unit : prev_unit >> 1;
             if ((prev_first && use > 0 && !ta_wait_all(&bars.o_free[ob], (use - 1) & 1, bars, p.err_flag)) ||
-                !ta_wait_all(&bars.v_ready[v_slot], v_par, bars, p.err_flag) ||
-                !ta_wait_all(&bars.p_full[prev & 1], (uint32_t)(prev >> 1) & 1, bars, p.err_flag))
+                !ta_wait_both(&bars.v_ready[v_slot], v_par, &bars.p_full[prev & 1], (uint32_t)(prev >> 1) & 1, bars,
+                              p.err_flag))
                 break;
             tc_fence_after();
             const uint32_t o = tmem + ob * D;
             uint32_t a = tmem + C::kColS + (uint32_t)(prev & 1) * C::kTile;
             uint64_t vd = vd0 + (uint64_t)(v_slot * C::kItemBytes >> 4);
-            // 16 keys a step: P's hi parts, then the lo parts 16 columns on
+            int k = 0;
+            constexpr uint32_t kStep = 2 * C::kGroupStride >> 4; // 16 keys of V
 #pragma unroll 1
-            for (int k = 0; k < prev_tokens; k += 32) {
-                ta_mma_ts(o, a, vd, kIdescO, !prev_first || k > 0 ? 1u : 0u);
-                ta_mma_ts(o, a + 16, vd, kIdescO, 1u);
-                vd += (uint64_t)(2 * C::kGroupStride >> 4);
-                if (k + 16 < prev_tokens) {
-                    ta_mma_ts(o, a + 8, vd, kIdescO, 1u);
-                    ta_mma_ts(o, a + 24, vd, kIdescO, 1u);
-                }
-                vd += (uint64_t)(2 * C::kGroupStride >> 4);
+            for (; k + 16 < prev_tokens; k += 32) {
+                ta_mma_pv2<kStep>(o, a, vd, kIdescO, !prev_first || k > 0 ? 1u : 0u);
+                vd += 2 * kStep;
                 a += 32;
             }
-            ta_commit(&bars.o_done[prev & 1]);
-            ta_commit(&bars.v_empty[v_slot]);
+            if (k < prev_tokens)
+                ta_mma_pv(o, a, vd, kIdescO, !prev_first || k > 0 ? 1u : 0u);
+            ta_commit(&bars.o_done[v_slot]);
             if (prev_last)
                 ta_commit(&bars.o_last[prev_unit & 1]);
             if (++v_slot == C::kVStages) {
@@ -818,6 +853,8 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
     const float qs = p.q_scale, qse = qs > 0.f ? qs : 1.f;
     const int node_in_tile = r / p.group;
     int gt = 0;          // tiles before this one
+    int k_slot = 0;
+    uint32_t k_par = 0;
     uint32_t meetings = 0; // of the two warps of this quarter
 
 #pragma unroll 1
@@ -842,8 +879,12 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                 for (int c = 0; c <= kChunks; ++c)
                     words[c] = ta_mask_word(mask, s.nodes, w0 + c);
             }
-            if (!ta_wait_all(&bars.s_full[gt & 1], (uint32_t)(gt >> 1) & 1, bars, p.err_flag))
+            if (!ta_wait_all(&bars.s_full[k_slot], k_par, bars, p.err_flag))
                 return;
+            if (++k_slot == C::kKStages) {
+                k_slot = 0;
+                k_par ^= 1;
+            }
             tc_fence_after();
             const uint32_t s_col = t_row + C::kColS + (uint32_t)(gt & 1) * C::kTile + half * (C::kTile / 2);
             float alpha = 1.f;
@@ -929,7 +970,8 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                 l = l * alpha + (sum2.x + sum2.y);
             }
             if (__any_sync(0xffffffffu, rescale)) {
-                if (!ta_wait_all(&bars.o_done[(gt - 1) & 1], (uint32_t)((gt - 1) >> 1) & 1, bars, p.err_flag))
+                if (!ta_wait_all(&bars.o_done[(gt - 1) % C::kVStages], (uint32_t)((gt - 1) / C::kVStages) & 1, bars,
+                                 p.err_flag))
                     return;
                 tc_fence_after();
                 const float a = rescale ? alpha : 1.f;
@@ -1167,18 +1209,16 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kKStages; ++i) {
             mbar_init(&bars.k_full[i], 1);
-            mbar_init(&bars.k_empty[i], 1);
+            mbar_init(&bars.s_full[i], 1);
         }
         for (int i = 0; i < C::kVStages; ++i) {
             mbar_init(&bars.v_full[i], 1);
             mbar_init(&bars.v_ready[i], 1);
-            mbar_init(&bars.v_empty[i], 1);
+            mbar_init(&bars.o_done[i], 1);
         }
         mbar_init(&bars.q_full, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.s_full[i], 1);
             mbar_init(&bars.p_full[i], 8); // the softmax warps
-            mbar_init(&bars.o_done[i], 1);
             mbar_init(&bars.o_last[i], 1);
             mbar_init(&bars.o_free[i], 4); // the finishing warps
             mbar_init(&bars.ml_full[i], 8);
@@ -1243,8 +1283,7 @@ constexpr int kCombineThreads = 256;
 // the one that ended it, in that order.  D / 8 threads per MMA row; gridDim.y
 // blocks take one row per thread, so that all of a thread's loads are under way
 // at once: what bounds this kernel is the chain record, (m, l) and O (4.5 us
-// from its start to its end with 16 trees of 64 nodes, where 70 KB a unit are
-// joined from about 5 slices; 7 when a block took 16 rows).
+// for 32 rows of 512 .. 1024 tokens with trees of 16 nodes).
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __grid_constant__ TaParams p, int ctas)
 {
