@@ -31,6 +31,12 @@
 //    fixed cost of a unit, then its 64-token blocks) and every CTA takes an
 //    equal range, so a long row is shared by many CTAs.  Each CTA finds its
 //    range itself from the row arrays: no plan kernel, no host readback.
+//    Where rows may have more nodes than a tile holds (and kv heads are even in
+//    number), two CTAs go along the line side by side, one on the even, one on
+//    the odd units of a row: they read the same K/V at the same time, so HBM
+//    delivers it once.  With the tiles one after the other in a CTA, long rows'
+//    K/V have left the L2 in between: 64 uneven rows of two tiles took 157 us
+//    for 149, 805 MB from HBM for 497.
 //  - A unit inside one CTA's range is finished there.  The others leave (m, l)
 //    and O in the workspace, fp32, and a second kernel joins them in range
 //    order (results do not depend on timing).  A CTA has at most two such
@@ -152,6 +158,7 @@ struct TaParams {
     uint32_t q_box_bytes;
     float q_scale;
     int pdl;
+    int pair;          // 1: two CTAs side by side on a row's units
     uint32_t k65536;   // 65536: a shift by 16 as a multiplication, in the FMA pipe beside the busy ALU
     bool wide;         // out is 32-byte aligned
 };
@@ -264,9 +271,19 @@ __device__ __forceinline__ bool ta_wait_all(uint64_t *bar, uint32_t parity, TaBa
 // Where a CTA's range starts, and its length in positions.
 struct TaStart {
     int64_t off, left; // position within the unit, positions of the range
-    int b, unit;       // row, unit within the row
+    int b, unit;       // row, unit (with p.pair: two units, one for each CTA) within the row
     TaRow row;
 };
+
+// Which of the CTAs of a pair this is, and the index of the pair.
+__device__ __forceinline__ int ta_member(const TaParams &p)
+{
+    return p.pair && blockIdx.x >= gridDim.x >> 1 ? 1 : 0;
+}
+__device__ __forceinline__ int ta_index(const TaParams &p)
+{
+    return (int)blockIdx.x - ta_member(p) * (int)(gridDim.x >> 1);
+}
 
 // Zeros and -inf for a unit of a row that is inactive or in error.  A whole warp.
 template <int D>
@@ -307,7 +324,7 @@ template <int D> struct TaWalk {
         s.flags = kOver;
 #pragma unroll 1
         while (at.left > 0) {
-            if (at.unit >= row.tiles * p.num_kv_heads) {
+            if (at.unit >= row.tiles * p.num_kv_heads >> p.pair) {
                 ++at.b;
                 at.unit = 0;
                 at.off = 0;
@@ -318,7 +335,7 @@ template <int D> struct TaWalk {
             const int64_t size = kStartCost + row.blocks, take = min(size - at.off, at.left);
             const bool at_start = at.off == 0, at_end = at.off + take >= size;
             const int a = ta_cut(at.off, row.blocks), z = at_end ? row.blocks : ta_cut(at.off + take, row.blocks);
-            const int unit = at.unit;
+            const int unit = (at.unit << p.pair) + ta_member(p);
             at.left -= take;
             at.off += take;
             if (at_end) {
@@ -1110,7 +1127,7 @@ __device__ void ta_finish(const TaParams &p, TaBars &bars, uint32_t tmem, int wa
 // Positions of row b on the work line.
 __device__ __forceinline__ int64_t ta_positions(const TaParams &p, const TaRow &r)
 {
-    return (int64_t)r.tiles * p.num_kv_heads * (kStartCost + r.blocks);
+    return (int64_t)(r.tiles * p.num_kv_heads >> p.pair) * (kStartCost + r.blocks);
 }
 
 // a / b for a >= 0, b > 0: 64-bit division only where it is needed (it is long,
@@ -1164,8 +1181,8 @@ __device__ TaStart ta_start(const TaParams &p, int64_t *scratch)
         total += v;
     }
     x -= sum;
-    const int64_t ctas = total >= (int64_t)gridDim.x * kMinRange ? gridDim.x : max(1, (int)total / kMinRange);
-    const int c = blockIdx.x;
+    const int most = (int)gridDim.x >> p.pair, c = ta_index(p);
+    const int64_t ctas = total >= (int64_t)most * kMinRange ? most : max(1, (int)total / kMinRange);
     if (c < ctas) {
         // as the quotient and remainder of total / ctas, with small numbers
         const int64_t q = ta_div(total, ctas);
@@ -1467,6 +1484,7 @@ cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t stream)
     p.slot_rows = a.shape.slot_rows;
     p.q_scale = a.q_scale;
     p.pdl = a.after_append ? 1 : 0;
+    p.pair = a.desc.num_kv_heads % 2 == 0 && a.max_nodes > a.shape.q_tile && sm_count(dev) > 1 ? 1 : 0;
     p.k65536 = 65536u;
     p.wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     const int box_nodes = a.shape.slot_rows / a.shape.group < a.total_q ? a.shape.slot_rows / a.shape.group : a.total_q;
