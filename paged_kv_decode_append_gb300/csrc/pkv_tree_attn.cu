@@ -9,18 +9,17 @@
 // MMA row tile, so a K/V byte is read once for all of them.  Per 128 keys at
 // head_dim 128 a unit reads 64 KB, 1.45 us of an SM's share of the measured HBM
 // rate, and needs 24 MMAs of 128 x 128 x 16 (8 for S, 16 for P V, whose P is
-// kept as two bf16 parts), 0.8 us at the tensor peak.  Measured (stamps of the
-// SM clock): a step takes 1.56 us, the MMA warp busy throughout -- S 0.25, P V
-// 0.74 (46 ns an MMA against 33 at the peak, its A operand coming from TMEM
-// beside the softmax's loads), commits 0.13, the rest waits between them.  So
-// the issue of MMAs bounds long rows, and memory is near: 64 uneven rows of 64
-// nodes with 4 heads a kv head (two row tiles, the second finds K/V in L2)
-// take 168.7 us = 541 TFLOP/s, 2.9 TB/s of algorithmic bytes, and the counters
-// show the tensor pipe active 43 % of the cycles, issue slots 39 %.  Short calls
-// are bound by latency: 32 rows of 512 .. 1024 tokens with trees of 16 nodes
-// take 37 us, of which the start of the CTAs is 3, the append 3, the tail and
-// the combine kernel 6; one node over 64 tokens takes 11.5 us for its three
-// kernels.
+// kept as two bf16 parts), 0.8 us at the tensor peak: memory bounds it up to 128
+// pairs whatever their number, the tensor pipe beyond (two row tiles read the
+// same K/V from L2).  Measured (stamps of the SM clock): a step takes 1.33 us.
+// With one row tile it waits for K, so memory it is; with more the MMA warp is
+// busy throughout (S 0.25, P V 0.53, the rest its waits, commits and the walk:
+// 0.1 us more in it is 0.1 us more a step, in the softmax half of that).  64
+// uneven rows of two tiles, 64 nodes x 4 heads, take 149 us = 613 TFLOP/s (168
+// with one election an MMA and the tiles not side by side, 157 with one for
+// four).  Short calls are bound by latency: 32 rows of 512 .. 1024 tokens with trees of 16 nodes take 36 us,
+// 3.1 TB/s, of which the start of the CTAs is 4, the append 3, the tail and the
+// combine kernel 6; one node over 64 tokens takes 11.3 us for its three kernels.
 //
 // The roles' code is kept short (one walk of the range, loops not unrolled
 // beyond 32 columns): at 120 KB a sixth of the instruction fetches missed the
@@ -60,9 +59,8 @@
 //    for the MMA (0 * inf would reach nodes that do not see it) and added in
 //    the epilogue to the nodes that do.
 //  - Cutting the line: kStartCost 1 .. 4 and kMinRange 4 .. 16 were measured on
-//    short, long, even and uneven batches; 2 and 6 are within 1 % of the best
-//    everywhere (kMinRange 12: 16 trees 5 % slower; a minimum that grows with
-//    the rows in use: head_dim 256 43 -> 55 us).
+//    short, long, even and uneven batches: nothing better than 2 and 6 (a
+//    minimum that grows with the rows in use: head_dim 256 43 -> 55 us).
 #include <cuda_bf16.h>
 #include <math.h>
 
