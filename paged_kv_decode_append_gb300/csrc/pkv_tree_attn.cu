@@ -121,11 +121,12 @@ struct TaSlice {
 constexpr int kBegins = 1, kEnds = 2, kOver = 4; // it starts / ends the unit; no more slices
 
 struct TaBars {
-    uint64_t k_full[6], v_full[6], v_ready[6];
+    uint64_t k_full[6], v_full[6];
+    uint64_t p_full[6];       // P of the tile whose V is in slot i written, and that V looked through
     uint64_t s_full[6];       // S of the tile in K slot i is complete: K is free, too
     uint64_t o_done[6];       // P V of the tile in V slot i is complete: V is free, too
     uint64_t q_full;
-    uint64_t p_full[2], o_free[2];
+    uint64_t o_free[2];
     uint64_t o_last[2];       // O of a slice (by its parity) is complete
     uint64_t ml_full[2], ml_free[2]; // (m, l) of a slice written / read
     uint64_t pair[4];         // the two softmax warps of each TMEM lane quarter
@@ -250,13 +251,6 @@ __device__ __forceinline__ bool ta_wait(uint64_t *bar, uint32_t parity, TaBars &
     if (mbar_try_wait(bar, parity))
         return true;
     return ta_wait_slow(bar, parity, bars, err_flag);
-}
-// Two phases at once, odd lanes on the second; all lanes of the warp get the same answer.
-__device__ __forceinline__ bool ta_wait_both(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1,
-                                             TaBars &bars, int32_t *err_flag)
-{
-    const bool odd = threadIdx.x & 1;
-    return __all_sync(0xffffffffu, ta_wait(odd ? bar1 : bar0, odd ? parity1 : parity0, bars, err_flag));
 }
 // The same for a whole warp: all lanes get the same answer.
 __device__ __forceinline__ bool ta_wait_all(uint64_t *bar, uint32_t parity, TaBars &bars, int32_t *err_flag)
@@ -600,7 +594,7 @@ __device__ void ta_walk(const TaParams &p, uint8_t *smem, TaBars &bars, const Ta
         }
         __syncwarp();
         if (lane == 0)
-            mbar_arrive(&bars.v_ready[v_slot]);
+            mbar_arrive(&bars.p_full[v_slot]);
         if (++v_slot == C::kVStages) {
             v_slot = 0;
             v_par ^= 1;
@@ -723,8 +717,7 @@ __device__ void ta_mma(const TaParams &p, uint8_t *smem, TaBars &bars, uint32_t 
             const uint32_t ob = C::kOBufs == 1 ? 0 : prev_unit & 1;
             const uint32_t use = C::kOBufs == 1 ? prev_unit : prev_unit >> 1;
             if ((prev_first && use > 0 && !ta_wait_all(&bars.o_free[ob], (use - 1) & 1, bars, p.err_flag)) ||
-                !ta_wait_both(&bars.v_ready[v_slot], v_par, &bars.p_full[prev & 1], (uint32_t)(prev >> 1) & 1, bars,
-                              p.err_flag))
+                !ta_wait_all(&bars.p_full[v_slot], v_par, bars, p.err_flag))
                 break;
             tc_fence_after();
             const uint32_t o = tmem + ob * D;
@@ -868,7 +861,7 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
     const float qs = p.q_scale, qse = qs > 0.f ? qs : 1.f;
     const int node_in_tile = r / p.group;
     int gt = 0;          // tiles before this one
-    int k_slot = 0;
+    int k_slot = 0, v_slot = 0;
     uint32_t k_par = 0;
     uint32_t meetings = 0; // of the two warps of this quarter
 
@@ -1003,7 +996,9 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&bars.p_full[gt & 1]);
+                mbar_arrive(&bars.p_full[v_slot]);
+            if (++v_slot == C::kVStages)
+                v_slot = 0;
         }
         // (m, l) to the warps that finish the slice
         if (n >= 2 && !ta_wait_all(&bars.ml_free[n & 1], (uint32_t)(n / 2 - 1) & 1, bars, p.err_flag))
@@ -1228,12 +1223,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
         for (int i = 0; i < C::kVStages; ++i) {
             mbar_init(&bars.v_full[i], 1);
-            mbar_init(&bars.v_ready[i], 1);
+            mbar_init(&bars.p_full[i], 9); // the softmax warps and the one that looks V through
             mbar_init(&bars.o_done[i], 1);
         }
         mbar_init(&bars.q_full, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.p_full[i], 8); // the softmax warps
             mbar_init(&bars.o_last[i], 1);
             mbar_init(&bars.o_free[i], 4); // the finishing warps
             mbar_init(&bars.ml_full[i], 8);
