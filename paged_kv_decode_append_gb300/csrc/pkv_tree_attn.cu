@@ -11,15 +11,16 @@
 // rate, and needs 24 MMAs of 128 x 128 x 16 (8 for S, 16 for P V, whose P is
 // kept as two bf16 parts), 0.8 us at the tensor peak: memory bounds it up to 128
 // pairs whatever their number, the tensor pipe beyond (two row tiles read the
-// same K/V from L2).  Measured (stamps of the SM clock): a step takes 1.33 us.
+// same K/V from L2).  Measured (stamps of the SM clock): a step takes 1.3 us.
 // With one row tile it waits for K, so memory it is; with more the MMA warp is
 // busy throughout (S 0.25, P V 0.53, the rest its waits, commits and the walk:
 // 0.1 us more in it is 0.1 us more a step, in the softmax half of that).  64
-// uneven rows of two tiles, 64 nodes x 4 heads, take 149 us = 613 TFLOP/s (168
-// with one election an MMA and the tiles not side by side, 157 with one for
-// four).  Short calls are bound by latency: 32 rows of 512 .. 1024 tokens with trees of 16 nodes take 36 us,
+// uneven rows of two tiles, 64 nodes x 4 heads, take 147 us = 620 TFLOP/s, the
+// tensor pipe active 55 % of the cycles (168 us with an election for every MMA
+// and a row's tiles in one CTA, 157 with one for four MMAs, 149 with the tiles
+// side by side).  Short calls are bound by latency: 32 rows of 512 .. 1024 tokens with trees of 16 nodes take 36 us,
 // 3.1 TB/s, of which the start of the CTAs is 4, the append 3, the tail and the
-// combine kernel 6; one node over 64 tokens takes 11.3 us for its three kernels.
+// combine kernel 6; one node over 64 tokens takes 11.2 us for its three kernels.
 //
 // The roles' code is kept short (one walk of the range, loops not unrolled
 // beyond 32 columns): at 120 KB a sixth of the instruction fetches missed the
@@ -35,7 +36,7 @@
 //    the odd units of a row: they read the same K/V at the same time, so HBM
 //    delivers it once.  With the tiles one after the other in a CTA, long rows'
 //    K/V have left the L2 in between: 64 uneven rows of two tiles took 157 us
-//    for 149, 805 MB from HBM for 497.
+//    for 149 and read 805 MB from HBM for 465.
 //  - A unit inside one CTA's range is finished there.  The others leave (m, l)
 //    and O in the workspace, fp32, and a second kernel joins them in range
 //    order (results do not depend on timing).  A CTA has at most two such
