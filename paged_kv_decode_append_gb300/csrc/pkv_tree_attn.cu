@@ -18,9 +18,10 @@
 // uneven rows of two tiles, 64 nodes x 4 heads, take 147 us = 620 TFLOP/s, the
 // tensor pipe active 55 % of the cycles (168 us with an election for every MMA
 // and a row's tiles in one CTA, 157 with one for four MMAs, 149 with the tiles
-// side by side).  Short calls are bound by latency: 32 rows of 512 .. 1024 tokens with trees of 16 nodes take 36 us,
-// 3.1 TB/s, of which the start of the CTAs is 4, the append 3, the tail and the
-// combine kernel 6; one node over 64 tokens takes 11.2 us for its three kernels.
+// side by side).  Short calls are bound by latency: 32 rows of 512 .. 1024
+// tokens with trees of 16 nodes take 36 us, 3.1 TB/s, of which the start of the
+// CTAs is 4, the append 3, the tail and the combine kernel 6; one node over 64
+// tokens takes 11.2 us for its three kernels.
 //
 // The roles' code is kept short (one walk of the range, loops not unrolled
 // beyond 32 columns): at 120 KB a sixth of the instruction fetches missed the
