@@ -566,7 +566,9 @@ PKV_API size_t pkv_tree_workspace_size(int32_t batch, int32_t total_q, int32_t m
  *  batch             0 .. 1024; total_q * num_q_heads < 2^31; at most 128
  *                    query heads per kv head; page_size at least 8.
  * K/V of a drafted token reach only the nodes that see it, whatever they hold
- * (infinities and NaN included).  Other row fates as pkv_mixed_attn:
+ * (infinities and NaN included).  An infinity or NaN among the values that a
+ * node sees, cached or drafted, reaches it in its column, however small its
+ * weight (infinities of both signs: NaN).  Other row fates as pkv_mixed_attn:
  * inactive; PKV_ERR_OVERFLOW when L_b + n_b exceeds max_blocks * page_size or
  * 2^31 - 256; PKV_ERR_PAGE for a bad page among the first ceil((L_b + n_b) / page_size).
  */

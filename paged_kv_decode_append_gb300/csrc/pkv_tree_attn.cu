@@ -59,7 +59,9 @@
 //    out of the node's mask.  V of drafted tokens is looked through in shared
 //    memory before the MMAs read it: an infinity or NaN there is replaced by 0
 //    for the MMA (0 * inf would reach nodes that do not see it) and added in
-//    the epilogue to the nodes that do.
+//    the epilogue to the nodes that do.  Cached tokens are seen by all: there
+//    the finishing warps look at O, and where it is not finite they put the sum
+//    of the values that are not (ta_mend_cached).
 //  - Cutting the line: kStartCost 1 .. 4 and kMinRange 4 .. 16 were measured on
 //    short, long, even and uneven batches: nothing better than 2 and 6 (a
 //    minimum that grows with the rows in use: head_dim 256 43 -> 55 us).
@@ -848,6 +850,56 @@ __device__ __noinline__ void ta_add_nonfinite(const TaParams &p, int b, int len,
     }
 }
 
+// O of a slice with infinities or NaN among its cached values.  A weight goes
+// into the MMAs as two parts whose second may be negative or 0, so such a value
+// arrives as a NaN or an infinity of either sign; all that is certain is that
+// it is not finite.  The columns where it is not become the sum of the slice's
+// cached values there that are not finite, which is what the formula gives for
+// positive weights, the same for every node.  A whole warp, rare: it reads the
+// slice's V again, D / 8 lanes to a token.  Lanes with `mend` false change nothing.
+template <int D>
+__device__ __noinline__ void ta_mend_cached(const TaParams &p, int b, int g, int tok0, int tok1, bool mend, uint32_t o_col,
+                                            int lane)
+{
+    constexpr int kLanes = D / 8;
+    const int piece = lane % kLanes;
+    const int32_t *row = p.table + (int64_t)b * p.max_blocks;
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int tok = tok0 + lane / kLanes; tok < tok1; tok += 32 / kLanes) {
+        const int64_t page = row[tok >> p.page_shift];
+        if (page < 1 || page >= p.num_pages)
+            continue;
+        const int64_t slot = tok & ((1 << p.page_shift) - 1);
+        const int64_t at = p.layout == PKV_NHD ? (((page << p.page_shift) + slot) * p.num_kv_heads + g) * D
+                                               : (((page * p.num_kv_heads + g) << p.page_shift) + slot) * D;
+        const uint4 x = *reinterpret_cast<const uint4 *>(p.v_cache + at + piece * 8);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            sum[2 * e] += bf16_nonfinite(w[e]) ? __uint_as_float(w[e] << 16) : 0.f;
+            sum[2 * e + 1] += bf16_nonfinite(w[e] >> 16) ? __uint_as_float(w[e] & 0xffff0000u) : 0.f;
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        for (int o = kLanes; o < 32; o <<= 1)
+            sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], o);
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_col + c, o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float v = __shfl_sync(0xffffffffu, sum[i & 7], (c + i) >> 3);
+            if (mend && v != 0.f && (o[i] & 0x7f800000u) == 0x7f800000u)
+                o[i] = __float_as_uint(v);
+        }
+        tmem_st32(o_col + c, o);
+    }
+}
+
 // The softmax: two threads per MMA row, each on half of a tile's columns and
 // (where O is rescaled) half of O's.
 template <int D>
@@ -1061,32 +1113,48 @@ __device__ void ta_finish(const TaParams &p, TaBars &bars, uint32_t tmem, int wa
         const int64_t part = (int64_t)(2 * blockIdx.x + (begins ? 1 : 0)) * p.slot_rows + r;
         const bool zero = bad || l == 0.f;
         const float inv = 1.f / l;
-        if (nonfinite && warp_live) {
-            if (p.pdl) // V is read from the cache again, where this call's append puts it
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-            ta_add_nonfinite<D>(p, s.b, s.len, s.g, p.mask + token * p.words, max(0, s.tok0 - s.len),
-                                min(s.nodes, s.tok1 - s.len), live, o_col, 0, D);
-        }
 #pragma unroll 1
-        for (int c = 0; warp_live && c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_col + c, o);
-            if (!live)
-                continue;
-            if (whole) {
-                uint32_t w[16];
+        for (bool again = false;; again = true) { // twice where V is not finite
+            float2 odd = make_float2(0.f, 0.f); // NaN once O is not finite
+#pragma unroll 1
+            for (int c = 0; warp_live && c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o_col + c, o);
+                if (!live)
+                    continue;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv,
-                                                                   __uint_as_float(o[2 * e + 1]) * inv);
-                    w[e] = zero ? 0u : *reinterpret_cast<const uint32_t *>(&h);
+                for (int e = 0; e < 32; e += 2)
+                    odd = ffma2(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), make_float2(0.f, 0.f), odd);
+                if (whole) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv,
+                                                                       __uint_as_float(o[2 * e + 1]) * inv);
+                        w[e] = zero ? 0u : *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                    store32(p.out + out_row * D + c, w, p.wide);
+                    store32(p.out + out_row * D + c + 16, w + 8, p.wide);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        store32(p.part_o + part * D + c + e, o + e, true);
                 }
-                store32(p.out + out_row * D + c, w, p.wide);
-                store32(p.out + out_row * D + c + 16, w + 8, p.wide);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                    store32(p.part_o + part * D + c + e, o + e, true);
+            }
+            if (again || !warp_live)
+                break;
+            // cached values first, while O shows where they are; not where the scores are NaN
+            const bool mend = live && !zero && l < INFINITY && !(odd.x + odd.y == 0.f);
+            const bool any = __any_sync(0xffffffffu, mend);
+            if (!any && !nonfinite)
+                break;
+            if (any)
+                ta_mend_cached<D>(p, s.b, s.g, s.tok0, min(s.tok1, s.len), mend, o_col, lane);
+            if (nonfinite) {
+                if (p.pdl) // V is read from the cache again, where this call's append puts it
+                    asm volatile("griddepcontrol.wait;" ::: "memory");
+                ta_add_nonfinite<D>(p, s.b, s.len, s.g, p.mask + token * p.words, max(0, s.tok0 - s.len),
+                                    min(s.nodes, s.tok1 - s.len), live, o_col, 0, D);
             }
         }
         tc_fence_before();
@@ -1289,6 +1357,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 
 constexpr int kCombineThreads = 256;
 
+// x * w; an infinity stays one where its weight is nothing in 32 bits.
+__device__ __forceinline__ float ta_weighed(float x, float w)
+{
+    return fabsf(x) == INFINITY ? x : x * w;
+}
+
 // Joins the slices of the unit that CTA blockIdx.x began and did not end: out =
 // sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, over the CTAs after it up to
 // the one that ended it, in that order.  D / 8 threads per MMA row; gridDim.y
@@ -1353,7 +1427,7 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __g
                                     y[i][1].x, y[i][1].y, y[i][1].z, y[i][1].w};
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    o[e] = o[e] * w0 + x[e] * w1;
+                    o[e] = ta_weighed(o[e], w0) + ta_weighed(x[e], w1);
             }
             n = 0;
         }

@@ -218,6 +218,52 @@ def test_infinities_and_nan_in_masked_places(geom, L):
     check(case, got, want)
 
 
+def place(case, pool, b, pos, head):
+    """The head_dim values of row b's cached position pos."""
+    page, slot = int(case.block_table[b, pos // case.page_size]), pos % case.page_size
+    return pool[page, slot, head] if case.layout == wl.NHD else pool[page, head, slot]
+
+
+def check_kinds(case, got, want):
+    """Infinities and NaN of out where the formula has them, the rest within the bound."""
+    out = got[0].double().cpu().numpy()
+    for kind in (np.isposinf, np.isneginf, np.isnan):
+        assert np.array_equal(kind(out), kind(want[0])), kind.__name__
+    fine = np.isfinite(want[0])
+    assert (np.abs(out[fine] - want[0][fine]) <= want[2][fine]).all()
+
+
+@pytest.mark.parametrize("geom", [(128, 16, 4, 16, wl.NHD), (64, 8, 8, 32, wl.HND), (256, 8, 2, 8, wl.NHD)], ids=name)
+@pytest.mark.parametrize("L,far", [(40, 1), (300, 1), (5000, 1), (5000, 64)])
+def test_infinities_and_nan_of_cached_values(geom, L, far):
+    """A cached value that is not finite reaches every node of its kv head, in its
+    column alone, as it does while it is drafted; whole units and split ones, and
+    (far) where its weight is nothing in 32 bits."""
+    D, Hq, Hkv, P, layout = geom
+    case = wl.mixed_step(900 + L, [20, 3, 5], [L, 10, 77], Hq, Hkv, D, P, layout, device=DEV)
+    case.q.mul_(far)  # scores within +-300: a weight is positive in 64 bits
+    seen = trees(case, 11)
+    seen[0][:, 7] = False
+    seen[0][[7, 9], 7] = True
+    inf = float("inf")
+    for pos, head, col, x in [(L // 2, 0, 3, inf), (L // 3, 0, 5, float("nan")), (0, 0, D - 1, -inf), (1, 0, 8, inf),
+                              (L - 1, 0, 8, -inf), (L - 1, Hkv - 1, 0, inf), (L - 2, Hkv - 1, 0, inf)]:
+        place(case, case.v_cache, 0, pos, head)[col] = x
+    place(case, case.v_cache, 2, 64, Hkv - 1)[:] = -inf
+    case.v_new[7, 0, 3] = -inf     # against the cached infinity of that column: NaN at the two nodes that see it
+    case.v_new[7, 0, 17] = inf
+    got = run_attn(case, seen)
+    assert got[2] == 0
+    want = ref.attention(case, seen)
+    check_kinds(case, got, want)
+    out = got[0]
+    G = Hq // Hkv
+    assert torch.isposinf(out[[0, 19], :G, 3]).all() and torch.isnan(out[[7, 9], :G, 3]).all()
+    assert torch.isnan(out[:20, :G, 5]).all() and torch.isnan(out[:20, :G, 8]).all()
+    assert torch.isneginf(out[:20, :G, D - 1]).all() and torch.isneginf(out[23:, -G:]).all()
+    assert torch.isposinf(out[:20, -G:, 0]).all() and torch.isfinite(out[20:23]).all()
+
+
 def test_values_of_the_types_ends():
     """Scores of thousands, and the lowest finite value among the values."""
     case = wl.mixed_step(41, [12, 5], [150, 20], 8, 2, 64, 16, wl.NHD, device=DEV)
