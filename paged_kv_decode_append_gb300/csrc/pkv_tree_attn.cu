@@ -1417,7 +1417,7 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __g
             }
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
-                if (i >= n || ml[i].x == -INFINITY) // (nothing is seen there)
+                if (i >= n || ml[i].y == 0.f) // (nothing is seen there; NaN scores leave m at -inf, but l NaN)
                     continue;
                 const float top = fmaxf(m, ml[i].x);
                 const float w0 = m == -INFINITY ? 0.f : ex2_approx(m - top), w1 = ex2_approx(ml[i].x - top);

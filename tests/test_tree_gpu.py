@@ -264,6 +264,37 @@ def test_infinities_and_nan_of_cached_values(geom, L, far):
     assert torch.isposinf(out[:20, -G:, 0]).all() and torch.isfinite(out[20:23]).all()
 
 
+@pytest.mark.parametrize("L", [40, 9000, 30000])
+def test_nan_scores_stay_nan(L):
+    """A node whose scores are NaN, all of them or those of a long run of keys,
+    is NaN; its neighbours are not touched."""
+    case = wl.mixed_step(1000 + L, [6, 4], [L, 50], 8, 2, 128, 16, wl.NHD, extra_pages=0, device=DEV)
+    seen = trees(case, 12)
+    want = ref.attention(case, seen)
+    case.q[2] = float("nan")
+    case.q[7, 1] = float("nan")
+    got = run_attn(case, seen)
+    assert got[2] == 0
+    assert torch.isnan(got[0][2]).all() and torch.isnan(got[1][2]).all()
+    assert torch.isnan(got[0][7, 1]).all() and torch.isnan(got[1][7, 1])
+    for w in want:
+        w[2] = 0
+        w[7, 1] = 0
+    for g in got[:2]:
+        g[2] = 0
+        g[7, 1] = 0
+    check(case, got, want)
+    # all but the last cached keys of kv head 1: every node's heads 4 .. 7
+    case = wl.mixed_step(1000 + L, [6, 4], [L, 50], 8, 2, 128, 16, wl.NHD, extra_pages=0, device=DEV)
+    last = (L - 1) // 16
+    case.k_cache[torch.as_tensor(case.block_table[0, :last].astype(np.int64), device=DEV), :, 1] = float("nan")
+    want = ref.attention(case, seen, rows=[1])
+    got = run_attn(case, seen)
+    assert torch.isnan(got[0][:6, 4:]).all() and torch.isnan(got[1][:6, 4:]).all()
+    assert torch.isfinite(got[0][:6, :4]).all() and torch.isfinite(got[1][:6, :4]).all()
+    check(case, got, want, rows=[1])
+
+
 def test_values_of_the_types_ends():
     """Scores of thousands, and the lowest finite value among the values."""
     case = wl.mixed_step(41, [12, 5], [150, 20], 8, 2, 64, 16, wl.NHD, device=DEV)
