@@ -38,7 +38,7 @@
 //    delivers it once.  With the tiles one after the other in a CTA, long rows'
 //    K/V have left the L2 in between: 64 uneven rows of two tiles took 157 us
 //    for 149 and read 805 MB from HBM for 465.
-//  - A unit inside one CTA's range is finished there.  The others leave (m, l)
+//  - A unit inside one CTA's range is finished there.  The others leave (ref, l)
 //    and O in the workspace, fp32, and a second kernel joins them in range
 //    order (results do not depend on timing).  A CTA has at most two such
 //    slices: the one it starts in and the one it ends in.
@@ -51,8 +51,12 @@
 //    While the softmax is at tile t the tensor pipe runs S of tile t + 1 and P V
 //    of tile t - 1.
 //  - The running maximum m moves only when a score exceeds it by more than 2^8
-//    (then O is rescaled); the weights are taken as 2^(s - m - 8) <= 1, so a
-//    large value cannot overflow before the division.
+//    (then O is rescaled).  The weights are taken as 2^(s - ref), ref = m + 8 +
+//    slack with slack = 1 + ceil(log2 of the row's keys): none is above
+//    2^-slack and they sum to at most 1/2, so values at the end of bf16 cannot
+//    overflow O before the division.  What that costs is at the other end:
+//    weights below 2^(slack - 118) of the row's largest, and values below about
+//    that, are lost (slack is 17 at 64K keys).
 //  - P replaces S in TMEM as bf16 hi + lo parts (16 significant bits; 8 alone
 //    leave errors of 2^-9 of the row's scale in small outputs).
 //  - Tiles with drafted keys take their visibility as 32-bit words, shifted
@@ -132,7 +136,7 @@ struct TaBars {
     uint64_t q_full;
     uint64_t o_free[2];
     uint64_t o_last[2];       // O of a slice (by its parity) is complete
-    uint64_t ml_full[2], ml_free[2]; // (m, l) of a slice written / read
+    uint64_t ml_full[2], ml_free[2]; // (ref, l) of a slice written / read
     uint64_t pair[4];         // the two softmax warps of each TMEM lane quarter
     uint64_t slice_full[kSlices], slice_empty[kSlices];
     uint64_t drain;
@@ -928,7 +932,8 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
         const bool live = r < rows, warp_live = quarter * 32 < rows;
         const int32_t *mask = p.mask + ((int64_t)s.first + (live ? s.node0 + node_in_tile : 0)) * p.words;
         const uint32_t o_col = t_row + (C::kOBufs == 1 ? 0u : (n & 1) * D);
-        float m = -INFINITY, l = 0.f; // l: this half's part of the row's sum
+        const float slack = (float)(33 - __clz(s.len + s.nodes - 1));
+        float ref = -INFINITY, l = 0.f; // the weights' reference; this half's part of their sum
 #pragma unroll 1
         for (int tok = s.tok0; tok < s.tok1; tok += C::kTile, ++gt) {
             const int tok_h = tok + half * (C::kTile / 2), tokens = s.tok1 - tok_h; // this half's keys
@@ -996,13 +1001,14 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                     return;
                 ++meetings;
                 mx = fmaxf(mx, at[(1 - half) * kTaRows]);
-                if (mx > m + kRescaleLog2) {
-                    rescale = m != -INFINITY; // before the slice's first P V there is no O
-                    alpha = ex2_approx(m - mx);
-                    m = mx;
+                if (mx + slack > ref) {
+                    const float next = mx + (slack + kRescaleLog2);
+                    rescale = ref != -INFINITY; // before the slice's first P V there is no O
+                    alpha = ex2_approx(ref - next);
+                    ref = next;
                 }
                 float2 sum2 = make_float2(0.f, 0.f);
-                const float m_ref = m == -INFINITY ? 0.f : m + kRescaleLog2;
+                const float m_ref = ref == -INFINITY ? 0.f : ref;
                 const float2 q2 = make_float2(qse, qse), nm2 = make_float2(-m_ref, -m_ref);
 #pragma unroll 1
                 for (int c = 0; c < kChunks; ++c) {
@@ -1054,10 +1060,10 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
             if (++v_slot == C::kVStages)
                 v_slot = 0;
         }
-        // (m, l) to the warps that finish the slice
+        // (ref, l) to the warps that finish the slice
         if (n >= 2 && !ta_wait_all(&bars.ml_free[n & 1], (uint32_t)(n / 2 - 1) & 1, bars, p.err_flag))
             return;
-        p.row_ml[((int64_t)blockIdx.x * 4 + (n & 1) * 2 + half) * kTaRows + r] = make_float2(m, l);
+        p.row_ml[((int64_t)blockIdx.x * 4 + (n & 1) * 2 + half) * kTaRows + r] = make_float2(ref, l);
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&bars.ml_full[n & 1]);
@@ -1074,7 +1080,7 @@ __device__ __forceinline__ float2 load_fresh(const float2 *at)
 }
 
 // Finishes the slices, one thread per MMA row: O / l to out where the slice is a
-// whole unit, else O and (m, l) to the workspace.
+// whole unit, else O and (ref, l) to the workspace.
 template <int D>
 __device__ void ta_finish(const TaParams &p, TaBars &bars, uint32_t tmem, int warp, int lane)
 {
@@ -1165,7 +1171,7 @@ __device__ void ta_finish(const TaParams &p, TaBars &bars, uint32_t tmem, int wa
             if (!whole)
                 p.part_ml[part] = make_float2(m, l);
             else if (p.lse != nullptr)
-                p.lse[out_row] = zero ? -INFINITY : (m + kRescaleLog2 + log2f(l)) * kLn2;
+                p.lse[out_row] = zero ? -INFINITY : (m + log2f(l)) * kLn2;
         }
         if (r == 0) {
             if (bad)
@@ -1364,11 +1370,12 @@ __device__ __forceinline__ float ta_weighed(float x, float w)
 }
 
 // Joins the slices of the unit that CTA blockIdx.x began and did not end: out =
-// sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, over the CTAs after it up to
-// the one that ended it, in that order.  D / 8 threads per MMA row; gridDim.y
-// blocks take one row per thread, so that all of a thread's loads are under way
-// at once: what bounds this kernel is the chain record, (m, l) and O (4.5 us
-// for 32 rows of 512 .. 1024 tokens with trees of 16 nodes).
+// sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s (m_s the slice's ref), over the
+// CTAs after it up to the one that ended it, in that order.  D / 8 threads per
+// MMA row; gridDim.y blocks take one row per thread, so that all of a thread's
+// loads are under way at once: what bounds this kernel is the chain record,
+// (ref, l) and O (4.5 us for 32 rows of 512 .. 1024 tokens with trees of 16
+// nodes).
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __grid_constant__ TaParams p, int ctas)
 {
@@ -1447,7 +1454,7 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __g
     const int64_t out_row = ((int64_t)rec.y + row / p.group) * p.num_q_heads + rec.z * p.group + row % p.group;
     *reinterpret_cast<uint4 *>(p.out + out_row * D + col) = make_uint4(w[0], w[1], w[2], w[3]);
     if (col == 0 && p.lse != nullptr)
-        p.lse[out_row] = zero ? -INFINITY : (m + kRescaleLog2 + log2f(l)) * kLn2;
+        p.lse[out_row] = zero ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- host side

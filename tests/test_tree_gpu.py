@@ -314,6 +314,28 @@ def test_values_of_the_types_ends():
     assert np.isfinite(got[0].double().cpu().numpy()).all()
 
 
+@pytest.mark.parametrize("alike", [True, False], ids=["equal", "random"])
+@pytest.mark.parametrize("geom,L", [((128, 8, 2, 16, wl.NHD), 300), ((64, 8, 8, 32, wl.HND), 5000),
+                                    ((256, 8, 2, 16, wl.NHD), 2000), ((128, 8, 2, 16, wl.NHD), 60000)],
+                         ids=lambda x: str(x) if isinstance(x, int) else name(x))
+def test_values_at_the_largest_of_the_type(geom, L, alike):
+    """The mean of many values at the end of bf16 is finite, whatever the number of
+    keys and however their scores rise on the way."""
+    D, Hq, Hkv, P, layout = geom
+    case = wl.mixed_step(1100 + L, [6, 40], [L, 200], Hq, Hkv, D, P, layout, extra_pages=0, device=DEV)
+    if alike:
+        case.q.zero_()
+    top = torch.finfo(torch.bfloat16).max
+    case.v_cache.fill_(top)
+    case.v_new.fill_(top)
+    case.v_cache[..., D // 2:] = -top
+    case.v_new[..., D // 2:] = -top
+    seen = trees(case, 13)
+    got = run_attn(case, seen)
+    assert got[2] == 0
+    check(case, got, ref.attention(case, seen))
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
 def test_scales(scale):
     case = wl.mixed_step(42, [7, 33], [260, 0], 8, 2, 128, 16, wl.NHD, device=DEV)
