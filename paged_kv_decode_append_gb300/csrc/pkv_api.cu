@@ -660,6 +660,7 @@ pkv_status pkv_tree_attn(const pkv_cache_desc *desc, void *k_cache, void *v_cach
         a.err_flag = err_flag;
         a.max_count = max_nodes;
         a.max_len = kTreeMaxKeys;
+        a.any_order = true;
         if (launch_append(a, s) != cudaSuccess)
             return PKV_ECUDA;
     }

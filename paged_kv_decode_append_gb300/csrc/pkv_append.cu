@@ -25,8 +25,15 @@ struct AParams {
     int num_tokens, batch, max_blocks, page_size, page_shift, num_pages, num_kv_heads, head_dim, layout;
     int64_t max_len; // rows longer than this overflow
     int max_count; // rows appending more tokens than this append nothing
+    int any_order; // the ranges may be malformed in part: look at every row for one that owns the token
     int pdl_wait;  // launched as a programmatic dependent: wait for the preceding grid before exiting
 };
+
+// Whether [first, end) is a range of the call and holds token t.
+__device__ __forceinline__ bool owns(const AParams &p, int first, int end, int t)
+{
+    return first >= 0 && first <= t && t < end && end <= p.num_tokens;
+}
 
 // One CTA per new token.
 __device__ __forceinline__ void append_token(const AParams &p)
@@ -53,6 +60,26 @@ __device__ __forceinline__ void append_token(const AParams &p)
         s_count = count;
     }
     __syncthreads();
+    if (p.any_order && !owns(p, s_first, p.indptr[s_row + 1], t)) {
+        // Malformed ranges send the bisection astray; their neighbours are served
+        // all the same.  (The lowest row, where ranges overlap.)
+        __shared__ int s_found;
+        if (threadIdx.x == 0)
+            s_found = p.batch;
+        __syncthreads();
+        for (int b = threadIdx.x; b < p.batch; b += kAppendThreads)
+            if (owns(p, p.indptr[b], p.indptr[b + 1], t))
+                atomicMin(&s_found, b);
+        __syncthreads();
+        if (s_found == p.batch)
+            return;
+        if (threadIdx.x == 0) {
+            s_row = s_found;
+            s_first = p.indptr[s_found];
+            s_count = p.indptr[s_found + 1] - s_first;
+        }
+        __syncthreads();
+    }
     const int b = s_row, count = s_count;
     const int L = p.seqlens[b];
     // inactive row; a token outside its row's range (a malformed indptr); a
@@ -139,6 +166,7 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t stream)
     p.max_len = (int64_t)a.max_blocks * a.desc.page_size;
     if (p.max_len > a.max_len)
         p.max_len = a.max_len;
+    p.any_order = a.any_order ? 1 : 0;
     p.pdl_wait = a.overlap_prior ? 1 : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.num_tokens);

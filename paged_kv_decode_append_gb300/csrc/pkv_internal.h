@@ -122,6 +122,10 @@ struct AppendArgs {
     int32_t *err_flag;
     int max_count = 0x7fffffff; // rows appending more tokens than this append nothing
     int64_t max_len = 0x7fffffff; // rows of more tokens than this overflow, whatever their table holds
+    // Rows with a well-formed range append whatever the others' ranges are: a
+    // token that bisection gives to a row that does not own it is looked for
+    // in all of them (batch reads for each token that no row owns).
+    bool any_order = false;
     // Launch as a programmatic dependent of the preceding kernel: the two may
     // run side by side, so that kernel must not write what the append reads
     // or writes (k_new, v_new, the cache, indptr, cache_seqlens, block_table);

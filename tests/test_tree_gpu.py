@@ -395,6 +395,30 @@ def test_ranges_that_leave_the_batch():
             check(case, got, want, rows=[0])
 
 
+@pytest.mark.parametrize("geom", [(64, 8, 2, 16, wl.NHD), (128, 8, 8, 8, wl.HND)], ids=name)
+@pytest.mark.parametrize("counts,indptr", [
+    ([3, 0, 0, 2], [0, 3, -1, 3, 5]),
+    ([3, 0, 0, 2], [0, 3, 99, 3, 5]),
+    ([2, 0, 0, 2, 0, 0, 1], [0, 2, -5, 2, 4, 77, 4, 5]),
+    ([0, 0, 4, 0, 0, 0], [9, -3, 0, 4, 3, 2, 2 ** 31 - 1]),
+    ([0, 0, 250, 0, 0, 0], [9, -3, 0, 250, 3, 2, 2 ** 31 - 1]),
+    ([0, 0, 0, 1, 1], [-7, 2, 2, 0, 1, 2]),
+])
+def test_rows_among_malformed_ranges_are_served(geom, counts, indptr):
+    """Rows with a range of their own are appended and attended wherever the
+    malformed ones stand (their tokens cannot be found by bisection)."""
+    D, Hq, Hkv, P, layout = geom
+    lens = [20, 7, 33, 5, 60, 1, 90][: len(counts)]
+    case = wl.mixed_step(1200, counts, lens, Hq, Hkv, D, P, layout, device=DEV)
+    good = [b for b, n in enumerate(counts) if 0 < n <= 256]
+    seen = trees(case, 14)
+    want = ref.attention(case, seen, rows=good)
+    got = run_attn(case, seen, max_nodes=256, indptr=np.array(indptr))
+    assert got[2] == pkv.api.ERR_QLEN
+    check(case, got, want, rows=good)
+    check_cache(case, got[3], got[4], rows=good)
+
+
 def test_tokens_behind_the_last_row_are_left_alone():
     case = wl.mixed_step(46, [3, 2, 4], [20, 7, 5], 8, 2, 64, 16, wl.NHD, device=DEV)
     seen = trees(case, 1)
