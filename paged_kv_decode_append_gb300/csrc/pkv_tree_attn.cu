@@ -1007,6 +1007,7 @@ __device__ void ta_softmax(const TaParams &p, uint8_t *smem, TaBars &bars, uint3
                     alpha = ex2_approx(ref - next);
                     ref = next;
                 }
+                __syncwarp(); // the loads below are the whole warp's
                 float2 sum2 = make_float2(0.f, 0.f);
                 const float m_ref = ref == -INFINITY ? 0.f : ref;
                 const float2 q2 = make_float2(qse, qse), nm2 = make_float2(-m_ref, -m_ref);
@@ -1126,26 +1127,28 @@ __device__ void ta_finish(const TaParams &p, TaBars &bars, uint32_t tmem, int wa
             for (int c = 0; warp_live && c < D; c += 32) {
                 uint32_t o[32];
                 tmem_ld32(o_col + c, o);
-                if (!live)
-                    continue;
+                if (live) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                    odd = ffma2(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), make_float2(0.f, 0.f), odd);
-                if (whole) {
-                    uint32_t w[16];
+                    for (int e = 0; e < 32; e += 2)
+                        odd = ffma2(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
+                                    make_float2(0.f, 0.f), odd);
+                    if (whole) {
+                        uint32_t w[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv,
-                                                                       __uint_as_float(o[2 * e + 1]) * inv);
-                        w[e] = zero ? 0u : *reinterpret_cast<const uint32_t *>(&h);
+                        for (int e = 0; e < 16; ++e) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv,
+                                                                           __uint_as_float(o[2 * e + 1]) * inv);
+                            w[e] = zero ? 0u : *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                        store32(p.out + out_row * D + c, w, p.wide);
+                        store32(p.out + out_row * D + c + 16, w + 8, p.wide);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            store32(p.part_o + part * D + c + e, o + e, true);
                     }
-                    store32(p.out + out_row * D + c, w, p.wide);
-                    store32(p.out + out_row * D + c + 16, w + 8, p.wide);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        store32(p.part_o + part * D + c + e, o + e, true);
                 }
+                __syncwarp(); // the next load is the whole warp's
             }
             if (again || !warp_live)
                 break;
