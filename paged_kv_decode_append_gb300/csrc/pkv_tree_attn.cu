@@ -142,7 +142,7 @@ struct TaBars {
     uint64_t drain;
     TaSlice slice[kSlices];
     uint8_t bad[kSlices];       // a page of the slice is out of range
-    uint8_t nonfinite[kSlices]; // V of a drafted token holds an infinity or NaN
+    uint8_t nonfinite[kSlices]; // bit w: of drafted tokens 32 w .. 32 w + 31, V of some holds an infinity or NaN
     uint32_t tmem_base;
     int32_t abort;
 };
@@ -585,16 +585,23 @@ __device__ void ta_walk(const TaParams &p, uint8_t *smem, TaBars &bars, const Ta
                 sum = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&x.w), zero, sum);
             }
             if (__any_sync(0xffffffffu, __hisnan(sum.x) || __hisnan(sum.y))) {
+                uint32_t words = 0;
 #pragma unroll 1
                 for (int i = d0 * kPieces + lane; i < tokens * kPieces; i += 32) {
                     uint32_t *w = reinterpret_cast<uint32_t *>(ta_v_piece<D>(vb, i));
 #pragma unroll 1
-                    for (int k = 0; k < 4; ++k)
-                        w[k] &= (bf16_nonfinite(w[k]) ? 0xffff0000u : 0xffffffffu) &
-                                (bf16_nonfinite(w[k] >> 16) ? 0xffffu : 0xffffffffu);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t keep = (bf16_nonfinite(w[k]) ? 0xffff0000u : 0xffffffffu) &
+                                              (bf16_nonfinite(w[k] >> 16) ? 0xffffu : 0xffffffffu);
+                        w[k] &= keep;
+                        words |= keep != 0xffffffffu ? 1u << ((tok + i / kPieces - s.len) >> 5) : 0u;
+                    }
                 }
-                if (lane == 0)
-                    *(volatile uint8_t *)&bars.nonfinite[n % kSlices] = 1;
+                words = __reduce_or_sync(0xffffffffu, words);
+                if (lane == 0) {
+                    volatile uint8_t *set = &bars.nonfinite[n % kSlices];
+                    *set = (uint8_t)(*set | words);
+                }
             }
             for (int i = tokens * kPieces + lane; i < r1 * kPieces; i += 32)
                 *reinterpret_cast<uint4 *>(ta_v_piece<D>(vb, i)) = make_uint4(0u, 0u, 0u, 0u);
@@ -818,40 +825,71 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t *w, bool wide)
                  : "memory");
 }
 
-// Adds to columns c0 .. c1 - 1 of a node's O the infinities and NaN that the
-// drafted tokens j0 .. j1 - 1 it sees hold there (rare; read again from the
-// cache).  A whole warp; lanes with `live` false change nothing.
+// This lane's 8 values (piece lane % (D / 8)) of V of a token in the cache;
+// zeros for a page that is none.
 template <int D>
-__device__ __noinline__ void ta_add_nonfinite(const TaParams &p, int b, int len, int g, const int32_t *mask, int j0, int j1,
-                                              bool live, uint32_t o_col, int c0, int c1)
+__device__ __forceinline__ uint4 ta_cached_v(const TaParams &p, int b, int g, int tok, int lane)
 {
-    for (int c = c0; c < c1; ++c) {
-        float sum = 0.f;
-        for (int j = j0; j < j1; ++j) {
-            if (!live || !((uint32_t)mask[j >> 5] >> (j & 31) & 1u))
+    const int64_t page = p.table[(int64_t)b * p.max_blocks + (tok >> p.page_shift)];
+    if (page < 1 || page >= p.num_pages)
+        return make_uint4(0u, 0u, 0u, 0u);
+    const int64_t slot = tok & ((1 << p.page_shift) - 1);
+    const int64_t at = p.layout == PKV_NHD ? (((page << p.page_shift) + slot) * p.num_kv_heads + g) * D
+                                           : (((page * p.num_kv_heads + g) << p.page_shift) + slot) * D;
+    return *reinterpret_cast<const uint4 *>(p.v_cache + at + lane % (D / 8) * 8);
+}
+
+// Adds to a node's O the infinities and NaN that the drafted tokens j0 .. j1 - 1
+// it sees hold (rare; read again from the cache).  `words`: which 32 tokens to
+// look at; of them only those that some lane sees are read, so that padding
+// costs a vote.  A whole warp; lanes with `live` false change nothing.  Whether
+// any O changed.
+template <int D>
+__device__ __noinline__ bool ta_add_nonfinite(const TaParams &p, int b, int len, int g, const int32_t *mask, int j0, int j1,
+                                              uint32_t words, bool live, uint32_t o_col, int lane)
+{
+    bool changed = false;
+#pragma unroll 1
+    for (; words != 0; words &= words - 1) {
+        const int first = (__ffs(words) - 1) * 32, lo = max(j0 - first, 0), hi = min(j1 - first, 32);
+        if (lo >= hi)
+            continue;
+        const uint32_t mine = live ? (uint32_t)mask[first >> 5] & (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo) : 0u;
+#pragma unroll 1
+        for (uint32_t keys = __reduce_or_sync(0xffffffffu, mine); keys != 0; keys &= keys - 1) {
+            const int k = __ffs(keys) - 1;
+            const uint4 x = ta_cached_v<D>(p, b, g, len + first + k, lane);
+            uint32_t w[4] = {x.x, x.y, x.z, x.w}, any = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] &= (bf16_nonfinite(w[e]) ? 0xffffu : 0u) | (bf16_nonfinite(w[e] >> 16) ? 0xffff0000u : 0u);
+                any |= w[e];
+            }
+            const uint32_t pieces = __ballot_sync(0xffffffffu, any != 0);
+            if (pieces == 0)
                 continue;
-            const int tok = len + j;
-            const int64_t page = p.table[(int64_t)b * p.max_blocks + (tok >> p.page_shift)];
-            if (page < 1 || page >= p.num_pages)
-                continue;
-            const int64_t slot = tok & ((1 << p.page_shift) - 1);
-            const int64_t at = p.layout == PKV_NHD ? (((page << p.page_shift) + slot) * p.num_kv_heads + g) * D
-                                                   : (((page * p.num_kv_heads + g) << p.page_shift) + slot) * D;
-            const uint32_t v = reinterpret_cast<const uint16_t *>(p.v_cache)[at + c];
-            if (bf16_nonfinite(v))
-                sum += __uint_as_float(v << 16);
+            changed = true;
+            const bool sees = mine >> k & 1u;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                if (!(pieces >> (c >> 3) & 0xfu))
+                    continue;
+                uint32_t o[32];
+                tmem_ld32(o_col + c, o);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const uint32_t v = __shfl_sync(0xffffffffu, w[(i & 7) >> 1], (c + i) >> 3);
+                    if (sees) {
+                        o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(v << 16));
+                        o[i + 1] = __float_as_uint(__uint_as_float(o[i + 1]) + __uint_as_float(v & 0xffff0000u));
+                    }
+                }
+                __syncwarp();
+                tmem_st32(o_col + c, o);
+            }
         }
-        __syncwarp();
-        uint32_t x;
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
-                     : "=r"(x)
-                     : "r"(o_col + c)
-                     : "memory");
-        x = __float_as_uint(__uint_as_float(x) + sum);
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(o_col + c),
-                     "r"(x)
-                     : "memory");
     }
+    return changed;
 }
 
 // O of a slice with infinities or NaN among its cached values.  A weight goes
@@ -866,18 +904,10 @@ __device__ __noinline__ void ta_mend_cached(const TaParams &p, int b, int g, int
                                             int lane)
 {
     constexpr int kLanes = D / 8;
-    const int piece = lane % kLanes;
-    const int32_t *row = p.table + (int64_t)b * p.max_blocks;
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int tok = tok0 + lane / kLanes; tok < tok1; tok += 32 / kLanes) {
-        const int64_t page = row[tok >> p.page_shift];
-        if (page < 1 || page >= p.num_pages)
-            continue;
-        const int64_t slot = tok & ((1 << p.page_shift) - 1);
-        const int64_t at = p.layout == PKV_NHD ? (((page << p.page_shift) + slot) * p.num_kv_heads + g) * D
-                                               : (((page * p.num_kv_heads + g) << p.page_shift) + slot) * D;
-        const uint4 x = *reinterpret_cast<const uint4 *>(p.v_cache + at + piece * 8);
+        const uint4 x = ta_cached_v<D>(p, b, g, tok, lane);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -1114,7 +1144,7 @@ __device__ void ta_finish(const TaParams &p, TaBars &bars, uint32_t tmem, int wa
             return;
         tc_fence_after();
         const bool bad = *(volatile uint8_t *)&bars.bad[n % kSlices] != 0;
-        const bool nonfinite = *(volatile uint8_t *)&bars.nonfinite[n % kSlices] != 0;
+        const uint32_t nonfinite = *(volatile uint8_t *)&bars.nonfinite[n % kSlices];
         const uint32_t o_col = t_row + (C::kOBufs == 1 ? 0u : (n & 1) * D);
         const bool begins = s.flags & kBegins, ends = s.flags & kEnds, whole = begins && ends;
         const int64_t part = (int64_t)(2 * blockIdx.x + (begins ? 1 : 0)) * p.slot_rows + r;
@@ -1154,17 +1184,17 @@ __device__ void ta_finish(const TaParams &p, TaBars &bars, uint32_t tmem, int wa
                 break;
             // cached values first, while O shows where they are; not where the scores are NaN
             const bool mend = live && !zero && l < INFINITY && !(odd.x + odd.y == 0.f);
-            const bool any = __any_sync(0xffffffffu, mend);
-            if (!any && !nonfinite)
-                break;
-            if (any)
+            bool changed = __any_sync(0xffffffffu, mend);
+            if (changed)
                 ta_mend_cached<D>(p, s.b, s.g, s.tok0, min(s.tok1, s.len), mend, o_col, lane);
-            if (nonfinite) {
+            if (nonfinite != 0) {
                 if (p.pdl) // V is read from the cache again, where this call's append puts it
                     asm volatile("griddepcontrol.wait;" ::: "memory");
-                ta_add_nonfinite<D>(p, s.b, s.len, s.g, p.mask + token * p.words, max(0, s.tok0 - s.len),
-                                    min(s.nodes, s.tok1 - s.len), live, o_col, 0, D);
+                changed |= ta_add_nonfinite<D>(p, s.b, s.len, s.g, p.mask + token * p.words, max(0, s.tok0 - s.len),
+                                               min(s.nodes, s.tok1 - s.len), nonfinite, live, o_col, lane);
             }
+            if (!changed)
+                break;
         }
         tc_fence_before();
         __syncwarp();

@@ -295,6 +295,59 @@ def test_nan_scores_stay_nan(L):
     check(case, got, want, rows=[1])
 
 
+@pytest.mark.parametrize("geom", [(128, 16, 4, 16, wl.NHD), (256, 4, 2, 8, wl.HND)], ids=name)
+def test_many_values_that_are_not_finite(geom):
+    """Of 200 drafted tokens a third hold infinities or NaN, each seen by a few nodes."""
+    D, Hq, Hkv, P, layout = geom
+    case = wl.mixed_step(1300, [200, 30], [333, 10], Hq, Hkv, D, P, layout, device=DEV)
+    seen = trees(case, 15)
+    rng = np.random.default_rng(15)
+    for j in range(0, 200, 3):
+        seen[0][:, j] = False
+        seen[0][rng.integers(0, 200, 2), j] = True
+        x = (float("inf"), float("-inf"), float("nan"))[j // 3 % 3]
+        case.v_new[j, rng.integers(0, Hkv), rng.integers(0, D, 5)] = x
+    got = run_attn(case, seen, max_nodes=256)
+    assert got[2] == 0
+    check_kinds(case, got, ref.attention(case, seen))
+
+
+def test_padding_that_is_not_finite_costs_little():
+    """Nodes that nobody sees may hold anything in K and V: the call takes about
+    as long as with zeros there.  (Looking every key through again for every
+    column took several hundred times as long.)"""
+    case = wl.mixed_step(1400, [256] * 4, [100] * 4, 16, 2, 256, 16, wl.NHD, device=DEV)
+    seen = trees(case, 16)
+    for s in seen:
+        s[:, 200:] = False
+    mask, args = i32(ref.pack(seen, 8)), (i32(case.qo_indptr), i32(case.block_table), i32(case.cache_seqlens))
+    kc, vc, out = case.k_cache.clone(), case.v_cache.clone(), torch.empty_like(case.q)
+    ws = pkv.tree_workspace(4, 1024, case.max_blocks, 16, 256, pkv.cache_desc(kc), DEV)
+
+    def best(v_new):
+        times = []
+        for _ in range(12):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda.synchronize()
+            a.record()
+            for _ in range(4):
+                pkv.pkv_tree_attn(kc, vc, case.q, case.k_new, v_new, args[0], mask, args[1], args[2],
+                                  case.softmax_scale, 256, out=out, workspace=ws)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    padding = torch.arange(1024, device=DEV) % 256 >= 200
+    zeros, junk = case.v_new.clone(), case.v_new.clone()
+    zeros[padding] = 0
+    junk[padding] = float("nan")
+    plain = best(zeros)
+    first = out.clone()
+    assert best(junk) < 4 * plain
+    assert torch.equal(out.view(torch.int16), first.view(torch.int16))
+
+
 def test_values_of_the_types_ends():
     """Scores of thousands, and the lowest finite value among the values."""
     case = wl.mixed_step(41, [12, 5], [150, 20], 8, 2, 64, 16, wl.NHD, device=DEV)
