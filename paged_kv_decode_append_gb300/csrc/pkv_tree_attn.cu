@@ -825,10 +825,9 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t *w, bool wide)
                  : "memory");
 }
 
-// This lane's 8 values (piece lane % (D / 8)) of V of a token in the cache;
-// zeros for a page that is none.
+// Columns col .. col + 7 of V of a token in the cache; zeros for a page that is none.
 template <int D>
-__device__ __forceinline__ uint4 ta_cached_v(const TaParams &p, int b, int g, int tok, int lane)
+__device__ __forceinline__ uint4 ta_cached_v(const TaParams &p, int b, int g, int tok, int col)
 {
     const int64_t page = p.table[(int64_t)b * p.max_blocks + (tok >> p.page_shift)];
     if (page < 1 || page >= p.num_pages)
@@ -836,7 +835,7 @@ __device__ __forceinline__ uint4 ta_cached_v(const TaParams &p, int b, int g, in
     const int64_t slot = tok & ((1 << p.page_shift) - 1);
     const int64_t at = p.layout == PKV_NHD ? (((page << p.page_shift) + slot) * p.num_kv_heads + g) * D
                                            : (((page * p.num_kv_heads + g) << p.page_shift) + slot) * D;
-    return *reinterpret_cast<const uint4 *>(p.v_cache + at + lane % (D / 8) * 8);
+    return *reinterpret_cast<const uint4 *>(p.v_cache + at + col);
 }
 
 // Adds to a node's O the infinities and NaN that the drafted tokens j0 .. j1 - 1
@@ -858,7 +857,7 @@ __device__ __noinline__ bool ta_add_nonfinite(const TaParams &p, int b, int len,
 #pragma unroll 1
         for (uint32_t keys = __reduce_or_sync(0xffffffffu, mine); keys != 0; keys &= keys - 1) {
             const int k = __ffs(keys) - 1;
-            const uint4 x = ta_cached_v<D>(p, b, g, len + first + k, lane);
+            const uint4 x = ta_cached_v<D>(p, b, g, len + first + k, lane % (D / 8) * 8);
             uint32_t w[4] = {x.x, x.y, x.z, x.w}, any = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -897,40 +896,60 @@ __device__ __noinline__ bool ta_add_nonfinite(const TaParams &p, int b, int len,
 // arrives as a NaN or an infinity of either sign; all that is certain is that
 // it is not finite.  The columns where it is not become the sum of the slice's
 // cached values there that are not finite, which is what the formula gives for
-// positive weights, the same for every node.  A whole warp, rare: it reads the
-// slice's V again, D / 8 lanes to a token.  Lanes with `mend` false change nothing.
+// positive weights, the same for every node.  A whole warp, rare: it reads such
+// columns of the slice's V again, 8 at a time, a token per lane.  64 uneven rows
+// with an infinity in one column of the longest take 0.41 ms a call for 0.15
+// (2.2 with all columns read), with a token that is NaN throughout 2.6.  Lanes
+// with `mend` false change nothing.
 template <int D>
 __device__ __noinline__ void ta_mend_cached(const TaParams &p, int b, int g, int tok0, int tok1, bool mend, uint32_t o_col,
                                             int lane)
 {
-    constexpr int kLanes = D / 8;
-    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int tok = tok0 + lane / kLanes; tok < tok1; tok += 32 / kLanes) {
-        const uint4 x = ta_cached_v<D>(p, b, g, tok, lane);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            sum[2 * e] += bf16_nonfinite(w[e]) ? __uint_as_float(w[e] << 16) : 0.f;
-            sum[2 * e + 1] += bf16_nonfinite(w[e] >> 16) ? __uint_as_float(w[e] & 0xffff0000u) : 0.f;
-        }
-    }
-    __syncwarp();
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        for (int o = kLanes; o < 32; o <<= 1)
-            sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], o);
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(o_col + c, o);
+        uint32_t odd = 0;
+        {
+            uint32_t o[32];
+            tmem_ld32(o_col + c, o);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float v = __shfl_sync(0xffffffffu, sum[i & 7], (c + i) >> 3);
-            if (mend && v != 0.f && (o[i] & 0x7f800000u) == 0x7f800000u)
-                o[i] = __float_as_uint(v);
+            for (int i = 0; i < 32; ++i)
+                odd |= mend && (o[i] & 0x7f800000u) == 0x7f800000u ? 1u << i : 0u;
         }
-        tmem_st32(o_col + c, o);
+        odd = __reduce_or_sync(0xffffffffu, odd);
+#pragma unroll 1
+        while (odd != 0) {
+            const int in = (__ffs(odd) - 1) & ~7, col = c + in;
+            odd &= ~(0xffu << in);
+            float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (int tok = tok0 + lane; tok < tok1; tok += 32) {
+                const uint4 x = ta_cached_v<D>(p, b, g, tok, col);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sum[2 * e] += bf16_nonfinite(w[e]) ? __uint_as_float(w[e] << 16) : 0.f;
+                    sum[2 * e + 1] += bf16_nonfinite(w[e] >> 16) ? __uint_as_float(w[e] & 0xffff0000u) : 0.f;
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1)
+                    sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], o);
+                uint32_t x;
+                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                             : "=r"(x)
+                             : "r"(o_col + col + e)
+                             : "memory");
+                x = mend && sum[e] != 0.f && (x & 0x7f800000u) == 0x7f800000u ? __float_as_uint(sum[e]) : x;
+                asm volatile(
+                    "tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(
+                        o_col + col + e),
+                    "r"(x)
+                    : "memory");
+            }
+        }
     }
 }
 
