@@ -453,8 +453,8 @@ PKV_API pkv_status pkv_mixed_attn(const pkv_cache_desc *desc, void *k_cache, voi
  * ring of num_pages - 1 page ids.  Pages are handed out from the ring's head
  * and come back at its tail: first in, first out.  After the init every page
  * is free and they are handed out in ascending order; a caller that wants
- * another order writes the ring itself.  pkv_device_pool_bytes returns 0 if
- * num_pages < 2.
+ * another order writes the ring itself.  num_pages is 2 .. 2^30 here and in
+ * pkv_table_update; pkv_device_pool_bytes returns 0 for others.
  */
 PKV_API size_t pkv_device_pool_bytes(int32_t num_pages);
 PKV_API pkv_status pkv_device_pool_init(void *pool, size_t pool_bytes, int32_t num_pages, void *stream);

@@ -38,6 +38,7 @@ constexpr int kTableThreads = 1024;
 constexpr int kTableMaxBatch = kTableThreads; // one row per thread
 constexpr int kTablePiece = 64;               // tokens a warp lays out at a time
 constexpr int kTableTokensPerCta = 256;
+constexpr int kTableMaxPages = 1 << 30; // ring indices and their sums are 32-bit
 
 struct TableParams {
     int32_t *pool;
@@ -304,12 +305,16 @@ extern "C" {
 
 size_t pkv_device_pool_bytes(int32_t num_pages)
 {
-    return num_pages < 2 ? 0 : ((size_t)num_pages - 1 + kPoolHeader) * 4;
+    return num_pages < 2 || num_pages > kTableMaxPages ? 0 : ((size_t)num_pages - 1 + kPoolHeader) * 4;
 }
 
 pkv_status pkv_device_pool_init(void *pool, size_t pool_bytes, int32_t num_pages, void *stream)
 {
-    if (pool == nullptr || num_pages < 2 || pool_bytes < pkv_device_pool_bytes(num_pages) || !aligned4(pool))
+    if (pool == nullptr || num_pages < 2 || !aligned4(pool))
+        return PKV_EINVAL;
+    if (num_pages > kTableMaxPages)
+        return PKV_EUNSUPPORTED;
+    if (pool_bytes < pkv_device_pool_bytes(num_pages))
         return PKV_EINVAL;
     const int cap = num_pages - 1;
     pool_init_kernel<<<(cap > kPoolHeader ? cap - 1 : kPoolHeader - 1) / 256 + 1, 256, 0,
@@ -325,7 +330,7 @@ pkv_status pkv_table_update(void *pool, int32_t num_pages, int32_t page_size, in
     if (num_pages < 2 || page_size < 1 || max_blocks < 1 || batch < 0 || max_tokens < 0)
         return PKV_EINVAL;
     if (page_size > 256 || (page_size & (page_size - 1)) != 0 || batch > kTableMaxBatch ||
-        num_pages > (1 << 30))
+        num_pages > kTableMaxPages)
         return PKV_EUNSUPPORTED;
     if (batch == 0)
         return PKV_OK;

@@ -116,6 +116,17 @@ def test_table_refusals():
     assert lib.pkv_device_pool_init(FAKE, 1 << 20, 1, None) == EINVAL
 
 
+def test_pools_past_32_bit_ring_indices_are_refused():
+    lib = _lib.load()
+    most = 1 << 30
+    assert lib.pkv_device_pool_bytes(most) == 4 * (16 + most - 1)
+    for pages in (most + 1, 2 ** 31 - 1):
+        assert lib.pkv_device_pool_bytes(pages) == 0
+        assert lib.pkv_device_pool_init(FAKE, 1 << 40, pages, None) == EUNSUPPORTED
+        assert lib.pkv_table_update(FAKE, pages, 16, FAKE, 4, FAKE, FAKE, FAKE, 2, None, None, None, 0, None,
+                                    None) == EUNSUPPORTED
+
+
 def test_the_binding_refuses_host_tensors_and_wrong_types():
     x = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError):
