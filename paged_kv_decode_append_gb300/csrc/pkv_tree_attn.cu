@@ -145,6 +145,7 @@ struct TaBars {
     uint8_t nonfinite[kSlices]; // bit w: of drafted tokens 32 w .. 32 w + 31, V of some holds an infinity or NaN
     uint32_t tmem_base;
     int32_t abort;
+    int32_t mending; // finishing warps that read a slice's values again
 };
 static_assert(sizeof(TaBars) <= 1024, "barrier block");
 
@@ -237,14 +238,16 @@ __device__ __forceinline__ int ta_cut(int64_t x, int blocks)
 
 __device__ __noinline__ bool ta_wait_slow(uint64_t *bar, uint32_t parity, TaBars &bars, int32_t *err_flag)
 {
-    const uint64_t start = globaltimer_ns();
-    volatile int32_t *abort = &bars.abort;
+    uint64_t start = globaltimer_ns();
+    volatile int32_t *abort = &bars.abort, *mending = &bars.mending;
     for (;;) {
         for (int i = 0; i < 64; ++i)
             if (mbar_try_wait(bar, parity))
                 return true;
         if (*abort != 0)
             return false;
+        if (*mending != 0) // a bounded loop over a slice, whose length has no bearing on the limit
+            start = globaltimer_ns();
         if (globaltimer_ns() - start > kWaitLimitNs) {
             *abort = 1;
             set_error(err_flag, PKV_ERR_TIMEOUT);
@@ -899,8 +902,10 @@ __device__ __noinline__ bool ta_add_nonfinite(const TaParams &p, int b, int len,
 // positive weights, the same for every node.  A whole warp, rare: it reads such
 // columns of the slice's V again, 8 at a time, a token per lane.  64 uneven rows
 // with an infinity in one column of the longest take 0.41 ms a call for 0.15
-// (2.2 with all columns read), with a token that is NaN throughout 2.6.  Lanes
-// with `mend` false change nothing.
+// (2.2 with all columns read), with a token that is NaN throughout 0.58 (2.6
+// without the look at columns that are NaN already).  Lanes with `mend` false
+// change nothing.
+constexpr int kMendTokens = 2048; // between looks at whether all 8 columns are NaN
 template <int D>
 __device__ __noinline__ void ta_mend_cached(const TaParams &p, int b, int g, int tok0, int tok1, bool mend, uint32_t o_col,
                                             int lane)
@@ -921,17 +926,25 @@ __device__ __noinline__ void ta_mend_cached(const TaParams &p, int b, int g, int
             const int in = (__ffs(odd) - 1) & ~7, col = c + in;
             odd &= ~(0xffu << in);
             float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            uint32_t nan = 0; // columns that are NaN already
+#pragma unroll 1
+            for (int64_t t0 = tok0; t0 < tok1 && nan != 0xffu; t0 += kMendTokens) {
+                const int end = (int)min(t0 + kMendTokens, (int64_t)tok1);
 #pragma unroll 4
-            for (int tok = tok0 + lane; tok < tok1; tok += 32) {
-                const uint4 x = ta_cached_v<D>(p, b, g, tok, col);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                for (int tok = (int)t0 + lane; tok < end; tok += 32) {
+                    const uint4 x = ta_cached_v<D>(p, b, g, tok, col);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sum[2 * e] += bf16_nonfinite(w[e]) ? __uint_as_float(w[e] << 16) : 0.f;
-                    sum[2 * e + 1] += bf16_nonfinite(w[e] >> 16) ? __uint_as_float(w[e] & 0xffff0000u) : 0.f;
+                    for (int e = 0; e < 4; ++e) {
+                        sum[2 * e] += bf16_nonfinite(w[e]) ? __uint_as_float(w[e] << 16) : 0.f;
+                        sum[2 * e + 1] += bf16_nonfinite(w[e] >> 16) ? __uint_as_float(w[e] & 0xffff0000u) : 0.f;
+                    }
                 }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    nan |= isnan(sum[e]) ? 1u << e : 0u;
+                nan = __reduce_or_sync(0xffffffffu, nan);
             }
-            __syncwarp();
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
 #pragma unroll
@@ -1204,8 +1217,13 @@ __device__ void ta_finish(const TaParams &p, TaBars &bars, uint32_t tmem, int wa
             // cached values first, while O shows where they are; not where the scores are NaN
             const bool mend = live && !zero && l < INFINITY && !(odd.x + odd.y == 0.f);
             bool changed = __any_sync(0xffffffffu, mend);
-            if (changed)
+            if (changed) {
+                if (lane == 0)
+                    atomicAdd(&bars.mending, 1);
                 ta_mend_cached<D>(p, s.b, s.g, s.tok0, min(s.tok1, s.len), mend, o_col, lane);
+                if (lane == 0)
+                    atomicSub(&bars.mending, 1);
+            }
             if (nonfinite != 0) {
                 if (p.pdl) // V is read from the cache again, where this call's append puts it
                     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1368,7 +1386,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             mbar_init(&bars.slice_empty[i], kReaders);
         }
         mbar_init(&bars.drain, 1);
-        bars.abort = 0;
+        bars.abort = bars.mending = 0;
         mbar_init_fence();
         prefetch_tensormap(&maps.k);
         prefetch_tensormap(&maps.v);

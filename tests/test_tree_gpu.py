@@ -264,6 +264,27 @@ def test_infinities_and_nan_of_cached_values(geom, L, far):
     assert torch.isposinf(out[:20, -G:, 0]).all() and torch.isfinite(out[20:23]).all()
 
 
+def test_infinities_of_a_very_long_row():
+    """Slices of millions of keys (on shared pages) whose values are all infinite:
+    reading them again takes longer than a wait in the kernel may."""
+    P, D, B = 256, 256, 152
+    case = wl.mixed_step(1500, [1] * B, [P] * B, 1, 1, D, P, wl.NHD, device=DEV)
+    blocks = 2 ** 22 // P
+    table = np.tile(case.block_table[:, :1], (1, blocks + 1)).astype(np.int32)
+    table[:, blocks] = case.block_table[:, 1]
+    case.v_cache.fill_(float("inf"))
+    case.v_cache[..., D // 2:] = float("-inf")
+    case.v_new.zero_()
+    kc, vc = case.k_cache.clone(), case.v_cache.clone()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lse = torch.zeros(B, 1, device=DEV)
+    out = pkv.pkv_tree_attn(kc, vc, case.q, case.k_new, case.v_new, i32(case.qo_indptr), i32(np.ones((B, 1))), i32(table),
+                            i32(np.full(B, 2 ** 22)), case.softmax_scale, 1, lse=lse, err_flag=err)
+    assert int(err.item()) == 0
+    assert torch.isposinf(out[:, 0, : D // 2]).all() and torch.isneginf(out[:, 0, D // 2:]).all()
+    assert torch.isfinite(lse).all()
+
+
 @pytest.mark.parametrize("L", [40, 9000, 30000])
 def test_nan_scores_stay_nan(L):
     """A node whose scores are NaN, all of them or those of a long run of keys,
