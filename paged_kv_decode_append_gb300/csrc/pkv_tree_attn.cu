@@ -402,17 +402,15 @@ template <int D> struct TaTiles {
     TaSlice s;
     int n;    // index of the slice
     int tok;  // first token of the tile
-    int gt;   // tiles before this one
 
     __device__ __forceinline__ void start()
     {
-        n = gt = -1;
+        n = -1;
         tok = s.tok1 = 0;
     }
     __device__ __forceinline__ bool next(const TaParams &p, TaBars &bars, int lane, bool done = true)
     {
         tok += TaCfg<D>::kTile;
-        ++gt;
         if (tok < s.tok1)
             return true;
         if (n >= 0 && done)
@@ -422,7 +420,6 @@ template <int D> struct TaTiles {
         return !(s.flags & kOver);
     }
     __device__ __forceinline__ bool first() const { return tok == s.tok0; }
-    __device__ __forceinline__ int tokens() const { return min(TaCfg<D>::kTile, s.tok1 - tok); }
 };
 
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z)
