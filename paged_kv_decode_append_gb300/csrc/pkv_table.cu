@@ -22,7 +22,9 @@
 // What bounds it.  A chain of dependent steps, not bytes: launch, the rows'
 // numbers, the scan, a ring entry, a table entry or slot, held_blocks.  A step
 // of 64 rows takes 4.9 us, of which the launch is 2; 1024 rows admitted at once,
-// 3.75 MB, 8.9 us.  Measured on the way: a scan for every sum and test and 4096
+// 3.75 MB, 8.8 us: 5.2 with neither pages nor lists (3.0 up to 256 rows: the scan
+// over 32 warps for 8, and CTAs of 1024 threads), 2 for the slots and positions,
+// 1.4 for the pages.  Measured on the way: a scan for every sum and test and 4096
 // tokens a CTA 10.8 and 17.2 us; blocks and tokens in the same warps, one after
 // the other, 6.8 and 9.6; a CTA per 2048, 1024, 512, 256 and 128 tokens 6.4,
 // 5.9, 5.1, 4.9 and 4.9 for the step, no difference for the other.  1024 threads

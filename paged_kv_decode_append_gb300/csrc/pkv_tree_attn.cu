@@ -15,13 +15,13 @@
 // With one row tile it waits for K, so memory it is; with more the MMA warp is
 // busy throughout (S 0.25, P V 0.53, the rest its waits, commits and the walk:
 // 0.1 us more in it is 0.1 us more a step, in the softmax half of that).  64
-// uneven rows of two tiles, 64 nodes x 4 heads, take 147 us = 620 TFLOP/s, the
-// tensor pipe active 55 % of the cycles (168 us with an election for every MMA
+// uneven rows of two tiles, 64 nodes x 4 heads, take 148 us = 615 TFLOP/s, the
+// tensor pipe active 54 % of the cycles (168 us with an election for every MMA
 // and a row's tiles in one CTA, 157 with one for four MMAs, 149 with the tiles
-// side by side).  Short calls are bound by latency: 32 rows of 512 .. 1024
-// tokens with trees of 16 nodes take 36 us, 3.1 TB/s, of which the start of the
-// CTAs is 4, the append 3, the tail and the combine kernel 6; one node over 64
-// tokens takes 11.2 us for its three kernels.
+// side by side, 147 with one barrier for P and V).  Short calls are bound by
+// latency: 32 rows of 512 .. 1024 tokens with trees of 16 nodes take 37 us, 3.0
+// TB/s, of which the start of the CTAs is 4, the append 3, the tail and the
+// combine kernel 6; one node over 64 tokens takes 11.8 us for its three kernels.
 //
 // The roles' code is kept short (one walk of the range, loops not unrolled
 // beyond 32 columns): at 120 KB a sixth of the instruction fetches missed the
@@ -32,12 +32,15 @@
 //    fixed cost of a unit, then its 64-token blocks) and every CTA takes an
 //    equal range, so a long row is shared by many CTAs.  Each CTA finds its
 //    range itself from the row arrays: no plan kernel, no host readback.
-//    Where rows may have more nodes than a tile holds (and kv heads are even in
-//    number), two CTAs go along the line side by side, one on the even, one on
-//    the odd units of a row: they read the same K/V at the same time, so HBM
-//    delivers it once.  With the tiles one after the other in a CTA, long rows'
-//    K/V have left the L2 in between: 64 uneven rows of two tiles took 157 us
-//    for 149 and read 805 MB from HBM for 465.
+//    Where rows may have more nodes than a tile holds, two CTAs go along the line
+//    side by side, one on the even, one on the odd units of a row: of a row of
+//    two tiles they read the same K/V at the same time, so HBM delivers it once.
+//    With the tiles one after the other in a CTA, long rows' K/V have left the L2
+//    in between: 64 uneven rows of two tiles took 157 us for 149 and read 805 MB
+//    from HBM for 465.  It takes an even number of units in every row, whatever
+//    its tiles, and so an even number of kv heads; with an odd one the tiles go
+//    one after the other, and rows of four tiles go as two such pairs (neither
+//    has been measured).
 //  - A unit inside one CTA's range is finished there.  The others leave (ref, l)
 //    and O in the workspace, fp32, and a second kernel joins them in range
 //    order (results do not depend on timing).  A CTA has at most two such
@@ -50,8 +53,8 @@
 //    finish slices, so that the softmax goes on with the next one meanwhile.
 //    While the softmax is at tile t the tensor pipe runs S of tile t + 1 and P V
 //    of tile t - 1.
-//  - The running maximum m moves only when a score exceeds it by more than 2^8
-//    (then O is rescaled).  The weights are taken as 2^(s - ref), ref = m + 8 +
+//  - The running maximum m moves only when a score exceeds it by more than 8, a
+//    factor 2^8 (then O is rescaled).  The weights are taken as 2^(s - ref), ref = m + 8 +
 //    slack with slack = 1 + ceil(log2 of the row's keys): none is above
 //    2^-slack and they sum to at most 1/2, so values at the end of bf16 cannot
 //    overflow O before the division.  What that costs is at the other end:
@@ -65,7 +68,8 @@
 //    for the MMA (0 * inf would reach nodes that do not see it) and added in
 //    the epilogue to the nodes that do.  Cached tokens are seen by all: there
 //    the finishing warps look at O, and where it is not finite they put the sum
-//    of the values that are not (ta_mend_cached).
+//    of the values that are not (ta_mend_cached).  The look costs 0.4 us of one
+//    node's 11.8, 0.8 of 37 and 1.6 of 148.
 //  - Cutting the line: kStartCost 1 .. 4 and kMinRange 4 .. 16 were measured on
 //    short, long, even and uneven batches: nothing better than 2 and 6 (a
 //    minimum that grows with the rows in use: head_dim 256 43 -> 55 us).
