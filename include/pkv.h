@@ -87,6 +87,7 @@ typedef enum {
                               plan: outputs and appends are unspecified) */
 #define PKV_ERR_POOL 32    /* pkv_table_update: too few free pages for a row, or a pool whose
                               header is not one */
+#define PKV_ERR_MOVE 128   /* pkv_evict_apply: a move outside its row, or more of them than there is room for */
 #define PKV_ERR_TREE 64    /* a drafted tree whose parents are not earlier nodes, or an accepted
                               path that does not rise */
 
@@ -623,6 +624,204 @@ PKV_API pkv_status pkv_tree_commit(const pkv_cache_desc *desc, int32_t num_layer
                                    void *const *v_caches, const int32_t *path, int32_t max_path,
                                    const int32_t *path_len, const int32_t *block_table, int32_t max_blocks,
                                    const int32_t *cache_seqlens, int32_t batch, int32_t *err_flag, void *stream);
+
+/* ---------------------------------------------------------------------
+ * Rotary positions.  Pair i of a head's first rot_dim values, (x, y), is turned
+ * by the angle t = 2 pi f_i pos and scaled: (a (x cos t - y sin t), a (y cos t +
+ * x sin t)); the other values are copied.  f_i is given in turns per token as a
+ * 64-bit fraction (units of 2^-64), so that far positions keep their angles.
+ * Positions are the tokens' own, not their slots: after an eviction
+ * (pkv_evict_apply) a slot's number says no longer when its token came.
+ * Source: "mini-infer系统实战-06 True PagedAttention", section 4 (the caller
+ * rotates q and k before the paged attention; the cache holds rotated keys).
+ * --------------------------------------------------------------------- */
+
+typedef enum {
+    PKV_ROPE_HALF = 0,       /* pair i: values i and i + rot_dim / 2 */
+    PKV_ROPE_INTERLEAVED = 1 /* pair i: values 2 i and 2 i + 1 */
+} pkv_rope_pairing;
+
+/* How frequencies are stretched for contexts longer than orig_len.  With g_i =
+ * base^(-2 i / rot_dim) radians per token:
+ *   PLAIN   g_i
+ *   LINEAR  g_i / factor
+ *   NTK     (base factor^(rot_dim / (rot_dim - 2)))^(-2 i / rot_dim)
+ *   PARTS   g_i where a pair makes at least `high` turns over orig_len tokens,
+ *           g_i / factor where at most `low`, a ramp over the pairs between
+ *           (from floor of the first pair to ceil of the last); attn_factor is
+ *           0.1 ln(factor) + 1
+ *   TURNS   the same with a ramp over the number of turns, and attn_factor 1 */
+typedef enum {
+    PKV_ROPE_PLAIN = 0,
+    PKV_ROPE_LINEAR = 1,
+    PKV_ROPE_NTK = 2,
+    PKV_ROPE_PARTS = 3,
+    PKV_ROPE_TURNS = 4
+} pkv_rope_scaling;
+
+/*
+ * pkv_rope_freqs -- the rot_dim / 2 frequencies f_i, on the host (the caller
+ * copies them to the device once), and the factor a of the rotated part
+ * (attn_factor, or NULL).  base > 1; factor >= 1 except for PLAIN; 0 < low < high
+ * and orig_len > 0 for PARTS and TURNS (ignored otherwise).
+ */
+PKV_API pkv_status pkv_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, double low,
+                                  double high, double orig_len, uint64_t *freqs, float *attn_factor);
+
+/*
+ * pkv_rope -- rotates queries and keys.
+ *  q, q_out          device bf16 [num_tokens, num_q_heads, head_dim], or both
+ *                    NULL; q_out may be q.
+ *  k, k_out          device bf16 [num_tokens, num_kv_heads, head_dim], or both
+ *                    NULL; k_out may be k.
+ *  positions         device int32 [num_tokens].
+ *  head_dim          64, 128 or 256; rot_dim a multiple of 16, at most head_dim.
+ *  freqs             device uint64 [rot_dim / 2].
+ *  attn_factor       a (finite).
+ * Computed in fp32 and rounded to bf16 once.  One kernel.
+ */
+PKV_API pkv_status pkv_rope(const void *q, const void *k, const int32_t *positions, int32_t num_tokens,
+                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, const uint64_t *freqs,
+                            int32_t rot_dim, int32_t pairing, float attn_factor, void *q_out, void *k_out,
+                            void *stream);
+
+/*
+ * pkv_rope_append -- pkv_append of rotated keys, and the rotation of the same
+ * tokens' queries: the arguments of pkv_append (k_new not yet rotated) and of
+ * pkv_rope.
+ *  q, q_out          device bf16 [num_tokens, num_q_heads, head_dim], or both
+ *                    NULL; q_out may be q.
+ *  positions         device int32 [num_tokens], or NULL: token i of row b is at
+ *                    cache_seqlens[b] + i + evicted[b].
+ *  evicted           device int32 [batch]: tokens that left the row's cache, or
+ *                    NULL for none (not read with positions).
+ * A row whose written pages or length fail (PKV_ERR_PAGE, PKV_ERR_OVERFLOW)
+ * appends nothing; its queries are rotated all the same.  Tokens of an inactive
+ * row, and tokens that no row owns, are left alone: nothing is appended and
+ * their q_out stays as it was.  One kernel.
+ */
+PKV_API pkv_status pkv_rope_append(const pkv_cache_desc *desc, void *k_cache, void *v_cache, const void *q,
+                                   const void *k_new, const void *v_new, int32_t num_tokens,
+                                   const int32_t *append_indptr, const int32_t *positions, const int32_t *evicted,
+                                   const uint64_t *freqs, int32_t rot_dim, int32_t pairing, float attn_factor,
+                                   const int32_t *block_table, int32_t max_blocks, const int32_t *cache_seqlens,
+                                   int32_t batch, int32_t num_q_heads, void *q_out, int32_t *err_flag, void *stream);
+
+/* ---------------------------------------------------------------------
+ * A row's cache kept inside a budget of slots by accumulated attention weight.
+ * A step: attention (which gives lse), pkv_attn_mass in every layer, then for
+ * all layers at once pkv_evict_plan and pkv_evict_apply, and pkv_table_update
+ * with no new tokens, which returns the pages behind the rows' new ends.
+ * Every (layer, row, kv head) keeps its own tokens, as many as the row's budget
+ * says.  The state of a layer is a score and a position per slot: mass fp32 and
+ * slot_pos int32, both [batch, num_kv_heads, slots].  Attention does not depend
+ * on the order of the cached tokens, so a cache that was cut down goes on to be
+ * used by every call here; only causal masks among tokens of one call look at
+ * slots, and those tokens are always the last.
+ * Source: "flex_attention + paged KV + CUDA graphs vs vLLM", "What each option
+ * did" (a page pool of fixed size reserved up front); "mini-infer系统实战-06 True
+ * PagedAttention", section 8 (what a pool of pages holds).
+ * --------------------------------------------------------------------- */
+
+/*
+ * pkv_mass_workspace_size -- bytes of device workspace pkv_attn_mass needs (0
+ * on invalid or unsupported arguments).  Like the decode workspace it must be
+ * zero-filled once before its first use; every completed call leaves it ready
+ * for the next (zero it again after PKV_ERR_TIMEOUT).  Calls that share a
+ * workspace must not run concurrently.
+ */
+PKV_API size_t pkv_mass_workspace_size(int32_t batch, int32_t total_q, int32_t max_blocks, int32_t num_q_heads,
+                                       const pkv_cache_desc *desc);
+
+/*
+ * pkv_attn_mass -- mass[b, g, t] += the sum of exp(softmax_scale q.k_t - lse)
+ * over the queries of row b that see slot t (end aligned: query i sees slots 0
+ * .. L_b + i) and the query heads of kv head g.
+ *  k_cache           device bf16 pool, the row's new tokens included (they were
+ *                    appended by the attention call or before).
+ *  q                 device bf16 [total_q, num_q_heads, head_dim], as the
+ *                    attention got it.
+ *  qo_indptr         device int32 [batch + 1], or NULL for one query per row
+ *                    (total_q = batch).
+ *  lse               device fp32 [total_q, num_q_heads], as the attention call
+ *                    wrote it; a query whose lse is -inf (it saw nothing) gives
+ *                    nothing.
+ *  cache_seqlens     device int32 [batch]: L_b, the length BEFORE this step's
+ *                    tokens; the row holds L_b + q_b keys.
+ *  fresh_from        device int32 [batch], or NULL for cache_seqlens: slots from
+ *                    there on are new, their mass is set and not added to, and
+ *                    their slot_pos becomes slot + evicted[b].  (A prompt whose
+ *                    last queries alone are scored: 0.)
+ *  evicted           device int32 [batch], or NULL for 0.
+ *  mass, slot_pos    device [batch, num_kv_heads, slots]; slot_pos may be NULL.
+ *                    Slots at and past L_b + q_b stay as they are.
+ *  batch             0 .. 1024; total_q * num_q_heads < 2^31; at most 128 query
+ *                    heads per kv head; page_size at least 8.
+ * Weights and sums are fp32; results do not depend on timing.  Rows that are
+ * inactive or bring no query stay as they are; so do rows with a range outside
+ * [0, total_q) (PKV_ERR_QLEN) and rows whose keys exceed max_blocks *
+ * page_size or slots (PKV_ERR_OVERFLOW).  Slots on a page outside [1,
+ * num_pages) stay as they are (PKV_ERR_PAGE).
+ */
+PKV_API pkv_status pkv_attn_mass(const pkv_cache_desc *desc, const void *k_cache, const void *q,
+                                 const int32_t *qo_indptr, const float *lse, const int32_t *block_table,
+                                 int32_t max_blocks, const int32_t *cache_seqlens, int32_t batch,
+                                 int32_t num_q_heads, int32_t total_q, float softmax_scale,
+                                 const int32_t *fresh_from, const int32_t *evicted, float *mass, int32_t *slot_pos,
+                                 int32_t slots, void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                                 void *stream);
+
+/*
+ * pkv_evict_plan -- which of a row's L_b = cache_seqlens[b] slots stay, for
+ * every layer and kv head, and the moves that bring them to the front.  A row
+ * keeps n_b = min(L_b, budgets[b]) slots (all, with a negative budget): first
+ * those whose position is among the row's newest `recent` ones (slot_pos >= L_b +
+ * evicted[b] - recent) or below `sink`, then by mass (NaN below all); among
+ * equals the lowest slot.
+ *  mass, slot_pos    device [num_layers, batch, num_kv_heads, slots], read only.
+ *  cache_seqlens, evicted, budgets  device int32 [batch]; evicted may be NULL.
+ *  moves             device int32 [num_layers, batch, num_kv_heads, max_moves,
+ *                    2]: (from, to), both rising: the i-th slot that stays at or
+ *                    behind n_b goes to the i-th hole before it.  Entries behind
+ *                    the last move stay as they were.
+ *  num_moves         device int32 [num_layers, batch, num_kv_heads].
+ *  row_lens          device int32 [batch, 2]: L_b and n_b.
+ * A row that is inactive keeps its length.  So does one with L_b > slots, or
+ * that may need more than max_moves moves (min(n_b, L_b - n_b)), and sets
+ * PKV_ERR_OVERFLOW.  slots is at most 2^19.  One kernel.
+ */
+PKV_API pkv_status pkv_evict_plan(const float *mass, const int32_t *slot_pos, int32_t num_layers, int32_t batch,
+                                  int32_t num_kv_heads, int32_t slots, const int32_t *cache_seqlens,
+                                  const int32_t *evicted, const int32_t *budgets, int32_t sink, int32_t recent,
+                                  int32_t *moves, int32_t max_moves, int32_t *num_moves, int32_t *row_lens,
+                                  int32_t *err_flag, void *stream);
+
+/*
+ * pkv_evict_apply -- carries a plan out in num_layers pools that share one
+ * block table: K, V, mass and slot_pos of every move (bit copies), then the
+ * rows' lengths.
+ *  k_caches, v_caches  host arrays of num_layers (1 .. 128) device pools, all
+ *                    distinct.
+ *  moves, num_moves, row_lens  as pkv_evict_plan writes them.
+ *  mass, slot_pos    device [num_layers, batch, num_kv_heads, slots], each may
+ *                    be NULL.
+ *  cache_seqlens     device int32 [batch], set to n_b; or NULL (layers of one
+ *                    plan in several calls: all but one of them).
+ *  evicted           device int32 [batch], increased by the slots that went; or
+ *                    NULL.  Needs cache_seqlens.
+ * Carrying out a plan twice changes nothing.  A row with a page outside [1,
+ * num_pages) among those of its L_b slots (PKV_ERR_PAGE), more of them than
+ * max_blocks * page_size or slots (PKV_ERR_OVERFLOW), or lengths that do not
+ * fall (PKV_ERR_MOVE) stays as it is.  A (layer, row, kv head) whose num_moves is
+ * outside [0, max_moves], and a move that does not lead from [n_b, L_b) to [0,
+ * n_b), is left out (PKV_ERR_MOVE).  One kernel.
+ */
+PKV_API pkv_status pkv_evict_apply(const pkv_cache_desc *desc, int32_t num_layers, void *const *k_caches,
+                                   void *const *v_caches, const int32_t *moves, int32_t max_moves,
+                                   const int32_t *num_moves, const int32_t *row_lens, const int32_t *block_table,
+                                   int32_t max_blocks, float *mass, int32_t *slot_pos, int32_t slots,
+                                   int32_t *cache_seqlens, int32_t *evicted, int32_t batch, int32_t *err_flag,
+                                   void *stream);
 
 /* ---------------------------------------------------------------------
  * Host page-pool and block-table helpers (no device memory involved).

@@ -7,6 +7,8 @@ binding (``api``) and the seeded synthetic workload generators
 """
 from .api import (  # noqa: F401
     HND,
+    ROPE_HALF,
+    ROPE_INTERLEAVED,
     DecodeStep,
     LayerCaches,
     NHD,
@@ -16,16 +18,23 @@ from .api import (  # noqa: F401
     decode_workspace,
     device_pool,
     default_decode_max_qlen,
+    mass_workspace,
     mixed_workspace,
     pkv_append,
+    pkv_attn_mass,
     pkv_decode_bucket,
     pkv_decode_attn,
     pkv_decode_workspace_size,
+    pkv_evict_apply,
+    pkv_evict_plan,
+    pkv_mass_workspace_size,
     pkv_mixed_attn,
     pkv_mixed_workspace_size,
     pkv_pool_bytes,
     pkv_prefill_attn,
     pkv_prefill_workspace_size,
+    pkv_rope,
+    pkv_rope_append,
     pkv_table_update,
     pkv_tree_accept,
     pkv_tree_attn,
@@ -34,5 +43,6 @@ from .api import (  # noqa: F401
     pkv_tree_workspace_size,
     prefill_workspace,
     pkv_validate_host,
+    rope_freqs,
     tree_workspace,
 )

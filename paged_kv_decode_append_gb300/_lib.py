@@ -15,6 +15,7 @@ P = ctypes.c_void_p
 I32 = ctypes.c_int32
 I32P = ctypes.POINTER(ctypes.c_int32)
 SIZE = ctypes.c_size_t
+F64 = ctypes.c_double
 
 
 class CacheDesc(ctypes.Structure):
@@ -58,6 +59,16 @@ SIGNATURES = {
                             SIZE, P, P]),
     "pkv_tree_accept": (I32, [P, P, P, P, P, P, I32, I32, I32, P, I32, P, P, P, P, P]),
     "pkv_tree_commit": (I32, [DESC_P, I32, P, P, P, I32, P, P, I32, P, I32, P, P]),
+    "pkv_rope_freqs": (I32, [I32, F64, I32, F64, F64, F64, F64, ctypes.POINTER(ctypes.c_uint64),
+                             ctypes.POINTER(ctypes.c_float)]),
+    "pkv_rope": (I32, [P, P, P, I32, I32, I32, I32, P, I32, I32, ctypes.c_float, P, P, P]),
+    "pkv_rope_append": (I32, [DESC_P, P, P, P, P, P, I32, P, P, P, P, I32, I32, ctypes.c_float, P, I32, P, I32, I32, P, P,
+                              P]),
+    "pkv_mass_workspace_size": (SIZE, [I32, I32, I32, I32, DESC_P]),
+    "pkv_attn_mass": (I32, [DESC_P, P, P, P, P, P, I32, P, I32, I32, I32, ctypes.c_float, P, P, P, P, I32, P, SIZE, P,
+                            P]),
+    "pkv_evict_plan": (I32, [P, P, I32, I32, I32, I32, P, P, P, I32, I32, P, I32, P, P, P, P]),
+    "pkv_evict_apply": (I32, [DESC_P, I32, P, P, P, I32, P, P, P, I32, P, P, I32, P, P, I32, P, P]),
     "pkv_pool_create": (P, [I32]),
     "pkv_pool_destroy": (None, [P]),
     "pkv_pool_alloc": (I32, [P, I32, I32P]),

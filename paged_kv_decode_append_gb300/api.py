@@ -21,7 +21,9 @@ DECODE_OVERLAP_PROLOGUE = 1  # pkv_decode_attn_ex flags (see include/pkv.h)
 DECODE_EARLY_KV = 2
 DECODE_MAKE_PLAN = 4
 DECODE_USE_PLAN = 8
-ERR_PAGE, ERR_OVERFLOW, ERR_TIMEOUT, ERR_QLEN, ERR_PLAN, ERR_POOL, ERR_TREE = 1, 2, 4, 8, 16, 32, 64
+ERR_PAGE, ERR_OVERFLOW, ERR_TIMEOUT, ERR_QLEN, ERR_PLAN, ERR_POOL, ERR_TREE, ERR_MOVE = 1, 2, 4, 8, 16, 32, 64, 128
+ROPE_HALF, ROPE_INTERLEAVED = range(2)
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "parts": 3, "turns": 4}
 
 
 class PkvError(RuntimeError):
@@ -498,6 +500,160 @@ def pkv_tree_commit(layers: LayerCaches, path, path_len, block_table, cache_seql
         _at(dev, "err_flag", err_flag, _I32), _stream_of(dev))
     if st:
         _check(st, "pkv_tree_commit")
+
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0, low: float = 1.0,
+               high: float = 32.0, orig_len: float = 0.0, device="cuda"):
+    """Frequencies of ``rot_dim / 2`` pairs for :func:`pkv_rope` (int64, turns
+    per token in units of 2^-64) and the factor of the rotated part
+    (``pkv_rope_freqs``; ``scaling`` one of ``ROPE_SCALINGS``)."""
+    freqs = np.zeros(max(rot_dim // 2, 1), np.uint64)
+    attn_factor = ctypes.c_float()
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling: one of {sorted(ROPE_SCALINGS)}")
+    _check(_lib.load().pkv_rope_freqs(rot_dim, base, ROPE_SCALINGS[scaling], factor, low, high, orig_len,
+                                      freqs.ctypes.data_as(ctypes.POINTER(ctypes.c_uint64)),
+                                      ctypes.byref(attn_factor)), "pkv_rope_freqs")
+    return torch.from_numpy(freqs.view(np.int64)).to(device), attn_factor.value
+
+
+def pkv_rope(q, k, positions, freqs, pairing: int = ROPE_HALF, attn_factor: float = 1.0, q_out=None, k_out=None):
+    """Rotates ``q`` ``[T, Hq, D]`` and ``k`` ``[T, Hkv, D]`` (either may be
+    None) by ``positions`` ``[T]``: the first ``2 * freqs.numel()`` values of
+    every head.  Returns ``(q_out, k_out)``, which may be the inputs."""
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("q or k")
+    dev = _device_of(some, "q" if q is not None else "k")
+    T, _, D = some.shape
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q)
+    if k is not None and k_out is None:
+        k_out = torch.empty_like(k)
+    Hq, Hk = (0 if t is None else t.size(1) for t in (q, k))
+    st = _lib.load().pkv_rope(
+        _at(dev, "q", q, _BF16, T, Hq, D), _at(dev, "k", k, _BF16, T, Hk, D), _at(dev, "positions", positions, _I32, T), T,
+        Hq, Hk, D, _at(dev, "freqs", freqs, _I64), 2 * freqs.numel(), pairing, attn_factor,
+        _at(dev, "q_out", q_out, _BF16, T, Hq, D), _at(dev, "k_out", k_out, _BF16, T, Hk, D), _stream_of(dev))
+    if st:
+        _check(st, "pkv_rope")
+    return q_out, k_out
+
+
+def pkv_rope_append(k_cache, v_cache, q, k_new, v_new, block_table, cache_seqlens, freqs, pairing: int = ROPE_HALF,
+                    attn_factor: float = 1.0, append_indptr=None, positions=None, evicted=None, q_out=None,
+                    err_flag=None, layout: int = NHD):
+    """:func:`pkv_append` of rotated ``k_new`` and the rotation of the same
+    tokens' ``q`` (or None), in one pass.  Token i of row b is at position
+    ``cache_seqlens[b] + i + evicted[b]`` unless ``positions`` ``[T]`` says
+    otherwise.  Returns ``q_out``, which may be ``q``."""
+    dev = _device_of(k_new, "k_new")
+    desc = cache_desc(k_cache, layout)
+    T, B, width = k_new.size(0), cache_seqlens.numel(), block_table.size(-1)
+    K, D = desc.num_kv_heads, desc.head_dim
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q)
+    Hq = 0 if q is None else q.size(1)
+    st = _lib.load().pkv_rope_append(
+        ctypes.byref(desc), _at(dev, "k_cache", k_cache, _BF16), _at(dev, "v_cache", v_cache, _BF16, *k_cache.shape),
+        _at(dev, "q", q, _BF16, T, Hq, D), _at(dev, "k_new", k_new, _BF16, T, K, D), _at(dev, "v_new", v_new, _BF16, T, K, D),
+        T, _at(dev, "append_indptr", append_indptr, _I32, B + 1), _at(dev, "positions", positions, _I32, T),
+        _at(dev, "evicted", evicted, _I32, B), _at(dev, "freqs", freqs, _I64), 2 * freqs.numel(), pairing, attn_factor,
+        _at(dev, "block_table", block_table, _I32, B, width), width, _at(dev, "cache_seqlens", cache_seqlens, _I32, B), B,
+        Hq, _at(dev, "q_out", q_out, _BF16, T, Hq, D), _at(dev, "err_flag", err_flag, _I32), _stream_of(dev))
+    if st:
+        _check(st, "pkv_rope_append")
+    return q_out
+
+
+def pkv_mass_workspace_size(batch: int, total_q: int, max_blocks: int, num_q_heads: int, desc: CacheDesc) -> int:
+    return int(_lib.load().pkv_mass_workspace_size(batch, total_q, max_blocks, num_q_heads, ctypes.byref(desc)))
+
+
+def mass_workspace(batch: int, total_q: int, max_blocks: int, num_q_heads: int, desc: CacheDesc,
+                   device) -> torch.Tensor:
+    """A zero-filled workspace for pkv_attn_mass (reusable across calls)."""
+    n = pkv_mass_workspace_size(batch, total_q, max_blocks, num_q_heads, desc)
+    if n == 0:
+        raise PkvError(EUNSUPPORTED, "pkv_mass_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def pkv_attn_mass(k_cache, q, lse, block_table, cache_seqlens, softmax_scale: float, mass, qo_indptr=None,
+                  fresh_from=None, evicted=None, slot_pos=None, workspace=None, err_flag=None,
+                  layout: int = NHD) -> None:
+    """Adds to ``mass`` ``[B, Hkv, slots]`` the attention weights that a step's
+    queries ``q`` ``[total_q, Hq, D]`` with log-sum-exps ``lse`` give to every
+    cached token.  ``cache_seqlens`` are the lengths before the step's tokens;
+    slots from ``fresh_from[b]`` (``cache_seqlens[b]``) on are set, and their
+    ``slot_pos`` becomes ``slot + evicted[b]``."""
+    dev = _device_of(q, "q")
+    desc = cache_desc(k_cache, layout)
+    T, Hq, D = q.shape
+    B, width = block_table.shape
+    slots = mass.size(-1)
+    if workspace is None:
+        workspace = mass_workspace(B, T, width, Hq, desc, q.device)
+    if D != desc.head_dim:
+        raise ValueError("q: head_dim differs from the cache's")
+    K = desc.num_kv_heads
+    st = _lib.load().pkv_attn_mass(
+        ctypes.byref(desc), _at(dev, "k_cache", k_cache, _BF16), _at(dev, "q", q, _BF16),
+        _at(dev, "qo_indptr", qo_indptr, _I32, B + 1), _at(dev, "lse", lse, _F32, T, Hq),
+        _at(dev, "block_table", block_table, _I32), width, _at(dev, "cache_seqlens", cache_seqlens, _I32, B), B, Hq, T,
+        softmax_scale, _at(dev, "fresh_from", fresh_from, _I32, B), _at(dev, "evicted", evicted, _I32, B),
+        _at(dev, "mass", mass, _F32, B, K, slots), _at(dev, "slot_pos", slot_pos, _I32, B, K, slots), slots,
+        _at(dev, "workspace", workspace, _U8), workspace.numel(), _at(dev, "err_flag", err_flag, _I32), _stream_of(dev))
+    if st:
+        _check(st, "pkv_attn_mass")
+
+
+def pkv_evict_plan(mass, slot_pos, cache_seqlens, evicted, budgets, sink: int, recent: int, moves=None, num_moves=None,
+                   row_lens=None, err_flag=None):
+    """Which slots every (layer, row, kv head) keeps of ``mass`` ``[layers, B,
+    Hkv, slots]``, at most ``budgets[b]``, and the moves that fill the holes in
+    front.  Returns ``(moves [layers, B, Hkv, max_moves, 2], num_moves, row_lens
+    [B, 2])``."""
+    dev = _device_of(mass, "mass")
+    layers, B, K, slots = mass.shape
+    if moves is None:
+        moves = torch.empty(layers, B, K, max(1, slots // 2), 2, dtype=torch.int32, device=mass.device)
+    if num_moves is None:
+        num_moves = torch.empty(layers, B, K, dtype=torch.int32, device=mass.device)
+    if row_lens is None:
+        row_lens = torch.empty(B, 2, dtype=torch.int32, device=mass.device)
+    width = moves.size(-2)
+    st = _lib.load().pkv_evict_plan(
+        _at(dev, "mass", mass, _F32), _at(dev, "slot_pos", slot_pos, _I32, layers, B, K, slots), layers, B, K, slots,
+        _at(dev, "cache_seqlens", cache_seqlens, _I32, B), _at(dev, "evicted", evicted, _I32, B),
+        _at(dev, "budgets", budgets, _I32, B), sink, recent, _at(dev, "moves", moves, _I32, layers, B, K, width, 2), width,
+        _at(dev, "num_moves", num_moves, _I32, layers, B, K), _at(dev, "row_lens", row_lens, _I32, B, 2),
+        _at(dev, "err_flag", err_flag, _I32), _stream_of(dev))
+    if st:
+        _check(st, "pkv_evict_plan")
+    return moves, num_moves, row_lens
+
+
+def pkv_evict_apply(layers: LayerCaches, moves, num_moves, row_lens, block_table, cache_seqlens, evicted, mass=None,
+                    slot_pos=None, err_flag=None) -> None:
+    """Carries a plan out: K, V, ``mass`` and ``slot_pos`` of every move in
+    every layer, then ``cache_seqlens`` and ``evicted`` (either may be None)."""
+    dev = _device_of(moves, "moves")
+    if dev != layers.device:
+        raise ValueError("moves and caches on different devices")
+    B, width = block_table.shape
+    n, K, most = layers.num_layers, layers.desc.num_kv_heads, moves.size(-2)
+    state = mass if mass is not None else slot_pos
+    slots = 1 if state is None else state.size(-1)
+    st = _lib.load().pkv_evict_apply(
+        ctypes.byref(layers.desc), n, layers.k_ptrs, layers.v_ptrs, _at(dev, "moves", moves, _I32, n, B, K, most, 2), most,
+        _at(dev, "num_moves", num_moves, _I32, n, B, K), _at(dev, "row_lens", row_lens, _I32, B, 2),
+        _at(dev, "block_table", block_table, _I32), width, _at(dev, "mass", mass, _F32, n, B, K, slots),
+        _at(dev, "slot_pos", slot_pos, _I32, n, B, K, slots), slots,
+        _at(dev, "cache_seqlens", cache_seqlens, _I32, B), _at(dev, "evicted", evicted, _I32, B), B,
+        _at(dev, "err_flag", err_flag, _I32), _stream_of(dev))
+    if st:
+        _check(st, "pkv_evict_apply")
 
 
 def pkv_pool_bytes(desc: CacheDesc) -> int:

@@ -268,4 +268,19 @@ bool encode_tree_maps(const pkv_cache_desc &desc, const void *k_cache, const voi
                       int num_q_heads, int total_q, int group, int box_nodes, CUtensorMap *k, CUtensorMap *v,
                       CUtensorMap *qm);
 
+// ------------------------------------------------------- scores and eviction
+
+constexpr int kEvictMaxSlots = 1 << 19; // slots of a row of scores
+constexpr int kMaxMassBatch = 1024;
+constexpr int kMassMaxKeys = 0x7fffff00; // keys of a row (token arithmetic is 32-bit)
+
+struct MassShape {
+    int group; // num_q_heads / num_kv_heads
+    size_t bytes;
+};
+
+// Every size check of pkv_attn_mass; fills `s` on PKV_OK.
+pkv_status mass_shape(int batch, int total_q, int max_blocks, int num_q_heads, const pkv_cache_desc *desc,
+                      MassShape *s);
+
 } // namespace pkv
