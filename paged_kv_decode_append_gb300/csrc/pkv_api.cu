@@ -155,6 +155,21 @@ CUresult encode_group_map(CUtensorMap *map, const pkv_cache_desc &d, void *base,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+CUresult encode_q_map(CUtensorMap *map, const void *q, int head_dim, int num_q_heads, int total_q, int box_heads,
+                      int box_tokens)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr)
+        return CUDA_ERROR_NOT_FOUND;
+    const cuuint64_t D = (cuuint64_t)head_dim;
+    const cuuint64_t dims[3] = {D, (cuuint64_t)num_q_heads, (cuuint64_t)total_q};
+    const cuuint64_t strides[2] = {D * 2, D * 2 * (cuuint64_t)num_q_heads};
+    const cuuint32_t boxes[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens}, ones[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, boxes, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 bool encode_decode_maps(const pkv_cache_desc &desc, void *k_cache, void *v_cache, DecodeMaps *maps)
 {
     const int box = decode_box_tokens(desc.page_size);
@@ -181,13 +196,7 @@ bool encode_tree_maps(const pkv_cache_desc &desc, const void *k_cache, const voi
     if (encode_group_map(k, desc, const_cast<void *>(k_cache), box) != CUDA_SUCCESS ||
         encode_group_map(v, desc, const_cast<void *>(v_cache), box) != CUDA_SUCCESS)
         return false;
-    const cuuint64_t D = (cuuint64_t)desc.head_dim;
-    const cuuint64_t dims[3] = {D, (cuuint64_t)num_q_heads, (cuuint64_t)total_q};
-    const cuuint64_t strides[2] = {D * 2, D * 2 * (cuuint64_t)num_q_heads};
-    const cuuint32_t boxes[3] = {64, (cuuint32_t)group, (cuuint32_t)box_nodes}, ones[3] = {1, 1, 1};
-    return tensor_map_encoder()(qm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, boxes,
-                                ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_q_map(qm, q, desc.head_dim, num_q_heads, total_q, group, box_nodes) == CUDA_SUCCESS;
 }
 
 // Static split of a mixed step: the decode kernel's multi-query shape, and

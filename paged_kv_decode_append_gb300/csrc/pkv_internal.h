@@ -156,6 +156,11 @@ CUresult encode_pool_map(CUtensorMap *map, const pkv_cache_desc &d, void *base, 
 // box_blocks: 64-column blocks per box (0: all of head_dim).
 CUresult encode_group_map(CUtensorMap *map, const pkv_cache_desc &d, void *base, int box_tokens, int box_blocks = 0);
 
+// Tensor map over q [total_q, num_q_heads, head_dim] with boxes of box_tokens
+// tokens x box_heads heads x 64 columns (128-byte swizzle).
+CUresult encode_q_map(CUtensorMap *map, const void *q, int head_dim, int num_q_heads, int total_q, int box_heads,
+                      int box_tokens);
+
 int sm_count(int device);
 
 // Geometry checks shared by every entry point.
@@ -275,7 +280,11 @@ constexpr int kMaxMassBatch = 1024;
 constexpr int kMassMaxKeys = 0x7fffff00; // keys of a row (token arithmetic is 32-bit)
 
 struct MassShape {
-    int group; // num_q_heads / num_kv_heads
+    int group;        // num_q_heads / num_kv_heads
+    int heads;        // query heads of a query tile: all of a kv head's, or as many as it has columns
+    int head_tiles;   // query tiles side by side that hold them
+    int q_tile;       // queries of a query tile
+    size_t off_parts; // workspace: partial sums, after the tickets
     size_t bytes;
 };
 

@@ -1,79 +1,890 @@
 // pkv_mass.cu -- attention weight that every cached token receives, added up
-// over a step's queries and a kv head's query heads.
+// over a step's queries and a kv head's query heads, on the 5th-generation
+// tensor cores (tcgen05, TMEM accumulators).
+//
+// What it computes.  mass[t] += sum over the (query, head) columns c that see
+// slot t of exp2(k_t . q_c scale log2(e) - lse_c log2(e)).  The lse is given, so
+// there is no running maximum and nothing to rescale: S^T = K Q^T with the keys
+// on the MMA's rows, so that a TMEM lane is a key and a thread adds up its own
+// key's columns in a register.  No value crosses threads, and what a NaN in one
+// key or one column does stays there.
+//
+// What bounds it.  A decode step reads K once (32 KB for 128 keys at head_dim
+// 128, 0.74 us of an SM's share of the measured HBM rate) for 8 MMAs of 128 x 16
+// x 16: memory.  With many queries 128 keys x 128 columns take 8 MMAs of 128 x
+// 128 x 16 (0.33 us at the tensor peak) and 16384 exponentials.
+//
+// How (one persistent CTA per SM):
+//  - Work is laid out along a line: for every (row, kv head) its blocks of keys,
+//    for every block the steps through the query tiles that see it.  Every CTA
+//    takes an equal range; it finds it itself from the row arrays (no plan
+//    kernel, no host readback).  Rows whose queries fit one tile go by blocks of
+//    128 keys, others by 256: the query tiles then stream past two key tiles at
+//    once, which halves what they cost in L2 reads.
+//  - A block cut between CTAs leaves partial sums in the workspace; the last
+//    CTA to arrive (a ticket for every 32 keys) adds them up in the order of the
+//    line, so results do not depend on timing.
+//  - Warps: 3 walks the CTA's range and hands out its blocks through a ring; 0
+//    loads K and 2 the query tiles, with TMA; 1 owns TMEM and issues the MMAs;
+//    4-7 and 8-11 add up, a key tile each, two accumulators each.
+//  - Sums of a step's columns are plain fp32 (128 terms at most); steps are
+//    added up with a compensation for what the addition drops, so thousands of
+//    queries lose nothing.
+#include <cuda_bf16.h>
 #include <math.h>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "pkv_tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kMassThreads = 256;
+constexpr int kMmKeys = 128;     // keys of a tile: M of every MMA
+constexpr int kFixCost = 2;      // positions that a key tile costs before its first step
+constexpr int kMinRange = 6;     // positions that are worth a CTA of their own
+constexpr int kMmMaxCtas = 160;  // persistent CTAs the workspace has room for
+constexpr int kMmKWarp = 0, kMmMmaWarp = 1, kMmQWarp = 2, kMmWalkWarp = 3, kMmSumWarp = 4;
+constexpr int kMmThreads = 384;
+constexpr int kMmBlocks = 8;     // blocks handed out and not yet done with
+constexpr int kMmReaders = 11;   // warps that read them
 
-struct MassParams {
-    const __nv_bfloat16 *k_cache, *q;
+template <int D> struct MmCfg {
+    static constexpr int kCols = D == 256 ? 64 : 128;          // (query, head) columns of a query tile
+    static constexpr uint32_t kKBytes = kMmKeys * D * 2;
+    static constexpr uint32_t kQBytes = kCols * D * 2;         // [D / 64][kCols rows][128 B], swizzled
+    static constexpr int kKStages = D == 64 ? 8 : D == 128 ? 4 : 2;
+    static constexpr int kQStages = D == 64 ? 4 : 2;
+    static constexpr uint32_t kGroupStride = 8 * D * 2;        // 8 keys, all of head_dim
+    static constexpr uint32_t kQBlock = kCols * 128;
+    static constexpr uint32_t kOffK = 0;
+    static constexpr uint32_t kOffQ = kOffK + kKStages * kKBytes;
+    static constexpr uint32_t kOffLse = kOffQ + kQStages * kQBytes; // [group of warps][step parity][kCols]
+    static constexpr uint32_t kOffBar = kOffLse + 2 * 2 * 128 * 4;
+    static constexpr uint32_t kSmem = kOffBar + 2048;
+    static constexpr uint32_t kTmemCols = 4 * kCols;           // two accumulators for each group of warps
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+// What the roles need to know of a block of keys.
+struct MmBlock {
+    int32_t b, g;           // row, kv head
+    int32_t tok, toks;      // first key, keys
+    int32_t tiles;          // key tiles: 1 or 2; 0: no more blocks
+    int32_t first, queries; // the row's queries
+    int32_t len;            // cached tokens before the step
+    int32_t step0, step1;   // steps of this piece: query tile x head tile
+    int32_t fresh, gone;
+    int32_t piece0, pieces; // CTA of the block's first piece, pieces (1: whole)
+};
+
+// The line cut into `ctas` ranges as equal as can be.
+struct MmCut {
+    int64_t quot;
+    int rest, ctas;
+    __device__ __forceinline__ int64_t lo(int c) const { return quot * c + rest * c / ctas; }
+    // the CTA whose range holds position x
+    __device__ __forceinline__ int of(int64_t x) const
+    {
+        int c = (int)min((int64_t)ctas - 1, x / quot);
+        while (lo(c) > x)
+            --c;
+        return c;
+    }
+};
+
+// Where a CTA's range starts, and its length in positions.
+struct MmStart {
+    MmCut cut;
+    int64_t at, off, left; // position on the line, within the (row, kv head), positions of the range
+    int b, g;
+};
+
+struct MmBars {
+    uint64_t k_full[8], k_empty[8];
+    uint64_t q_full[4], q_empty[4];
+    uint64_t s_full[4], s_free[4]; // [group of warps][accumulator]
+    uint64_t z_full[2];            // [group of warps]: its columns' lse are there
+    uint64_t block_full[kMmBlocks], block_empty[kMmBlocks];
+    uint64_t drain;
+    MmStart start;
+    int64_t scratch[kMmThreads / 32];
+    MmBlock block[kMmBlocks];
+    uint16_t bad[kMmBlocks][2]; // bit i: the page of a tile's keys 8 i .. 8 i + 7 is out of range
+    uint32_t tmem_base;
+    int32_t abort;
+};
+static_assert(sizeof(MmBars) <= 2048, "barrier block");
+
+struct MmParams {
     const int32_t *indptr, *table, *seqlens, *fresh_from, *evicted;
     const float *lse;
     float *mass;
     int32_t *pos, *err_flag;
-    float scale;
-    int batch, num_q_heads, num_kv_heads, group, head_dim, total_q, max_blocks, page_shift, num_pages, layout, slots;
+    int32_t *tickets; // [CTA][tile][quarter]: pieces of a block's 32 keys that are there
+    float *parts;     // [CTA][begun before this CTA / in it][256 keys]
+    float q_scale;    // softmax_scale * log2(e)
+    int batch, num_q_heads, num_kv_heads, group, total_q, max_blocks;
+    int page_shift, box_shift, num_pages, layout, slots;
+    int heads, head_tiles, q_tile; // of a query tile
+    uint32_t q_box_bytes, q_one_bytes;
 };
 
-// A warp per key, one row and kv head per CTA in x and y.
-__global__ void __launch_bounds__(kMassThreads) mass_kernel(const __grid_constant__ MassParams p)
+struct MmMaps {
+    CUtensorMap k, q, q_one;
+};
+
+// ---------------------------------------------------------------- work line
+
+struct MmRow {
+    int first, queries, len;
+    int steps;  // of a block that all queries see
+    int tiles;  // key tiles of a block
+    int blocks; // of a kv head; 0: nothing to do
+    int full;   // blocks, from the first on, that all query tiles see
+    int err;
+    int64_t work; // positions of a kv head
+};
+
+__device__ __forceinline__ int mm_steps(const MmParams &p, const MmRow &r, int kb)
 {
-    const int b = blockIdx.x / p.num_kv_heads, g = blockIdx.x - b * p.num_kv_heads;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int L = p.seqlens[b];
-    const int first = p.indptr != nullptr ? p.indptr[b] : b;
-    const int64_t n = p.indptr != nullptr ? (int64_t)p.indptr[b + 1] - first : 1;
-    int err = 0;
-    if (first < 0 || n < 0 || n > (int64_t)p.total_q - first)
-        err = PKV_ERR_QLEN;
-    else if (L >= 0 && n > 0 &&
-             L + n > min(min((int64_t)p.max_blocks << p.page_shift, (int64_t)p.slots), (int64_t)kMassMaxKeys))
-        err = PKV_ERR_OVERFLOW;
-    if (err != 0)
-        set_error(p.err_flag, err);
-    if (err != 0 || L < 0 || n == 0)
-        return;
-    const int keys = L + (int)n, D = p.head_dim;
-    const int fresh = p.fresh_from != nullptr ? p.fresh_from[b] : L;
-    const int64_t P = (int64_t)1 << p.page_shift;
-    for (int t = blockIdx.y * (kMassThreads / 32) + warp; t < keys; t += gridDim.y * (kMassThreads / 32)) {
-        const int64_t page = p.table[(int64_t)b * p.max_blocks + (t >> p.page_shift)], at = t & (P - 1);
-        if (page < 1 || page >= p.num_pages) {
-            set_error(p.err_flag, PKV_ERR_PAGE);
-            continue;
+    const int i0 = kb * r.tiles * kMmKeys - r.len; // the block's first key is seen from this query on
+    return r.steps - (i0 > 0 ? i0 / p.q_tile : 0) * p.head_tiles;
+}
+__device__ __forceinline__ int64_t mm_cost(const MmRow &r, int steps)
+{
+    return (int64_t)r.tiles * (kFixCost + steps);
+}
+
+// A row's part in the call (see include/pkv.h).
+__device__ __forceinline__ MmRow mm_row(const MmParams &p, int b)
+{
+    MmRow r;
+    r.first = p.indptr != nullptr ? p.indptr[b] : b;
+    const int64_t n = p.indptr != nullptr ? (int64_t)p.indptr[b + 1] - r.first : 1;
+    r.len = p.seqlens[b];
+    r.err = r.blocks = r.full = r.queries = r.steps = 0;
+    r.tiles = 1;
+    r.work = 0;
+    if (r.first < 0 || n < 0 || n > (int64_t)p.total_q - r.first) {
+        r.err = PKV_ERR_QLEN;
+        return r;
+    }
+    if (n == 0 || r.len < 0)
+        return r;
+    const int64_t keys = (int64_t)r.len + n;
+    if (keys > min(min((int64_t)p.max_blocks << p.page_shift, (int64_t)p.slots), (int64_t)kMassMaxKeys)) {
+        r.err = PKV_ERR_OVERFLOW;
+        return r;
+    }
+    r.queries = (int)n;
+    r.steps = (r.queries + p.q_tile - 1) / p.q_tile * p.head_tiles;
+    r.tiles = r.steps > 1 ? 2 : 1;
+    const int size = r.tiles * kMmKeys;
+    r.blocks = (int)((keys + size - 1) / size);
+    r.full = (int)min((int64_t)r.blocks, ((int64_t)r.len + p.q_tile - 1) / size + 1);
+    r.work = r.full * mm_cost(r, r.steps);
+    for (int kb = r.full; kb < r.blocks; ++kb)
+        r.work += mm_cost(r, mm_steps(p, r, kb));
+    return r;
+}
+
+// Finds the CTA's range: a prefix sum over the rows' work.  The whole CTA.
+__device__ MmStart mm_start(const MmParams &p, int64_t *scratch, MmStart *found)
+{
+    constexpr int kPer = (kMaxMassBatch + kMmThreads - 1) / kMmThreads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = min(kPer, (p.batch + kMmThreads - 1) / kMmThreads);
+    int64_t work[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int b = tid * per + i;
+        work[i] = 0;
+        if (i < per && b < p.batch) {
+            const MmRow r = mm_row(p, b);
+            work[i] = r.work;
+            if (blockIdx.x == 0)
+                set_error(p.err_flag, r.err);
         }
-        const __nv_bfloat16 *k = p.k_cache + (p.layout == PKV_NHD ? ((page * P + at) * p.num_kv_heads + g) * D
-                                                                 : ((page * p.num_kv_heads + g) * P + at) * D);
-        float kv[8];
-        for (int j = 0; j < D / 32; ++j)
-            kv[j] = __bfloat162float(k[j * 32 + lane]);
-        float sum = 0.f, part = 0.f;
-        for (int i = max(0, t - L); i < n; ++i) {
-            part = 0.f;
-            for (int h = 0; h < p.group; ++h) {
-                const int64_t head = ((int64_t)first + i) * p.num_q_heads + g * p.group + h;
-                float s = 0.f;
-                for (int j = 0; j < D / 32; ++j)
-                    s += kv[j] * __bfloat162float(p.q[head * D + j * 32 + lane]);
-                for (int d = 16; d > 0; d >>= 1)
-                    s += __shfl_xor_sync(0xffffffffu, s, d);
-                const float z = p.lse[head];
-                part += z == -INFINITY ? 0.f : expf(s * p.scale - z);
+        sum += work[i] * p.num_kv_heads;
+    }
+    int64_t x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    if (lane == 31)
+        scratch[warp] = x;
+    if (tid == 0) { // an empty range, at row 0
+        found->at = found->off = found->left = 0;
+        found->b = found->g = 0;
+    }
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kMmThreads / 32; ++w) {
+        const int64_t v = scratch[w];
+        x += w < warp ? v : 0;
+        total += v;
+    }
+    x -= sum;
+    const int c = blockIdx.x;
+    MmCut cut;
+    cut.ctas = total >= (int64_t)gridDim.x * kMinRange ? (int)gridDim.x : max(1, (int)total / kMinRange);
+    cut.quot = total / cut.ctas;
+    cut.rest = (int)(total - cut.quot * cut.ctas);
+    if (c < cut.ctas) {
+        const int64_t lo = cut.lo(c), hi = cut.lo(c + 1);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int64_t size = work[i] * p.num_kv_heads, in_row = lo - x;
+            if (hi > lo && in_row >= 0 && in_row < size) {
+                MmStart at;
+                at.cut = cut;
+                at.at = lo;
+                at.left = hi - lo;
+                at.b = tid * per + i;
+                at.g = (int)(in_row / work[i]);
+                at.off = in_row - at.g * work[i];
+                *found = at;
             }
-            sum += part;
-        }
-        if (lane == 0) {
-            const int64_t to = ((int64_t)b * p.num_kv_heads + g) * p.slots + t;
-            p.mass[to] = t >= fresh ? sum : p.mass[to] + sum;
-            if (t >= fresh && p.pos != nullptr)
-                p.pos[to] = t + (p.evicted != nullptr ? p.evicted[b] : 0);
+            x += size;
         }
     }
+    __syncthreads();
+    return *found;
+}
+
+// ---------------------------------------------------------------- waits
+
+__device__ __noinline__ bool mm_wait_slow(uint64_t *bar, uint32_t parity, MmBars &bars, int32_t *err_flag)
+{
+    const uint64_t start = globaltimer_ns();
+    volatile int32_t *abort = &bars.abort;
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity))
+                return true;
+        if (*abort != 0)
+            return false;
+        if (globaltimer_ns() - start > kWaitLimitNs) {
+            *abort = 1;
+            set_error(err_flag, PKV_ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// Bounded wait for the phase of the given parity; gives up when another role
+// has.  A whole warp: all lanes get the same answer.
+__device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity, MmBars &bars, int32_t *err_flag)
+{
+    bool done = mbar_try_wait(bar, parity);
+    if (!done)
+        done = mm_wait_slow(bar, parity, bars, err_flag);
+    return __all_sync(0xffffffffu, done);
+}
+
+// ---------------------------------------------------------------- blocks
+
+// One warp cuts the CTA's range into blocks, in order.
+__device__ void mm_walk(const MmParams &p, MmBars &bars, const MmStart &from, int lane)
+{
+    int n = 0, b = from.b, g = from.g, kb = 0;
+    int64_t at = from.at, left = from.left, off = from.off;
+    MmRow r = mm_row(p, b);
+    MmRow then = r;
+    int fresh = 0, gone = 0, next_fresh = 0, next_gone = 0;
+    auto more_of = [&](int row, int &f, int &e) {
+        f = p.fresh_from != nullptr ? p.fresh_from[row] : p.seqlens[row];
+        e = p.evicted != nullptr ? p.evicted[row] : 0;
+    };
+    if (left > 0) {
+        more_of(b, fresh, gone);
+        // the block that the range starts in
+        const int64_t size = mm_cost(r, r.steps);
+        kb = (int)min((int64_t)r.full, off / size);
+        off -= kb * size;
+        while (kb >= r.full && off >= mm_cost(r, mm_steps(p, r, kb)))
+            off -= mm_cost(r, mm_steps(p, r, kb++));
+    }
+    bool ahead = false; // the next row is read
+    for (;;) {
+        MmBlock s;
+        s.tiles = 0;
+        while (left > 0) {
+            if (!ahead && b + 1 < p.batch) {
+                then = mm_row(p, b + 1);
+                more_of(b + 1, next_fresh, next_gone);
+                ahead = true;
+            }
+            if (kb >= r.blocks) {
+                kb = 0;
+                if (r.blocks == 0 || ++g == p.num_kv_heads) { // (positions are left: there is a next row)
+                    g = 0;
+                    ++b;
+                    r = then;
+                    fresh = next_fresh;
+                    gone = next_gone;
+                    ahead = false;
+                }
+                continue;
+            }
+            const int steps = mm_steps(p, r, kb), t = r.tiles;
+            const int64_t size = mm_cost(r, steps), take = min(size - off, left);
+            auto step_at = [&](int64_t x) { // first step whose position is x or more
+                return (int)max((int64_t)0, min((int64_t)steps, (x + t - 1) / t - kFixCost));
+            };
+            const int s0 = step_at(off), s1 = step_at(off + take);
+            const int64_t start = at - off; // of the block
+            const int block = kb;
+            at += take;
+            left -= take;
+            off += take;
+            if (off >= size) {
+                off = 0;
+                ++kb;
+            }
+            if (s0 >= s1)
+                continue;
+            s.b = b;
+            s.g = g;
+            s.tok = block * t * kMmKeys;
+            s.toks = min(t * kMmKeys, r.len + r.queries - s.tok);
+            s.tiles = t;
+            s.first = r.first;
+            s.queries = r.queries;
+            s.len = r.len;
+            s.step0 = r.steps - steps + s0;
+            s.step1 = r.steps - steps + s1;
+            s.fresh = fresh;
+            s.gone = gone;
+            s.piece0 = blockIdx.x;
+            s.pieces = 1;
+            if (s1 - s0 < steps) {
+                s.piece0 = from.cut.of(start + (int64_t)t * kFixCost);
+                s.pieces = from.cut.of(start + (int64_t)t * (kFixCost + steps - 1)) - s.piece0 + 1;
+            }
+            break;
+        }
+        const int slot = n % kMmBlocks;
+        if (n >= kMmBlocks && !mm_wait(&bars.block_empty[slot], (uint32_t)(n / kMmBlocks - 1) & 1, bars, p.err_flag))
+            return;
+        if (lane == 0) {
+            bars.block[slot] = s;
+            bars.bad[slot][0] = bars.bad[slot][1] = 0;
+            mbar_arrive(&bars.block_full[slot]);
+        }
+        ++n;
+        if (s.tiles == 0)
+            return;
+    }
+}
+
+// The n-th block; a role that gave up sees the end.
+__device__ __forceinline__ MmBlock mm_block(const MmParams &p, MmBars &bars, int n)
+{
+    MmBlock s;
+    if (mm_wait(&bars.block_full[n % kMmBlocks], (uint32_t)(n / kMmBlocks) & 1, bars, p.err_flag))
+        s = bars.block[n % kMmBlocks];
+    else
+        s.tiles = 0;
+    return s;
+}
+__device__ __forceinline__ void mm_block_done(MmBars &bars, int n, int lane)
+{
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(&bars.block_empty[n % kMmBlocks]);
+}
+
+// ---------------------------------------------------------------- loads
+
+// One warp loads all key tiles, one box per lane: boxes of min(page, 64) keys, at
+// most 16 a tile.  A page id outside the pool loads nothing and marks the block.
+template <int D>
+__device__ void mm_load_k(const MmParams &p, const MmMaps &maps, uint8_t *smem, MmBars &bars, int lane)
+{
+    using C = MmCfg<D>;
+    const int bsh = p.box_shift, boxes = kMmKeys >> bsh;
+    const uint32_t box_bytes = (uint32_t)(1 << bsh) * D * 2;
+    const bool nhd = p.layout == PKV_NHD;
+    int slot = 0, issued = 0;
+    uint32_t round = 0; // times the ring has been filled
+    int id[2], next_id[2];
+    auto pages = [&](const MmBlock &s, int (&to)[2]) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int in = j * kMmKeys + (lane << bsh);
+            to[j] = lane < boxes && j < s.tiles && in < s.toks
+                        ? p.table[(int64_t)s.b * p.max_blocks + ((s.tok + in) >> p.page_shift)]
+                        : 0;
+        }
+    };
+    MmBlock s = mm_block(p, bars, 0);
+    if (s.tiles > 0)
+        pages(s, id);
+    bool going = true;
+    for (int n = 0; s.tiles > 0 && going; ++n) {
+        const MmBlock next = mm_block(p, bars, n + 1);
+        if (next.tiles > 0)
+            pages(next, next_id);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (j >= s.tiles || !going)
+                continue;
+            if (round > 0 && !mm_wait(&bars.k_empty[slot], (round - 1) & 1, bars, p.err_flag)) {
+                going = false;
+                continue;
+            }
+            const int in = j * kMmKeys + (lane << bsh), tok = s.tok + in;
+            const bool want = lane < boxes && in < s.toks;
+            const bool good = want && id[j] >= 1 && id[j] < p.num_pages;
+            const uint32_t count = __popc(__ballot_sync(0xffffffffu, good));
+            const uint32_t miss = __ballot_sync(0xffffffffu, want && !good);
+            if (miss != 0 && lane == 0) {
+                uint32_t bits = 0; // a bit for 8 keys
+                for (uint32_t m = miss; m != 0; m &= m - 1)
+                    bits |= ((1u << (1 << bsh >> 3)) - 1) << ((__ffs(m) - 1) << bsh >> 3);
+                *(volatile uint16_t *)&bars.bad[n % kMmBlocks][j] = (uint16_t)bits;
+                set_error(p.err_flag, PKV_ERR_PAGE);
+            }
+            if (lane == 0)
+                mbar_arrive_expect_tx(&bars.k_full[slot], count * box_bytes);
+            __syncwarp();
+            if (good) {
+                const int in_page = tok & ((1 << p.page_shift) - 1);
+                const int c3 = nhd ? ((id[j] << p.page_shift) + in_page) >> 3 : in_page >> 3;
+                const int c4 = nhd ? s.g : id[j] * p.num_kv_heads + s.g;
+                tma_load_5d_plain(smem + C::kOffK + slot * C::kKBytes + lane * box_bytes, &maps.k, 0, 0, 0, c3, c4,
+                                  &bars.k_full[slot]);
+            }
+            ++issued;
+            if (++slot == C::kKStages) {
+                slot = 0;
+                ++round;
+            }
+        }
+        mm_block_done(bars, n, lane);
+        s = next;
+        id[0] = next_id[0];
+        id[1] = next_id[1];
+    }
+    // Copies still in flight (a role gave up): they land before the CTA ends.
+    for (int k = issued > C::kKStages ? issued - C::kKStages : 0; k < issued; ++k)
+        mbar_wait(&bars.k_full[k % C::kKStages], (uint32_t)(k / C::kKStages) & 1);
+}
+
+// One warp loads the query tiles of every step, a box per 64 columns.
+template <int D>
+__device__ void mm_load_q(const MmParams &p, const MmMaps &maps, uint8_t *smem, MmBars &bars, int lane)
+{
+    using C = MmCfg<D>;
+    int slot = 0, issued = 0;
+    uint32_t round = 0;
+    bool going = true;
+    for (int n = 0; going; ++n) {
+        const MmBlock s = mm_block(p, bars, n);
+        if (s.tiles == 0)
+            break;
+        const bool one = s.queries == 1; // a box of one query: no other row's are fetched
+        for (int st = s.step0; st < s.step1; ++st) {
+            if (round > 0 && !mm_wait(&bars.q_empty[slot], (round - 1) & 1, bars, p.err_flag)) {
+                going = false;
+                break;
+            }
+            const int t = p.head_tiles == 1 ? st : st / p.head_tiles, h = st - t * p.head_tiles;
+            if (lane == 0)
+                mbar_arrive_expect_tx(&bars.q_full[slot], (one ? p.q_one_bytes : p.q_box_bytes) * (D / 64));
+            __syncwarp();
+            if (lane < D / 64)
+                tma_load_3d_plain(smem + C::kOffQ + slot * C::kQBytes + lane * C::kQBlock, one ? &maps.q_one : &maps.q,
+                                  lane * 64, s.g * p.group + h * p.heads, s.first + t * p.q_tile, &bars.q_full[slot]);
+            ++issued;
+            if (++slot == C::kQStages) {
+                slot = 0;
+                ++round;
+            }
+        }
+        mm_block_done(bars, n, lane);
+    }
+    for (int k = issued > C::kQStages ? issued - C::kQStages : 0; k < issued; ++k)
+        mbar_wait(&bars.q_full[k % C::kQStages], (uint32_t)(k / C::kQStages) & 1);
+}
+
+// ---------------------------------------------------------------- MMA
+
+// Four MMAs of 64 values of the inner dimension: A and B 32 bytes on each time.
+// The whole warp; one elected thread (always the same) issues.
+__device__ __forceinline__ void mm_mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred e, p, t;\n\t"
+                 ".reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "setp.eq.b32 t, 0, 0;\n\t"
+                 "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+                 "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+__device__ __forceinline__ void mm_commit(uint64_t *bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+                     smem_addr(bar))
+                 : "memory");
+}
+
+// Columns of a step that hold a (query, head).
+__device__ __forceinline__ int mm_cols(const MmParams &p, int queries, int t, int h)
+{
+    return p.head_tiles == 1 ? min(p.q_tile, queries - t * p.q_tile) * p.heads
+                             : min(p.heads, p.group - h * p.heads);
+}
+
+template <int D>
+__device__ void mm_mma(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t tmem, int lane)
+{
+    using C = MmCfg<D>;
+    const uint64_t kd0 = tc_sw128_desc(smem_addr(smem + C::kOffK), 16, C::kGroupStride);
+    const uint64_t qd0 = tc_sw128_desc(smem_addr(smem + C::kOffQ), 16, 1024);
+    int tile = 0; // key tiles before the block
+    uint32_t used[2] = {0, 0};
+    int q_slot = 0;
+    uint32_t q_par = 0;
+    bool going = true;
+    for (int n = 0; going; ++n) {
+        const MmBlock s = mm_block(p, bars, n);
+        // warp-uniform values (read from one lane) stay in uniform registers
+        const int tiles = __shfl_sync(0xffffffffu, s.tiles, 0);
+        if (tiles == 0)
+            break;
+        const int step0 = __shfl_sync(0xffffffffu, s.step0, 0), step1 = __shfl_sync(0xffffffffu, s.step1, 0);
+        const int queries = __shfl_sync(0xffffffffu, s.queries, 0);
+        mm_block_done(bars, n, lane);
+#pragma unroll 1
+        for (int st = step0; st < step1 && going; ++st) {
+            const int t = p.head_tiles == 1 ? st : st / p.head_tiles, h = st - t * p.head_tiles;
+            const int cols = (mm_cols(p, queries, t, h) + 15) & ~15;
+            const uint32_t idesc = tc_idesc_bf16(kMmKeys, 0, false, false) | (uint32_t)(cols >> 3) << 17;
+            if (!mm_wait(&bars.q_full[q_slot], q_par, bars, p.err_flag)) {
+                going = false;
+                break;
+            }
+            const uint64_t qd = qd0 + (uint64_t)(q_slot * C::kQBytes >> 4);
+#pragma unroll 1
+            for (int j = 0; j < tiles; ++j) {
+                const int x = tile + j, k_slot = x % C::kKStages, w = x & 1;
+                const uint32_t u = w ? used[1] : used[0], buf = 2 * w + (u & 1);
+                if ((st == step0 && !mm_wait(&bars.k_full[k_slot], (uint32_t)(x / C::kKStages) & 1, bars, p.err_flag)) ||
+                    (u >= 2 && !mm_wait(&bars.s_free[buf], ((u >> 1) - 1) & 1, bars, p.err_flag))) {
+                    going = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t kd = kd0 + (uint64_t)(k_slot * C::kKBytes >> 4);
+#pragma unroll 1
+                for (int blk = 0; blk < D / 64; ++blk)
+                    mm_mma4(tmem + buf * C::kCols, kd + (uint64_t)(blk * 1024 >> 4),
+                            qd + (uint64_t)(blk * C::kQBlock >> 4), idesc, blk > 0 ? 1u : 0u);
+                mm_commit(&bars.s_full[buf]);
+                if (w)
+                    ++used[1];
+                else
+                    ++used[0];
+            }
+            mm_commit(&bars.q_empty[q_slot]);
+            if (++q_slot == C::kQStages) {
+                q_slot = 0;
+                q_par ^= 1;
+            }
+        }
+        for (int j = 0; j < tiles; ++j)
+            mm_commit(&bars.k_empty[(tile + j) % C::kKStages]);
+        tile += tiles;
+    }
+    mm_commit(&bars.drain); // the commits have arrived before the CTA ends
+    mbar_wait(&bars.drain, 0);
+}
+
+// ---------------------------------------------------------------- sums
+
+#define PKV_R8(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
+                  "+r"(r[i + 6]), "+r"(r[i + 7])
+__device__ __forceinline__ void mm_ld32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : PKV_R8(0), PKV_R8(8), PKV_R8(16), PKV_R8(24)
+                 : "r"(taddr)
+                 : "memory");
+}
+// Waits for this thread's TMEM loads; `r` is not read before.
+__device__ __forceinline__ void mm_ld_wait(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : PKV_R8(0), PKV_R8(8), PKV_R8(16), PKV_R8(24)::"memory");
+}
+#undef PKV_R8
+
+// The sum of 2^(x scale + z) over 32 columns; z holds -lse log2(e).
+template <bool MASKED>
+__device__ __forceinline__ void mm_add32(const uint32_t (&x)[32], const float *z, float scale, int from, int to,
+                                         float2 &sum0, float2 &sum1)
+{
+    const float2 s2 = make_float2(scale, scale);
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const float4 z4 = *reinterpret_cast<const float4 *>(z + i);
+        const float2 a = ffma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), s2,
+                               make_float2(z4.x, z4.y));
+        const float2 c = ffma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), s2,
+                               make_float2(z4.z, z4.w));
+        float2 w0 = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+        float2 w1 = make_float2(ex2_approx(c.x), ex2_approx(c.y));
+        if (MASKED) {
+            w0.x = i >= from && i < to ? w0.x : 0.f;
+            w0.y = i + 1 >= from && i + 1 < to ? w0.y : 0.f;
+            w1.x = i + 2 >= from && i + 2 < to ? w1.x : 0.f;
+            w1.y = i + 3 >= from && i + 3 < to ? w1.y : 0.f;
+        }
+        sum0 = __fadd2_rn(sum0, w0);
+        sum1 = __fadd2_rn(sum1, w1);
+    }
+}
+
+// Adds one to a ticket, ordering this warp's stores before it and the other
+// pieces' stores before what follows.
+__device__ __forceinline__ int mm_ticket(int32_t *ticket)
+{
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(ticket) : "memory");
+    return old;
+}
+
+template <int D>
+__device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t tmem, int warp, int lane)
+{
+    using C = MmCfg<D>;
+    const int w = (warp - kMmSumWarp) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16) + 2 * w * C::kCols;
+    float *lse = reinterpret_cast<float *>(smem + C::kOffLse) + w * 256;
+    int tile = 0;
+    uint32_t used = 0;
+    for (int n = 0;; ++n) {
+        const MmBlock s = mm_block(p, bars, n);
+        if (s.tiles == 0)
+            return;
+        const int j = (w - tile) & 1;
+        tile += s.tiles;
+        if (j >= s.tiles) {
+            mm_block_done(bars, n, lane);
+            continue;
+        }
+        const int tok = s.tok + j * kMmKeys, key = tok + r;
+        // -lse log2(e) of this thread's column of a step
+        auto lse_at = [&](int st) {
+            const int t = p.head_tiles == 1 ? st : st / p.head_tiles, h = st - t * p.head_tiles;
+            float z = 0.f;
+            if (r < mm_cols(p, s.queries, t, h)) {
+                const int i = r / p.heads;
+                z = p.lse[((int64_t)s.first + t * p.q_tile + i) * p.num_q_heads + s.g * p.group + h * p.heads +
+                          (r - i * p.heads)];
+                z = z == -INFINITY ? z : z * -1.4426950408889634f;
+            }
+            return z;
+        };
+        float z = lse_at(s.step0), sum = 0.f, dropped = 0.f;
+        for (int st = s.step0; st < s.step1; ++st) {
+            const int t = p.head_tiles == 1 ? st : st / p.head_tiles, h = st - t * p.head_tiles;
+            const int cols = mm_cols(p, s.queries, t, h);
+            float *zs = lse + (used & 1) * 128;
+            zs[r] = z; // (all have read what was there two steps ago: they have been at the barrier since)
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars.z_full[w]);
+            if (st + 1 < s.step1)
+                z = lse_at(st + 1);
+            const uint32_t buf = used & 1;
+            if (!mm_wait(&bars.z_full[w], used & 1, bars, p.err_flag) ||
+                !mm_wait(&bars.s_full[2 * w + buf], (used >> 1) & 1, bars, p.err_flag))
+                return;
+            tc_fence_after();
+            const uint32_t at = t_row + buf * C::kCols;
+            // columns of queries before the key's own see nothing of it
+            const int blind = max(0, key - s.len - t * p.q_tile); // queries
+            const int seen = p.head_tiles == 1 ? blind * p.heads : blind > 0 ? C::kCols : 0;
+            const bool edge = tok + kMmKeys - 1 - s.len > t * p.q_tile;
+            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+            uint32_t x[32];
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 32) {
+                mm_ld32(at + c, x);
+                mm_ld_wait(x);
+                if (!edge && c + 32 <= cols)
+                    mm_add32<false>(x, zs + c, p.q_scale, 0, 32, sum0, sum1);
+                else
+                    mm_add32<true>(x, zs + c, p.q_scale, seen - c, cols - c, sum0, sum1);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars.s_free[2 * w + buf]);
+            ++used;
+            // compensated: what an addition drops is added with the next
+            const float part = (sum0.x + sum1.x) + (sum0.y + sum1.y) + dropped;
+            const float next = sum + part;
+            dropped = part - (next - sum);
+            sum = next;
+            if (!(fabsf(sum) < INFINITY))
+                dropped = 0.f;
+        }
+        const bool bad = (*(volatile uint16_t *)&bars.bad[n % kMmBlocks][j] >> (r >> 3)) & 1;
+        const bool mine = tok + r < s.tok + s.toks && !bad;
+        bool last = true;
+        if (s.pieces > 1) {
+            float *part = p.parts + j * kMmKeys + r;
+            __stcg(part + (2 * blockIdx.x + (s.piece0 == blockIdx.x ? 1 : 0)) * 256, sum);
+            int32_t *ticket = p.tickets + (s.piece0 * 2 + j) * 4 + quarter;
+            __syncwarp();
+            int old = 0;
+            if (lane == 0)
+                old = mm_ticket(ticket);
+            last = __shfl_sync(0xffffffffu, old, 0) == s.pieces - 1;
+            __syncwarp();
+            if (last) {
+                if (lane == 0)
+                    *ticket = 0;
+                sum = __ldcg(part + (2 * s.piece0 + 1) * 256);
+                dropped = 0.f;
+                for (int c = 1; c < s.pieces; ++c) {
+                    const float y = __ldcg(part + 2 * (s.piece0 + c) * 256) + dropped, next = sum + y;
+                    dropped = y - (next - sum);
+                    sum = next;
+                    if (!(fabsf(sum) < INFINITY))
+                        dropped = 0.f;
+                }
+            }
+        }
+        if (last && mine) {
+            const int64_t to = ((int64_t)s.b * p.num_kv_heads + s.g) * p.slots + key;
+            const bool fresh = key >= s.fresh;
+            p.mass[to] = fresh ? sum : p.mass[to] + sum;
+            if (fresh && p.pos != nullptr)
+                p.pos[to] = key + s.gone;
+        }
+        mm_block_done(bars, n, lane);
+    }
+}
+
+// ---------------------------------------------------------------- kernel
+
+template <int D>
+__global__ void __launch_bounds__(kMmThreads, 1)
+    mass_kernel(const __grid_constant__ MmParams p, const __grid_constant__ MmMaps maps)
+{
+    using C = MmCfg<D>;
+    extern __shared__ __align__(1024) unsigned char mm_smem[];
+    uint8_t *smem = mm_smem;
+    if ((smem_addr(smem) & 1023u) != 0) { // the swizzled tiles need it; dynamic shared memory starts so
+        set_error(p.err_flag, PKV_ERR_TIMEOUT);
+        return;
+    }
+    MmBars &bars = *reinterpret_cast<MmBars *>(smem + C::kOffBar);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kKStages; ++i) {
+            mbar_init(&bars.k_full[i], 1);
+            mbar_init(&bars.k_empty[i], 1);
+        }
+        for (int i = 0; i < C::kQStages; ++i) {
+            mbar_init(&bars.q_full[i], 1);
+            mbar_init(&bars.q_empty[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.s_free[i], 4);
+        }
+        for (int i = 0; i < kMmBlocks; ++i) {
+            mbar_init(&bars.block_full[i], 1);
+            mbar_init(&bars.block_empty[i], kMmReaders);
+        }
+        mbar_init(&bars.z_full[0], 4);
+        mbar_init(&bars.z_full[1], 4);
+        mbar_init(&bars.drain, 1);
+        bars.abort = 0;
+        mbar_init_fence();
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.q);
+        prefetch_tensormap(&maps.q_one);
+    }
+    if (warp == kMmMmaWarp) {
+        tmem_alloc(&bars.tmem_base, C::kTmemCols);
+        tmem_relinquish();
+    }
+    const MmStart from = mm_start(p, bars.scratch, &bars.start);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem_base, 0);
+    if (warp == kMmWalkWarp)
+        mm_walk(p, bars, from, lane);
+    else if (warp == kMmKWarp)
+        mm_load_k<D>(p, maps, smem, bars, lane);
+    else if (warp == kMmQWarp)
+        mm_load_q<D>(p, maps, smem, bars, lane);
+    else if (warp == kMmMmaWarp)
+        mm_mma<D>(p, smem, bars, tmem, lane);
+    else
+        mm_sum<D>(p, smem, bars, tmem, warp, lane);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmMmaWarp)
+        tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// ---------------------------------------------------------------- host side
+
+struct MmEntry {
+    int D, cols;
+    const void *kernel;
+    uint32_t smem;
+};
+
+const MmEntry kMmTable[] = {
+    {64, MmCfg<64>::kCols, reinterpret_cast<const void *>(&mass_kernel<64>), MmCfg<64>::kSmem},
+    {128, MmCfg<128>::kCols, reinterpret_cast<const void *>(&mass_kernel<128>), MmCfg<128>::kSmem},
+    {256, MmCfg<256>::kCols, reinterpret_cast<const void *>(&mass_kernel<256>), MmCfg<256>::kSmem},
+};
+
+const MmEntry *mm_find(int D)
+{
+    for (const MmEntry &e : kMmTable)
+        if (e.D == D)
+            return &e;
+    return nullptr;
+}
+
+// Once per device: the kernel's shared memory.
+bool mm_ready(int device, const MmEntry *e)
+{
+    constexpr int kDevices = 64;
+    static bool done[kDevices][3] = {};
+    if (device < 0 || device >= kDevices)
+        return false;
+    bool &slot = done[device][e - kMmTable];
+    if (!slot)
+        slot = cudaFuncSetAttribute(e->kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)e->smem) == cudaSuccess;
+    return slot;
 }
 
 bool aligned16(const void *p)
@@ -95,7 +906,12 @@ pkv_status mass_shape(int batch, int total_q, int max_blocks, int num_q_heads, c
     if (batch > kMaxMassBatch || desc->page_size < 8 || s->group > 128 ||
         (int64_t)total_q * num_q_heads >= ((int64_t)1 << 31))
         return PKV_EUNSUPPORTED;
-    s->bytes = 256;
+    const int cols = mm_find(desc->head_dim)->cols;
+    s->heads = s->group < cols ? s->group : cols;
+    s->head_tiles = (s->group + s->heads - 1) / s->heads;
+    s->q_tile = s->head_tiles == 1 ? cols / s->heads : 1;
+    s->off_parts = kMmMaxCtas * 8 * sizeof(int32_t);
+    s->bytes = 256 + s->off_parts + (size_t)kMmMaxCtas * 2 * 256 * sizeof(float);
     return PKV_OK;
 }
 
@@ -133,9 +949,13 @@ pkv_status pkv_attn_mass(const pkv_cache_desc *desc, const void *k_cache, const 
         return PKV_EINVAL;
     if (workspace == nullptr || workspace_bytes < shape.bytes || !aligned16(workspace))
         return PKV_EWORKSPACE;
-    MassParams p;
-    p.k_cache = static_cast<const __nv_bfloat16 *>(k_cache);
-    p.q = static_cast<const __nv_bfloat16 *>(q);
+    const MmEntry *e = mm_find(desc->head_dim);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || !mm_ready(dev, e))
+        return PKV_ECUDA;
+    unsigned char *ws =
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
+    MmParams p;
     p.indptr = qo_indptr;
     p.table = block_table;
     p.seqlens = cache_seqlens;
@@ -145,24 +965,39 @@ pkv_status pkv_attn_mass(const pkv_cache_desc *desc, const void *k_cache, const 
     p.mass = mass;
     p.pos = slot_pos;
     p.err_flag = err_flag;
-    p.scale = softmax_scale;
+    p.tickets = reinterpret_cast<int32_t *>(ws);
+    p.parts = reinterpret_cast<float *>(ws + shape.off_parts);
+    p.q_scale = softmax_scale * 1.4426950408889634f;
     p.batch = batch;
     p.num_q_heads = num_q_heads;
     p.num_kv_heads = desc->num_kv_heads;
     p.group = shape.group;
-    p.head_dim = desc->head_dim;
     p.total_q = total_q;
     p.max_blocks = max_blocks;
     p.page_shift = 0;
     while ((1 << p.page_shift) < desc->page_size)
         ++p.page_shift;
+    p.box_shift = p.page_shift < 6 ? p.page_shift : 6;
     p.num_pages = desc->num_pages;
     p.layout = desc->layout;
     p.slots = slots;
-    const int64_t keys = (int64_t)max_blocks * desc->page_size;
-    const unsigned y = (unsigned)(keys / 8 + 1 < 512 ? keys / 8 + 1 : 512);
-    mass_kernel<<<dim3((unsigned)batch * desc->num_kv_heads, y), kMassThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ECUDA;
+    p.heads = shape.heads;
+    p.head_tiles = shape.head_tiles;
+    p.q_tile = shape.q_tile;
+    const int box_q = shape.q_tile < total_q ? shape.q_tile : total_q;
+    p.q_box_bytes = (uint32_t)box_q * shape.heads * 128;
+    p.q_one_bytes = (uint32_t)shape.heads * 128;
+    MmMaps m;
+    if (encode_group_map(&m.k, *desc, const_cast<void *>(k_cache), 1 << p.box_shift) != CUDA_SUCCESS ||
+        encode_q_map(&m.q, q, desc->head_dim, num_q_heads, total_q, shape.heads, box_q) != CUDA_SUCCESS ||
+        encode_q_map(&m.q_one, q, desc->head_dim, num_q_heads, total_q, shape.heads, 1) != CUDA_SUCCESS)
+        return PKV_ECUDA;
+    const int grid = sm_count(dev) < kMmMaxCtas ? sm_count(dev) : kMmMaxCtas;
+    void *args[] = {&p, &m};
+    return cudaLaunchKernel(e->kernel, dim3(grid), dim3(kMmThreads), args, e->smem, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? PKV_OK
+               : PKV_ECUDA;
 }
 
 } // extern "C"
