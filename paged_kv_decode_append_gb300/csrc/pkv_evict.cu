@@ -15,9 +15,10 @@ namespace {
 
 // ------------------------------------------------------------------- plan
 
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 128;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kBins = 256;
+constexpr int kPlanList = 128;           // slots that are ranked against one another
 constexpr uint32_t kSafeKey = 0xffffffffu; // protected slots: above +inf's key
 
 struct PlanParams {
@@ -49,42 +50,160 @@ __device__ __forceinline__ PlanRow plan_row(const PlanParams &p, int b)
 
 // Importance of a slot as a whole number: protected above all, then by mass
 // (NaN below all), the order of floats.
-__device__ __forceinline__ uint32_t plan_key(float mass, int pos, int sink, int64_t recent_from)
+__device__ __forceinline__ uint32_t plan_key(float mass, int pos, int sink, int oldest)
 {
     const uint32_t u = __float_as_uint(mass + 0.0f); // -0 counts as 0
-    const uint32_t k = mass != mass ? 0u : u & 0x80000000u ? ~u : u | 0x80000000u;
-    return pos < sink || pos >= recent_from ? kSafeKey : k;
+    const uint32_t k = mass != mass ? 0u : u ^ (uint32_t)((int32_t)u >> 31 | 0x80000000);
+    return pos < sink || pos > oldest ? kSafeKey : k;
 }
 
-__device__ __forceinline__ int plan_sum(int x, int *scratch, int tid)
-{
-    x = __reduce_add_sync(0xffffffffu, x);
-    __syncthreads();
-    if ((tid & 31) == 0)
-        scratch[tid >> 5] = x;
-    __syncthreads();
-    x = 0;
+// The keys of a (layer, row, kv head), KEYS of them in every thread's registers,
+// slot tid + 128 k in place k (past the row: kSafeKey); or (KEYS = 0) as many as
+// fit in shared memory and the others made anew whenever they are looked at.
+template <int KEYS> struct PlanKeys {
+    uint32_t k[KEYS > 0 ? KEYS : 1];
+    const float *mass;
+    const int32_t *pos;
+    uint32_t *held; // KEYS > 0: the masses, then the positions
+    int L, cached, sink, oldest; // positions below sink or above oldest are protected
+    int pos_at;
+
+    __device__ __forceinline__ uint32_t at(int i) const
+    {
+        if (KEYS > 0)
+            return plan_key(__uint_as_float(held[i]), (int)held[pos_at + i], sink, oldest);
+        return i < cached ? held[i] : plan_key(mass[i], pos[i], sink, oldest);
+    }
+    // Through shared memory all of a row is under way at once and takes no
+    // registers meanwhile (loads into registers, for which the compiler has none to
+    // spare and waits one by one, took 10 us).  The whole CTA.
+    __device__ __forceinline__ void load(int tid, int slots)
+    {
+        if (KEYS > 0) {
+            pos_at = (slots + 3) / 4 * 4;
+            if (slots % 4 == 0) { // every row begins on 16 bytes
+                for (int i = 4 * tid; i < L; i += 4 * kPlanThreads) {
+                    copy16(held + i, mass + i);
+                    copy16(held + pos_at + i, pos + i);
+                }
+            } else {
+                for (int i = tid; i < L; i += kPlanThreads) {
+                    copy4(held + i, mass + i);
+                    copy4(held + pos_at + i, pos + i);
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kPlanWarps; ++w)
-        x += scratch[w];
-    return x;
+            for (int j = 0; j < KEYS; ++j) {
+                const int i = tid + j * kPlanThreads;
+                const uint32_t key = at(min(i, L - 1));
+                k[j] = i < L ? key : kSafeKey;
+            }
+        } else {
+            for (int i = tid; i < min(L, cached); i += kPlanThreads)
+                held[i] = plan_key(mass[i], pos[i], sink, oldest);
+        }
+    }
+    static __device__ __forceinline__ void copy16(void *to, const void *from)
+    {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+    }
+    static __device__ __forceinline__ void copy4(void *to, const void *from)
+    {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+    }
+    // f(slot, key) for the slots of this thread, and for the places past the row
+    template <typename F> __device__ __forceinline__ void each(int tid, F f) const
+    {
+        if (KEYS > 0) {
+#pragma unroll
+            for (int j = 0; j < KEYS; ++j)
+                f(tid + j * kPlanThreads, k[j]);
+        } else {
+            for (int i = tid; i < L; i += kPlanThreads)
+                f(i, at(i));
+        }
+    }
+    // the same one by one, in less code
+    template <typename F> __device__ __forceinline__ void each_rarely(int tid, F f) const
+    {
+#pragma unroll 1
+        for (int i = tid; i < L; i += kPlanThreads)
+            f(i, at(i));
+    }
+    // A bit for every slot that f(slot, key) says, 32 slots a word.  The whole CTA.
+    template <typename F> __device__ __forceinline__ void mark(int tid, uint32_t *bits, F f) const
+    {
+        const int lane = tid & 31;
+        if (KEYS > 0) {
+#pragma unroll
+            for (int j = 0; j < KEYS; ++j) {
+                const uint32_t word = __ballot_sync(0xffffffffu, f(tid + j * kPlanThreads, k[j]));
+                if (lane == 0) // (there is room for all places)
+                    bits[(tid >> 5) + j * kPlanWarps] = word;
+            }
+        } else {
+            for (int i = tid; (i & ~31) < L; i += kPlanThreads) {
+                const uint32_t word = __ballot_sync(0xffffffffu, i < L && f(i, at(i)));
+                if (lane == 0)
+                    bits[i >> 5] = word;
+            }
+        }
+    }
+};
+
+// One more in the bin of x = key - from, if that is in the open range.  Without a
+// branch: there are many and most are in range or most are not.
+__device__ __forceinline__ void plan_count(uint32_t bins, uint32_t x, uint32_t width, int shift)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.le.u32 p, %0, %1;\n\t"
+                 "@p red.shared.add.u32 [%2], 1;\n\t}" ::"r"(x),
+                 "r"(width), "r"(bins + ((x >> shift) << 2))
+                 : "memory");
+}
+// Appends (key, ~slot) to the list, if x = key - from is in the open range.
+__device__ __forceinline__ void plan_append(uint32_t count, uint32_t list, uint32_t x, uint32_t width, uint32_t key, int i)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
+                 "setp.le.u32 p, %0, %1;\n\t"
+                 "@p atom.shared.add.u32 n, [%2], 1;\n\t"
+                 "@p mad.lo.u32 n, n, 8, %3;\n\t"
+                 "@p st.shared.v2.u32 [n], {%4, %5};\n\t}" ::"r"(x),
+                 "r"(width), "r"(count), "r"(list), "r"(~(uint32_t)i), "r"(key)
+                 : "memory");
 }
 
-// One CTA for each (layer, row, kv head).
-__global__ void __launch_bounds__(kPlanThreads) evict_plan_kernel(const __grid_constant__ PlanParams p)
+// One CTA for each (layer, row, kv head).  Slots are ranked by key, equal keys
+// by slot, the lowest first.  The key of the last slot that stays is found by
+// counting into 256 bins over the range that is still open, narrowed until a bin
+// is to be taken whole or has at most 128 slots, which are ranked against one
+// another.  Masses of a row spread over many powers of two and a float's bits
+// are its logarithm, so that the first count nearly always does.  Where more
+// slots than that have one and the same key, the count goes on over the slots.
+// Few threads with many keys each: what a warp does once (votes, scans, waits)
+// then weighs less.
+template <int KEYS>
+__global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 : 10)
+    evict_plan_kernel(const __grid_constant__ PlanParams p)
 {
-    extern __shared__ uint32_t s_dyn[]; // keys, then a bit for every slot that stays
-    __shared__ int s_bins[kBins];
-    __shared__ int s_scratch[kPlanWarps];
+    extern __shared__ __align__(16) uint32_t s_dyn[]; // keys (or what they are made from), a bit for every slot that stays
+    __shared__ __align__(16) int s_bins[kBins];
+    __shared__ uint64_t s_list[kPlanList];
     __shared__ int2 s_scan[kPlanWarps];
     __shared__ uint32_t s_lo, s_hi;
-    __shared__ int s_k, s_all;
+    __shared__ int s_safe, s_count, s_k, s_in;
+    __shared__ uint32_t s_from;
+    __shared__ uint64_t s_least;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t unit = blockIdx.x;
     const int per_layer = p.batch * p.num_kv_heads;
-    const int layer = (int)(unit / per_layer), rest = (int)(unit - (int64_t)layer * per_layer);
+    const int layer = (int)(blockIdx.x / (unsigned)per_layer), rest = (int)(blockIdx.x - (unsigned)(layer * per_layer));
     const int b = rest / p.num_kv_heads, g = rest - b * p.num_kv_heads;
+    const int gone = p.evicted != nullptr ? p.evicted[b] : 0;
     const PlanRow r = plan_row(p, b);
+    const int64_t oldest = (int64_t)r.L + gone - p.recent - 1; // position before the newest `recent` ones
     if (tid == 0) {
         if (layer == 0 && g == 0) {
             p.row_lens[2 * b] = r.L;
@@ -93,152 +212,154 @@ __global__ void __launch_bounds__(kPlanThreads) evict_plan_kernel(const __grid_c
         }
         if (r.keep >= r.L || r.keep == 0)
             p.num_moves[unit] = 0;
+        s_lo = kSafeKey;
+        s_hi = 0;
+        s_safe = s_count = 0;
     }
     if (r.keep >= r.L || r.keep == 0)
         return;
-    const int L = r.L, keep = r.keep;
-    const float *mass = p.mass + unit * p.slots;
-    const int32_t *pos = p.pos + unit * p.slots;
-    const int64_t recent_from = (int64_t)L + (p.evicted != nullptr ? p.evicted[b] : 0) - p.recent;
-    const bool held = L <= p.cached;
-    uint32_t *keys = s_dyn, *bits = s_dyn + p.cached;
-    auto key_at = [&](int i) { return held ? keys[i] : plan_key(mass[i], pos[i], p.sink, recent_from); };
+    const int L = r.L, keep = r.keep, words = (L + 31) / 32;
+    uint32_t *bits = s_dyn + (KEYS > 0 ? 2 * ((p.slots + 3) / 4 * 4) : p.cached);
+    PlanKeys<KEYS> keys;
+    keys.mass = p.mass + unit * p.slots;
+    keys.pos = p.pos + unit * p.slots;
+    keys.held = s_dyn;
+    keys.L = L;
+    keys.cached = p.cached;
+    keys.sink = p.sink;
+    keys.oldest = (int)min((int64_t)INT32_MAX, max((int64_t)INT32_MIN, oldest));
+    keys.load(tid, p.slots);
+    auto no_bins = [&] {
+        for (int i = tid; i < kBins / 4; i += kPlanThreads)
+            reinterpret_cast<int4 *>(s_bins)[i] = make_int4(0, 0, 0, 0);
+    };
+    no_bins();
+    __syncthreads();
 
     // Protected slots, and the range of the others' keys.
     uint32_t lo = kSafeKey, hi = 0;
     int safe = 0;
-    for (int i = tid; i < L; i += kPlanThreads) {
-        const uint32_t k = plan_key(mass[i], pos[i], p.sink, recent_from);
-        if (held)
-            keys[i] = k;
-        if (k == kSafeKey) {
-            ++safe;
-        } else {
-            lo = min(lo, k);
-            hi = max(hi, k);
-        }
-    }
-    if (tid == 0) {
-        s_lo = kSafeKey;
-        s_hi = 0;
-    }
-    safe = plan_sum(safe, s_scratch, tid);
+    keys.each(tid, [&](int, uint32_t k) {
+        safe += k == kSafeKey ? 1 : 0;
+        lo = min(lo, k);     // (a protected slot's key changes nothing)
+        hi = max(hi, k + 1); // (that of a protected slot becomes 0)
+    });
+    safe = __reduce_add_sync(0xffffffffu, safe);
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     if (lane == 0) {
+        atomicAdd(&s_safe, safe);
         atomicMin(&s_lo, lo);
         atomicMax(&s_hi, hi);
     }
     __syncthreads();
-    lo = s_lo;
-    hi = s_hi;
+    safe = s_safe - (KEYS > 0 ? KEYS * kPlanThreads - L : 0);
 
-    // The least key that stays, `least`: with `all`, every slot of that key or
-    // above; otherwise every one above and the first `ties` of that key.
-    uint32_t least;
-    int ties = 0;
-    bool all = false;
-    if (keep <= safe) {
-        least = kSafeKey;
-        ties = keep;
-        all = keep == safe;
-    } else {
-        int k = keep - safe; // the k-th greatest key of [lo, hi] is looked for
-        for (;;) {
-            if (lo == hi) {
-                least = lo;
-                ties = k;
-                break;
+    // The open range [from, from + width]: of keys, or (`among`) of ~slot among the
+    // slots of key `tie`.
+    uint32_t from = s_lo, width = s_hi - 1 - s_lo, tie = 0;
+    int k = keep - safe, in = L - safe; // the k-th greatest of `in` slots there is looked for
+    bool among = keep <= safe;
+    auto ties = [&](uint32_t key) {
+        among = true;
+        tie = key;
+        from = ~(uint32_t)(L - 1);
+        width = L - 1;
+    };
+    if (among) {
+        ties(kSafeKey);
+        k = keep;
+        in = safe;
+    }
+    while (in > kPlanList && k < in) {
+        if (!among && width == 0)
+            ties(from);
+        const int shift = max(0, 24 - __clz(width)); // 256 bins over the range
+        if (among)
+            keys.each_rarely(tid, [&](int i, uint32_t key) {
+                if (key == tie && ~(uint32_t)i - from <= width)
+                    atomicAdd(&s_bins[(~(uint32_t)i - from) >> shift], 1);
+            });
+        else
+            keys.each(tid, [&](int, uint32_t key) { plan_count(smem_addr(s_bins), key - from, width, shift); });
+        __syncthreads();
+        if (warp == 0) { // from the top: a lane holds 8 bins
+            const int4 *at = reinterpret_cast<const int4 *>(s_bins) + 2 * (31 - lane);
+            const int4 x = at[0], y = at[1];
+            const int n[8] = {y.w, y.z, y.y, y.x, x.w, x.z, x.y, x.x};
+            const int sum = (n[0] + n[1]) + (n[2] + n[3]) + (n[4] + n[5]) + (n[6] + n[7]);
+            int before = sum;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, before, d);
+                before += lane >= d ? up : 0;
             }
-            const int shift = max(0, 24 - __clz(hi - lo)); // 256 bins over the range
-            for (int i = tid; i < kBins; i += kPlanThreads)
-                s_bins[i] = 0;
-            __syncthreads();
-            for (int i = tid; i < L; i += kPlanThreads) {
-                const uint32_t x = key_at(i);
-                if (x >= lo && x <= hi)
-                    atomicAdd(&s_bins[(x - lo) >> shift], 1);
-            }
-            __syncthreads();
-            if (warp == 0) { // from the top: a lane holds 8 bins
-                int n[8], sum = 0;
+            before -= sum;
+            if (before < k && before + sum >= k) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    n[j] = s_bins[kBins - 1 - (8 * lane + j)];
-                    sum += n[j];
+                    if (before < k && before + n[j] >= k) {
+                        s_from = (uint32_t)(kBins - 1 - (8 * lane + j)) << shift;
+                        s_k = k - before;
+                        s_in = n[j];
+                    }
+                    before += n[j];
                 }
-                int before = sum;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int up = __shfl_up_sync(0xffffffffu, before, d);
-                    before += lane >= d ? up : 0;
-                }
-                before -= sum;
-                if (before < k && before + sum >= k) {
-                    int j = 0;
-                    while (before + n[j] < k)
-                        before += n[j++];
-                    const uint32_t bin = kBins - 1 - (8 * lane + j);
-                    s_k = k - before;
-                    s_all = k - before == n[j];
-                    const uint32_t from = lo + (bin << shift);
-                    s_lo = from;
-                    s_hi = from + min(hi - from, (1u << shift) - 1);
-                }
-            }
-            __syncthreads();
-            lo = s_lo;
-            hi = s_hi;
-            k = s_k;
-            all = s_all != 0;
-            if (all) {
-                least = lo;
-                break;
             }
         }
+        __syncthreads();
+        width = min(width - s_from, (1u << shift) - 1);
+        from += s_from;
+        k = s_k;
+        in = s_in;
+        no_bins();
+        __syncthreads();
+    }
+    // The last that stays: key `least`, and among equals slot `last`.
+    uint32_t least = among ? tie : from;
+    int last = among ? (int)~from : 0x7fffffff;
+    if (k < in) {
+        if (among)
+            keys.each_rarely(tid, [&](int i, uint32_t key) {
+                if (key == tie && ~(uint32_t)i - from <= width)
+                    s_list[atomicAdd(&s_count, 1)] = (uint64_t)key << 32 | ~(uint32_t)i;
+            });
+        else
+            keys.each(tid, [&](int i, uint32_t key) {
+                plan_append(smem_addr(&s_count), smem_addr(s_list), key - from, width, key, i);
+            });
+        __syncthreads();
+        if (tid < in) {
+            const uint64_t x = s_list[tid];
+            int above = 0;
+            for (int j = 0; j < in; ++j)
+                above += s_list[j] > x ? 1 : 0;
+            if (above == k - 1)
+                s_least = x;
+        }
+        __syncthreads();
+        least = (uint32_t)(s_least >> 32);
+        last = (int)~(uint32_t)s_least;
     }
 
-    // A bit for every slot that stays.
-    const int words = (L + 31) / 32, per_warp = (words + kPlanWarps - 1) / kPlanWarps;
-    const int w0 = warp * per_warp, w1 = min(words, w0 + per_warp);
-    int tied = 0; // slots of the least key before this warp's
-    if (!all) {
-        for (int w = w0; w < w1; ++w) {
-            const int i = w * 32 + lane;
-            tied += __popc(__ballot_sync(0xffffffffu, i < L && key_at(i) == least));
-        }
-        __syncthreads();
-        if (lane == 0)
-            s_scratch[warp] = tied;
-        __syncthreads();
-        tied = 0;
-        for (int w = 0; w < warp; ++w)
-            tied += s_scratch[w];
-    }
-    for (int w = w0; w < w1; ++w) {
-        const int i = w * 32 + lane;
-        const uint32_t k = i < L ? key_at(i) : 0;
-        uint32_t stay = __ballot_sync(0xffffffffu, i < L && (all ? k >= least : k > least));
-        if (!all) {
-            const uint32_t same = __ballot_sync(0xffffffffu, i < L && k == least);
-            stay |= __ballot_sync(0xffffffffu, (same >> lane & 1) && tied + __popc(same & ((1u << lane) - 1)) < ties);
-            tied += __popc(same);
-        }
-        if (lane == 0)
-            bits[w] = stay;
-    }
+    keys.mark(tid, bits, [&](int i, uint32_t key) { return (key > least) | ((key == least) & (i <= last)); });
     __syncthreads();
 
-    // Holes before the budget and slots that stay behind it, i-th to i-th.
-    const int per_thread = (words + kPlanThreads - 1) / kPlanThreads;
+    // Holes before the budget and slots that stay behind it, i-th to i-th.  Rows in
+    // registers have at most four words for each lane of one warp.
+    constexpr int kHands = KEYS > 0 ? 32 : kPlanThreads;
+    if (tid >= kHands)
+        return;
+    const int per_thread = (words + kHands - 1) / kHands;
     const int a = min(words, tid * per_thread), z = min(words, a + per_thread);
     auto holes_of = [&](int w) {
-        const int n = keep - w * 32;
+        const int n = keep - w * 32; // (below L)
         return n <= 0 ? 0u : ~bits[w] & (n >= 32 ? 0xffffffffu : (1u << n) - 1);
     };
     auto extra_of = [&](int w) {
-        const int n = keep - w * 32;
-        return n <= 0 ? bits[w] : n >= 32 ? 0u : bits[w] & ~((1u << n) - 1);
+        const int n = keep - w * 32, e = L - w * 32;
+        const uint32_t word = bits[w] & (e >= 32 ? 0xffffffffu : (1u << e) - 1); // of the row's slots
+        return n <= 0 ? word : n >= 32 ? 0u : word & ~((1u << n) - 1);
     };
     int2 mine = make_int2(0, 0);
     for (int w = a; w < z; ++w) {
@@ -252,13 +373,15 @@ __global__ void __launch_bounds__(kPlanThreads) evict_plan_kernel(const __grid_c
         upto.x += lane >= d ? x : 0;
         upto.y += lane >= d ? y : 0;
     }
-    if (lane == 31)
-        s_scan[warp] = upto;
-    __syncthreads();
     int2 at = make_int2(upto.x - mine.x, upto.y - mine.y);
-    for (int w = 0; w < warp; ++w) {
-        at.x += s_scan[w].x;
-        at.y += s_scan[w].y;
+    if (kHands > 32) {
+        if (lane == 31)
+            s_scan[warp] = upto;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) {
+            at.x += s_scan[w].x;
+            at.y += s_scan[w].y;
+        }
     }
     int32_t *out = reinterpret_cast<int32_t *>(p.moves + unit * p.max_moves);
     for (int w = a; w < z; ++w) {
@@ -267,7 +390,7 @@ __global__ void __launch_bounds__(kPlanThreads) evict_plan_kernel(const __grid_c
         for (uint32_t m = holes_of(w); m != 0; m &= m - 1)
             out[2 * at.y++ + 1] = w * 32 + __ffs(m) - 1;
     }
-    if (tid == kPlanThreads - 1)
+    if (tid == kHands - 1)
         p.num_moves[unit] = at.x;
 }
 
@@ -380,9 +503,24 @@ bool aligned16(const void *p)
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
-constexpr int kPlanCached = 32768; // keys in shared memory at most; longer rows read theirs again
+constexpr int kPlanCached = 32768; // keys in shared memory at most; longer rows make theirs again
 
-// Once per device: the plan kernel's shared memory.
+// Keys in registers up to 4096 slots (32 a thread), then in shared memory.
+struct PlanEntry {
+    int slots;
+    const void *kernel;
+};
+const PlanEntry kPlanTable[] = {
+    {1 * kPlanThreads, reinterpret_cast<const void *>(&evict_plan_kernel<1>)},
+    {4 * kPlanThreads, reinterpret_cast<const void *>(&evict_plan_kernel<4>)},
+    {9 * kPlanThreads, reinterpret_cast<const void *>(&evict_plan_kernel<9>)},
+    {17 * kPlanThreads, reinterpret_cast<const void *>(&evict_plan_kernel<17>)},
+    {32 * kPlanThreads, reinterpret_cast<const void *>(&evict_plan_kernel<32>)},
+    {kEvictMaxSlots, reinterpret_cast<const void *>(&evict_plan_kernel<0>)},
+};
+constexpr int kPlanLong = 5; // the last of them
+
+// Once per device: the last kernel's shared memory.
 bool plan_ready(int device)
 {
     constexpr int kDevices = 64;
@@ -390,8 +528,7 @@ bool plan_ready(int device)
     if (device < 0 || device >= kDevices)
         return false;
     if (!done[device])
-        done[device] = cudaFuncSetAttribute(reinterpret_cast<const void *>(&evict_plan_kernel),
-                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
+        done[device] = cudaFuncSetAttribute(kPlanTable[kPlanLong].kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             (kPlanCached + kEvictMaxSlots / 32) * 4) == cudaSuccess;
     return done[device];
 }
@@ -434,13 +571,21 @@ pkv_status pkv_evict_plan(const float *mass, const int32_t *slot_pos, int32_t nu
     p.sink = sink;
     p.recent = recent;
     p.max_moves = max_moves;
+    const PlanEntry *e = kPlanTable;
+    while (slots > e->slots)
+        ++e;
     p.cached = slots < kPlanCached ? slots : kPlanCached;
-    const size_t smem = ((size_t)p.cached + (slots + 31) / 32) * sizeof(uint32_t);
+    const size_t held = e == &kPlanTable[kPlanLong] ? (size_t)p.cached : 2 * ((size_t)(slots + 3) / 4 * 4);
+    const size_t words = e == &kPlanTable[kPlanLong] ? (slots + 31) / 32 : e->slots / 32;
+    const size_t smem = (held + words) * sizeof(uint32_t);
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || !plan_ready(dev))
         return PKV_ECUDA;
-    evict_plan_kernel<<<(unsigned)units, kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ECUDA;
+    void *args[] = {&p};
+    return cudaLaunchKernel(e->kernel, dim3((unsigned)units), dim3(kPlanThreads), args, smem,
+                            static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PKV_OK
+               : PKV_ECUDA;
 }
 
 pkv_status pkv_evict_apply(const pkv_cache_desc *desc, int32_t num_layers, void *const *k_caches,

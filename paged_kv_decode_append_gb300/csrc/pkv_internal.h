@@ -277,12 +277,10 @@ bool encode_tree_maps(const pkv_cache_desc &desc, const void *k_cache, const voi
 
 constexpr int kEvictMaxSlots = 1 << 19; // slots of a row of scores
 constexpr int kMaxMassBatch = 1024;
-constexpr int kMassMaxKeys = 0x7fffff00; // keys of a row (token arithmetic is 32-bit)
+constexpr int kMassMaxKeys = 0x7ffff000; // keys of a row (token arithmetic is 32-bit)
 
 struct MassShape {
     int group;        // num_q_heads / num_kv_heads
-    int heads;        // query heads of a query tile: all of a kv head's, or as many as it has columns
-    int head_tiles;   // query tiles side by side that hold them
     int q_tile;       // queries of a query tile
     size_t off_parts; // workspace: partial sums, after the tickets
     size_t bytes;

@@ -41,39 +41,45 @@ namespace pkv {
 namespace {
 
 constexpr int kMmKeys = 128;     // keys of a tile: M of every MMA
+constexpr int kMmCols = 128;     // (query, head) columns of a query tile
+constexpr int kMmWide = 8;       // steps from which a block has four key tiles
 constexpr int kFixCost = 2;      // positions that a key tile costs before its first step
 constexpr int kMinRange = 6;     // positions that are worth a CTA of their own
 constexpr int kMmMaxCtas = 160;  // persistent CTAs the workspace has room for
 constexpr int kMmKWarp = 0, kMmMmaWarp = 1, kMmQWarp = 2, kMmWalkWarp = 3, kMmSumWarp = 4;
-constexpr int kMmThreads = 384;
-constexpr int kMmBlocks = 8;     // blocks handed out and not yet done with
-constexpr int kMmReaders = 11;   // warps that read them
+constexpr int kMmThreads = 640;
+constexpr int kMmRuns = 8;       // runs of blocks handed out and not yet done with
+constexpr int kMmReaders = 19;   // warps that read them
+constexpr int kMmBadTiles = 16;  // key tiles whose bad pages are remembered
 
 template <int D> struct MmCfg {
-    static constexpr int kCols = D == 256 ? 64 : 128;          // (query, head) columns of a query tile
+    static constexpr int kMostTiles = D == 256 ? 2 : 4;        // key tiles of a block
     static constexpr uint32_t kKBytes = kMmKeys * D * 2;
-    static constexpr uint32_t kQBytes = kCols * D * 2;         // [D / 64][kCols rows][128 B], swizzled
     static constexpr int kKStages = D == 64 ? 8 : D == 128 ? 4 : 2;
-    static constexpr int kQStages = D == 64 ? 4 : 2;
+    static constexpr int kChunks = D / 64;                     // a query tile comes in chunks of 64 values
+    static constexpr uint32_t kQBytes = kMmCols * 128;         // chunk: 128 rows of 128 B, swizzled
+    static constexpr int kQStages = 5;
     static constexpr uint32_t kGroupStride = 8 * D * 2;        // 8 keys, all of head_dim
-    static constexpr uint32_t kQBlock = kCols * 128;
     static constexpr uint32_t kOffK = 0;
     static constexpr uint32_t kOffQ = kOffK + kKStages * kKBytes;
-    static constexpr uint32_t kOffLse = kOffQ + kQStages * kQBytes; // [group of warps][step parity][kCols]
-    static constexpr uint32_t kOffBar = kOffLse + 2 * 2 * 128 * 4;
+    static constexpr uint32_t kOffLse = kOffQ + kQStages * kQBytes; // [group of warps][its step's parity][128]
+    static constexpr uint32_t kOffHalf = kOffLse + 4 * 2 * 128 * 4; // [pair of groups][128 keys]
+    static constexpr uint32_t kOffBar = kOffHalf + 2 * 128 * 4;
     static constexpr uint32_t kSmem = kOffBar + 2048;
-    static constexpr uint32_t kTmemCols = 4 * kCols;           // two accumulators for each group of warps
+    static constexpr uint32_t kTmemCols = 4 * kMmCols;         // an accumulator for each group of warps
     static_assert(kSmem <= 232448, "shared memory");
 };
 
-// What the roles need to know of a block of keys.
-struct MmBlock {
+// What the roles need to know of a run: blocks of keys of one (row, kv head),
+// one after the other.  More than one block only where each has one key tile
+// and one step; a block with more steps is a run of its own.
+struct MmRun {
     int32_t b, g;           // row, kv head
-    int32_t tok, toks;      // first key, keys
-    int32_t tiles;          // key tiles: 1 or 2; 0: no more blocks
+    int32_t tok, blocks;    // first key, blocks
+    int32_t tiles;          // key tiles of a block: 1, 2 or 4; 0: no more runs
     int32_t first, queries; // the row's queries
-    int32_t len;            // cached tokens before the step
-    int32_t step0, step1;   // steps of this piece: query tile x head tile
+    int32_t len, keys;      // cached tokens before the step, and with it
+    int32_t step0, step1;   // steps of this piece: query tiles
     int32_t fresh, gone;
     int32_t piece0, pieces; // CTA of the block's first piece, pieces (1: whole)
 };
@@ -102,15 +108,16 @@ struct MmStart {
 
 struct MmBars {
     uint64_t k_full[8], k_empty[8];
-    uint64_t q_full[4], q_empty[4];
-    uint64_t s_full[4], s_free[4]; // [group of warps][accumulator]
-    uint64_t z_full[2];            // [group of warps]: its columns' lse are there
-    uint64_t block_full[kMmBlocks], block_empty[kMmBlocks];
+    uint64_t q_full[5], q_empty[5];
+    uint64_t s_full[4], s_free[4]; // [group of warps]
+    uint64_t z_full[4];            // [group of warps]: its columns' lse are there
+    uint64_t half_full[2], half_free[2]; // [pair of groups]: the one's sums for the other
+    uint64_t run_full[kMmRuns], run_empty[kMmRuns];
     uint64_t drain;
     MmStart start;
     int64_t scratch[kMmThreads / 32];
-    MmBlock block[kMmBlocks];
-    uint16_t bad[kMmBlocks][2]; // bit i: the page of a tile's keys 8 i .. 8 i + 7 is out of range
+    MmRun run[kMmRuns];
+    uint16_t bad[kMmBadTiles]; // bit i: the page of a tile's keys 8 i .. 8 i + 7 is out of range
     uint32_t tmem_base;
     int32_t abort;
 };
@@ -122,11 +129,12 @@ struct MmParams {
     float *mass;
     int32_t *pos, *err_flag;
     int32_t *tickets; // [CTA][tile][quarter]: pieces of a block's 32 keys that are there
-    float *parts;     // [CTA][begun before this CTA / in it][256 keys]
+    float *parts;     // [CTA][begun before this CTA / in it][512 keys]
     float q_scale;    // softmax_scale * log2(e)
     int batch, num_q_heads, num_kv_heads, group, total_q, max_blocks;
     int page_shift, box_shift, num_pages, layout, slots;
-    int heads, head_tiles, q_tile; // of a query tile
+    int q_tile;     // queries of a query tile
+    int most_tiles; // key tiles of a block
     uint32_t q_box_bytes, q_one_bytes;
 };
 
@@ -149,7 +157,7 @@ struct MmRow {
 __device__ __forceinline__ int mm_steps(const MmParams &p, const MmRow &r, int kb)
 {
     const int i0 = kb * r.tiles * kMmKeys - r.len; // the block's first key is seen from this query on
-    return r.steps - (i0 > 0 ? i0 / p.q_tile : 0) * p.head_tiles;
+    return r.steps - (i0 > 0 ? i0 / p.q_tile : 0);
 }
 __device__ __forceinline__ int64_t mm_cost(const MmRow &r, int steps)
 {
@@ -178,8 +186,8 @@ __device__ __forceinline__ MmRow mm_row(const MmParams &p, int b)
         return r;
     }
     r.queries = (int)n;
-    r.steps = (r.queries + p.q_tile - 1) / p.q_tile * p.head_tiles;
-    r.tiles = r.steps > 1 ? 2 : 1;
+    r.steps = (r.queries + p.q_tile - 1) / p.q_tile;
+    r.tiles = r.steps == 1 ? 1 : r.steps < kMmWide ? 2 : p.most_tiles;
     const int size = r.tiles * kMmKeys;
     r.blocks = (int)((keys + size - 1) / size);
     r.full = (int)min((int64_t)r.blocks, ((int64_t)r.len + p.q_tile - 1) / size + 1);
@@ -287,13 +295,13 @@ __device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity, MmBars &
     return __all_sync(0xffffffffu, done);
 }
 
-// ---------------------------------------------------------------- blocks
+// ---------------------------------------------------------------- runs
 
-// One warp cuts the CTA's range into blocks, in order.
+// One warp cuts the CTA's range into runs, in order.
 __device__ void mm_walk(const MmParams &p, MmBars &bars, const MmStart &from, int lane)
 {
     int n = 0, b = from.b, g = from.g, kb = 0;
-    int64_t at = from.at, left = from.left, off = from.off;
+    int64_t at = from.at, left = from.left, off = from.off; // (off: within the block)
     MmRow r = mm_row(p, b);
     MmRow then = r;
     int fresh = 0, gone = 0, next_fresh = 0, next_gone = 0;
@@ -312,7 +320,7 @@ __device__ void mm_walk(const MmParams &p, MmBars &bars, const MmStart &from, in
     }
     bool ahead = false; // the next row is read
     for (;;) {
-        MmBlock s;
+        MmRun s;
         s.tiles = 0;
         while (left > 0) {
             if (!ahead && b + 1 < p.batch) {
@@ -332,50 +340,71 @@ __device__ void mm_walk(const MmParams &p, MmBars &bars, const MmStart &from, in
                 }
                 continue;
             }
-            const int steps = mm_steps(p, r, kb), t = r.tiles;
-            const int64_t size = mm_cost(r, steps), take = min(size - off, left);
-            auto step_at = [&](int64_t x) { // first step whose position is x or more
-                return (int)max((int64_t)0, min((int64_t)steps, (x + t - 1) / t - kFixCost));
-            };
-            const int s0 = step_at(off), s1 = step_at(off + take);
-            const int64_t start = at - off; // of the block
-            const int block = kb;
-            at += take;
-            left -= take;
-            off += take;
-            if (off >= size) {
-                off = 0;
-                ++kb;
+            const int t = r.tiles;
+            s.piece0 = blockIdx.x;
+            s.pieces = 1;
+            s.blocks = 1;
+            int block = kb;
+            if (r.steps == 1) { // blocks of one step: those whose step lies in the range
+                constexpr int kSize = kFixCost + 1;
+                const int64_t most = (int64_t)(r.blocks - kb) * kSize - off, take = min(most, left);
+                const int first = off > kFixCost ? kb + 1 : kb;
+                // positions from block kb's start; a step at or past them belongs to the next CTA
+                const int end = (int)((off + take + kSize - 1 - kFixCost) / kSize) + kb;
+                left -= take;
+                at += take;
+                off += take;
+                kb += (int)(off / kSize);
+                off -= (int64_t)(off / kSize) * kSize;
+                if (first >= end)
+                    continue;
+                block = first;
+                s.blocks = end - first;
+                s.step0 = 0;
+                s.step1 = 1;
+            } else {
+                const int steps = mm_steps(p, r, kb);
+                const int64_t size = mm_cost(r, steps), take = min(size - off, left);
+                const int shift = t >> 1; // log2 of t
+                auto step_at = [&](int64_t x) { // first step whose position is x or more
+                    return (int)max((int64_t)0, min((int64_t)steps, ((x + t - 1) >> shift) - kFixCost));
+                };
+                const int s0 = step_at(off), s1 = step_at(off + take);
+                const int64_t start = at - off; // of the block
+                at += take;
+                left -= take;
+                off += take;
+                if (off >= size) {
+                    off = 0;
+                    ++kb;
+                }
+                if (s0 >= s1)
+                    continue;
+                s.step0 = r.steps - steps + s0;
+                s.step1 = r.steps - steps + s1;
+                if (s1 - s0 < steps) {
+                    s.piece0 = from.cut.of(start + (int64_t)t * kFixCost);
+                    s.pieces = from.cut.of(start + (int64_t)t * (kFixCost + steps - 1)) - s.piece0 + 1;
+                }
             }
-            if (s0 >= s1)
-                continue;
             s.b = b;
             s.g = g;
             s.tok = block * t * kMmKeys;
-            s.toks = min(t * kMmKeys, r.len + r.queries - s.tok);
             s.tiles = t;
             s.first = r.first;
             s.queries = r.queries;
             s.len = r.len;
-            s.step0 = r.steps - steps + s0;
-            s.step1 = r.steps - steps + s1;
+            s.keys = r.len + r.queries;
             s.fresh = fresh;
             s.gone = gone;
-            s.piece0 = blockIdx.x;
-            s.pieces = 1;
-            if (s1 - s0 < steps) {
-                s.piece0 = from.cut.of(start + (int64_t)t * kFixCost);
-                s.pieces = from.cut.of(start + (int64_t)t * (kFixCost + steps - 1)) - s.piece0 + 1;
-            }
             break;
         }
-        const int slot = n % kMmBlocks;
-        if (n >= kMmBlocks && !mm_wait(&bars.block_empty[slot], (uint32_t)(n / kMmBlocks - 1) & 1, bars, p.err_flag))
+        const int slot = n % kMmRuns;
+        if (n >= kMmRuns && !mm_wait(&bars.run_empty[slot], (uint32_t)(n / kMmRuns - 1) & 1, bars, p.err_flag))
             return;
         if (lane == 0) {
-            bars.block[slot] = s;
-            bars.bad[slot][0] = bars.bad[slot][1] = 0;
-            mbar_arrive(&bars.block_full[slot]);
+            bars.run[slot] = s;
+            mbar_arrive(&bars.run_full[slot]);
         }
         ++n;
         if (s.tiles == 0)
@@ -383,27 +412,27 @@ __device__ void mm_walk(const MmParams &p, MmBars &bars, const MmStart &from, in
     }
 }
 
-// The n-th block; a role that gave up sees the end.
-__device__ __forceinline__ MmBlock mm_block(const MmParams &p, MmBars &bars, int n)
+// The n-th run; a role that gave up sees the end.
+__device__ __forceinline__ MmRun mm_run(const MmParams &p, MmBars &bars, int n)
 {
-    MmBlock s;
-    if (mm_wait(&bars.block_full[n % kMmBlocks], (uint32_t)(n / kMmBlocks) & 1, bars, p.err_flag))
-        s = bars.block[n % kMmBlocks];
+    MmRun s;
+    if (mm_wait(&bars.run_full[n % kMmRuns], (uint32_t)(n / kMmRuns) & 1, bars, p.err_flag))
+        s = bars.run[n % kMmRuns];
     else
         s.tiles = 0;
     return s;
 }
-__device__ __forceinline__ void mm_block_done(MmBars &bars, int n, int lane)
+__device__ __forceinline__ void mm_run_done(MmBars &bars, int n, int lane)
 {
     __syncwarp();
     if (lane == 0)
-        mbar_arrive(&bars.block_empty[n % kMmBlocks]);
+        mbar_arrive(&bars.run_empty[n % kMmRuns]);
 }
 
 // ---------------------------------------------------------------- loads
 
 // One warp loads all key tiles, one box per lane: boxes of min(page, 64) keys, at
-// most 16 a tile.  A page id outside the pool loads nothing and marks the block.
+// most 16 a tile.  A page id outside the pool loads nothing and marks the tile.
 template <int D>
 __device__ void mm_load_k(const MmParams &p, const MmMaps &maps, uint8_t *smem, MmBars &bars, int lane)
 {
@@ -411,66 +440,57 @@ __device__ void mm_load_k(const MmParams &p, const MmMaps &maps, uint8_t *smem, 
     const int bsh = p.box_shift, boxes = kMmKeys >> bsh;
     const uint32_t box_bytes = (uint32_t)(1 << bsh) * D * 2;
     const bool nhd = p.layout == PKV_NHD;
-    int slot = 0, issued = 0;
+    int n = 0, slot = 0, issued = 0;
     uint32_t round = 0; // times the ring has been filled
-    int id[2], next_id[2];
-    auto pages = [&](const MmBlock &s, int (&to)[2]) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int in = j * kMmKeys + (lane << bsh);
-            to[j] = lane < boxes && j < s.tiles && in < s.toks
-                        ? p.table[(int64_t)s.b * p.max_blocks + ((s.tok + in) >> p.page_shift)]
-                        : 0;
-        }
+    MmRun s = mm_run(p, bars, 0);
+    int tok = s.tok, end = s.tok + s.blocks * s.tiles * kMmKeys;
+    auto page_of = [&](int at) { // this lane's page of the tile at `at`
+        at += lane << bsh;
+        return lane < boxes && at < s.keys ? p.table[(int64_t)s.b * p.max_blocks + (at >> p.page_shift)] : 0;
     };
-    MmBlock s = mm_block(p, bars, 0);
-    if (s.tiles > 0)
-        pages(s, id);
-    bool going = true;
-    for (int n = 0; s.tiles > 0 && going; ++n) {
-        const MmBlock next = mm_block(p, bars, n + 1);
-        if (next.tiles > 0)
-            pages(next, next_id);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (j >= s.tiles || !going)
-                continue;
-            if (round > 0 && !mm_wait(&bars.k_empty[slot], (round - 1) & 1, bars, p.err_flag)) {
-                going = false;
-                continue;
-            }
-            const int in = j * kMmKeys + (lane << bsh), tok = s.tok + in;
-            const bool want = lane < boxes && in < s.toks;
-            const bool good = want && id[j] >= 1 && id[j] < p.num_pages;
-            const uint32_t count = __popc(__ballot_sync(0xffffffffu, good));
-            const uint32_t miss = __ballot_sync(0xffffffffu, want && !good);
-            if (miss != 0 && lane == 0) {
-                uint32_t bits = 0; // a bit for 8 keys
-                for (uint32_t m = miss; m != 0; m &= m - 1)
-                    bits |= ((1u << (1 << bsh >> 3)) - 1) << ((__ffs(m) - 1) << bsh >> 3);
-                *(volatile uint16_t *)&bars.bad[n % kMmBlocks][j] = (uint16_t)bits;
-                set_error(p.err_flag, PKV_ERR_PAGE);
-            }
-            if (lane == 0)
-                mbar_arrive_expect_tx(&bars.k_full[slot], count * box_bytes);
-            __syncwarp();
-            if (good) {
-                const int in_page = tok & ((1 << p.page_shift) - 1);
-                const int c3 = nhd ? ((id[j] << p.page_shift) + in_page) >> 3 : in_page >> 3;
-                const int c4 = nhd ? s.g : id[j] * p.num_kv_heads + s.g;
-                tma_load_5d_plain(smem + C::kOffK + slot * C::kKBytes + lane * box_bytes, &maps.k, 0, 0, 0, c3, c4,
-                                  &bars.k_full[slot]);
-            }
-            ++issued;
-            if (++slot == C::kKStages) {
-                slot = 0;
-                ++round;
-            }
+    int id = s.tiles > 0 ? page_of(tok) : 0;
+    while (s.tiles > 0) {
+        const int at = tok + (lane << bsh), g = s.g, page = id;
+        const bool want = lane < boxes && at < s.keys; // (of tiles behind the row's end, none)
+        const bool good = want && page >= 1 && page < p.num_pages;
+        // the page of the next tile, a tile ahead
+        const int then = tok + kMmKeys;
+        if (then >= end) {
+            mm_run_done(bars, n, lane);
+            s = mm_run(p, bars, ++n);
+            tok = s.tok;
+            end = s.tok + s.blocks * s.tiles * kMmKeys;
+        } else {
+            tok = then;
         }
-        mm_block_done(bars, n, lane);
-        s = next;
-        id[0] = next_id[0];
-        id[1] = next_id[1];
+        if (s.tiles > 0)
+            id = page_of(tok);
+        if (round > 0 && !mm_wait(&bars.k_empty[slot], (round - 1) & 1, bars, p.err_flag))
+            break;
+        const uint32_t count = __popc(__ballot_sync(0xffffffffu, good));
+        const uint32_t miss = __ballot_sync(0xffffffffu, want && !good);
+        if (lane == 0) {
+            uint32_t bits = 0; // a bit for 8 keys
+            for (uint32_t m = miss; m != 0; m &= m - 1)
+                bits |= ((1u << (1 << bsh >> 3)) - 1) << ((__ffs(m) - 1) << bsh >> 3);
+            *(volatile uint16_t *)&bars.bad[issued % kMmBadTiles] = (uint16_t)bits;
+            if (miss != 0)
+                set_error(p.err_flag, PKV_ERR_PAGE);
+            mbar_arrive_expect_tx(&bars.k_full[slot], count * box_bytes);
+        }
+        __syncwarp();
+        if (good) {
+            const int in_page = at & ((1 << p.page_shift) - 1);
+            const int c3 = nhd ? ((page << p.page_shift) + in_page) >> 3 : in_page >> 3;
+            const int c4 = nhd ? g : page * p.num_kv_heads + g;
+            tma_load_5d_plain(smem + C::kOffK + slot * C::kKBytes + lane * box_bytes, &maps.k, 0, 0, 0, c3, c4,
+                              &bars.k_full[slot]);
+        }
+        ++issued;
+        if (++slot == C::kKStages) {
+            slot = 0;
+            ++round;
+        }
     }
     // Copies still in flight (a role gave up): they land before the CTA ends.
     for (int k = issued > C::kKStages ? issued - C::kKStages : 0; k < issued; ++k)
@@ -486,29 +506,30 @@ __device__ void mm_load_q(const MmParams &p, const MmMaps &maps, uint8_t *smem, 
     uint32_t round = 0;
     bool going = true;
     for (int n = 0; going; ++n) {
-        const MmBlock s = mm_block(p, bars, n);
+        const MmRun s = mm_run(p, bars, n);
         if (s.tiles == 0)
             break;
         const bool one = s.queries == 1; // a box of one query: no other row's are fetched
-        for (int st = s.step0; st < s.step1; ++st) {
-            if (round > 0 && !mm_wait(&bars.q_empty[slot], (round - 1) & 1, bars, p.err_flag)) {
-                going = false;
-                break;
+        const uint32_t bytes = one ? p.q_one_bytes : p.q_box_bytes;
+        for (int st = s.step0; st < s.step1 && going; ++st)
+            for (int c = 0; c < C::kChunks; ++c) {
+                if (round > 0 && !mm_wait(&bars.q_empty[slot], (round - 1) & 1, bars, p.err_flag)) {
+                    going = false;
+                    break;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars.q_full[slot], bytes);
+                    tma_load_3d_plain(smem + C::kOffQ + slot * C::kQBytes, one ? &maps.q_one : &maps.q, c * 64,
+                                      s.g * p.group, s.first + st * p.q_tile, &bars.q_full[slot]);
+                }
+                __syncwarp();
+                ++issued;
+                if (++slot == C::kQStages) {
+                    slot = 0;
+                    ++round;
+                }
             }
-            const int t = p.head_tiles == 1 ? st : st / p.head_tiles, h = st - t * p.head_tiles;
-            if (lane == 0)
-                mbar_arrive_expect_tx(&bars.q_full[slot], (one ? p.q_one_bytes : p.q_box_bytes) * (D / 64));
-            __syncwarp();
-            if (lane < D / 64)
-                tma_load_3d_plain(smem + C::kOffQ + slot * C::kQBytes + lane * C::kQBlock, one ? &maps.q_one : &maps.q,
-                                  lane * 64, s.g * p.group + h * p.heads, s.first + t * p.q_tile, &bars.q_full[slot]);
-            ++issued;
-            if (++slot == C::kQStages) {
-                slot = 0;
-                ++round;
-            }
-        }
-        mm_block_done(bars, n, lane);
+        mm_run_done(bars, n, lane);
     }
     for (int k = issued > C::kQStages ? issued - C::kQStages : 0; k < issued; ++k)
         mbar_wait(&bars.q_full[k % C::kQStages], (uint32_t)(k / C::kQStages) & 1);
@@ -543,73 +564,118 @@ __device__ __forceinline__ void mm_commit(uint64_t *bar)
                  : "memory");
 }
 
-// Columns of a step that hold a (query, head).
-__device__ __forceinline__ int mm_cols(const MmParams &p, int queries, int t, int h)
-{
-    return p.head_tiles == 1 ? min(p.q_tile, queries - t * p.q_tile) * p.heads
-                             : min(p.heads, p.group - h * p.heads);
-}
-
 template <int D>
 __device__ void mm_mma(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t tmem, int lane)
 {
     using C = MmCfg<D>;
+    constexpr int kChunks = C::kChunks;
     const uint64_t kd0 = tc_sw128_desc(smem_addr(smem + C::kOffK), 16, C::kGroupStride);
     const uint64_t qd0 = tc_sw128_desc(smem_addr(smem + C::kOffQ), 16, 1024);
-    int tile = 0; // key tiles before the block
-    uint32_t used[2] = {0, 0};
-    int q_slot = 0;
-    uint32_t q_par = 0;
+    uint32_t k_slot0 = 0, k_par0 = 0; // of the block's first key tile
+    uint32_t seq = 0;                 // (key tile, step) pairs before
+    uint32_t q_slot0 = 0, q_par0 = 0; // of the step's first chunk
     bool going = true;
     for (int n = 0; going; ++n) {
-        const MmBlock s = mm_block(p, bars, n);
+        const MmRun s = mm_run(p, bars, n);
         // warp-uniform values (read from one lane) stay in uniform registers
         const int tiles = __shfl_sync(0xffffffffu, s.tiles, 0);
         if (tiles == 0)
             break;
         const int step0 = __shfl_sync(0xffffffffu, s.step0, 0), step1 = __shfl_sync(0xffffffffu, s.step1, 0);
-        const int queries = __shfl_sync(0xffffffffu, s.queries, 0);
-        mm_block_done(bars, n, lane);
+        const int queries = __shfl_sync(0xffffffffu, s.queries, 0), blocks = __shfl_sync(0xffffffffu, s.blocks, 0);
+        // key tiles of the run that lie before the row's end
+        const int real = __shfl_sync(0xffffffffu, (s.keys - s.tok + kMmKeys - 1) / kMmKeys, 0);
+        mm_run_done(bars, n, lane);
 #pragma unroll 1
-        for (int st = step0; st < step1 && going; ++st) {
-            const int t = p.head_tiles == 1 ? st : st / p.head_tiles, h = st - t * p.head_tiles;
-            const int cols = (mm_cols(p, queries, t, h) + 15) & ~15;
-            const uint32_t idesc = tc_idesc_bf16(kMmKeys, 0, false, false) | (uint32_t)(cols >> 3) << 17;
-            if (!mm_wait(&bars.q_full[q_slot], q_par, bars, p.err_flag)) {
-                going = false;
-                break;
-            }
-            const uint64_t qd = qd0 + (uint64_t)(q_slot * C::kQBytes >> 4);
+        for (int blk = 0; blk < blocks && going; ++blk) {
 #pragma unroll 1
-            for (int j = 0; j < tiles; ++j) {
-                const int x = tile + j, k_slot = x % C::kKStages, w = x & 1;
-                const uint32_t u = w ? used[1] : used[0], buf = 2 * w + (u & 1);
-                if ((st == step0 && !mm_wait(&bars.k_full[k_slot], (uint32_t)(x / C::kKStages) & 1, bars, p.err_flag)) ||
-                    (u >= 2 && !mm_wait(&bars.s_free[buf], ((u >> 1) - 1) & 1, bars, p.err_flag))) {
-                    going = false;
-                    break;
+            for (int st = step0; st < step1 && going; ++st) {
+                const int cols = (min(p.q_tile, queries - st * p.q_tile) * p.group + 15) & ~15;
+                const uint32_t idesc = tc_idesc_bf16(kMmKeys, 0, false, false) | (uint32_t)(cols >> 3) << 17;
+                const bool leaves = blk == blocks - 1; // the query tile is not wanted any more
+                uint32_t q_slot = q_slot0, q_par = q_par0;
+                auto q_next = [&] {
+                    if (++q_slot == C::kQStages) {
+                        q_slot = 0;
+                        q_par ^= 1;
+                    }
+                };
+                // the key tile and the accumulator of tile j are there
+                auto tile_ready = [&](int j) {
+                    const uint32_t u = seq + j, buf = u & 3;
+                    const uint32_t slot = k_slot0 + j, over = slot >= C::kKStages ? 1 : 0;
+                    return (st > step0 ||
+                            mm_wait(&bars.k_full[slot - over * C::kKStages], k_par0 ^ over, bars, p.err_flag)) &&
+                           (u < 4 || mm_wait(&bars.s_free[buf], ((u >> 2) - 1) & 1, bars, p.err_flag));
+                };
+                auto k_desc = [&](int j) {
+                    const uint32_t slot = k_slot0 + j;
+                    return kd0 + (uint64_t)((slot >= C::kKStages ? slot - C::kKStages : slot) * C::kKBytes >> 4);
+                };
+                if (kChunks <= 2) { // tile by tile, so that three accumulators can be read meanwhile
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        if (blk == 0 && !mm_wait(&bars.q_full[q_slot], q_par, bars, p.err_flag))
+                            going = false;
+                        q_next();
+                    }
+#pragma unroll 1
+                    for (int j = 0; j < tiles && going; ++j) {
+                        if (!tile_ready(j)) {
+                            going = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t buf = (seq + j) & 3;
+                        const uint64_t kd = k_desc(j);
+                        uint32_t slot = q_slot0;
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c) {
+                            if (blk * tiles + j < real)
+                                mm_mma4(tmem + buf * kMmCols, kd + (uint64_t)(c * 1024 >> 4),
+                                        qd0 + (uint64_t)(slot * C::kQBytes >> 4), idesc, c > 0 ? 1u : 0u);
+                            slot = slot + 1 == C::kQStages ? 0 : slot + 1;
+                        }
+                        mm_commit(&bars.s_full[buf]);
+                    }
+                } else { // chunk by chunk past the (at most two) key tiles: a query tile fills the ring
+#pragma unroll 1
+                    for (int c = 0; c < kChunks && going; ++c) {
+                        if (blk == 0 && !mm_wait(&bars.q_full[q_slot], q_par, bars, p.err_flag)) {
+                            going = false;
+                            break;
+                        }
+#pragma unroll 1
+                        for (int j = 0; j < tiles; ++j) {
+                            if (c == 0 && !tile_ready(j)) {
+                                going = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint32_t buf = (seq + j) & 3;
+                            if (blk * tiles + j < real)
+                                mm_mma4(tmem + buf * kMmCols, k_desc(j) + (uint64_t)(c * 1024 >> 4),
+                                        qd0 + (uint64_t)(q_slot * C::kQBytes >> 4), idesc, c > 0 ? 1u : 0u);
+                            if (c == kChunks - 1)
+                                mm_commit(&bars.s_full[buf]);
+                        }
+                        if (leaves)
+                            mm_commit(&bars.q_empty[q_slot]);
+                        q_next();
+                    }
                 }
-                tc_fence_after();
-                const uint64_t kd = kd0 + (uint64_t)(k_slot * C::kKBytes >> 4);
-#pragma unroll 1
-                for (int blk = 0; blk < D / 64; ++blk)
-                    mm_mma4(tmem + buf * C::kCols, kd + (uint64_t)(blk * 1024 >> 4),
-                            qd + (uint64_t)(blk * C::kQBlock >> 4), idesc, blk > 0 ? 1u : 0u);
-                mm_commit(&bars.s_full[buf]);
-                if (w)
-                    ++used[1];
-                else
-                    ++used[0];
+                seq += tiles;
+                if (leaves) {
+                    q_slot0 = q_slot;
+                    q_par0 = q_par;
+                }
             }
-            mm_commit(&bars.q_empty[q_slot]);
-            if (++q_slot == C::kQStages) {
-                q_slot = 0;
-                q_par ^= 1;
+            k_slot0 += tiles;
+            if (k_slot0 >= C::kKStages) {
+                k_slot0 -= C::kKStages;
+                k_par0 ^= 1;
             }
         }
-        for (int j = 0; j < tiles; ++j)
-            mm_commit(&bars.k_empty[(tile + j) % C::kKStages]);
-        tile += tiles;
     }
     mm_commit(&bars.drain); // the commits have arrived before the CTA ends
     mbar_wait(&bars.drain, 0);
@@ -617,6 +683,8 @@ __device__ void mm_mma(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
 
 // ---------------------------------------------------------------- sums
 
+#define PKV_O8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
+                  "=r"(r[i + 6]), "=r"(r[i + 7])
 #define PKV_R8(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
                   "+r"(r[i + 6]), "+r"(r[i + 7])
 __device__ __forceinline__ void mm_ld32(uint32_t taddr, uint32_t (&r)[32])
@@ -624,7 +692,7 @@ __device__ __forceinline__ void mm_ld32(uint32_t taddr, uint32_t (&r)[32])
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
                  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
                  "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-                 : PKV_R8(0), PKV_R8(8), PKV_R8(16), PKV_R8(24)
+                 : PKV_O8(0), PKV_O8(8), PKV_O8(16), PKV_O8(24)
                  : "r"(taddr)
                  : "memory");
 }
@@ -633,6 +701,7 @@ __device__ __forceinline__ void mm_ld_wait(uint32_t (&r)[32])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : PKV_R8(0), PKV_R8(8), PKV_R8(16), PKV_R8(24)::"memory");
 }
+#undef PKV_O8
 #undef PKV_R8
 
 // The sum of 2^(x scale + z) over 32 columns; z holds -lse log2(e).
@@ -670,118 +739,176 @@ __device__ __forceinline__ int mm_ticket(int32_t *ticket)
     return old;
 }
 
+// Adds y to a sum, with what earlier additions dropped.
+__device__ __forceinline__ void mm_add(float &sum, float &dropped, float y)
+{
+    y += dropped;
+    const float next = sum + y;
+    dropped = fabsf(next) < INFINITY ? y - (next - sum) : 0.f;
+    sum = next;
+}
+
 template <int D>
 __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t tmem, int warp, int lane)
 {
     using C = MmCfg<D>;
+    // Group w takes every fourth (key tile, step) pair of the CTA: of a block of
+    // four key tiles one of them, of two every other step of one.
     const int w = (warp - kMmSumWarp) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16) + 2 * w * C::kCols;
+    const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + w * kMmCols;
     float *lse = reinterpret_cast<float *>(smem + C::kOffLse) + w * 256;
-    int tile = 0;
-    uint32_t used = 0;
+    float *half = reinterpret_cast<float *>(smem + C::kOffHalf) + (w & 1) * 128;
+    // the (query, head) of this thread's column, whose lse it fetches for the group
+    const int my_query = r / p.group, my_head = r - my_query * p.group;
+    uint32_t tile0 = 0;
+    uint32_t q0 = 0; // chunks of query tiles before the run
+    uint32_t seq = 0, taken = 0, staged = 0, halves = 0; // pairs before the run, taken by the group; lse; shared blocks
     for (int n = 0;; ++n) {
-        const MmBlock s = mm_block(p, bars, n);
+        const MmRun s = mm_run(p, bars, n);
         if (s.tiles == 0)
             return;
-        const int j = (w - tile) & 1;
-        tile += s.tiles;
-        if (j >= s.tiles) {
-            mm_block_done(bars, n, lane);
-            continue;
-        }
-        const int tok = s.tok + j * kMmKeys, key = tok + r;
-        // -lse log2(e) of this thread's column of a step
-        auto lse_at = [&](int st) {
-            const int t = p.head_tiles == 1 ? st : st / p.head_tiles, h = st - t * p.head_tiles;
-            float z = 0.f;
-            if (r < mm_cols(p, s.queries, t, h)) {
-                const int i = r / p.heads;
-                z = p.lse[((int64_t)s.first + t * p.q_tile + i) * p.num_q_heads + s.g * p.group + h * p.heads +
-                          (r - i * p.heads)];
-                z = z == -INFINITY ? z : z * -1.4426950408889634f;
-            }
-            return z;
+        const int steps = s.step1 - s.step0, rank = (w - seq) & 3;
+        // tile within the block, first step and block of this group's, the way to the next
+        const int j = s.tiles == 4 ? rank : s.tiles == 2 ? rank & 1 : 0;
+        int st = s.step0 + (s.tiles == 2 ? rank >> 1 : 0), blk = s.tiles == 1 ? rank : 0;
+        const int next_step = s.tiles == 4 ? 1 : 2;
+        const bool shared = s.tiles == 2 && steps > 1; // with the group that has the other steps
+        const bool ends = !shared || ((s.step1 - st) & 1) != 0; // this group finishes the block
+        const float *z_at = p.lse + ((int64_t)s.first + my_query) * p.num_q_heads + s.g * p.group + my_head;
+        auto lse_at = [&](int step) {
+            const int q = step * p.q_tile;
+            return my_query < p.q_tile && q + my_query < s.queries ? z_at[(int64_t)q * p.num_q_heads] : 0.f;
         };
-        float z = lse_at(s.step0), sum = 0.f, dropped = 0.f;
-        for (int st = s.step0; st < s.step1; ++st) {
-            const int t = p.head_tiles == 1 ? st : st / p.head_tiles, h = st - t * p.head_tiles;
-            const int cols = mm_cols(p, s.queries, t, h);
-            float *zs = lse + (used & 1) * 128;
-            zs[r] = z; // (all have read what was there two steps ago: they have been at the barrier since)
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bars.z_full[w]);
-            if (st + 1 < s.step1)
-                z = lse_at(st + 1);
-            const uint32_t buf = used & 1;
-            if (!mm_wait(&bars.z_full[w], used & 1, bars, p.err_flag) ||
-                !mm_wait(&bars.s_full[2 * w + buf], (used >> 1) & 1, bars, p.err_flag))
+        float z = 0.f, sum = 0.f, dropped = 0.f, was = 0.f;
+        if (st < s.step1 && blk < s.blocks)
+            z = lse_at(st);
+        bool new_z = true, begins = true;
+        const int64_t unit = ((int64_t)s.b * p.num_kv_heads + s.g) * p.slots;
+#pragma unroll 1
+        while (st < s.step1 && blk < s.blocks) {
+            const int tok = s.tok + (blk * s.tiles + j) * kMmKeys, key = tok + r;
+            const bool fresh = key >= s.fresh, mine = ends && key < s.keys;
+            if (begins) {
+                sum = dropped = was = 0.f;
+                if (mine && !fresh)
+                    was = p.mass[unit + key];
+            }
+            // (nothing to sum in a tile behind the row's end)
+            const int cols = tok < s.keys ? min(p.q_tile, s.queries - st * p.q_tile) * p.group : 0;
+            if (new_z) { // (all have read what was there two steps ago: they have been at the barrier since)
+                lse[(staged & 1) * 128 + r] = z == -INFINITY ? z : z * -1.4426950408889634f;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bars.z_full[w]);
+                ++staged;
+            }
+            const int now = st;
+            if (s.tiles == 1) {
+                blk += 4;
+            } else {
+                st += next_step;
+                if (st < s.step1)
+                    z = lse_at(st);
+            }
+            if ((new_z && !mm_wait(&bars.z_full[w], (staged - 1) & 1, bars, p.err_flag)) ||
+                !mm_wait(&bars.s_full[w], taken & 1, bars, p.err_flag))
                 return;
+            ++taken;
+            // What the MMAs have read is free: the key tile after its last step, the
+            // query tile after its last key tile.  (Told from here: a commit of the
+            // MMA warp's own for it would cost that warp more than an MMA does.)
+            const uint32_t tile = tile0 + (uint32_t)(tok - s.tok) / kMmKeys;
+            if (quarter == 0 && lane == 0) {
+                if (now == s.step1 - 1)
+                    mbar_arrive(&bars.k_empty[tile % C::kKStages]);
+                if (C::kChunks <= 2 && j == s.tiles - 1 && (s.tiles > 1 || blk >= s.blocks + 3))
+#pragma unroll
+                    for (int c = 0; c < C::kChunks; ++c)
+                        mbar_arrive(&bars.q_empty[(q0 + (now - s.step0) * C::kChunks + c) % C::kQStages]);
+            }
             tc_fence_after();
-            const uint32_t at = t_row + buf * C::kCols;
+            const float *zs = lse + ((staged - 1) & 1) * 128;
             // columns of queries before the key's own see nothing of it
-            const int blind = max(0, key - s.len - t * p.q_tile); // queries
-            const int seen = p.head_tiles == 1 ? blind * p.heads : blind > 0 ? C::kCols : 0;
-            const bool edge = tok + kMmKeys - 1 - s.len > t * p.q_tile;
+            const int seen = max(0, key - s.len - now * p.q_tile) * p.group;
+            const bool edge = tok + kMmKeys - 1 - s.len > now * p.q_tile;
             float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
             uint32_t x[32];
+            const int whole = edge ? 0 : cols & ~31;
 #pragma unroll 1
-            for (int c = 0; c < cols; c += 32) {
-                mm_ld32(at + c, x);
+            for (int c = 0; c < whole; c += 32) {
+                mm_ld32(acc + c, x);
                 mm_ld_wait(x);
-                if (!edge && c + 32 <= cols)
-                    mm_add32<false>(x, zs + c, p.q_scale, 0, 32, sum0, sum1);
-                else
-                    mm_add32<true>(x, zs + c, p.q_scale, seen - c, cols - c, sum0, sum1);
+                mm_add32<false>(x, zs + c, p.q_scale, 0, 32, sum0, sum1);
+            }
+#pragma unroll 1
+            for (int c = whole; c < cols; c += 32) {
+                mm_ld32(acc + c, x);
+                mm_ld_wait(x);
+                mm_add32<true>(x, zs + c, p.q_scale, seen - c, cols - c, sum0, sum1);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&bars.s_free[2 * w + buf]);
-            ++used;
-            // compensated: what an addition drops is added with the next
-            const float part = (sum0.x + sum1.x) + (sum0.y + sum1.y) + dropped;
-            const float next = sum + part;
-            dropped = part - (next - sum);
-            sum = next;
-            if (!(fabsf(sum) < INFINITY))
-                dropped = 0.f;
-        }
-        const bool bad = (*(volatile uint16_t *)&bars.bad[n % kMmBlocks][j] >> (r >> 3)) & 1;
-        const bool mine = tok + r < s.tok + s.toks && !bad;
-        bool last = true;
-        if (s.pieces > 1) {
-            float *part = p.parts + j * kMmKeys + r;
-            __stcg(part + (2 * blockIdx.x + (s.piece0 == blockIdx.x ? 1 : 0)) * 256, sum);
-            int32_t *ticket = p.tickets + (s.piece0 * 2 + j) * 4 + quarter;
-            __syncwarp();
-            int old = 0;
-            if (lane == 0)
-                old = mm_ticket(ticket);
-            last = __shfl_sync(0xffffffffu, old, 0) == s.pieces - 1;
-            __syncwarp();
-            if (last) {
-                if (lane == 0)
-                    *ticket = 0;
-                sum = __ldcg(part + (2 * s.piece0 + 1) * 256);
-                dropped = 0.f;
-                for (int c = 1; c < s.pieces; ++c) {
-                    const float y = __ldcg(part + 2 * (s.piece0 + c) * 256) + dropped, next = sum + y;
-                    dropped = y - (next - sum);
-                    sum = next;
-                    if (!(fabsf(sum) < INFINITY))
-                        dropped = 0.f;
+                mbar_arrive(&bars.s_free[w]);
+            mm_add(sum, dropped, (sum0.x + sum1.x) + (sum0.y + sum1.y));
+            new_z = begins = s.tiles == 1;
+            if (s.tiles > 1) {
+                new_z = true;
+                if (st < s.step1)
+                    continue;
+            } else {
+                new_z = false;
+            }
+            // the block's sums
+            if (shared) {
+                if (!ends) {
+                    if (halves > 0 && !mm_wait(&bars.half_free[w & 1], (halves - 1) & 1, bars, p.err_flag))
+                        return;
+                    half[r] = sum;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bars.half_full[w & 1]);
+                } else {
+                    if (!mm_wait(&bars.half_full[w & 1], halves & 1, bars, p.err_flag))
+                        return;
+                    mm_add(sum, dropped, half[r]);
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bars.half_free[w & 1]);
                 }
             }
+            bool last = ends;
+            if (ends && s.pieces > 1) {
+                float *part = p.parts + j * kMmKeys + r;
+                __stcg(part + (2 * blockIdx.x + (s.piece0 == blockIdx.x ? 1 : 0)) * 512, sum);
+                int32_t *ticket = p.tickets + (s.piece0 * 4 + j) * 4 + quarter;
+                __syncwarp();
+                int old = 0;
+                if (lane == 0)
+                    old = mm_ticket(ticket);
+                last = __shfl_sync(0xffffffffu, old, 0) == s.pieces - 1;
+                __syncwarp();
+                if (last) {
+                    if (lane == 0)
+                        *ticket = 0;
+                    sum = __ldcg(part + (2 * s.piece0 + 1) * 512);
+                    dropped = 0.f;
+                    for (int c = 1; c < s.pieces; ++c)
+                        mm_add(sum, dropped, __ldcg(part + 2 * (s.piece0 + c) * 512));
+                }
+            }
+            const bool bad = (*(volatile uint16_t *)&bars.bad[tile % kMmBadTiles] >> (r >> 3)) & 1;
+            if (last && mine && !bad) {
+                p.mass[unit + key] = was + sum;
+                if (fresh && p.pos != nullptr)
+                    p.pos[unit + key] = key + s.gone;
+            }
         }
-        if (last && mine) {
-            const int64_t to = ((int64_t)s.b * p.num_kv_heads + s.g) * p.slots + key;
-            const bool fresh = key >= s.fresh;
-            p.mass[to] = fresh ? sum : p.mass[to] + sum;
-            if (fresh && p.pos != nullptr)
-                p.pos[to] = key + s.gone;
-        }
-        mm_block_done(bars, n, lane);
+        halves += shared ? 1 : 0;
+        seq += (uint32_t)(s.tiles * steps * s.blocks);
+        tile0 += s.blocks * s.tiles;
+        q0 = (q0 + steps * C::kChunks) % C::kQStages;
+        mm_run_done(bars, n, lane);
     }
 }
 
@@ -812,13 +939,16 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bars.s_full[i], 1);
             mbar_init(&bars.s_free[i], 4);
+            mbar_init(&bars.z_full[i], 4);
         }
-        for (int i = 0; i < kMmBlocks; ++i) {
-            mbar_init(&bars.block_full[i], 1);
-            mbar_init(&bars.block_empty[i], kMmReaders);
+        for (int i = 0; i < kMmRuns; ++i) {
+            mbar_init(&bars.run_full[i], 1);
+            mbar_init(&bars.run_empty[i], kMmReaders);
         }
-        mbar_init(&bars.z_full[0], 4);
-        mbar_init(&bars.z_full[1], 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.half_full[i], 4);
+            mbar_init(&bars.half_free[i], 4);
+        }
         mbar_init(&bars.drain, 1);
         bars.abort = 0;
         mbar_init_fence();
@@ -855,15 +985,15 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 // ---------------------------------------------------------------- host side
 
 struct MmEntry {
-    int D, cols;
+    int D, most_tiles;
     const void *kernel;
     uint32_t smem;
 };
 
 const MmEntry kMmTable[] = {
-    {64, MmCfg<64>::kCols, reinterpret_cast<const void *>(&mass_kernel<64>), MmCfg<64>::kSmem},
-    {128, MmCfg<128>::kCols, reinterpret_cast<const void *>(&mass_kernel<128>), MmCfg<128>::kSmem},
-    {256, MmCfg<256>::kCols, reinterpret_cast<const void *>(&mass_kernel<256>), MmCfg<256>::kSmem},
+    {64, MmCfg<64>::kMostTiles, reinterpret_cast<const void *>(&mass_kernel<64>), MmCfg<64>::kSmem},
+    {128, MmCfg<128>::kMostTiles, reinterpret_cast<const void *>(&mass_kernel<128>), MmCfg<128>::kSmem},
+    {256, MmCfg<256>::kMostTiles, reinterpret_cast<const void *>(&mass_kernel<256>), MmCfg<256>::kSmem},
 };
 
 const MmEntry *mm_find(int D)
@@ -903,15 +1033,12 @@ pkv_status mass_shape(int batch, int total_q, int max_blocks, int num_q_heads, c
     if (batch < 0 || total_q < 0 || max_blocks < 1 || num_q_heads < 1 || num_q_heads % desc->num_kv_heads != 0)
         return PKV_EINVAL;
     s->group = num_q_heads / desc->num_kv_heads;
-    if (batch > kMaxMassBatch || desc->page_size < 8 || s->group > 128 ||
+    if (batch > kMaxMassBatch || desc->page_size < 8 || s->group > kMmCols ||
         (int64_t)total_q * num_q_heads >= ((int64_t)1 << 31))
         return PKV_EUNSUPPORTED;
-    const int cols = mm_find(desc->head_dim)->cols;
-    s->heads = s->group < cols ? s->group : cols;
-    s->head_tiles = (s->group + s->heads - 1) / s->heads;
-    s->q_tile = s->head_tiles == 1 ? cols / s->heads : 1;
-    s->off_parts = kMmMaxCtas * 8 * sizeof(int32_t);
-    s->bytes = 256 + s->off_parts + (size_t)kMmMaxCtas * 2 * 256 * sizeof(float);
+    s->q_tile = kMmCols / s->group;
+    s->off_parts = kMmMaxCtas * 16 * sizeof(int32_t);
+    s->bytes = 256 + s->off_parts + (size_t)kMmMaxCtas * 2 * 512 * sizeof(float);
     return PKV_OK;
 }
 
@@ -981,16 +1108,15 @@ pkv_status pkv_attn_mass(const pkv_cache_desc *desc, const void *k_cache, const 
     p.num_pages = desc->num_pages;
     p.layout = desc->layout;
     p.slots = slots;
-    p.heads = shape.heads;
-    p.head_tiles = shape.head_tiles;
     p.q_tile = shape.q_tile;
+    p.most_tiles = e->most_tiles;
     const int box_q = shape.q_tile < total_q ? shape.q_tile : total_q;
-    p.q_box_bytes = (uint32_t)box_q * shape.heads * 128;
-    p.q_one_bytes = (uint32_t)shape.heads * 128;
+    p.q_box_bytes = (uint32_t)box_q * shape.group * 128;
+    p.q_one_bytes = (uint32_t)shape.group * 128;
     MmMaps m;
     if (encode_group_map(&m.k, *desc, const_cast<void *>(k_cache), 1 << p.box_shift) != CUDA_SUCCESS ||
-        encode_q_map(&m.q, q, desc->head_dim, num_q_heads, total_q, shape.heads, box_q) != CUDA_SUCCESS ||
-        encode_q_map(&m.q_one, q, desc->head_dim, num_q_heads, total_q, shape.heads, 1) != CUDA_SUCCESS)
+        encode_q_map(&m.q, q, desc->head_dim, num_q_heads, total_q, shape.group, box_q) != CUDA_SUCCESS ||
+        encode_q_map(&m.q_one, q, desc->head_dim, num_q_heads, total_q, shape.group, 1) != CUDA_SUCCESS)
         return PKV_ECUDA;
     const int grid = sm_count(dev) < kMmMaxCtas ? sm_count(dev) : kMmMaxCtas;
     void *args[] = {&p, &m};

@@ -17,9 +17,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 8; // tokens of a CTA at most: one warp looks each up
-constexpr int kRopeAhead = 4;  // 32-byte items of a thread under way at once
+constexpr int kRopeAhead = 4; // 32-byte items of a thread under way at once
 
 struct RopeParams {
     const __nv_bfloat16 *q, *k, *v;
@@ -29,7 +27,7 @@ struct RopeParams {
     const int32_t *positions, *indptr, *evicted, *table, *seqlens;
     int32_t *err_flag;
     float attn_factor;
-    int tokens, per_cta, batch, num_q_heads, num_kv_heads, head_dim, rot_dim, interleaved;
+    int tokens, batch, num_q_heads, num_kv_heads, head_dim, rot_dim, interleaved;
     int max_blocks, page_shift, num_pages, layout;
 };
 
@@ -37,7 +35,7 @@ struct RopeParams {
 struct RopeToken {
     int64_t slot; // element of (token's slot, head 0) in the pools; -1: not appended
     int64_t pos;
-    int row, live; // live: rotated at all
+    int live;     // rotated at all
 };
 
 __device__ __forceinline__ bool rope_owns(const RopeParams &p, int b, int t)
@@ -46,22 +44,19 @@ __device__ __forceinline__ bool rope_owns(const RopeParams &p, int b, int t)
     return first >= 0 && first <= t && t < end && end <= p.tokens;
 }
 
-// Row of token t, or -1 (a whole warp).  Malformed ranges send the bisection
-// astray; then every row is looked at, so that their neighbours are served.
+// Row of token t, or -1 (a whole warp).  Malformed ranges send the count of
+// rows that begin at or before it astray; then every row is looked at, so that
+// their neighbours are served.
 __device__ __forceinline__ int rope_row(const RopeParams &p, int t, int lane)
 {
     if (p.indptr == nullptr)
         return t;
-    int lo = 0, hi = p.batch - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.indptr[mid] <= t)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    if (rope_owns(p, lo, t))
-        return lo;
+    int n = 0;
+    for (int b = 1 + lane; b < p.batch; b += 32) // (loads that do not wait for one another)
+        n += p.indptr[b] <= t ? 1 : 0;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (rope_owns(p, n, t))
+        return n;
     int found = p.batch;
     for (int b = lane; b < p.batch; b += 32)
         if (rope_owns(p, b, t)) {
@@ -72,170 +67,159 @@ __device__ __forceinline__ int rope_row(const RopeParams &p, int t, int lane)
     return found < p.batch ? found : -1;
 }
 
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p)
+// Looks token t up (a whole warp).
+__device__ __forceinline__ RopeToken rope_look_up(const RopeParams &p, int t, int lane)
 {
-    __shared__ RopeToken s_tok[kRopeTokens];
-    __shared__ int s_bad[kRopeTokens]; // of the row that first appears at this token: its error
-    extern __shared__ float s_cs[];    // [token][cos | sin][rot_dim / 2]
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int t0 = blockIdx.x * p.per_cta, n = min(p.per_cta, p.tokens - t0);
-    const bool append = p.k_cache != nullptr;
-    const int D = p.head_dim, half = p.rot_dim / 2;
-
-    if (warp < n) { // a warp for each token
-        const int t = t0 + warp;
-        RopeToken tok = {-1, 0, -1, 1};
-        int bad = 0;
-        if (append) {
-            const int b = rope_row(p, t, lane);
-            const int L = b >= 0 ? p.seqlens[b] : -1;
-            tok.row = b;
-            tok.live = L >= 0;
-            if (L >= 0) {
-                const int first = p.indptr == nullptr ? t : p.indptr[b];
-                const int count = p.indptr == nullptr ? 1 : p.indptr[b + 1] - first;
-                const int64_t at = (int64_t)L + (t - first);
-                tok.pos = at + (p.evicted != nullptr ? p.evicted[b] : 0);
-                // a row is appended as a whole or not at all; its first token in this CTA looks
-                if ((int64_t)L + count > (int64_t)p.max_blocks << p.page_shift) {
-                    bad = PKV_ERR_OVERFLOW;
-                } else {
-                    const int32_t *row = p.table + (int64_t)b * p.max_blocks;
-                    if (warp == 0 || t == first) {
-                        const int last = (int)(((int64_t)L + count - 1) >> p.page_shift);
-                        for (int k = (L >> p.page_shift) + lane; k <= last; k += 32)
-                            if (row[k] < 1 || row[k] >= p.num_pages)
-                                bad = PKV_ERR_PAGE;
-                        bad = __any_sync(0xffffffffu, bad) ? PKV_ERR_PAGE : 0;
-                    }
-                    const int64_t page = row[at >> p.page_shift], in_page = at & ((1 << p.page_shift) - 1);
-                    if (page < 1 || page >= p.num_pages)
+    RopeToken tok = {-1, 0, 1};
+    if (p.k_cache != nullptr) {
+        const int b = rope_row(p, t, lane);
+        const int L = b >= 0 ? p.seqlens[b] : -1;
+        tok.live = L >= 0;
+        if (L >= 0) {
+            const int first = p.indptr == nullptr ? t : p.indptr[b];
+            const int count = p.indptr == nullptr ? 1 : p.indptr[b + 1] - first;
+            const int64_t at = (int64_t)L + (t - first);
+            int bad = 0;
+            tok.pos = at + (p.evicted != nullptr ? p.evicted[b] : 0);
+            if ((int64_t)L + count > (int64_t)p.max_blocks << p.page_shift) {
+                bad = PKV_ERR_OVERFLOW;
+            } else { // a row is appended as a whole or not at all
+                const int32_t *row = p.table + (int64_t)b * p.max_blocks;
+                const int64_t page = row[at >> p.page_shift], in_page = at & ((1 << p.page_shift) - 1);
+                const int end = (int)(((int64_t)L + count - 1) >> p.page_shift);
+                for (int k = (L >> p.page_shift) + lane; k <= end; k += 32)
+                    if (row[k] < 1 || row[k] >= p.num_pages)
                         bad = PKV_ERR_PAGE;
-                    else
-                        tok.slot = p.layout == PKV_NHD
-                                       ? ((page << p.page_shift) + in_page) * p.num_kv_heads * D
-                                       : ((page * p.num_kv_heads << p.page_shift) + in_page) * D;
-                }
+                bad = __any_sync(0xffffffffu, bad) ? PKV_ERR_PAGE : 0;
+                if (bad == 0)
+                    tok.slot = p.layout == PKV_NHD ? ((page << p.page_shift) + in_page) * p.num_kv_heads * p.head_dim
+                                                   : ((page * p.num_kv_heads << p.page_shift) + in_page) * p.head_dim;
             }
-        }
-        if (p.positions != nullptr)
-            tok.pos = p.positions[t];
-        if (lane == 0) {
-            s_tok[warp] = tok;
-            s_bad[warp] = bad;
-            if (bad != 0)
+            if (bad != 0 && lane == 0)
                 set_error(p.err_flag, bad);
         }
     }
-    __syncthreads();
-    for (int i = tid; i < n * half; i += kRopeThreads) {
-        const int k = i / half, f = i - k * half;
-        const uint64_t turn = (uint64_t)s_tok[k].pos * p.freqs[f];
-        float s, c; // 2^-31: half turns
-        sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);
-        s_cs[2 * k * half + f] = c * p.attn_factor;
-        s_cs[(2 * k + 1) * half + f] = s * p.attn_factor;
-    }
-    __syncthreads();
+    if (p.positions != nullptr)
+        tok.pos = p.positions[t];
+    return tok;
+}
 
-    // Items of 32 bytes: 8 pairs of a head, or 16 values that are copied.  A
-    // thread has the same place in the head in all of its items.
-    const int per_head = D / 16, heads_at_once = kRopeThreads / per_head;
-    const int j = tid % per_head;
+// A CTA per token.  Its items of 32 bytes are 8 pairs of a head, or 16 values that
+// are copied; a thread has the same place in the head in all of its items, and so
+// the same angles.  kRopeAhead items at a time, and the next ones are read before
+// those are turned and written: the first before the token's row is known, which
+// one warp finds out meanwhile, with the angles.
+template <int THREADS, bool INTERLEAVED>
+__global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ RopeParams p)
+{
+    __shared__ RopeToken s_tok;
+    __shared__ __align__(16) float s_cos[128], s_sin[128];
+    const int tid = threadIdx.x;
+    const int64_t t = blockIdx.x;
+    const bool append = p.k_cache != nullptr;
+    const int D = p.head_dim, half = p.rot_dim / 2;
+    const int per_head = D / 16, heads_at_once = THREADS / per_head, j = tid % per_head;
     const int q_heads = p.q != nullptr ? p.num_q_heads : 0, k_heads = p.k != nullptr ? p.num_kv_heads : 0;
     const int heads = q_heads + k_heads + (append ? p.num_kv_heads : 0);
-    const int items = n * heads;
-    const int64_t head_step = p.layout == PKV_NHD ? D : (int64_t)D << p.page_shift;
-    const bool rotated = 16 * j < p.rot_dim;
-    // the two 16-byte pieces of an item
-    const int e0 = rotated && !p.interleaved ? 8 * j : 16 * j;
-    const int e1 = rotated && !p.interleaved ? half + 8 * j : 16 * j + 8;
-    for (int x0 = tid / per_head; x0 < items; x0 += heads_at_once * kRopeAhead) {
-        uint4 a[kRopeAhead], b[kRopeAhead];
-        __nv_bfloat16 *to[kRopeAhead], *also[kRopeAhead];
-        int cs[kRopeAhead]; // token, or -1 for a copy
+    const bool turns = 16 * j < p.rot_dim; // (heads of V do not)
+    // the two 16-byte pieces of an item that turns, and of another
+    const int e0 = turns && !INTERLEAVED ? 8 * j : 16 * j;
+    const int e1 = turns && !INTERLEAVED ? half + 8 * j : 16 * j + 8;
+
+    auto load = [&](int h0, uint4 (&a)[kRopeAhead], uint4 (&b)[kRopeAhead]) {
 #pragma unroll
         for (int u = 0; u < kRopeAhead; ++u) {
-            const int x = x0 + u * heads_at_once;
-            to[u] = also[u] = nullptr;
-            if (x >= items)
+            const int h = h0 + u * heads_at_once;
+            if (h >= heads)
                 continue;
-            const int k = x / heads, h = x - k * heads;
-            const RopeToken &tok = s_tok[k];
-            const int64_t t = t0 + k;
-            if (!tok.live)
-                continue;
-            const __nv_bfloat16 *from;
-            if (h < q_heads) {
-                const int64_t at = (t * q_heads + h) * D;
-                from = p.q + at;
-                to[u] = p.q_out + at;
-                cs[u] = rotated ? k : -1;
-            } else {
-                const bool is_k = h < q_heads + k_heads;
-                const int g = is_k ? h - q_heads : h - q_heads - k_heads;
-                const int64_t at = (t * p.num_kv_heads + g) * D;
-                from = (is_k ? p.k : p.v) + at;
-                cs[u] = is_k && rotated ? k : -1;
-                if (is_k && p.k_out != nullptr)
-                    also[u] = p.k_out + at;
-                if (append && tok.slot >= 0) {
-                    int first = k; // the token that looked at the row's pages
-                    while (first > 0 && s_tok[first - 1].row == tok.row)
-                        --first;
-                    if (s_bad[first] == 0)
-                        to[u] = (is_k ? p.k_cache : p.v_cache) + tok.slot + g * head_step;
-                }
-                if (to[u] == nullptr && also[u] == nullptr)
-                    continue;
-            }
-            const bool pieces = cs[u] >= 0;
-            a[u] = *reinterpret_cast<const uint4 *>(from + (pieces ? e0 : 16 * j));
-            b[u] = *reinterpret_cast<const uint4 *>(from + (pieces ? e1 : 16 * j + 8));
+            const bool is_v = h >= q_heads + k_heads;
+            const __nv_bfloat16 *from = h < q_heads ? p.q + (t * q_heads + h) * D
+                                        : is_v      ? p.v + (t * p.num_kv_heads + h - q_heads - k_heads) * D
+                                                    : p.k + (t * p.num_kv_heads + h - q_heads) * D;
+            a[u] = *reinterpret_cast<const uint4 *>(from + (is_v ? 16 * j : e0));
+            b[u] = *reinterpret_cast<const uint4 *>(from + (is_v ? 16 * j + 8 : e1));
         }
+    };
+    int h0 = tid / per_head;
+    uint4 a[kRopeAhead], b[kRopeAhead];
+    load(h0, a, b);
+
+    if (tid < 32) {
+        const RopeToken tok = rope_look_up(p, (int)t, tid);
+        for (int f = tid; f < half; f += 32) {
+            const uint64_t turn = (uint64_t)tok.pos * p.freqs[f];
+            float s, c; // 2^-31: half turns
+            sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);
+            s_cos[f] = c * p.attn_factor;
+            s_sin[f] = s * p.attn_factor;
+        }
+        if (tid == 0)
+            s_tok = tok;
+    }
+    __syncthreads();
+    const RopeToken tok = s_tok;
+    const int64_t head_step = p.layout == PKV_NHD ? D : (int64_t)D << p.page_shift;
+    for (;;) {
 #pragma unroll
         for (int u = 0; u < kRopeAhead; ++u) {
-            if (to[u] == nullptr && also[u] == nullptr)
+            const int h = h0 + u * heads_at_once;
+            if (h >= heads)
                 continue;
-            const bool pieces = cs[u] >= 0;
+            const bool is_v = h >= q_heads + k_heads, pieces = turns && !is_v;
+            const int g = h - q_heads - (is_v ? k_heads : 0);
+            __nv_bfloat16 *to = nullptr, *also = nullptr;
+            if (h < q_heads) {
+                if (tok.live)
+                    to = p.q_out + (t * q_heads + h) * D;
+            } else {
+                if (!is_v && p.k_out != nullptr)
+                    also = p.k_out + (t * p.num_kv_heads + g) * D;
+                if (tok.slot >= 0)
+                    to = (is_v ? p.v_cache : p.k_cache) + tok.slot + g * head_step;
+            }
+            uint32_t w[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b[u].x, b[u].y, b[u].z, b[u].w};
             if (pieces) {
-                const float4 *cp = reinterpret_cast<const float4 *>(s_cs + 2 * cs[u] * half + 8 * j);
-                const float4 *sp = reinterpret_cast<const float4 *>(s_cs + (2 * cs[u] + 1) * half + 8 * j);
-                const float4 c4[2] = {cp[0], cp[1]}, s4[2] = {sp[0], sp[1]};
-                const float *c = &c4[0].x, *s = &s4[0].x;
-                uint32_t w[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b[u].x, b[u].y, b[u].z, b[u].w};
+                const float4 *cp = reinterpret_cast<const float4 *>(s_cos) + 2 * j;
+                const float4 *sp = reinterpret_cast<const float4 *>(s_sin) + 2 * j;
+                const float4 c0 = cp[0], c1 = cp[1], s0 = sp[0], s1 = sp[1];
+                const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if (p.interleaved) {
+                    if (INTERLEAVED) {
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) { // words i and i + 4: pairs i and i + 4
-                            const float2 z = bf16x2_to_float2(w[i + 4 * m]);
-                            const float cc = c[i + 4 * m], ss = s[i + 4 * m];
-                            const __nv_bfloat162 r = __floats2bfloat162_rn(z.x * cc - z.y * ss, z.y * cc + z.x * ss);
-                            w[i + 4 * m] = *reinterpret_cast<const uint32_t *>(&r);
+                        for (int m = 0; m < 8; m += 4) { // words i and i + 4: pairs i and i + 4
+                            const float2 y = bf16x2_to_float2(w[i + m]);
+                            const __nv_bfloat162 r = __floats2bfloat162_rn(y.x * c[i + m] - y.y * s[i + m],
+                                                                           y.y * c[i + m] + y.x * s[i + m]);
+                            w[i + m] = *reinterpret_cast<const uint32_t *>(&r);
                         }
                     } else { // words i and i + 4: pairs 2 i and 2 i + 1
                         const float2 lo = bf16x2_to_float2(w[i]), hi = bf16x2_to_float2(w[i + 4]);
-                        const float c0 = c[2 * i], c1 = c[2 * i + 1], s0 = s[2 * i], s1 = s[2 * i + 1];
-                        const __nv_bfloat162 r0 = __floats2bfloat162_rn(lo.x * c0 - hi.x * s0, lo.y * c1 - hi.y * s1);
-                        const __nv_bfloat162 r1 = __floats2bfloat162_rn(hi.x * c0 + lo.x * s0, hi.y * c1 + lo.y * s1);
+                        const __nv_bfloat162 r0 = __floats2bfloat162_rn(lo.x * c[2 * i] - hi.x * s[2 * i],
+                                                                        lo.y * c[2 * i + 1] - hi.y * s[2 * i + 1]);
+                        const __nv_bfloat162 r1 = __floats2bfloat162_rn(hi.x * c[2 * i] + lo.x * s[2 * i],
+                                                                        hi.y * c[2 * i + 1] + lo.y * s[2 * i + 1]);
                         w[i] = *reinterpret_cast<const uint32_t *>(&r0);
                         w[i + 4] = *reinterpret_cast<const uint32_t *>(&r1);
                     }
                 }
-                a[u] = make_uint4(w[0], w[1], w[2], w[3]);
-                b[u] = make_uint4(w[4], w[5], w[6], w[7]);
             }
-            const int o0 = pieces ? e0 : 16 * j, o1 = pieces ? e1 : 16 * j + 8;
-            if (to[u] != nullptr) {
-                *reinterpret_cast<uint4 *>(to[u] + o0) = a[u];
-                *reinterpret_cast<uint4 *>(to[u] + o1) = b[u];
+            const uint4 y0 = make_uint4(w[0], w[1], w[2], w[3]), y1 = make_uint4(w[4], w[5], w[6], w[7]);
+            const int o0 = is_v ? 16 * j : e0, o1 = is_v ? 16 * j + 8 : e1;
+            if (to != nullptr) {
+                *reinterpret_cast<uint4 *>(to + o0) = y0;
+                *reinterpret_cast<uint4 *>(to + o1) = y1;
             }
-            if (also[u] != nullptr) {
-                *reinterpret_cast<uint4 *>(also[u] + o0) = a[u];
-                *reinterpret_cast<uint4 *>(also[u] + o1) = b[u];
+            if (also != nullptr) {
+                *reinterpret_cast<uint4 *>(also + o0) = y0;
+                *reinterpret_cast<uint4 *>(also + o1) = y1;
             }
         }
+        h0 += heads_at_once * kRopeAhead;
+        if (h0 >= heads)
+            break;
+        load(h0, a, b);
     }
 }
 
@@ -258,10 +242,20 @@ pkv_status rope_check(int head_dim, int num_q_heads, int num_kv_heads, int num_t
 
 pkv_status launch_rope(RopeParams &p, cudaStream_t stream)
 {
-    // tokens of a CTA: more share a look at the page table, as long as every SM has CTAs enough
-    p.per_cta = p.tokens <= 1216 ? 1 : p.tokens <= 4864 ? 4 : kRopeTokens;
-    const size_t smem = (size_t)p.per_cta * p.rot_dim * sizeof(float);
-    rope_kernel<<<(p.tokens + p.per_cta - 1) / p.per_cta, kRopeThreads, smem, stream>>>(p);
+    // 256 threads where a token has more items than 128 threads read at once
+    const int heads = (p.q != nullptr ? p.num_q_heads : 0) + (p.k != nullptr ? p.num_kv_heads : 0) +
+                      (p.k_cache != nullptr ? p.num_kv_heads : 0);
+    if (heads * (p.head_dim / 16) <= 128 * kRopeAhead) {
+        if (p.interleaved)
+            rope_kernel<128, true><<<p.tokens, 128, 0, stream>>>(p);
+        else
+            rope_kernel<128, false><<<p.tokens, 128, 0, stream>>>(p);
+    } else {
+        if (p.interleaved)
+            rope_kernel<256, true><<<p.tokens, 256, 0, stream>>>(p);
+        else
+            rope_kernel<256, false><<<p.tokens, 256, 0, stream>>>(p);
+    }
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
