@@ -3,6 +3,8 @@ function that ``include/pkv.h`` declares."""
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -10,6 +12,7 @@ from . import build as _build
 
 _lock = threading.Lock()
 _lib = None
+_calls = None
 
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
@@ -107,3 +110,22 @@ def load(build_if_missing: bool = True):
                 fn.argtypes = args
             _lib = lib
     return _lib
+
+
+def calls():
+    """The module ``pkv_torch``: calls from torch tensors to the library, checked
+    in C++ (builds the library first if need be, as :func:`load`)."""
+    global _calls
+    if _calls is None:
+        load()
+        path = _build.TORCH_LIB_PATH
+        if not os.path.exists(path):
+            raise RuntimeError(f"Python module missing: {path} (run __graft_entry__.build())")
+        with _lock:
+            if _calls is None:
+                loader = importlib.machinery.ExtensionFileLoader("pkv_torch", path)
+                spec = importlib.util.spec_from_file_location("pkv_torch", path, loader=loader)
+                module = importlib.util.module_from_spec(spec)
+                loader.exec_module(module)
+                _calls = module
+    return _calls

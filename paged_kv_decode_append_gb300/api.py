@@ -469,7 +469,8 @@ def pkv_tree_accept(parents, draft_tokens, target_tokens, root_targets, qo_indpt
 
 class LayerCaches:
     """The K and V pools of a model's layers, which share one block table, as
-    :func:`pkv_tree_commit` takes them (keeps the tensors alive)."""
+    :func:`pkv_tree_commit` and :func:`pkv_evict_apply` take them (keeps the
+    tensors alive)."""
 
     def __init__(self, k_caches, v_caches, layout: int = NHD):
         if len(k_caches) != len(v_caches) or len(k_caches) < 1:
@@ -482,6 +483,7 @@ class LayerCaches:
                                     for side in self._keep)
         self.num_layers = len(k_caches)
         self.desc = cache_desc(k_caches[0], layout)
+        self.k_at, self.v_at, self.desc_at = (ctypes.addressof(x) for x in (self.k_ptrs, self.v_ptrs, self.desc))
 
 
 def pkv_tree_commit(layers: LayerCaches, path, path_len, block_table, cache_seqlens, err_flag=None) -> None:
@@ -521,20 +523,13 @@ def pkv_rope(q, k, positions, freqs, pairing: int = ROPE_HALF, attn_factor: floa
     """Rotates ``q`` ``[T, Hq, D]`` and ``k`` ``[T, Hkv, D]`` (either may be
     None) by ``positions`` ``[T]``: the first ``2 * freqs.numel()`` values of
     every head.  Returns ``(q_out, k_out)``, which may be the inputs."""
-    some = q if q is not None else k
-    if some is None:
+    if q is None and k is None:
         raise ValueError("q or k")
-    dev = _device_of(some, "q" if q is not None else "k")
-    T, _, D = some.shape
     if q is not None and q_out is None:
         q_out = torch.empty_like(q)
     if k is not None and k_out is None:
         k_out = torch.empty_like(k)
-    Hq, Hk = (0 if t is None else t.size(1) for t in (q, k))
-    st = _lib.load().pkv_rope(
-        _at(dev, "q", q, _BF16, T, Hq, D), _at(dev, "k", k, _BF16, T, Hk, D), _at(dev, "positions", positions, _I32, T), T,
-        Hq, Hk, D, _at(dev, "freqs", freqs, _I64), 2 * freqs.numel(), pairing, attn_factor,
-        _at(dev, "q_out", q_out, _BF16, T, Hq, D), _at(dev, "k_out", k_out, _BF16, T, Hk, D), _stream_of(dev))
+    st = _lib.calls().rope(q, k, positions, freqs, pairing, attn_factor, q_out, k_out)
     if st:
         _check(st, "pkv_rope")
     return q_out, k_out
@@ -547,20 +542,10 @@ def pkv_rope_append(k_cache, v_cache, q, k_new, v_new, block_table, cache_seqlen
     tokens' ``q`` (or None), in one pass.  Token i of row b is at position
     ``cache_seqlens[b] + i + evicted[b]`` unless ``positions`` ``[T]`` says
     otherwise.  Returns ``q_out``, which may be ``q``."""
-    dev = _device_of(k_new, "k_new")
-    desc = cache_desc(k_cache, layout)
-    T, B, width = k_new.size(0), cache_seqlens.numel(), block_table.size(-1)
-    K, D = desc.num_kv_heads, desc.head_dim
     if q is not None and q_out is None:
         q_out = torch.empty_like(q)
-    Hq = 0 if q is None else q.size(1)
-    st = _lib.load().pkv_rope_append(
-        ctypes.byref(desc), _at(dev, "k_cache", k_cache, _BF16), _at(dev, "v_cache", v_cache, _BF16, *k_cache.shape),
-        _at(dev, "q", q, _BF16, T, Hq, D), _at(dev, "k_new", k_new, _BF16, T, K, D), _at(dev, "v_new", v_new, _BF16, T, K, D),
-        T, _at(dev, "append_indptr", append_indptr, _I32, B + 1), _at(dev, "positions", positions, _I32, T),
-        _at(dev, "evicted", evicted, _I32, B), _at(dev, "freqs", freqs, _I64), 2 * freqs.numel(), pairing, attn_factor,
-        _at(dev, "block_table", block_table, _I32, B, width), width, _at(dev, "cache_seqlens", cache_seqlens, _I32, B), B,
-        Hq, _at(dev, "q_out", q_out, _BF16, T, Hq, D), _at(dev, "err_flag", err_flag, _I32), _stream_of(dev))
+    st = _lib.calls().rope_append(k_cache, v_cache, q, k_new, v_new, block_table, cache_seqlens, freqs, pairing, attn_factor,
+                                  append_indptr, positions, evicted, q_out, err_flag, layout)
     if st:
         _check(st, "pkv_rope_append")
     return q_out
@@ -587,23 +572,11 @@ def pkv_attn_mass(k_cache, q, lse, block_table, cache_seqlens, softmax_scale: fl
     cached token.  ``cache_seqlens`` are the lengths before the step's tokens;
     slots from ``fresh_from[b]`` (``cache_seqlens[b]``) on are set, and their
     ``slot_pos`` becomes ``slot + evicted[b]``."""
-    dev = _device_of(q, "q")
-    desc = cache_desc(k_cache, layout)
-    T, Hq, D = q.shape
-    B, width = block_table.shape
-    slots = mass.size(-1)
     if workspace is None:
-        workspace = mass_workspace(B, T, width, Hq, desc, q.device)
-    if D != desc.head_dim:
-        raise ValueError("q: head_dim differs from the cache's")
-    K = desc.num_kv_heads
-    st = _lib.load().pkv_attn_mass(
-        ctypes.byref(desc), _at(dev, "k_cache", k_cache, _BF16), _at(dev, "q", q, _BF16),
-        _at(dev, "qo_indptr", qo_indptr, _I32, B + 1), _at(dev, "lse", lse, _F32, T, Hq),
-        _at(dev, "block_table", block_table, _I32), width, _at(dev, "cache_seqlens", cache_seqlens, _I32, B), B, Hq, T,
-        softmax_scale, _at(dev, "fresh_from", fresh_from, _I32, B), _at(dev, "evicted", evicted, _I32, B),
-        _at(dev, "mass", mass, _F32, B, K, slots), _at(dev, "slot_pos", slot_pos, _I32, B, K, slots), slots,
-        _at(dev, "workspace", workspace, _U8), workspace.numel(), _at(dev, "err_flag", err_flag, _I32), _stream_of(dev))
+        workspace = mass_workspace(block_table.size(0), q.size(0), block_table.size(1), q.size(1), cache_desc(k_cache, layout),
+                                   q.device)
+    st = _lib.calls().attn_mass(k_cache, q, lse, block_table, cache_seqlens, softmax_scale, mass, qo_indptr, fresh_from,
+                                evicted, slot_pos, workspace, err_flag, layout)
     if st:
         _check(st, "pkv_attn_mass")
 
@@ -614,21 +587,14 @@ def pkv_evict_plan(mass, slot_pos, cache_seqlens, evicted, budgets, sink: int, r
     Hkv, slots]``, at most ``budgets[b]``, and the moves that fill the holes in
     front.  Returns ``(moves [layers, B, Hkv, max_moves, 2], num_moves, row_lens
     [B, 2])``."""
-    dev = _device_of(mass, "mass")
-    layers, B, K, slots = mass.shape
     if moves is None:
-        moves = torch.empty(layers, B, K, max(1, slots // 2), 2, dtype=torch.int32, device=mass.device)
+        moves = torch.empty(*mass.shape[:3], max(1, mass.size(3) // 2), 2, dtype=torch.int32, device=mass.device)
     if num_moves is None:
-        num_moves = torch.empty(layers, B, K, dtype=torch.int32, device=mass.device)
+        num_moves = torch.empty(mass.shape[:3], dtype=torch.int32, device=mass.device)
     if row_lens is None:
-        row_lens = torch.empty(B, 2, dtype=torch.int32, device=mass.device)
-    width = moves.size(-2)
-    st = _lib.load().pkv_evict_plan(
-        _at(dev, "mass", mass, _F32), _at(dev, "slot_pos", slot_pos, _I32, layers, B, K, slots), layers, B, K, slots,
-        _at(dev, "cache_seqlens", cache_seqlens, _I32, B), _at(dev, "evicted", evicted, _I32, B),
-        _at(dev, "budgets", budgets, _I32, B), sink, recent, _at(dev, "moves", moves, _I32, layers, B, K, width, 2), width,
-        _at(dev, "num_moves", num_moves, _I32, layers, B, K), _at(dev, "row_lens", row_lens, _I32, B, 2),
-        _at(dev, "err_flag", err_flag, _I32), _stream_of(dev))
+        row_lens = torch.empty(mass.size(1), 2, dtype=torch.int32, device=mass.device)
+    st = _lib.calls().evict_plan(mass, slot_pos, cache_seqlens, evicted, budgets, sink, recent, moves, num_moves, row_lens,
+                                 err_flag)
     if st:
         _check(st, "pkv_evict_plan")
     return moves, num_moves, row_lens
@@ -638,20 +604,9 @@ def pkv_evict_apply(layers: LayerCaches, moves, num_moves, row_lens, block_table
                     slot_pos=None, err_flag=None) -> None:
     """Carries a plan out: K, V, ``mass`` and ``slot_pos`` of every move in
     every layer, then ``cache_seqlens`` and ``evicted`` (either may be None)."""
-    dev = _device_of(moves, "moves")
-    if dev != layers.device:
-        raise ValueError("moves and caches on different devices")
-    B, width = block_table.shape
-    n, K, most = layers.num_layers, layers.desc.num_kv_heads, moves.size(-2)
-    state = mass if mass is not None else slot_pos
-    slots = 1 if state is None else state.size(-1)
-    st = _lib.load().pkv_evict_apply(
-        ctypes.byref(layers.desc), n, layers.k_ptrs, layers.v_ptrs, _at(dev, "moves", moves, _I32, n, B, K, most, 2), most,
-        _at(dev, "num_moves", num_moves, _I32, n, B, K), _at(dev, "row_lens", row_lens, _I32, B, 2),
-        _at(dev, "block_table", block_table, _I32), width, _at(dev, "mass", mass, _F32, n, B, K, slots),
-        _at(dev, "slot_pos", slot_pos, _I32, n, B, K, slots), slots,
-        _at(dev, "cache_seqlens", cache_seqlens, _I32, B), _at(dev, "evicted", evicted, _I32, B), B,
-        _at(dev, "err_flag", err_flag, _I32), _stream_of(dev))
+    st = _lib.calls().evict_apply(layers.desc_at, layers.k_at, layers.v_at, layers.num_layers, layers.desc.num_kv_heads,
+                                  layers.device, moves, num_moves, row_lens, block_table, cache_seqlens, evicted, mass,
+                                  slot_pos, err_flag)
     if st:
         _check(st, "pkv_evict_apply")
 
