@@ -40,6 +40,7 @@
 namespace pkv {
 namespace {
 
+constexpr int kMmKeysLog = 7;
 constexpr int kMmKeys = 128;     // keys of a tile: M of every MMA
 constexpr int kMmCols = 128;     // (query, head) columns of a query tile
 constexpr int kMmWide = 8;       // steps from which a block has four key tiles
@@ -62,8 +63,8 @@ template <int D> struct MmCfg {
     static constexpr uint32_t kGroupStride = 8 * D * 2;        // 8 keys, all of head_dim
     static constexpr uint32_t kOffK = 0;
     static constexpr uint32_t kOffQ = kOffK + kKStages * kKBytes;
-    static constexpr uint32_t kOffLse = kOffQ + kQStages * kQBytes; // [group of warps][its step's parity][128]
-    static constexpr uint32_t kOffHalf = kOffLse + 4 * 2 * 128 * 4; // [pair of groups][128 keys]
+    static constexpr uint32_t kOffLse = kOffQ + kQStages * kQBytes; // [group of warps][three steps][128]
+    static constexpr uint32_t kOffHalf = kOffLse + 4 * 3 * 128 * 4; // [pair of groups][128 keys]
     static constexpr uint32_t kOffBar = kOffHalf + 2 * 128 * 4;
     static constexpr uint32_t kSmem = kOffBar + 2048;
     static constexpr uint32_t kTmemCols = 4 * kMmCols;         // an accumulator for each group of warps
@@ -84,6 +85,22 @@ struct MmRun {
     int32_t piece0, pieces; // CTA of the block's first piece, pieces (1: whole)
 };
 
+struct MmRow {
+    int first, queries, len, fresh, gone;
+    int steps;  // of a block that all queries see
+    int tiles;  // key tiles of a block
+    int blocks; // of a kv head; 0: nothing to do
+    int full;   // blocks, from the first on, that all query tiles see
+    int err;
+    int64_t work; // positions of a kv head
+};
+
+// a / b for a >= 0 and b > 0: nearly always small ones, whose division is a fraction of a 64-bit one.
+__device__ __forceinline__ int64_t mm_div(int64_t a, int64_t b)
+{
+    return ((uint64_t)a | (uint64_t)b) >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // The line cut into `ctas` ranges as equal as can be.
 struct MmCut {
     int64_t quot;
@@ -92,7 +109,7 @@ struct MmCut {
     // the CTA whose range holds position x
     __device__ __forceinline__ int of(int64_t x) const
     {
-        int c = (int)min((int64_t)ctas - 1, x / quot);
+        int c = (int)min((int64_t)ctas - 1, mm_div(x, quot));
         while (lo(c) > x)
             --c;
         return c;
@@ -104,6 +121,7 @@ struct MmStart {
     MmCut cut;
     int64_t at, off, left; // position on the line, within the (row, kv head), positions of the range
     int b, g;
+    MmRow row;
 };
 
 struct MmBars {
@@ -144,16 +162,6 @@ struct MmMaps {
 
 // ---------------------------------------------------------------- work line
 
-struct MmRow {
-    int first, queries, len;
-    int steps;  // of a block that all queries see
-    int tiles;  // key tiles of a block
-    int blocks; // of a kv head; 0: nothing to do
-    int full;   // blocks, from the first on, that all query tiles see
-    int err;
-    int64_t work; // positions of a kv head
-};
-
 __device__ __forceinline__ int mm_steps(const MmParams &p, const MmRow &r, int kb)
 {
     const int i0 = kb * r.tiles * kMmKeys - r.len; // the block's first key is seen from this query on
@@ -164,13 +172,31 @@ __device__ __forceinline__ int64_t mm_cost(const MmRow &r, int steps)
     return (int64_t)r.tiles * (kFixCost + steps);
 }
 
+// What a row's part in the call is made from.
+struct MmRaw {
+    int first, end, len, fresh, gone;
+};
+__device__ __forceinline__ MmRaw mm_raw(const MmParams &p, int b)
+{
+    MmRaw raw;
+    b = max(0, min(b, p.batch - 1));
+    raw.first = p.indptr != nullptr ? p.indptr[b] : b;
+    raw.end = p.indptr != nullptr ? p.indptr[b + 1] : b + 1;
+    raw.len = p.seqlens[b];
+    raw.fresh = p.fresh_from != nullptr ? p.fresh_from[b] : raw.len;
+    raw.gone = p.evicted != nullptr ? p.evicted[b] : 0;
+    return raw;
+}
+
 // A row's part in the call (see include/pkv.h).
-__device__ __forceinline__ MmRow mm_row(const MmParams &p, int b)
+__device__ __forceinline__ MmRow mm_row(const MmParams &p, const MmRaw &raw)
 {
     MmRow r;
-    r.first = p.indptr != nullptr ? p.indptr[b] : b;
-    const int64_t n = p.indptr != nullptr ? (int64_t)p.indptr[b + 1] - r.first : 1;
-    r.len = p.seqlens[b];
+    r.first = raw.first;
+    r.len = raw.len;
+    r.fresh = raw.fresh;
+    r.gone = raw.gone;
+    const int64_t n = (int64_t)raw.end - raw.first;
     r.err = r.blocks = r.full = r.queries = r.steps = 0;
     r.tiles = 1;
     r.work = 0;
@@ -186,11 +212,11 @@ __device__ __forceinline__ MmRow mm_row(const MmParams &p, int b)
         return r;
     }
     r.queries = (int)n;
-    r.steps = (r.queries + p.q_tile - 1) / p.q_tile;
+    r.steps = r.queries <= p.q_tile ? 1 : (r.queries + p.q_tile - 1) / p.q_tile;
     r.tiles = r.steps == 1 ? 1 : r.steps < kMmWide ? 2 : p.most_tiles;
-    const int size = r.tiles * kMmKeys;
-    r.blocks = (int)((keys + size - 1) / size);
-    r.full = (int)min((int64_t)r.blocks, ((int64_t)r.len + p.q_tile - 1) / size + 1);
+    const int shift = kMmKeysLog + (r.tiles >> 1); // log2 of a block's keys
+    r.blocks = (int)((keys + (1 << shift) - 1) >> shift);
+    r.full = (int)min((int64_t)r.blocks, (((int64_t)r.len + p.q_tile - 1) >> shift) + 1);
     r.work = r.full * mm_cost(r, r.steps);
     for (int kb = r.full; kb < r.blocks; ++kb)
         r.work += mm_cost(r, mm_steps(p, r, kb));
@@ -203,18 +229,18 @@ __device__ MmStart mm_start(const MmParams &p, int64_t *scratch, MmStart *found)
     constexpr int kPer = (kMaxMassBatch + kMmThreads - 1) / kMmThreads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = min(kPer, (p.batch + kMmThreads - 1) / kMmThreads);
-    int64_t work[kPer], sum = 0;
+    MmRow row[kPer];
+    int64_t sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int b = tid * per + i;
-        work[i] = 0;
+        row[i].work = 0;
         if (i < per && b < p.batch) {
-            const MmRow r = mm_row(p, b);
-            work[i] = r.work;
+            row[i] = mm_row(p, mm_raw(p, b));
             if (blockIdx.x == 0)
-                set_error(p.err_flag, r.err);
+                set_error(p.err_flag, row[i].err);
         }
-        sum += work[i] * p.num_kv_heads;
+        sum += row[i].work * p.num_kv_heads;
     }
     int64_t x = sum;
 #pragma unroll
@@ -228,6 +254,7 @@ __device__ MmStart mm_start(const MmParams &p, int64_t *scratch, MmStart *found)
     if (tid == 0) { // an empty range, at row 0
         found->at = found->off = found->left = 0;
         found->b = found->g = 0;
+        found->row = row[0];
     }
     __syncthreads();
     int64_t total = 0;
@@ -241,21 +268,22 @@ __device__ MmStart mm_start(const MmParams &p, int64_t *scratch, MmStart *found)
     const int c = blockIdx.x;
     MmCut cut;
     cut.ctas = total >= (int64_t)gridDim.x * kMinRange ? (int)gridDim.x : max(1, (int)total / kMinRange);
-    cut.quot = total / cut.ctas;
+    cut.quot = mm_div(total, cut.ctas);
     cut.rest = (int)(total - cut.quot * cut.ctas);
     if (c < cut.ctas) {
         const int64_t lo = cut.lo(c), hi = cut.lo(c + 1);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int64_t size = work[i] * p.num_kv_heads, in_row = lo - x;
+            const int64_t size = row[i].work * p.num_kv_heads, in_row = lo - x;
             if (hi > lo && in_row >= 0 && in_row < size) {
                 MmStart at;
                 at.cut = cut;
                 at.at = lo;
                 at.left = hi - lo;
                 at.b = tid * per + i;
-                at.g = (int)(in_row / work[i]);
-                at.off = in_row - at.g * work[i];
+                at.g = (int)mm_div(in_row, row[i].work);
+                at.off = in_row - at.g * row[i].work;
+                at.row = row[i];
                 *found = at;
             }
             x += size;
@@ -302,41 +330,26 @@ __device__ void mm_walk(const MmParams &p, MmBars &bars, const MmStart &from, in
 {
     int n = 0, b = from.b, g = from.g, kb = 0;
     int64_t at = from.at, left = from.left, off = from.off; // (off: within the block)
-    MmRow r = mm_row(p, b);
-    MmRow then = r;
-    int fresh = 0, gone = 0, next_fresh = 0, next_gone = 0;
-    auto more_of = [&](int row, int &f, int &e) {
-        f = p.fresh_from != nullptr ? p.fresh_from[row] : p.seqlens[row];
-        e = p.evicted != nullptr ? p.evicted[row] : 0;
-    };
-    if (left > 0) {
-        more_of(b, fresh, gone);
-        // the block that the range starts in
+    MmRow r = from.row;
+    MmRaw then = mm_raw(p, b + 1); // the next row, read ahead
+    if (left > 0) { // the block that the range starts in
         const int64_t size = mm_cost(r, r.steps);
-        kb = (int)min((int64_t)r.full, off / size);
+        kb = (int)min((int64_t)r.full, mm_div(off, size));
         off -= kb * size;
         while (kb >= r.full && off >= mm_cost(r, mm_steps(p, r, kb)))
             off -= mm_cost(r, mm_steps(p, r, kb++));
     }
-    bool ahead = false; // the next row is read
     for (;;) {
         MmRun s;
         s.tiles = 0;
         while (left > 0) {
-            if (!ahead && b + 1 < p.batch) {
-                then = mm_row(p, b + 1);
-                more_of(b + 1, next_fresh, next_gone);
-                ahead = true;
-            }
             if (kb >= r.blocks) {
                 kb = 0;
                 if (r.blocks == 0 || ++g == p.num_kv_heads) { // (positions are left: there is a next row)
                     g = 0;
                     ++b;
-                    r = then;
-                    fresh = next_fresh;
-                    gone = next_gone;
-                    ahead = false;
+                    r = mm_row(p, then);
+                    then = mm_raw(p, b + 1);
                 }
                 continue;
             }
@@ -350,12 +363,13 @@ __device__ void mm_walk(const MmParams &p, MmBars &bars, const MmStart &from, in
                 const int64_t most = (int64_t)(r.blocks - kb) * kSize - off, take = min(most, left);
                 const int first = off > kFixCost ? kb + 1 : kb;
                 // positions from block kb's start; a step at or past them belongs to the next CTA
-                const int end = (int)((off + take + kSize - 1 - kFixCost) / kSize) + kb;
+                const int end = (int)mm_div(off + take + kSize - 1 - kFixCost, kSize) + kb;
                 left -= take;
                 at += take;
                 off += take;
-                kb += (int)(off / kSize);
-                off -= (int64_t)(off / kSize) * kSize;
+                const int passed = (int)mm_div(off, kSize);
+                kb += passed;
+                off -= (int64_t)passed * kSize;
                 if (first >= end)
                     continue;
                 block = first;
@@ -395,8 +409,8 @@ __device__ void mm_walk(const MmParams &p, MmBars &bars, const MmStart &from, in
             s.queries = r.queries;
             s.len = r.len;
             s.keys = r.len + r.queries;
-            s.fresh = fresh;
-            s.gone = gone;
+            s.fresh = r.fresh;
+            s.gone = r.gone;
             break;
         }
         const int slot = n % kMmRuns;
@@ -756,7 +770,7 @@ __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
     // four key tiles one of them, of two every other step of one.
     const int w = (warp - kMmSumWarp) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + w * kMmCols;
-    float *lse = reinterpret_cast<float *>(smem + C::kOffLse) + w * 256;
+    float *lse = reinterpret_cast<float *>(smem + C::kOffLse) + w * 384;
     float *half = reinterpret_cast<float *>(smem + C::kOffHalf) + (w & 1) * 128;
     // the (query, head) of this thread's column, whose lse it fetches for the group
     const int my_query = r / p.group, my_head = r - my_query * p.group;
@@ -779,39 +793,55 @@ __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
             const int q = step * p.q_tile;
             return my_query < p.q_tile && q + my_query < s.queries ? z_at[(int64_t)q * p.num_q_heads] : 0.f;
         };
+        // The columns' lse go through shared memory, a step ahead: while step k is
+        // summed those of k + 1 are written and those of k + 2 are on their way.
+        auto stage = [&](float z) {
+            lse[staged % 3 * 128 + r] = z == -INFINITY ? z : z * -1.4426950408889634f;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars.z_full[w]);
+            ++staged;
+        };
         float z = 0.f, sum = 0.f, dropped = 0.f, was = 0.f;
-        if (st < s.step1 && blk < s.blocks)
+        if (st < s.step1 && blk < s.blocks) {
             z = lse_at(st);
-        bool new_z = true, begins = true;
+            const float z1 = s.tiles > 1 && st + next_step < s.step1 ? lse_at(st + next_step) : 0.f;
+            stage(z);
+            z = z1;
+        }
+        bool begins = true;
         const int64_t unit = ((int64_t)s.b * p.num_kv_heads + s.g) * p.slots;
+        const float *zs = lse;
 #pragma unroll 1
         while (st < s.step1 && blk < s.blocks) {
             const int tok = s.tok + (blk * s.tiles + j) * kMmKeys, key = tok + r;
             const bool fresh = key >= s.fresh, mine = ends && key < s.keys;
-            if (begins) {
+            if (begins || s.tiles == 1) {
                 sum = dropped = was = 0.f;
                 if (mine && !fresh)
                     was = p.mass[unit + key];
             }
             // (nothing to sum in a tile behind the row's end)
             const int cols = tok < s.keys ? min(p.q_tile, s.queries - st * p.q_tile) * p.group : 0;
-            if (new_z) { // (all have read what was there two steps ago: they have been at the barrier since)
-                lse[(staged & 1) * 128 + r] = z == -INFINITY ? z : z * -1.4426950408889634f;
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&bars.z_full[w]);
-                ++staged;
-            }
             const int now = st;
+            if (begins || s.tiles > 1) {
+                if (!mm_wait(&bars.z_full[w], (staged - 1) & 1, bars, p.err_flag))
+                    return;
+                zs = lse + (staged - 1) % 3 * 128;
+            }
+            begins = false;
             if (s.tiles == 1) {
                 blk += 4;
             } else {
                 st += next_step;
-                if (st < s.step1)
-                    z = lse_at(st);
+                if (st < s.step1) {
+                    // (the room was last read three steps ago: all of the group have staged since)
+                    stage(z);
+                    if (st + next_step < s.step1)
+                        z = lse_at(st + next_step);
+                }
             }
-            if ((new_z && !mm_wait(&bars.z_full[w], (staged - 1) & 1, bars, p.err_flag)) ||
-                !mm_wait(&bars.s_full[w], taken & 1, bars, p.err_flag))
+            if (!mm_wait(&bars.s_full[w], taken & 1, bars, p.err_flag))
                 return;
             ++taken;
             // What the MMAs have read is free: the key tile after its last step, the
@@ -827,38 +857,39 @@ __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
                         mbar_arrive(&bars.q_empty[(q0 + (now - s.step0) * C::kChunks + c) % C::kQStages]);
             }
             tc_fence_after();
-            const float *zs = lse + ((staged - 1) & 1) * 128;
             // columns of queries before the key's own see nothing of it
             const int seen = max(0, key - s.len - now * p.q_tile) * p.group;
             const bool edge = tok + kMmKeys - 1 - s.len > now * p.q_tile;
             float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
             uint32_t x[32];
             const int whole = edge ? 0 : cols & ~31;
+            auto leave = [&] { // all of the accumulator is in registers
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bars.s_free[w]);
+            };
+            if (cols == 0)
+                leave();
 #pragma unroll 1
             for (int c = 0; c < whole; c += 32) {
                 mm_ld32(acc + c, x);
                 mm_ld_wait(x);
+                if (c + 32 >= cols)
+                    leave();
                 mm_add32<false>(x, zs + c, p.q_scale, 0, 32, sum0, sum1);
             }
 #pragma unroll 1
             for (int c = whole; c < cols; c += 32) {
                 mm_ld32(acc + c, x);
                 mm_ld_wait(x);
+                if (c + 32 >= cols)
+                    leave();
                 mm_add32<true>(x, zs + c, p.q_scale, seen - c, cols - c, sum0, sum1);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bars.s_free[w]);
             mm_add(sum, dropped, (sum0.x + sum1.x) + (sum0.y + sum1.y));
-            new_z = begins = s.tiles == 1;
-            if (s.tiles > 1) {
-                new_z = true;
-                if (st < s.step1)
-                    continue;
-            } else {
-                new_z = false;
-            }
+            if (s.tiles > 1 && st < s.step1)
+                continue;
             // the block's sums
             if (shared) {
                 if (!ends) {
