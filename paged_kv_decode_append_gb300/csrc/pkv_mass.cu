@@ -47,10 +47,10 @@ constexpr int kMmWide = 8;       // steps from which a block has four key tiles
 constexpr int kFixCost = 2;      // positions that a key tile costs before its first step
 constexpr int kMinRange = 6;     // positions that are worth a CTA of their own
 constexpr int kMmMaxCtas = 160;  // persistent CTAs the workspace has room for
-constexpr int kMmKWarp = 0, kMmMmaWarp = 1, kMmQWarp = 2, kMmWalkWarp = 3, kMmSumWarp = 4;
+constexpr int kMmKWarp = 0, kMmMmaWarp = 1, kMmQWarp = 2, kMmMmaWarp2 = 3, kMmSumWarp = 4;
 constexpr int kMmThreads = 640;
 constexpr int kMmRuns = 8;       // runs of blocks handed out and not yet done with
-constexpr int kMmReaders = 19;   // warps that read them
+constexpr int kMmReaders = 20;   // warps that read them
 constexpr int kMmBadTiles = 16;  // key tiles whose bad pages are remembered
 
 template <int D> struct MmCfg {
@@ -325,21 +325,46 @@ __device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity, MmBars &
 
 // ---------------------------------------------------------------- runs
 
-// One warp cuts the CTA's range into runs, in order.
-__device__ void mm_walk(const MmParams &p, MmBars &bars, const MmStart &from, int lane)
-{
-    int n = 0, b = from.b, g = from.g, kb = 0;
-    int64_t at = from.at, left = from.left, off = from.off; // (off: within the block)
-    MmRow r = from.row;
-    MmRaw then = mm_raw(p, b + 1); // the next row, read ahead
-    if (left > 0) { // the block that the range starts in
-        const int64_t size = mm_cost(r, r.steps);
-        kb = (int)min((int64_t)r.full, mm_div(off, size));
-        off -= kb * size;
-        while (kb >= r.full && off >= mm_cost(r, mm_steps(p, r, kb)))
-            off -= mm_cost(r, mm_steps(p, r, kb++));
+// Cuts the CTA's range into runs, in order.  A whole warp.
+struct MmWalk {
+    MmCut cut;
+    int64_t at, left, off; // position on the line, positions left, position within the block
+    int b, g, kb;
+    MmRow r;
+    MmRaw then; // the next row, read ahead
+    int n;      // runs handed out
+    bool over;
+
+    __device__ __forceinline__ void start(const MmParams &p, const MmStart &from)
+    {
+        cut = from.cut;
+        at = from.at;
+        left = from.left;
+        off = from.off;
+        b = from.b;
+        g = from.g;
+        kb = 0;
+        r = from.row;
+        then = mm_raw(p, b + 1);
+        n = 0;
+        over = false;
+        if (left > 0) { // the block that the range starts in
+            const int64_t size = mm_cost(r, r.steps);
+            kb = (int)min((int64_t)r.full, mm_div(off, size));
+            off -= kb * size;
+            while (kb >= r.full && off >= mm_cost(r, mm_steps(p, r, kb)))
+                off -= mm_cost(r, mm_steps(p, r, kb++));
+        }
     }
-    for (;;) {
+    // Whether the next run has a slot that all readers are done with.
+    __device__ __forceinline__ bool room(MmBars &bars) const
+    {
+        return n < kMmRuns ||
+               __all_sync(0xffffffffu, mbar_test_wait(&bars.run_empty[n % kMmRuns], (uint32_t)(n / kMmRuns - 1) & 1));
+    }
+    // Hands the next run out.
+    __device__ __forceinline__ void publish(const MmParams &p, MmBars &bars, int lane)
+    {
         MmRun s;
         s.tiles = 0;
         while (left > 0) {
@@ -397,8 +422,8 @@ __device__ void mm_walk(const MmParams &p, MmBars &bars, const MmStart &from, in
                 s.step0 = r.steps - steps + s0;
                 s.step1 = r.steps - steps + s1;
                 if (s1 - s0 < steps) {
-                    s.piece0 = from.cut.of(start + (int64_t)t * kFixCost);
-                    s.pieces = from.cut.of(start + (int64_t)t * (kFixCost + steps - 1)) - s.piece0 + 1;
+                    s.piece0 = cut.of(start + (int64_t)t * kFixCost);
+                    s.pieces = cut.of(start + (int64_t)t * (kFixCost + steps - 1)) - s.piece0 + 1;
                 }
             }
             s.b = b;
@@ -414,17 +439,14 @@ __device__ void mm_walk(const MmParams &p, MmBars &bars, const MmStart &from, in
             break;
         }
         const int slot = n % kMmRuns;
-        if (n >= kMmRuns && !mm_wait(&bars.run_empty[slot], (uint32_t)(n / kMmRuns - 1) & 1, bars, p.err_flag))
-            return;
         if (lane == 0) {
             bars.run[slot] = s;
             mbar_arrive(&bars.run_full[slot]);
         }
         ++n;
-        if (s.tiles == 0)
-            return;
+        over = s.tiles == 0;
     }
-}
+};
 
 // The n-th run; a role that gave up sees the end.
 __device__ __forceinline__ MmRun mm_run(const MmParams &p, MmBars &bars, int n)
@@ -511,21 +533,34 @@ __device__ void mm_load_k(const MmParams &p, const MmMaps &maps, uint8_t *smem, 
         mbar_wait(&bars.k_full[k % C::kKStages], (uint32_t)(k / C::kKStages) & 1);
 }
 
-// One warp loads the query tiles of every step, a box per 64 columns.
+// One warp cuts the range into runs and loads the query tiles of every step, a box
+// per 64 columns.  It hands runs out ahead of what it loads itself, two a step,
+// so that the key tiles of the next runs are on their way.
 template <int D>
-__device__ void mm_load_q(const MmParams &p, const MmMaps &maps, uint8_t *smem, MmBars &bars, int lane)
+__device__ void mm_load_q(const MmParams &p, const MmMaps &maps, uint8_t *smem, MmBars &bars, const MmStart &from, int lane)
 {
     using C = MmCfg<D>;
+    MmWalk walk;
+    walk.start(p, from);
+    walk.publish(p, bars, lane);
     int slot = 0, issued = 0;
     uint32_t round = 0;
     bool going = true;
     for (int n = 0; going; ++n) {
+        while (!walk.over && walk.n <= n) {
+            if (!walk.room(bars) && !mm_wait(&bars.run_empty[walk.n % kMmRuns], (uint32_t)(walk.n / kMmRuns - 1) & 1, bars,
+                                             p.err_flag)) {
+                going = false;
+                break;
+            }
+            walk.publish(p, bars, lane);
+        }
         const MmRun s = mm_run(p, bars, n);
         if (s.tiles == 0)
             break;
         const bool one = s.queries == 1; // a box of one query: no other row's are fetched
         const uint32_t bytes = one ? p.q_one_bytes : p.q_box_bytes;
-        for (int st = s.step0; st < s.step1 && going; ++st)
+        for (int st = s.step0; st < s.step1 && going; ++st) {
             for (int c = 0; c < C::kChunks; ++c) {
                 if (round > 0 && !mm_wait(&bars.q_empty[slot], (round - 1) & 1, bars, p.err_flag)) {
                     going = false;
@@ -543,6 +578,9 @@ __device__ void mm_load_q(const MmParams &p, const MmMaps &maps, uint8_t *smem, 
                     ++round;
                 }
             }
+            for (int k = 0; k < 2 && !walk.over && walk.room(bars); ++k)
+                walk.publish(p, bars, lane);
+        }
         mm_run_done(bars, n, lane);
     }
     for (int k = issued > C::kQStages ? issued - C::kQStages : 0; k < issued; ++k)
@@ -578,16 +616,19 @@ __device__ __forceinline__ void mm_commit(uint64_t *bar)
                  : "memory");
 }
 
+// Two warps issue, every other (key tile, step) pair each (`half`: which), and so
+// have two accumulators and every other key slot to themselves: what a pair costs
+// a warp besides its MMAs (waits, votes, descriptors: 500 cycles) then overlaps
+// the other warp's.
 template <int D>
-__device__ void mm_mma(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t tmem, int lane)
+__device__ void mm_mma(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t tmem, uint32_t half, int lane)
 {
     using C = MmCfg<D>;
     constexpr int kChunks = C::kChunks;
     const uint64_t kd0 = tc_sw128_desc(smem_addr(smem + C::kOffK), 16, C::kGroupStride);
     const uint64_t qd0 = tc_sw128_desc(smem_addr(smem + C::kOffQ), 16, 1024);
-    uint32_t k_slot0 = 0, k_par0 = 0; // of the block's first key tile
-    uint32_t seq = 0;                 // (key tile, step) pairs before
-    uint32_t q_slot0 = 0, q_par0 = 0; // of the step's first chunk
+    uint32_t tile0 = 0, seq = 0; // key tiles, pairs before the block (alike modulo 2)
+    uint32_t q_slot = 0, q_par = 0; // of the next chunk
     bool going = true;
     for (int n = 0; going; ++n) {
         const MmRun s = mm_run(p, bars, n);
@@ -600,96 +641,74 @@ __device__ void mm_mma(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
         // key tiles of the run that lie before the row's end
         const int real = __shfl_sync(0xffffffffu, (s.keys - s.tok + kMmKeys - 1) / kMmKeys, 0);
         mm_run_done(bars, n, lane);
+        // the accumulator of pair u, and the key tile x if it is new, are there
+        auto ready = [&](uint32_t u, uint32_t x, bool new_k) {
+            return (!new_k || mm_wait(&bars.k_full[x % C::kKStages], x / C::kKStages & 1, bars, p.err_flag)) &&
+                   (u < 4 || mm_wait(&bars.s_free[u & 3], ((u >> 2) - 1) & 1, bars, p.err_flag));
+        };
+        auto k_desc = [&](uint32_t x) { return kd0 + (uint64_t)(x % C::kKStages * C::kKBytes >> 4); };
 #pragma unroll 1
-        for (int blk = 0; blk < blocks && going; ++blk) {
-#pragma unroll 1
-            for (int st = step0; st < step1 && going; ++st) {
-                const int cols = (min(p.q_tile, queries - st * p.q_tile) * p.group + 15) & ~15;
-                const uint32_t idesc = tc_idesc_bf16(kMmKeys, 0, false, false) | (uint32_t)(cols >> 3) << 17;
-                const bool leaves = blk == blocks - 1; // the query tile is not wanted any more
-                uint32_t q_slot = q_slot0, q_par = q_par0;
-                auto q_next = [&] {
-                    if (++q_slot == C::kQStages) {
-                        q_slot = 0;
-                        q_par ^= 1;
-                    }
-                };
-                // the key tile and the accumulator of tile j are there
-                auto tile_ready = [&](int j) {
-                    const uint32_t u = seq + j, buf = u & 3;
-                    const uint32_t slot = k_slot0 + j, over = slot >= C::kKStages ? 1 : 0;
-                    return (st > step0 ||
-                            mm_wait(&bars.k_full[slot - over * C::kKStages], k_par0 ^ over, bars, p.err_flag)) &&
-                           (u < 4 || mm_wait(&bars.s_free[buf], ((u >> 2) - 1) & 1, bars, p.err_flag));
-                };
-                auto k_desc = [&](int j) {
-                    const uint32_t slot = k_slot0 + j;
-                    return kd0 + (uint64_t)((slot >= C::kKStages ? slot - C::kKStages : slot) * C::kKBytes >> 4);
-                };
-                if (kChunks <= 2) { // tile by tile, so that three accumulators can be read meanwhile
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        if (blk == 0 && !mm_wait(&bars.q_full[q_slot], q_par, bars, p.err_flag))
-                            going = false;
-                        q_next();
-                    }
-#pragma unroll 1
-                    for (int j = 0; j < tiles && going; ++j) {
-                        if (!tile_ready(j)) {
-                            going = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t buf = (seq + j) & 3;
-                        const uint64_t kd = k_desc(j);
-                        uint32_t slot = q_slot0;
-#pragma unroll
-                        for (int c = 0; c < kChunks; ++c) {
-                            if (blk * tiles + j < real)
-                                mm_mma4(tmem + buf * kMmCols, kd + (uint64_t)(c * 1024 >> 4),
-                                        qd0 + (uint64_t)(slot * C::kQBytes >> 4), idesc, c > 0 ? 1u : 0u);
-                            slot = slot + 1 == C::kQStages ? 0 : slot + 1;
-                        }
-                        mm_commit(&bars.s_full[buf]);
-                    }
-                } else { // chunk by chunk past the (at most two) key tiles: a query tile fills the ring
-#pragma unroll 1
-                    for (int c = 0; c < kChunks && going; ++c) {
-                        if (blk == 0 && !mm_wait(&bars.q_full[q_slot], q_par, bars, p.err_flag)) {
-                            going = false;
-                            break;
-                        }
-#pragma unroll 1
-                        for (int j = 0; j < tiles; ++j) {
-                            if (c == 0 && !tile_ready(j)) {
-                                going = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            const uint32_t buf = (seq + j) & 3;
-                            if (blk * tiles + j < real)
-                                mm_mma4(tmem + buf * kMmCols, k_desc(j) + (uint64_t)(c * 1024 >> 4),
-                                        qd0 + (uint64_t)(q_slot * C::kQBytes >> 4), idesc, c > 0 ? 1u : 0u);
-                            if (c == kChunks - 1)
-                                mm_commit(&bars.s_full[buf]);
-                        }
-                        if (leaves)
-                            mm_commit(&bars.q_empty[q_slot]);
-                        q_next();
-                    }
+        for (int st = step0; st < step1 && going; ++st) {
+            const int cols = (min(p.q_tile, queries - st * p.q_tile) * p.group + 15) & ~15;
+            const uint32_t idesc = tc_idesc_bf16(kMmKeys, 0, false, false) | (uint32_t)(cols >> 3) << 17;
+            uint64_t qd[kChunks]; // of the step's chunks
+            const bool by_chunk = kChunks > 2 && tiles > 1;
+            // (every phase of these barriers is waited for, with pairs to issue or not)
+            auto next_chunk = [&](int c) {
+                if (!mm_wait(&bars.q_full[q_slot], q_par, bars, p.err_flag))
+                    going = false;
+                qd[c] = qd0 + (uint64_t)(q_slot * C::kQBytes >> 4);
+                const uint32_t slot = q_slot;
+                if (++q_slot == C::kQStages) {
+                    q_slot = 0;
+                    q_par ^= 1;
                 }
+                return slot;
+            };
+            if (!by_chunk) { // all chunks, then the key tiles (or the run's blocks) one by one
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+                    next_chunk(c);
+                const int pairs = tiles == 1 ? blocks : tiles;
+#pragma unroll 1
+                for (int j = (half ^ seq) & 1; j < pairs && going; j += 2) {
+                    const uint32_t u = seq + j, x = tile0 + j;
+                    if (!ready(u, x, st == step0)) {
+                        going = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t kd = k_desc(x);
+                    const uint32_t d = tmem + (u & 3) * kMmCols;
+                    if (j < real) {
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c)
+                            mm_mma4(d, kd + (uint64_t)(c * 1024 >> 4), qd[c], idesc, c > 0 ? 1u : 0u);
+                    }
+                    mm_commit(&bars.s_full[u & 3]);
+                }
+                seq += pairs;
+            } else { // head_dim 256: a query tile nearly fills the ring, so its chunks are freed one by one
+                const int j = (half ^ seq) & 1; // (two key tiles)
+                const uint32_t u = seq + j, x = tile0 + j;
+                const uint64_t kd = k_desc(x);
+#pragma unroll 1
+                for (int c = 0; c < kChunks && going; ++c) {
+                    const uint32_t slot = next_chunk(0);
+                    if (!going || (c == 0 && !ready(u, x, st == step0))) {
+                        going = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (j < real)
+                        mm_mma4(tmem + (u & 3) * kMmCols, kd + (uint64_t)(c * 1024 >> 4), qd[0], idesc, c > 0 ? 1u : 0u);
+                    mm_commit(&bars.q_empty[slot]);
+                }
+                mm_commit(&bars.s_full[u & 3]);
                 seq += tiles;
-                if (leaves) {
-                    q_slot0 = q_slot;
-                    q_par0 = q_par;
-                }
-            }
-            k_slot0 += tiles;
-            if (k_slot0 >= C::kKStages) {
-                k_slot0 -= C::kKStages;
-                k_par0 ^= 1;
             }
         }
+        tile0 += tiles * blocks;
     }
     mm_commit(&bars.drain); // the commits have arrived before the CTA ends
     mbar_wait(&bars.drain, 0);
@@ -701,31 +720,30 @@ __device__ void mm_mma(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
                   "=r"(r[i + 6]), "=r"(r[i + 7])
 #define PKV_R8(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
                   "+r"(r[i + 6]), "+r"(r[i + 7])
-__device__ __forceinline__ void mm_ld32(uint32_t taddr, uint32_t (&r)[32])
+__device__ __forceinline__ void mm_ld16(uint32_t taddr, uint32_t (&r)[16])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-                 : PKV_O8(0), PKV_O8(8), PKV_O8(16), PKV_O8(24)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : PKV_O8(0), PKV_O8(8)
                  : "r"(taddr)
                  : "memory");
 }
 // Waits for this thread's TMEM loads; `r` is not read before.
-__device__ __forceinline__ void mm_ld_wait(uint32_t (&r)[32])
+__device__ __forceinline__ void mm_ld_wait(uint32_t (&r)[16])
 {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : PKV_R8(0), PKV_R8(8), PKV_R8(16), PKV_R8(24)::"memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : PKV_R8(0), PKV_R8(8)::"memory");
 }
 #undef PKV_O8
 #undef PKV_R8
 
-// The sum of 2^(x scale + z) over 32 columns; z holds -lse log2(e).
+// The sum of 2^(x scale + z) over 16 columns; z holds -lse log2(e).
 template <bool MASKED>
-__device__ __forceinline__ void mm_add32(const uint32_t (&x)[32], const float *z, float scale, int from, int to,
+__device__ __forceinline__ void mm_add16(const uint32_t (&x)[16], const float *z, float scale, int from, int to,
                                          float2 &sum0, float2 &sum1)
 {
     const float2 s2 = make_float2(scale, scale);
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
+    for (int i = 0; i < 16; i += 4) {
         const float4 z4 = *reinterpret_cast<const float4 *>(z + i);
         const float2 a = ffma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), s2,
                                make_float2(z4.x, z4.y));
@@ -851,41 +869,50 @@ __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
             if (quarter == 0 && lane == 0) {
                 if (now == s.step1 - 1)
                     mbar_arrive(&bars.k_empty[tile % C::kKStages]);
-                if (C::kChunks <= 2 && j == s.tiles - 1 && (s.tiles > 1 || blk >= s.blocks + 3))
+                // (the last pair of each of the two issuing warps; blk has gone on by 4)
+                const int pairs = s.tiles == 1 ? s.blocks : s.tiles, pair = s.tiles == 1 ? blk - 4 : j;
+                if ((C::kChunks <= 2 || s.tiles == 1) && pair >= pairs - 2)
 #pragma unroll
                     for (int c = 0; c < C::kChunks; ++c)
-                        mbar_arrive(&bars.q_empty[(q0 + (now - s.step0) * C::kChunks + c) % C::kQStages]);
+                        mbar_arrive_cnt(&bars.q_empty[(q0 + (now - s.step0) * C::kChunks + c) % C::kQStages],
+                                        pairs == 1 ? 2 : 1);
             }
             tc_fence_after();
             // columns of queries before the key's own see nothing of it
             const int seen = max(0, key - s.len - now * p.q_tile) * p.group;
             const bool edge = tok + kMmKeys - 1 - s.len > now * p.q_tile;
             float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-            uint32_t x[32];
-            const int whole = edge ? 0 : cols & ~31;
             auto leave = [&] { // all of the accumulator is in registers
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bars.s_free[w]);
             };
+            uint32_t x[16], y[16];
+            const int whole = edge ? 0 : cols & ~31;
             if (cols == 0)
                 leave();
+            if (whole > 0)
+                mm_ld16(acc, x);
 #pragma unroll 1
-            for (int c = 0; c < whole; c += 32) {
-                mm_ld32(acc + c, x);
+            for (int c = 0; c < whole; c += 32) { // 16 columns are summed while the next are read
                 mm_ld_wait(x);
-                if (c + 32 >= cols)
+                mm_ld16(acc + c + 16, y);
+                mm_add16<false>(x, zs + c, p.q_scale, 0, 16, sum0, sum1);
+                mm_ld_wait(y);
+                if (c + 32 < whole)
+                    mm_ld16(acc + c + 32, x);
+                else if (whole == cols)
                     leave();
-                mm_add32<false>(x, zs + c, p.q_scale, 0, 32, sum0, sum1);
+                mm_add16<false>(y, zs + c + 16, p.q_scale, 0, 16, sum0, sum1);
             }
 #pragma unroll 1
-            for (int c = whole; c < cols; c += 32) {
-                mm_ld32(acc + c, x);
+            for (int c = whole; c < cols; c += 16) {
+                mm_ld16(acc + c, x);
                 mm_ld_wait(x);
-                if (c + 32 >= cols)
+                if (c + 16 >= cols)
                     leave();
-                mm_add32<true>(x, zs + c, p.q_scale, seen - c, cols - c, sum0, sum1);
+                mm_add16<true>(x, zs + c, p.q_scale, seen - c, cols - c, sum0, sum1);
             }
             mm_add(sum, dropped, (sum0.x + sum1.x) + (sum0.y + sum1.y));
             if (s.tiles > 1 && st < s.step1)
@@ -965,7 +992,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         }
         for (int i = 0; i < C::kQStages; ++i) {
             mbar_init(&bars.q_full[i], 1);
-            mbar_init(&bars.q_empty[i], 1);
+            mbar_init(&bars.q_empty[i], 2); // once for each issuing warp's MMAs
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bars.s_full[i], 1);
@@ -980,7 +1007,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             mbar_init(&bars.half_full[i], 4);
             mbar_init(&bars.half_free[i], 4);
         }
-        mbar_init(&bars.drain, 1);
+        mbar_init(&bars.drain, 2);
         bars.abort = 0;
         mbar_init_fence();
         prefetch_tensormap(&maps.k);
@@ -996,14 +1023,12 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem_base, 0);
-    if (warp == kMmWalkWarp)
-        mm_walk(p, bars, from, lane);
-    else if (warp == kMmKWarp)
+    if (warp == kMmKWarp)
         mm_load_k<D>(p, maps, smem, bars, lane);
     else if (warp == kMmQWarp)
-        mm_load_q<D>(p, maps, smem, bars, lane);
-    else if (warp == kMmMmaWarp)
-        mm_mma<D>(p, smem, bars, tmem, lane);
+        mm_load_q<D>(p, maps, smem, bars, from, lane);
+    else if (warp == kMmMmaWarp || warp == kMmMmaWarp2)
+        mm_mma<D>(p, smem, bars, tmem, warp == kMmMmaWarp2 ? 1 : 0, lane);
     else
         mm_sum<D>(p, smem, bars, tmem, warp, lane);
     tc_fence_before();
