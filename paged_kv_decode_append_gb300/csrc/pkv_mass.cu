@@ -51,6 +51,7 @@ constexpr int kMmKWarp = 0, kMmMmaWarp = 1, kMmQWarp = 2, kMmMmaWarp2 = 3, kMmSu
 constexpr int kMmThreads = 640;
 constexpr int kMmRuns = 8;       // runs of blocks handed out and not yet done with
 constexpr int kMmReaders = 20;   // warps that read them
+constexpr int kMmNoQuery = 0x7fffffff; // of a column that a query tile does not have
 constexpr int kMmBadTiles = 16;  // key tiles whose bad pages are remembered
 
 template <int D> struct MmCfg {
@@ -63,7 +64,7 @@ template <int D> struct MmCfg {
     static constexpr uint32_t kGroupStride = 8 * D * 2;        // 8 keys, all of head_dim
     static constexpr uint32_t kOffK = 0;
     static constexpr uint32_t kOffQ = kOffK + kKStages * kKBytes;
-    static constexpr uint32_t kOffLse = kOffQ + kQStages * kQBytes; // [group of warps][three steps][128]
+    static constexpr uint32_t kOffLse = kOffQ + kQStages * kQBytes; // [group of warps][three steps][128 columns]
     static constexpr uint32_t kOffHalf = kOffLse + 4 * 3 * 128 * 4; // [pair of groups][128 keys]
     static constexpr uint32_t kOffBar = kOffHalf + 2 * 128 * 4;
     static constexpr uint32_t kSmem = kOffBar + 2048;
@@ -95,7 +96,8 @@ struct MmRow {
     int64_t work; // positions of a kv head
 };
 
-// a / b for a >= 0 and b > 0: nearly always small ones, whose division is a fraction of a 64-bit one.
+// a / b for a >= 0 and b > 0: nearly always small ones, whose division is a
+// fraction of a 64-bit one.
 __device__ __forceinline__ int64_t mm_div(int64_t a, int64_t b)
 {
     return ((uint64_t)a | (uint64_t)b) >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
@@ -218,6 +220,7 @@ __device__ __forceinline__ MmRow mm_row(const MmParams &p, const MmRaw &raw)
     r.blocks = (int)((keys + (1 << shift) - 1) >> shift);
     r.full = (int)min((int64_t)r.blocks, (((int64_t)r.len + p.q_tile - 1) >> shift) + 1);
     r.work = r.full * mm_cost(r, r.steps);
+#pragma unroll 1
     for (int kb = r.full; kb < r.blocks; ++kb)
         r.work += mm_cost(r, mm_steps(p, r, kb));
     return r;
@@ -314,7 +317,8 @@ __device__ __noinline__ bool mm_wait_slow(uint64_t *bar, uint32_t parity, MmBars
 }
 
 // Bounded wait for the phase of the given parity; gives up when another role
-// has.  A whole warp: all lanes get the same answer.
+// has.  A whole warp: all lanes get the same answer.  (Asking without being put to
+// sleep takes issue slots from the sums: 2 to 15 % more time.)
 __device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity, MmBars &bars, int32_t *err_flag)
 {
     bool done = mbar_try_wait(bar, parity);
@@ -352,6 +356,7 @@ struct MmWalk {
             const int64_t size = mm_cost(r, r.steps);
             kb = (int)min((int64_t)r.full, mm_div(off, size));
             off -= kb * size;
+#pragma unroll 1
             while (kb >= r.full && off >= mm_cost(r, mm_steps(p, r, kb)))
                 off -= mm_cost(r, mm_steps(p, r, kb++));
         }
@@ -716,34 +721,38 @@ __device__ void mm_mma(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
 
 // ---------------------------------------------------------------- sums
 
+// 32 (16) consecutive columns of this thread's lane, waited for.  (With the wait
+// apart from the load, so that sums could go on meanwhile, every value was moved
+// once more between the two.)
 #define PKV_O8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
                   "=r"(r[i + 6]), "=r"(r[i + 7])
-#define PKV_R8(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
-                  "+r"(r[i + 6]), "+r"(r[i + 7])
-__device__ __forceinline__ void mm_ld16(uint32_t taddr, uint32_t (&r)[16])
+__device__ __forceinline__ void mm_ld(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : PKV_O8(0), PKV_O8(8), PKV_O8(16), PKV_O8(24)
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void mm_ld(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
                  : PKV_O8(0), PKV_O8(8)
-                 : "r"(taddr)
-                 : "memory");
-}
-// Waits for this thread's TMEM loads; `r` is not read before.
-__device__ __forceinline__ void mm_ld_wait(uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : PKV_R8(0), PKV_R8(8)::"memory");
+                 : "r"(taddr));
 }
 #undef PKV_O8
-#undef PKV_R8
 
-// The sum of 2^(x scale + z) over 16 columns; z holds -lse log2(e).
-template <bool MASKED>
-__device__ __forceinline__ void mm_add16(const uint32_t (&x)[16], const float *z, float scale, int from, int to,
-                                         float2 &sum0, float2 &sum1)
+// The sum of 2^(x scale + z) over N columns; z holds -lse log2(e).
+template <bool MASKED, int N>
+__device__ __forceinline__ void mm_sum_of(const uint32_t (&x)[N], const float *z, float scale, int from, int to,
+                                          float2 &sum0, float2 &sum1)
 {
     const float2 s2 = make_float2(scale, scale);
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
+    for (int i = 0; i < N; i += 4) {
         const float4 z4 = *reinterpret_cast<const float4 *>(z + i);
         const float2 a = ffma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), s2,
                                make_float2(z4.x, z4.y));
@@ -791,7 +800,8 @@ __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
     float *lse = reinterpret_cast<float *>(smem + C::kOffLse) + w * 384;
     float *half = reinterpret_cast<float *>(smem + C::kOffHalf) + (w & 1) * 128;
     // the (query, head) of this thread's column, whose lse it fetches for the group
-    const int my_query = r / p.group, my_head = r - my_query * p.group;
+    const int my_query = r / p.group < p.q_tile ? r / p.group : kMmNoQuery, my_head = r % p.group;
+    int room = 256; // where the lse written last are
     uint32_t tile0 = 0;
     uint32_t q0 = 0; // chunks of query tiles before the run
     uint32_t seq = 0, taken = 0, staged = 0, halves = 0; // pairs before the run, taken by the group; lse; shared blocks
@@ -806,70 +816,73 @@ __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
         const int next_step = s.tiles == 4 ? 1 : 2;
         const bool shared = s.tiles == 2 && steps > 1; // with the group that has the other steps
         const bool ends = !shared || ((s.step1 - st) & 1) != 0; // this group finishes the block
-        const float *z_at = p.lse + ((int64_t)s.first + my_query) * p.num_q_heads + s.g * p.group + my_head;
-        auto lse_at = [&](int step) {
-            const int q = step * p.q_tile;
-            return my_query < p.q_tile && q + my_query < s.queries ? z_at[(int64_t)q * p.num_q_heads] : 0.f;
-        };
         // The columns' lse go through shared memory, a step ahead: while step k is
         // summed those of k + 1 are written and those of k + 2 are on their way.
+        const float *z_at = p.lse + ((int64_t)s.first + (my_query == kMmNoQuery ? 0 : my_query)) * p.num_q_heads +
+                            s.g * p.group + my_head;
+        auto fetch = [&](int step) {
+            const int q = step * p.q_tile;
+            return step < s.step1 && my_query < s.queries - q ? z_at[(int64_t)q * p.num_q_heads] : 0.f;
+        };
         auto stage = [&](float z) {
-            lse[staged % 3 * 128 + r] = z == -INFINITY ? z : z * -1.4426950408889634f;
+            room = room == 256 ? 0 : room + 128;
+            lse[room + r] = z == -INFINITY ? z : z * -1.4426950408889634f;
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&bars.z_full[w]);
             ++staged;
         };
-        float z = 0.f, sum = 0.f, dropped = 0.f, was = 0.f;
+        float z = 0.f;
         if (st < s.step1 && blk < s.blocks) {
-            z = lse_at(st);
-            const float z1 = s.tiles > 1 && st + next_step < s.step1 ? lse_at(st + next_step) : 0.f;
-            stage(z);
-            z = z1;
+            const float first = fetch(st);
+            z = s.tiles > 1 ? fetch(st + next_step) : 0.f;
+            stage(first);
         }
-        bool begins = true;
+        float sum = 0.f, dropped = 0.f, was = 0.f;
         const int64_t unit = ((int64_t)s.b * p.num_kv_heads + s.g) * p.slots;
+        const int whole_steps = p.q_tile * p.group == kMmCols ? s.queries / p.q_tile : 0; // with all columns
         const float *zs = lse;
+        int tok = 0, key = 0;
+        bool fresh = false, mine = false, new_z = true, begins = true;
 #pragma unroll 1
         while (st < s.step1 && blk < s.blocks) {
-            const int tok = s.tok + (blk * s.tiles + j) * kMmKeys, key = tok + r;
-            const bool fresh = key >= s.fresh, mine = ends && key < s.keys;
-            if (begins || s.tiles == 1) {
+            if (begins) {
+                tok = s.tok + (blk * s.tiles + j) * kMmKeys;
+                key = tok + r;
+                fresh = key >= s.fresh;
+                mine = ends && key < s.keys;
                 sum = dropped = was = 0.f;
                 if (mine && !fresh)
                     was = p.mass[unit + key];
             }
-            // (nothing to sum in a tile behind the row's end)
-            const int cols = tok < s.keys ? min(p.q_tile, s.queries - st * p.q_tile) * p.group : 0;
-            const int now = st;
-            if (begins || s.tiles > 1) {
+            if (new_z) {
                 if (!mm_wait(&bars.z_full[w], (staged - 1) & 1, bars, p.err_flag))
                     return;
-                zs = lse + (staged - 1) % 3 * 128;
+                zs = lse + room;
             }
-            begins = false;
+            const int now = st;
             if (s.tiles == 1) {
                 blk += 4;
+                new_z = false;
             } else {
+                begins = false;
                 st += next_step;
                 if (st < s.step1) {
                     // (the room was last read three steps ago: all of the group have staged since)
                     stage(z);
-                    if (st + next_step < s.step1)
-                        z = lse_at(st + next_step);
+                    z = fetch(st + next_step);
                 }
             }
             if (!mm_wait(&bars.s_full[w], taken & 1, bars, p.err_flag))
                 return;
             ++taken;
             // What the MMAs have read is free: the key tile after its last step, the
-            // query tile after its last key tile.  (Told from here: a commit of the
-            // MMA warp's own for it would cost that warp more than an MMA does.)
+            // query tile after the last pairs of the two issuing warps.  (Told from
+            // here: a commit for it would cost those warps more than an MMA does.)
             const uint32_t tile = tile0 + (uint32_t)(tok - s.tok) / kMmKeys;
             if (quarter == 0 && lane == 0) {
                 if (now == s.step1 - 1)
                     mbar_arrive(&bars.k_empty[tile % C::kKStages]);
-                // (the last pair of each of the two issuing warps; blk has gone on by 4)
                 const int pairs = s.tiles == 1 ? s.blocks : s.tiles, pair = s.tiles == 1 ? blk - 4 : j;
                 if ((C::kChunks <= 2 || s.tiles == 1) && pair >= pairs - 2)
 #pragma unroll
@@ -878,41 +891,47 @@ __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
                                         pairs == 1 ? 2 : 1);
             }
             tc_fence_after();
-            // columns of queries before the key's own see nothing of it
-            const int seen = max(0, key - s.len - now * p.q_tile) * p.group;
-            const bool edge = tok + kMmKeys - 1 - s.len > now * p.q_tile;
-            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
             auto leave = [&] { // all of the accumulator is in registers
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bars.s_free[w]);
             };
-            uint32_t x[16], y[16];
-            const int whole = edge ? 0 : cols & ~31;
-            if (cols == 0)
-                leave();
-            if (whole > 0)
-                mm_ld16(acc, x);
-#pragma unroll 1
-            for (int c = 0; c < whole; c += 32) { // 16 columns are summed while the next are read
-                mm_ld_wait(x);
-                mm_ld16(acc + c + 16, y);
-                mm_add16<false>(x, zs + c, p.q_scale, 0, 16, sum0, sum1);
-                mm_ld_wait(y);
-                if (c + 32 < whole)
-                    mm_ld16(acc + c + 32, x);
-                else if (whole == cols)
+            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+            const int start = now * p.q_tile;                    // query of the first column
+            const bool edge = tok + kMmKeys - 1 - s.len > start; // some queries do not see all of the tile
+            if (now < whole_steps && !edge && tok < s.keys) {    // all columns
+#pragma unroll
+                for (int c = 0; c < kMmCols; c += 32) {
+                    uint32_t x[32];
+                    mm_ld(acc + c, x);
+                    if (c + 32 == kMmCols)
+                        leave();
+                    mm_sum_of<false>(x, zs + c, p.q_scale, 0, 32, sum0, sum1);
+                }
+            } else {
+                // columns of queries before the key's own see nothing of it; of a tile
+                // behind the row's end there is nothing to sum
+                const int seen = max(0, key - s.len - start) * p.group;
+                const int cols = tok < s.keys ? min(p.q_tile, s.queries - start) * p.group : 0;
+                const int whole = edge ? 0 : cols & ~15;
+                uint32_t x[16];
+                if (cols == 0)
                     leave();
-                mm_add16<false>(y, zs + c + 16, p.q_scale, 0, 16, sum0, sum1);
-            }
 #pragma unroll 1
-            for (int c = whole; c < cols; c += 16) {
-                mm_ld16(acc + c, x);
-                mm_ld_wait(x);
-                if (c + 16 >= cols)
-                    leave();
-                mm_add16<true>(x, zs + c, p.q_scale, seen - c, cols - c, sum0, sum1);
+                for (int c = 0; c < whole; c += 16) {
+                    mm_ld(acc + c, x);
+                    if (c + 16 >= cols)
+                        leave();
+                    mm_sum_of<false>(x, zs + c, p.q_scale, 0, 16, sum0, sum1);
+                }
+#pragma unroll 1
+                for (int c = whole; c < cols; c += 16) {
+                    mm_ld(acc + c, x);
+                    if (c + 16 >= cols)
+                        leave();
+                    mm_sum_of<true>(x, zs + c, p.q_scale, seen - c, cols - c, sum0, sum1);
+                }
             }
             mm_add(sum, dropped, (sum0.x + sum1.x) + (sum0.y + sum1.y));
             if (s.tiles > 1 && st < s.step1)
@@ -937,8 +956,8 @@ __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
             }
             bool last = ends;
             if (ends && s.pieces > 1) {
-                float *part = p.parts + j * kMmKeys + r;
-                __stcg(part + (2 * blockIdx.x + (s.piece0 == blockIdx.x ? 1 : 0)) * 512, sum);
+                float *slot = p.parts + j * kMmKeys + r;
+                __stcg(slot + (2 * blockIdx.x + (s.piece0 == blockIdx.x ? 1 : 0)) * 512, sum);
                 int32_t *ticket = p.tickets + (s.piece0 * 4 + j) * 4 + quarter;
                 __syncwarp();
                 int old = 0;
@@ -949,10 +968,10 @@ __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
                 if (last) {
                     if (lane == 0)
                         *ticket = 0;
-                    sum = __ldcg(part + (2 * s.piece0 + 1) * 512);
+                    sum = __ldcg(slot + (2 * s.piece0 + 1) * 512);
                     dropped = 0.f;
                     for (int c = 1; c < s.pieces; ++c)
-                        mm_add(sum, dropped, __ldcg(part + 2 * (s.piece0 + c) * 512));
+                        mm_add(sum, dropped, __ldcg(slot + 2 * (s.piece0 + c) * 512));
                 }
             }
             const bool bad = (*(volatile uint16_t *)&bars.bad[tile % kMmBadTiles] >> (r >> 3)) & 1;
@@ -1014,15 +1033,19 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         prefetch_tensormap(&maps.q);
         prefetch_tensormap(&maps.q_one);
     }
-    if (warp == kMmMmaWarp) {
-        tmem_alloc(&bars.tmem_base, C::kTmemCols);
-        tmem_relinquish();
-    }
     const MmStart from = mm_start(p, bars.scratch, &bars.start);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem_base, 0);
+    // TMEM while the first loads are on their way: those who load have no use for it.
+    uint32_t tmem = 0;
+    if (warp != kMmKWarp && warp != kMmQWarp) {
+        if (warp == kMmMmaWarp) {
+            tmem_alloc(&bars.tmem_base, C::kTmemCols);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        named_sync(1, kMmThreads - 64);
+        tc_fence_after();
+        tmem = __shfl_sync(0xffffffffu, bars.tmem_base, 0);
+    }
     if (warp == kMmKWarp)
         mm_load_k<D>(p, maps, smem, bars, lane);
     else if (warp == kMmQWarp)
