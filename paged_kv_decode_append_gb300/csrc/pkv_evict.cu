@@ -49,12 +49,13 @@ __device__ __forceinline__ PlanRow plan_row(const PlanParams &p, int b)
 }
 
 // Importance of a slot as a whole number: protected above all, then by mass
-// (NaN below all), the order of floats.
-__device__ __forceinline__ uint32_t plan_key(float mass, int pos, int sink, int oldest)
+// (NaN below all), the order of floats.  Positions sink .. sink + open - 1 are not
+// protected.
+__device__ __forceinline__ uint32_t plan_key(float mass, int pos, int sink, uint32_t open)
 {
     const uint32_t u = __float_as_uint(mass + 0.0f); // -0 counts as 0
     const uint32_t k = mass != mass ? 0u : u ^ (uint32_t)((int32_t)u >> 31 | 0x80000000);
-    return pos < sink || pos > oldest ? kSafeKey : k;
+    return (uint32_t)pos - (uint32_t)sink >= open ? kSafeKey : k;
 }
 
 // The keys of a (layer, row, kv head), KEYS of them in every thread's registers,
@@ -65,14 +66,14 @@ template <int KEYS> struct PlanKeys {
     const float *mass;
     const int32_t *pos;
     uint32_t *held; // KEYS > 0: the masses, then the positions
-    int L, cached, sink, oldest; // positions below sink or above oldest are protected
-    int pos_at;
+    int L, cached, sink;
+    uint32_t open; // positions from sink on that are not protected
 
     __device__ __forceinline__ uint32_t at(int i) const
     {
         if (KEYS > 0)
-            return plan_key(__uint_as_float(held[i]), (int)held[pos_at + i], sink, oldest);
-        return i < cached ? held[i] : plan_key(mass[i], pos[i], sink, oldest);
+            return plan_key(__uint_as_float(held[i]), (int)held[KEYS * kPlanThreads + i], sink, open);
+        return i < cached ? held[i] : plan_key(mass[i], pos[i], sink, open);
     }
     // Through shared memory all of a row is under way at once and takes no
     // registers meanwhile (loads into registers, for which the compiler has none to
@@ -80,29 +81,28 @@ template <int KEYS> struct PlanKeys {
     __device__ __forceinline__ void load(int tid, int slots)
     {
         if (KEYS > 0) {
-            pos_at = (slots + 3) / 4 * 4;
+            uint32_t *held_pos = held + KEYS * kPlanThreads;
             if (slots % 4 == 0) { // every row begins on 16 bytes
                 for (int i = 4 * tid; i < L; i += 4 * kPlanThreads) {
                     copy16(held + i, mass + i);
-                    copy16(held + pos_at + i, pos + i);
+                    copy16(held_pos + i, pos + i);
                 }
             } else {
                 for (int i = tid; i < L; i += kPlanThreads) {
                     copy4(held + i, mass + i);
-                    copy4(held + pos_at + i, pos + i);
+                    copy4(held_pos + i, pos + i);
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < KEYS; ++j) {
-                const int i = tid + j * kPlanThreads;
-                const uint32_t key = at(min(i, L - 1));
-                k[j] = i < L ? key : kSafeKey;
+            for (int j = 0; j < KEYS; ++j) { // (there is room for all places; what lies past the row is not looked at)
+                const uint32_t key = at(tid + j * kPlanThreads);
+                k[j] = L - tid > j * kPlanThreads ? key : kSafeKey;
             }
         } else {
             for (int i = tid; i < min(L, cached); i += kPlanThreads)
-                held[i] = plan_key(mass[i], pos[i], sink, oldest);
+                held[i] = plan_key(mass[i], pos[i], sink, open);
         }
     }
     static __device__ __forceinline__ void copy16(void *to, const void *from)
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 
     if (r.keep >= r.L || r.keep == 0)
         return;
     const int L = r.L, keep = r.keep, words = (L + 31) / 32;
-    uint32_t *bits = s_dyn + (KEYS > 0 ? 2 * ((p.slots + 3) / 4 * 4) : p.cached);
+    uint32_t *bits = s_dyn + (KEYS > 0 ? 2 * KEYS * kPlanThreads : p.cached);
     PlanKeys<KEYS> keys;
     keys.mass = p.mass + unit * p.slots;
     keys.pos = p.pos + unit * p.slots;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 
     keys.L = L;
     keys.cached = p.cached;
     keys.sink = p.sink;
-    keys.oldest = (int)min((int64_t)INT32_MAX, max((int64_t)INT32_MIN, oldest));
+    keys.open = (uint32_t)min((int64_t)INT32_MAX + 1, max((int64_t)0, oldest - p.sink + 1));
     keys.load(tid, p.slots);
     auto no_bins = [&] {
         for (int i = tid; i < kBins / 4; i += kPlanThreads)
@@ -312,8 +312,10 @@ __global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 
         from += s_from;
         k = s_k;
         in = s_in;
-        no_bins();
-        __syncthreads();
+        if (in > kPlanList && k < in) { // once more
+            no_bins();
+            __syncthreads();
+        }
     }
     // The last that stays: key `least`, and among equals slot `last`.
     uint32_t least = among ? tie : from;
@@ -345,13 +347,8 @@ __global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 
     keys.mark(tid, bits, [&](int i, uint32_t key) { return (key > least) | ((key == least) & (i <= last)); });
     __syncthreads();
 
-    // Holes before the budget and slots that stay behind it, i-th to i-th.  Rows in
-    // registers have at most four words for each lane of one warp.
-    constexpr int kHands = KEYS > 0 ? 32 : kPlanThreads;
-    if (tid >= kHands)
-        return;
-    const int per_thread = (words + kHands - 1) / kHands;
-    const int a = min(words, tid * per_thread), z = min(words, a + per_thread);
+    // Holes before the budget and slots that stay behind it, i-th to i-th: how many
+    // there are before every word, then the words' bits.
     auto holes_of = [&](int w) {
         const int n = keep - w * 32; // (below L)
         return n <= 0 ? 0u : ~bits[w] & (n >= 32 ? 0xffffffffu : (1u << n) - 1);
@@ -361,37 +358,73 @@ __global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 
         const uint32_t word = bits[w] & (e >= 32 ? 0xffffffffu : (1u << e) - 1); // of the row's slots
         return n <= 0 ? word : n >= 32 ? 0u : word & ~((1u << n) - 1);
     };
-    int2 mine = make_int2(0, 0);
-    for (int w = a; w < z; ++w) {
-        mine.x += __popc(extra_of(w));
-        mine.y += __popc(holes_of(w));
-    }
-    int2 upto = mine;
+    constexpr int kHands = KEYS > 0 ? 32 : kPlanThreads; // rows in registers have at most four words for each lane of a warp
+    const int per_thread = (words + kHands - 1) / kHands;
+    const int a = min(words, tid * per_thread), z = min(words, a + per_thread);
+    int2 at = make_int2(0, 0);
+    if (tid < kHands) {
+        int2 mine = make_int2(0, 0);
+        for (int w = a; w < z; ++w) {
+            mine.x += __popc(extra_of(w));
+            mine.y += __popc(holes_of(w));
+        }
+        int2 upto = mine;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, upto.x, d), y = __shfl_up_sync(0xffffffffu, upto.y, d);
-        upto.x += lane >= d ? x : 0;
-        upto.y += lane >= d ? y : 0;
-    }
-    int2 at = make_int2(upto.x - mine.x, upto.y - mine.y);
-    if (kHands > 32) {
-        if (lane == 31)
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto.x, d), y = __shfl_up_sync(0xffffffffu, upto.y, d);
+            upto.x += lane >= d ? x : 0;
+            upto.y += lane >= d ? y : 0;
+        }
+        if (kHands > 32 && lane == 31)
             s_scan[warp] = upto;
+        at = make_int2(upto.x - mine.x, upto.y - mine.y);
+    }
+    int32_t *out = reinterpret_cast<int32_t *>(p.moves + unit * p.max_moves);
+    if (KEYS > 0) {
+        // A word has holes or slots that stay; the one that the budget cuts may have
+        // both, and its holes come last in the list.
+        __shared__ uint2 s_words[KEYS > 0 ? KEYS * kPlanWarps + 1 : 1]; // (bits, how many before)
+        const int cut = keep >> 5;
+        if (tid < kHands) {
+            for (int w = a; w < z; ++w) {
+                const uint32_t extra = extra_of(w), holes = holes_of(w);
+                s_words[w] = w < cut ? make_uint2(holes, at.y) : make_uint2(extra, at.x);
+                if (w == cut)
+                    s_words[words] = make_uint2(holes, at.y);
+                at.x += __popc(extra);
+                at.y += __popc(holes);
+            }
+            if (tid == kHands - 1)
+                p.num_moves[unit] = at.x;
+        }
+        __syncthreads();
+        const uint32_t before = (1u << lane) - 1;
+        for (int i0 = warp; i0 <= words; i0 += 32 * kPlanWarps) { // a word a lane, then those that have a bit
+            const int i = i0 + lane * kPlanWarps;
+            const uint2 mine = i <= words ? s_words[i] : make_uint2(0, 0);
+            for (uint32_t m = __ballot_sync(0xffffffffu, mine.x != 0); m != 0; m &= m - 1) {
+                const int from = __ffs(m) - 1, w = i0 + from * kPlanWarps;
+                const uint32_t word = __shfl_sync(0xffffffffu, mine.x, from), n = __shfl_sync(0xffffffffu, mine.y, from);
+                if ((word >> lane & 1) != 0)
+                    out[2 * (n + __popc(word & before)) + (w < cut || w == words ? 1 : 0)] =
+                        (w == words ? cut : w) * 32 + lane;
+            }
+        }
+    } else {
         __syncthreads();
         for (int w = 0; w < warp; ++w) {
             at.x += s_scan[w].x;
             at.y += s_scan[w].y;
         }
+        for (int w = a; w < z; ++w) {
+            for (uint32_t m = extra_of(w); m != 0; m &= m - 1)
+                out[2 * at.x++] = w * 32 + __ffs(m) - 1;
+            for (uint32_t m = holes_of(w); m != 0; m &= m - 1)
+                out[2 * at.y++ + 1] = w * 32 + __ffs(m) - 1;
+        }
+        if (tid == kHands - 1)
+            p.num_moves[unit] = at.x;
     }
-    int32_t *out = reinterpret_cast<int32_t *>(p.moves + unit * p.max_moves);
-    for (int w = a; w < z; ++w) {
-        for (uint32_t m = extra_of(w); m != 0; m &= m - 1)
-            out[2 * at.x++] = w * 32 + __ffs(m) - 1;
-        for (uint32_t m = holes_of(w); m != 0; m &= m - 1)
-            out[2 * at.y++ + 1] = w * 32 + __ffs(m) - 1;
-    }
-    if (tid == kHands - 1)
-        p.num_moves[unit] = at.x;
 }
 
 // ------------------------------------------------------------------- apply
@@ -575,7 +608,7 @@ pkv_status pkv_evict_plan(const float *mass, const int32_t *slot_pos, int32_t nu
     while (slots > e->slots)
         ++e;
     p.cached = slots < kPlanCached ? slots : kPlanCached;
-    const size_t held = e == &kPlanTable[kPlanLong] ? (size_t)p.cached : 2 * ((size_t)(slots + 3) / 4 * 4);
+    const size_t held = e == &kPlanTable[kPlanLong] ? (size_t)p.cached : 2 * (size_t)e->slots;
     const size_t words = e == &kPlanTable[kPlanLong] ? (slots + 31) / 32 : e->slots / 32;
     const size_t smem = (held + words) * sizeof(uint32_t);
     int dev = 0;
