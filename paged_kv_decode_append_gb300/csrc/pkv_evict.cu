@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 
     keys.L = L;
     keys.cached = p.cached;
     keys.sink = p.sink;
-    keys.open = (uint32_t)min((int64_t)INT32_MAX + 1, max((int64_t)0, oldest - p.sink + 1));
+    keys.open = (uint32_t)(max((int64_t)p.sink - 1, min((int64_t)INT32_MAX, oldest)) - p.sink + 1);
     keys.load(tid, p.slots);
     auto no_bins = [&] {
         for (int i = tid; i < kBins / 4; i += kPlanThreads)

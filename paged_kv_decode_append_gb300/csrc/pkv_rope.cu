@@ -315,12 +315,10 @@ pkv_status pkv_rope(const void *q, const void *k, const int32_t *positions, int3
                     float attn_factor, void *q_out, void *k_out, void *stream)
 {
     const pkv_status st = rope_check(head_dim, num_q_heads, num_kv_heads, num_tokens, rot_dim, pairing, attn_factor);
-    if (st != PKV_OK)
+    if (st != PKV_OK || num_tokens == 0) // (tensors of no tokens may have no address)
         return st;
     if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr) || (q == nullptr && k == nullptr))
         return PKV_EINVAL;
-    if (num_tokens == 0)
-        return PKV_OK;
     if (freqs == nullptr || positions == nullptr || (q != nullptr && num_q_heads < 1) ||
         (k != nullptr && num_kv_heads < 1) || !aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out))
         return PKV_EINVAL;
@@ -353,11 +351,12 @@ pkv_status pkv_rope_append(const pkv_cache_desc *desc, void *k_cache, void *v_ca
         st = rope_check(desc->head_dim, num_q_heads, desc->num_kv_heads, num_tokens, rot_dim, pairing, attn_factor);
     if (st != PKV_OK)
         return st;
-    if (batch < 0 || max_blocks < 1 || (q == nullptr) != (q_out == nullptr) ||
-        (append_indptr == nullptr && num_tokens != batch))
+    if (batch < 0 || max_blocks < 1 || (append_indptr == nullptr && num_tokens != batch))
         return PKV_EINVAL;
     if (batch == 0 || num_tokens == 0)
         return PKV_OK;
+    if ((q == nullptr) != (q_out == nullptr))
+        return PKV_EINVAL;
     if (k_cache == nullptr || v_cache == nullptr || k_new == nullptr || v_new == nullptr || freqs == nullptr ||
         block_table == nullptr || cache_seqlens == nullptr || (q != nullptr && num_q_heads < 1))
         return PKV_EINVAL;

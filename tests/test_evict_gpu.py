@@ -786,3 +786,129 @@ def test_a_step_in_a_graph():
         got.append([*c.k, *c.v, c.mass, c.pos, lens, c.gone, *outs])
     assert got[0][6].tolist() == [30, 43, 20]
     assert all(same_bits(a, b) for a, b in zip(*got))
+
+
+# ------------------------------------------------------------------- the calls themselves
+
+
+def test_wrong_tensors_are_refused():
+    case, lse = mass_case(22, [1, 1], [20, 5], 4, 2, 64, 8)
+    f, _ = freqs_of(64)
+    z, table, lens = lse.to(DEV), i32(case.block_table), i32(case.cache_seqlens)
+    mass, pos = torch.zeros(2, 2, 40, device=DEV), torch.zeros(2, 2, 40, dtype=torch.int32, device=DEV)
+    good = dict(k_cache=case.k_cache, q=case.q, lse=z, block_table=table, cache_seqlens=lens, softmax_scale=0.1, mass=mass,
+                slot_pos=pos)
+    pkv.pkv_attn_mass(**good)
+    for name, bad in (("lse", z.double()), ("lse", z.cpu()), ("lse", z[:, :3]), ("q", case.q[:, :, :32].contiguous()),
+                      ("q", case.q.transpose(0, 1)), ("mass", mass[:, :1].contiguous()), ("mass", mass[0]), ("mass", mass.half()),
+                      ("slot_pos", pos[..., 1:].contiguous()), ("slot_pos", pos.long()), ("cache_seqlens", lens[:1]),
+                      ("block_table", table.long()), ("k_cache", case.k_cache[0]), ("k_cache", case.k_cache.float()),
+                      ("qo_indptr", i32([0, 1])), ("workspace", torch.zeros(64, device=DEV)), ("err_flag", torch.zeros(1))):
+        with pytest.raises(ValueError):
+            pkv.pkv_attn_mass(**{**good, name: bad})
+    with pytest.raises(pkv.PkvError):
+        pkv.pkv_attn_mass(**good, workspace=torch.zeros(64, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError):
+        pkv.pkv_rope(case.q, case.k_new, i32([0]), f)
+    with pytest.raises(ValueError):
+        pkv.pkv_rope(case.q, None, i32([0, 1]), f.int())
+    with pytest.raises(ValueError):
+        pkv.pkv_rope(case.q, None, i32([0, 1]), f, q_out=case.q.float())
+    with pytest.raises(ValueError):
+        pkv.pkv_rope_append(case.k_cache, case.v_cache, case.q, case.k_new, case.v_new[:1], table, lens, f)
+    with pytest.raises(ValueError):
+        pkv.pkv_rope_append(case.k_cache, case.v_cache[:1], case.q, case.k_new, case.v_new, table, lens, f)
+    with pytest.raises(TypeError):
+        pkv.pkv_rope_append(case.k_cache, case.v_cache, case.q, case.k_new, case.v_new, table, lens, f, attn_factor="1")
+    with pytest.raises(ValueError):
+        pkv.pkv_evict_plan(mass[None], pos, lens, None, lens, 0, 0)
+    with pytest.raises(ValueError):
+        pkv.pkv_evict_plan(mass[None], pos[None], lens, None, lens, 2 ** 31, 0)
+    moves, num, rows = pkv.pkv_evict_plan(mass[None], pos[None], lens, None, i32([3, 3]), 0, 0)
+    layers = pkv.LayerCaches([case.k_cache], [case.v_cache])
+    for bad in (dict(mass=mass), dict(slot_pos=pos[None].float()), dict(err_flag=lens.long())):
+        with pytest.raises(ValueError):
+            pkv.pkv_evict_apply(layers, moves, num, rows, table, lens, None, **bad)
+    with pytest.raises(ValueError):
+        pkv.pkv_evict_apply(layers, moves, num[..., :1], rows, table, lens, None)
+
+
+def test_calls_of_no_tokens():
+    f, _ = freqs_of(64)
+    q = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device=DEV)
+    out, _ = pkv.pkv_rope(q, None, i32([]), f)
+    assert out.shape == q.shape
+    mass = torch.zeros(1, 0, 2, 8, device=DEV)
+    moves, num, rows = pkv.pkv_evict_plan(mass, mass.int(), i32([]), None, i32([]), 0, 0)
+    assert num.shape == (1, 0, 2) and rows.shape == (0, 2)
+
+
+def test_calls_on_another_stream():
+    """A step on a side stream behind a long kernel there: nothing runs ahead of it."""
+    case, lse = mass_case(23, [3, 1], [60, 40], 4, 2, 64, 8)
+    f, _ = freqs_of(64)
+    want = run_mass(case, lse)[1]
+    z, table, lens, ptr = lse.to(DEV), i32(case.block_table), i32(case.cache_seqlens), i32(case.qo_indptr)
+    start = torch.rand((2, 2, case.max_blocks * 8 + 3), generator=torch.Generator().manual_seed(1)).to(DEV)
+    mass, q0 = torch.empty_like(start), torch.empty_like(case.q)
+    q_ref, _ = pkv.pkv_rope(case.q, None, i32([5, 6, 7, 8]), f)
+    pos4 = i32([5, 6, 7, 8])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    big = torch.empty(1 << 28, device=DEV)
+    with torch.cuda.stream(side):
+        for _ in range(10):
+            big.fill_(1.0)
+        mass.copy_(start)
+        q0.copy_(case.q)
+        pkv.pkv_attn_mass(case.k_cache, q0, z, table, lens, case.softmax_scale, mass, qo_indptr=ptr)
+        q1, _ = pkv.pkv_rope(q0, None, pos4, f)
+    side.synchronize()
+    assert same_bits(mass.cpu(), want) and same_bits(q1, q_ref)
+
+
+def test_two_graphs_share_a_workspace():
+    """Rows cut between many CTAs, captured twice with one workspace, replayed in turn."""
+    case, lse = mass_case(24, [900, 700], [300, 0], 8, 2, 128, 16)
+    want = run_mass(case, lse, fresh=[0, 0])[1]
+    ws = pkv.mass_workspace(2, 1600, case.max_blocks, 8, pkv.cache_desc(case.k_cache), DEV)
+    z, table, lens, ptr, none = lse.to(DEV), i32(case.block_table), i32(case.cache_seqlens), i32(case.qo_indptr), i32([0, 0])
+    mass = [torch.zeros(2, 2, want.shape[-1], device=DEV) for _ in range(2)]
+    graphs = []
+    for m in mass:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            pkv.pkv_attn_mass(case.k_cache, case.q, z, table, lens, case.softmax_scale, m, qo_indptr=ptr, fresh_from=none,
+                              workspace=ws)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for m in mass:
+        for b, n in enumerate((1200, 700)):
+            assert same_bits(m[b, :, :n].cpu(), want[b, :, :n])
+
+
+@pytest.mark.parametrize("P", [8, 64, 128, 256])
+def test_mass_of_bad_pages_of_every_size(P):
+    case, lse = mass_case(25, [2, 150], [600, 450], 4, 2, 64, P)
+    blk = 250 // P
+    case.block_table[1, blk] = case.num_pages + 7
+    got = run_mass(case, lse)
+    assert got[3] == pkv.api.ERR_PAGE
+    case.block_table[1, blk] = 1
+    keys = {b: np.ones(700, bool) for b in range(2)}
+    keys[1][blk * P:(blk + 1) * P] = False
+    check_mass(case, lse, got, keys=keys)
+
+
+def test_plan_of_far_positions():
+    """Positions and counts at the ends of 32 bits."""
+    rng = np.random.default_rng(9)
+    mass = rng.random((1, 4, 1, 130)).astype(np.float32)
+    pos = rng.choice(np.array([-2 ** 31, -1, 0, 1, 7, 2 ** 30, 2 ** 31 - 2, 2 ** 31 - 1]), (1, 4, 1, 130))
+    lens, budgets = [130, 130, 130, 100], [60, 60, 60, 60]
+    gone = [2 ** 31 - 131, 2 ** 31 - 1, -2 ** 31, 0]
+    for sink, recent in ((0, 0), (1, 2), (2 ** 31 - 1, 0), (0, 2 ** 31 - 1), (8, 2 ** 30)):
+        got = plan(mass, pos, lens, gone, budgets, sink, recent)
+        check_plan(mass, pos, lens, gone, budgets, sink, recent, got)
