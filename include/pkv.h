@@ -632,7 +632,7 @@ PKV_API pkv_status pkv_tree_commit(const pkv_cache_desc *desc, int32_t num_layer
  * 64-bit fraction (units of 2^-64), so that far positions keep their angles.
  * Positions are the tokens' own, not their slots: after an eviction
  * (pkv_evict_apply) a slot's number says no longer when its token came.
- * Source: "mini-infer系统实战-06 True PagedAttention", section 4 (the caller
+ * Source: "mini-infer系统实战-06 True PagedAttention", section 3 (the caller
  * rotates q and k before the paged attention; the cache holds rotated keys).
  * --------------------------------------------------------------------- */
 
@@ -717,7 +717,8 @@ PKV_API pkv_status pkv_rope_append(const pkv_cache_desc *desc, void *k_cache, vo
  * slot_pos int32, both [batch, num_kv_heads, slots].  Attention does not depend
  * on the order of the cached tokens, so a cache that was cut down goes on to be
  * used by every call here; only causal masks among tokens of one call look at
- * slots, and those tokens are always the last.
+ * slots, and those tokens are always the last.  A row that is cut down needs
+ * pages of its own: a page that two block tables name would be moved in both.
  * Source: "flex_attention + paged KV + CUDA graphs vs vLLM", "What each option
  * did" (a page pool of fixed size reserved up front); "mini-infer系统实战-06 True
  * PagedAttention", section 8 (what a pool of pages holds).
@@ -745,7 +746,7 @@ PKV_API size_t pkv_mass_workspace_size(int32_t batch, int32_t total_q, int32_t m
  *                    (total_q = batch).
  *  lse               device fp32 [total_q, num_q_heads], as the attention call
  *                    wrote it; a query whose lse is -inf (it saw nothing) gives
- *                    nothing.
+ *                    nothing where its score is finite.
  *  cache_seqlens     device int32 [batch]: L_b, the length BEFORE this step's
  *                    tokens; the row holds L_b + q_b keys.
  *  fresh_from        device int32 [batch], or NULL for cache_seqlens: slots from

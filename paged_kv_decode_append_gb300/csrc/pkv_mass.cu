@@ -11,25 +11,39 @@
 //
 // What bounds it.  A decode step reads K once (32 KB for 128 keys at head_dim
 // 128, 0.74 us of an SM's share of the measured HBM rate) for 8 MMAs of 128 x 16
-// x 16: memory.  With many queries 128 keys x 128 columns take 8 MMAs of 128 x
-// 128 x 16 (0.33 us at the tensor peak) and 16384 exponentials.
+// x 16: memory.  64 uneven rows of 95,000 tokens in all, one of 32,768, take 39
+// us, 5.1 TB/s; while it streams it runs at 93 % of the copy rate, and the first
+// MMA comes 6.6 us after a CTA has begun (5.0 until its range and pages are known
+// and the first copy leaves, 1.6 until its data is there).  One token over 64: 7.4 us.
+// With many queries 128 keys x 128 columns (a pair) are 8 MMAs of 128 x 128 x 16,
+// 512 cycles at the tensor pipe's nominal rate, and 16,384 exponentials, 512
+// cycles at the 32 a cycle measured; a pair takes about 940.  No unit is full
+// (tensor 43 %, exponentials 43 %, issue slots 51 % of the elapsed cycles): a pair
+// goes from the MMAs to the sums and back in 3,700 cycles, and TMEM holds four.
+// Of those the sums take 2,350 (four TMEM loads at 300, the rest arithmetic), the
+// MMAs 700 from first to last.  Two rows of 3,500 .. 4,095 queries: 169 us, 1.0 PFLOP/s; head_dim 256, whose
+// pairs have twice the MMAs for the same sums: 107 us, 1.2 PFLOP/s (tensor 52 %).
 //
 // How (one persistent CTA per SM):
 //  - Work is laid out along a line: for every (row, kv head) its blocks of keys,
 //    for every block the steps through the query tiles that see it.  Every CTA
 //    takes an equal range; it finds it itself from the row arrays (no plan
 //    kernel, no host readback).  Rows whose queries fit one tile go by blocks of
-//    128 keys, others by 256: the query tiles then stream past two key tiles at
-//    once, which halves what they cost in L2 reads.
+//    128 keys, as runs; others by 256, and from eight query tiles on by 512 (head_dim
+//    128 and 64): the query tiles then stream past two or four key tiles at once,
+//    which halves what they cost in L2 reads each time.
 //  - A block cut between CTAs leaves partial sums in the workspace; the last
 //    CTA to arrive (a ticket for every 32 keys) adds them up in the order of the
 //    line, so results do not depend on timing.
-//  - Warps: 3 walks the CTA's range and hands out its blocks through a ring; 0
-//    loads K and 2 the query tiles, with TMA; 1 owns TMEM and issues the MMAs;
-//    4-7 and 8-11 add up, a key tile each, two accumulators each.
-//  - Sums of a step's columns are plain fp32 (128 terms at most); steps are
+//  - Warps: 0 loads K; 2 cuts the range into runs, hands them out through a ring
+//    and loads the query tiles; 1 and 3 issue the MMAs, every other pair each (one
+//    warp for all: 180 us for 106 at head_dim 256); 4-19 sum, four warps to a
+//    pair, each group with an accumulator of its own.  The sums tell the loaders
+//    what is free: as commits of the issuing warps that took 43 us for 41 (decode).
+//  - Sums of a step's columns are plain fp32 (four runs of 32 terms); steps are
 //    added up with a compensation for what the addition drops, so thousands of
-//    queries lose nothing.
+//    queries lose nothing.  Scores are exact products summed in fp32, and
+//    exponentials fp32: against 64 bits the result is off by 1e-7 .. 8e-7.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -57,7 +71,7 @@ constexpr int kMmBadTiles = 16;  // key tiles whose bad pages are remembered
 template <int D> struct MmCfg {
     static constexpr int kMostTiles = D == 256 ? 2 : 4;        // key tiles of a block
     static constexpr uint32_t kKBytes = kMmKeys * D * 2;
-    static constexpr int kKStages = D == 64 ? 8 : D == 128 ? 4 : 2;
+    static constexpr int kKStages = D == 64 ? 8 : D == 128 ? 4 : 2; // 128 KB
     static constexpr int kChunks = D / 64;                     // a query tile comes in chunks of 64 values
     static constexpr uint32_t kQBytes = kMmCols * 128;         // chunk: 128 rows of 128 B, swizzled
     static constexpr int kQStages = 5;

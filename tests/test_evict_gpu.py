@@ -637,13 +637,14 @@ def test_apply_row_fates():
         assert err == pkv.api.ERR_MOVE
         c.check(before, [[[m[1:] if (l, b, h) == (1, 0, 1) else m for h, m in enumerate(hs)] for b, hs in enumerate(bs)]
                          for l, bs in enumerate(lists)])
-    for n in (-1, moves.shape[3] + 1, 2 ** 31 - 1):
-        bad, before = num.clone(), c.clone()
-        bad[0, 2, 1] = n
-        _, _, err = c.apply(moves, bad, rows)
-        assert err == pkv.api.ERR_MOVE
-        c.check(before, [[[[] if (l, b, h) == (0, 2, 1) else m for h, m in enumerate(hs)] for b, hs in enumerate(bs)]
-                         for l, bs in enumerate(lists)])
+    for at in ((0, 2, 1), (0, 0, 0)):
+        for n in (-1, moves.shape[3] + 1, 2 ** 31 - 1):
+            bad, before = num.clone(), c.clone()
+            bad[at] = n
+            L, _, err = c.apply(moves, bad, rows)
+            assert err == pkv.api.ERR_MOVE and L.tolist() == [40, 40, 40]
+            c.check(before, [[[[] if (l, b, h) == at else m for h, m in enumerate(hs)] for b, hs in enumerate(bs)]
+                             for l, bs in enumerate(lists)])
 
 
 # ------------------------------------------------------------------- together
