@@ -23,8 +23,6 @@ namespace {
 
 // ------------------------------------------------------------------- plan
 
-constexpr int kPlanThreads = 128;
-constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kBins = 256;
 constexpr int kPlanList = 128;           // slots that are ranked against one another
 constexpr uint32_t kSafeKey = 0xffffffffu; // protected slots: above +inf's key
@@ -56,20 +54,22 @@ __device__ __forceinline__ PlanRow plan_row(const PlanParams &p, int b)
     return r;
 }
 
-// Importance of a slot as a whole number: protected above all, then by mass
-// (NaN below all), the order of floats.  Positions sink .. sink + open - 1 are not
-// protected.
-__device__ __forceinline__ uint32_t plan_key(float mass, int pos, int sink, uint32_t open)
+// A mass as a whole number, in the order of floats: NaN below all, -0 as 0.  Never
+// kSafeKey.
+__device__ __forceinline__ uint32_t plan_rank(uint32_t mass)
 {
-    const uint32_t u = __float_as_uint(mass + 0.0f); // -0 counts as 0
-    const uint32_t k = mass != mass ? 0u : u ^ (uint32_t)((int32_t)u >> 31 | 0x80000000);
-    return (uint32_t)pos - (uint32_t)sink >= open ? kSafeKey : k;
+    const float m = __uint_as_float(mass);
+    const uint32_t u = __float_as_uint(m + 0.0f);
+    return m != m ? 0u : u ^ (uint32_t)((int32_t)u >> 31 | 0x80000000);
 }
+constexpr uint32_t kPlainMost = 0x7f800000; // bits of masses 0 .. +inf are their order
 
-// The keys of a (layer, row, kv head), KEYS of them in every thread's registers,
-// slot tid + 128 k in place k (past the row: kSafeKey); or (KEYS = 0) as many as
+// The keys of a (layer, row, kv head), its slots' importance as whole numbers:
+// kSafeKey if protected, else by mass.  KEYS of them in every thread's registers,
+// slot tid + THREADS k in place k (past the row: kSafeKey); or (KEYS = 0) as many as
 // fit in shared memory and the others made anew whenever they are looked at.
-template <int KEYS> struct PlanKeys {
+template <int THREADS, int KEYS> struct PlanKeys {
+    static constexpr int kWarps = THREADS / 32;
     uint32_t k[KEYS > 0 ? KEYS : 1];
     const float *mass;
     const int32_t *pos;
@@ -77,11 +77,15 @@ template <int KEYS> struct PlanKeys {
     int L, cached, sink;
     uint32_t open; // positions from sink on that are not protected
 
+    __device__ __forceinline__ uint32_t key(uint32_t rank, int position) const
+    {
+        return (uint32_t)position - (uint32_t)sink >= open ? kSafeKey : rank;
+    }
     __device__ __forceinline__ uint32_t at(int i) const
     {
         if (KEYS > 0)
-            return plan_key(__uint_as_float(held[i]), (int)held[KEYS * kPlanThreads + i], sink, open);
-        return i < cached ? held[i] : plan_key(mass[i], pos[i], sink, open);
+            return key(held[i], (int)held[KEYS * THREADS + i]);
+        return i < cached ? held[i] : key(plan_rank(__float_as_uint(mass[i])), pos[i]);
     }
     // Through shared memory all of a row is under way at once and takes no
     // registers meanwhile (loads into registers, for which the compiler has none to
@@ -89,29 +93,42 @@ template <int KEYS> struct PlanKeys {
     __device__ __forceinline__ void load(int tid, int slots)
     {
         if (KEYS > 0) {
-            uint32_t *held_pos = held + KEYS * kPlanThreads;
+            uint32_t *held_pos = held + KEYS * THREADS;
             if (slots % 4 == 0) { // every row begins on 16 bytes
-                for (int i = 4 * tid; i < L; i += 4 * kPlanThreads) {
+                for (int i = 4 * tid; i < L; i += 4 * THREADS) {
                     copy16(held + i, mass + i);
                     copy16(held_pos + i, pos + i);
                 }
             } else {
-                for (int i = tid; i < L; i += kPlanThreads) {
+                for (int i = tid; i < L; i += THREADS) {
                     copy4(held + i, mass + i);
                     copy4(held_pos + i, pos + i);
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncthreads();
+        } else {
+            for (int i = tid; i < min(L, cached); i += THREADS)
+                held[i] = key(plan_rank(__float_as_uint(mass[i])), pos[i]);
+        }
+    }
+    // Keys into registers.  Masses are taken for their bits, which is right for 0 ..
+    // +inf; if there are others their ranks are put in their place first.
+    __device__ __forceinline__ void take(int tid)
+    {
+        if (KEYS > 0)
 #pragma unroll
             for (int j = 0; j < KEYS; ++j) { // (there is room for all places; what lies past the row is not looked at)
-                const uint32_t key = at(tid + j * kPlanThreads);
-                k[j] = L - tid > j * kPlanThreads ? key : kSafeKey;
+                const int i = tid + j * THREADS;
+                const uint32_t rank = min(held[i], kSafeKey - 1), from = held[KEYS * THREADS + i] - (uint32_t)sink;
+                k[j] = (from < open) & (L - tid > j * THREADS) ? rank : kSafeKey;
             }
-        } else {
-            for (int i = tid; i < min(L, cached); i += kPlanThreads)
-                held[i] = plan_key(mass[i], pos[i], sink, open);
-        }
+    }
+    __device__ __forceinline__ void rank(int tid)
+    {
+#pragma unroll 1
+        for (int i = tid; i < L; i += THREADS)
+            held[i] = plan_rank(held[i]);
     }
     static __device__ __forceinline__ void copy16(void *to, const void *from)
     {
@@ -127,9 +144,9 @@ template <int KEYS> struct PlanKeys {
         if (KEYS > 0) {
 #pragma unroll
             for (int j = 0; j < KEYS; ++j)
-                f(tid + j * kPlanThreads, k[j]);
+                f(tid + j * THREADS, k[j]);
         } else {
-            for (int i = tid; i < L; i += kPlanThreads)
+            for (int i = tid; i < L; i += THREADS)
                 f(i, at(i));
         }
     }
@@ -137,7 +154,7 @@ template <int KEYS> struct PlanKeys {
     template <typename F> __device__ __forceinline__ void each_rarely(int tid, F f) const
     {
 #pragma unroll 1
-        for (int i = tid; i < L; i += kPlanThreads)
+        for (int i = tid; i < L; i += THREADS)
             f(i, at(i));
     }
     // A bit for every slot that f(slot, key) says, 32 slots a word.  The whole CTA.
@@ -147,12 +164,12 @@ template <int KEYS> struct PlanKeys {
         if (KEYS > 0) {
 #pragma unroll
             for (int j = 0; j < KEYS; ++j) {
-                const uint32_t word = __ballot_sync(0xffffffffu, f(tid + j * kPlanThreads, k[j]));
+                const uint32_t word = __ballot_sync(0xffffffffu, f(tid + j * THREADS, k[j]));
                 if (lane == 0) // (there is room for all places)
-                    bits[(tid >> 5) + j * kPlanWarps] = word;
+                    bits[(tid >> 5) + j * kWarps] = word;
             }
         } else {
-            for (int i = tid; (i & ~31) < L; i += kPlanThreads) {
+            for (int i = tid; (i & ~31) < L; i += THREADS) {
                 const uint32_t word = __ballot_sync(0xffffffffu, i < L && f(i, at(i)));
                 if (lane == 0)
                     bits[i >> 5] = word;
@@ -192,14 +209,15 @@ __device__ __forceinline__ void plan_append(uint32_t count, uint32_t list, uint3
 // slots than that have one and the same key, the count goes on over the slots.
 // Few threads with many keys each: what a warp does once (votes, scans, waits)
 // then weighs less.
-template <int KEYS>
-__global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 : 10)
+template <int THREADS, int KEYS>
+__global__ void __launch_bounds__(THREADS, (KEYS == 17 || KEYS == 0 ? 1024 : 1280) / THREADS)
     evict_plan_kernel(const __grid_constant__ PlanParams p)
 {
+    constexpr int kWarps = THREADS / 32;
     extern __shared__ __align__(16) uint32_t s_dyn[]; // keys (or what they are made from), a bit for every slot that stays
     __shared__ __align__(16) int s_bins[kBins];
     __shared__ uint64_t s_list[kPlanList];
-    __shared__ int2 s_scan[kPlanWarps];
+    __shared__ int2 s_scan[kWarps];
     __shared__ uint32_t s_lo, s_hi;
     __shared__ int s_safe, s_count, s_k, s_in;
     __shared__ uint32_t s_from;
@@ -227,8 +245,8 @@ __global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 
     if (r.keep >= r.L || r.keep == 0)
         return;
     const int L = r.L, keep = r.keep, words = (L + 31) / 32;
-    uint32_t *bits = s_dyn + (KEYS > 0 ? 2 * KEYS * kPlanThreads : p.cached);
-    PlanKeys<KEYS> keys;
+    uint32_t *bits = s_dyn + (KEYS > 0 ? 2 * KEYS * THREADS : p.cached);
+    PlanKeys<THREADS, KEYS> keys;
     keys.mass = p.mass + unit * p.slots;
     keys.pos = p.pos + unit * p.slots;
     keys.held = s_dyn;
@@ -238,30 +256,44 @@ __global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 
     keys.open = (uint32_t)(max((int64_t)p.sink - 1, min((int64_t)INT32_MAX, oldest)) - p.sink + 1);
     keys.load(tid, p.slots);
     auto no_bins = [&] {
-        for (int i = tid; i < kBins / 4; i += kPlanThreads)
+        for (int i = tid; i < kBins / 4; i += THREADS)
             reinterpret_cast<int4 *>(s_bins)[i] = make_int4(0, 0, 0, 0);
     };
     no_bins();
     __syncthreads();
 
     // Protected slots, and the range of the others' keys.
-    uint32_t lo = kSafeKey, hi = 0;
-    int safe = 0;
-    keys.each(tid, [&](int, uint32_t k) {
-        safe += k == kSafeKey ? 1 : 0;
-        lo = min(lo, k);     // (a protected slot's key changes nothing)
-        hi = max(hi, k + 1); // (that of a protected slot becomes 0)
-    });
-    safe = __reduce_add_sync(0xffffffffu, safe);
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) {
-        atomicAdd(&s_safe, safe);
-        atomicMin(&s_lo, lo);
-        atomicMax(&s_hi, hi);
+    int safe;
+    for (bool ranked = KEYS == 0;; ranked = true) {
+        keys.take(tid);
+        uint32_t lo = kSafeKey, hi = 0;
+        safe = 0;
+        keys.each(tid, [&](int, uint32_t k) {
+            safe += k == kSafeKey ? 1 : 0;
+            lo = min(lo, k);     // (a protected slot's key changes nothing)
+            hi = max(hi, k + 1); // (that of a protected slot becomes 0)
+        });
+        safe = __reduce_add_sync(0xffffffffu, safe);
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (lane == 0) {
+            atomicAdd(&s_safe, safe);
+            atomicMin(&s_lo, lo);
+            atomicMax(&s_hi, hi);
+        }
+        __syncthreads();
+        if (ranked || s_hi <= kPlainMost + 1)
+            break;
+        __syncthreads();
+        keys.rank(tid); // negative masses, -0 or NaN
+        if (tid == 0) {
+            s_lo = kSafeKey;
+            s_hi = 0;
+            s_safe = 0;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    safe = s_safe - (KEYS > 0 ? KEYS * kPlanThreads - L : 0);
+    safe = s_safe - (KEYS > 0 ? KEYS * THREADS - L : 0);
 
     // The open range [from, from + width]: of keys, or (`among`) of ~slot among the
     // slots of key `tie`.
@@ -339,7 +371,7 @@ __global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 
                 plan_append(smem_addr(&s_count), smem_addr(s_list), key - from, width, key, i);
             });
         __syncthreads();
-        if (tid < in) {
+        if (tid < in) { // (at most 128)
             const uint64_t x = s_list[tid];
             int above = 0;
             for (int j = 0; j < in; ++j)
@@ -366,7 +398,7 @@ __global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 
         const uint32_t word = bits[w] & (e >= 32 ? 0xffffffffu : (1u << e) - 1); // of the row's slots
         return n <= 0 ? word : n >= 32 ? 0u : word & ~((1u << n) - 1);
     };
-    constexpr int kHands = KEYS > 0 ? 32 : kPlanThreads; // rows in registers have at most four words for each lane of a warp
+    constexpr int kHands = KEYS > 0 && KEYS * kWarps <= 128 ? 32 : THREADS; // up to four words a lane, one warp does
     const int per_thread = (words + kHands - 1) / kHands;
     const int a = min(words, tid * per_thread), z = min(words, a + per_thread);
     int2 at = make_int2(0, 0);
@@ -387,11 +419,18 @@ __global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 
             s_scan[warp] = upto;
         at = make_int2(upto.x - mine.x, upto.y - mine.y);
     }
+    if (kHands > 32) {
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) {
+            at.x += s_scan[w].x;
+            at.y += s_scan[w].y;
+        }
+    }
     int32_t *out = reinterpret_cast<int32_t *>(p.moves + unit * p.max_moves);
     if (KEYS > 0) {
         // A word has holes or slots that stay; the one that the budget cuts may have
         // both, and its holes come last in the list.
-        __shared__ uint2 s_words[KEYS > 0 ? KEYS * kPlanWarps + 1 : 1]; // (bits, how many before)
+        __shared__ uint2 s_words[KEYS > 0 ? KEYS * kWarps + 1 : 1]; // (bits, how many before)
         const int cut = keep >> 5;
         if (tid < kHands) {
             for (int w = a; w < z; ++w) {
@@ -407,11 +446,11 @@ __global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 
         }
         __syncthreads();
         const uint32_t before = (1u << lane) - 1;
-        for (int i0 = warp; i0 <= words; i0 += 32 * kPlanWarps) { // a word a lane, then those that have a bit
-            const int i = i0 + lane * kPlanWarps;
+        for (int i0 = warp; i0 <= words; i0 += 32 * kWarps) { // a word a lane, then those that have a bit
+            const int i = i0 + lane * kWarps;
             const uint2 mine = i <= words ? s_words[i] : make_uint2(0, 0);
             for (uint32_t m = __ballot_sync(0xffffffffu, mine.x != 0); m != 0; m &= m - 1) {
-                const int from = __ffs(m) - 1, w = i0 + from * kPlanWarps;
+                const int from = __ffs(m) - 1, w = i0 + from * kWarps;
                 const uint32_t word = __shfl_sync(0xffffffffu, mine.x, from), n = __shfl_sync(0xffffffffu, mine.y, from);
                 if ((word >> lane & 1) != 0)
                     out[2 * (n + __popc(word & before)) + (w < cut || w == words ? 1 : 0)] =
@@ -419,11 +458,6 @@ __global__ void __launch_bounds__(kPlanThreads, KEYS == 32 ? 5 : KEYS == 17 ? 8 
             }
         }
     } else {
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) {
-            at.x += s_scan[w].x;
-            at.y += s_scan[w].y;
-        }
         for (int w = a; w < z; ++w) {
             for (uint32_t m = extra_of(w); m != 0; m &= m - 1)
                 out[2 * at.x++] = w * 32 + __ffs(m) - 1;
@@ -549,33 +583,46 @@ bool aligned16(const void *p)
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
-constexpr int kPlanCached = 32768; // keys in shared memory at most; longer rows make theirs again
+constexpr int kPlanCached = 38912; // keys in shared memory at most; longer rows make theirs again
 
-// Keys in registers up to 4096 slots (32 a thread), then in shared memory.
+// Keys in registers up to 17,408 slots, then in shared memory.
 struct PlanEntry {
-    int slots;
+    int slots, threads;
     const void *kernel;
 };
+template <int THREADS, int KEYS> constexpr PlanEntry plan_entry()
+{
+    return {KEYS > 0 ? THREADS * KEYS : kEvictMaxSlots, THREADS,
+            reinterpret_cast<const void *>(&evict_plan_kernel<THREADS, KEYS>)};
+}
 const PlanEntry kPlanTable[] = {
-    {1 * kPlanThreads, reinterpret_cast<const void *>(&evict_plan_kernel<1>)},
-    {4 * kPlanThreads, reinterpret_cast<const void *>(&evict_plan_kernel<4>)},
-    {9 * kPlanThreads, reinterpret_cast<const void *>(&evict_plan_kernel<9>)},
-    {17 * kPlanThreads, reinterpret_cast<const void *>(&evict_plan_kernel<17>)},
-    {32 * kPlanThreads, reinterpret_cast<const void *>(&evict_plan_kernel<32>)},
-    {kEvictMaxSlots, reinterpret_cast<const void *>(&evict_plan_kernel<0>)},
+    plan_entry<128, 1>(),  plan_entry<128, 4>(),  plan_entry<128, 9>(),  plan_entry<128, 17>(),
+    plan_entry<256, 17>(), plan_entry<512, 17>(), plan_entry<1024, 17>(), plan_entry<1024, 0>(),
 };
-constexpr int kPlanLong = 5; // the last of them
+constexpr int kPlanEntries = 8, kPlanLong = kPlanEntries - 1; // the last of them
 
-// Once per device: the last kernel's shared memory.
+size_t plan_smem(const PlanEntry &e, int slots, int cached)
+{
+    const bool is_long = &e == &kPlanTable[kPlanLong];
+    const size_t held = is_long ? (size_t)cached : 2 * (size_t)e.slots;
+    const size_t words = is_long ? ((size_t)slots + 31) / 32 : (size_t)e.slots / 32;
+    return (held + words) * sizeof(uint32_t);
+}
+
+// Once per device: the shared memory of the kernels that take more than the default.
 bool plan_ready(int device)
 {
     constexpr int kDevices = 64;
     static bool done[kDevices] = {};
     if (device < 0 || device >= kDevices)
         return false;
-    if (!done[device])
-        done[device] = cudaFuncSetAttribute(kPlanTable[kPlanLong].kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            (kPlanCached + kEvictMaxSlots / 32) * 4) == cudaSuccess;
+    if (!done[device]) {
+        bool good = true;
+        for (const PlanEntry &e : kPlanTable)
+            good = good && cudaFuncSetAttribute(e.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                (int)plan_smem(e, e.slots, kPlanCached)) == cudaSuccess;
+        done[device] = good;
+    }
     return done[device];
 }
 
@@ -621,14 +668,12 @@ pkv_status pkv_evict_plan(const float *mass, const int32_t *slot_pos, int32_t nu
     while (slots > e->slots)
         ++e;
     p.cached = slots < kPlanCached ? slots : kPlanCached;
-    const size_t held = e == &kPlanTable[kPlanLong] ? (size_t)p.cached : 2 * (size_t)e->slots;
-    const size_t words = e == &kPlanTable[kPlanLong] ? (slots + 31) / 32 : e->slots / 32;
-    const size_t smem = (held + words) * sizeof(uint32_t);
+    const size_t smem = plan_smem(*e, slots, p.cached);
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || !plan_ready(dev))
         return PKV_ECUDA;
     void *args[] = {&p};
-    return cudaLaunchKernel(e->kernel, dim3((unsigned)units), dim3(kPlanThreads), args, smem,
+    return cudaLaunchKernel(e->kernel, dim3((unsigned)units), dim3(e->threads), args, smem,
                             static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PKV_OK
                : PKV_ECUDA;

@@ -507,6 +507,20 @@ def test_plan_of_long_rows(slots, budget):
     check_plan(mass, pos, lens, None, [budget, min(budget, slots - 78)], 4, 100, got)
 
 
+@pytest.mark.parametrize("slots", [128, 129, 513, 1153, 2177, 4352, 4353, 8704, 8706, 17408, 17409, 38912, 38913])
+@pytest.mark.parametrize("low", [None, -1e-30, -0.0, NAN])
+def test_plan_at_the_ends_of_its_variants(slots, low):
+    rng = np.random.default_rng(slots)
+    lens, budgets = [slots, slots - 1, slots // 2 + 1, slots], [slots // 2, 77, 60, slots - 1]
+    mass = np.exp(2 * rng.standard_normal((1, 4, 1, slots))).astype(np.float32)
+    if low is not None:
+        mass[0, :, 0, rng.integers(0, slots)] = low  # rows of masses that are not all 0 .. +inf
+        mass[0, 3, 0, : slots // 3] = low
+        mass[0, 1, 0, -1] = np.uint32(0xffffffff).view(np.float32)
+    pos = np.tile(np.arange(slots), (1, 4, 1, 1))
+    check_plan(mass, pos, lens, None, budgets, 3, 40, plan(mass, pos, lens, None, budgets, 3, 40))
+
+
 def test_plan_row_fates():
     rng = np.random.default_rng(8)
     mass = rng.random((1, 4, 2, 100)).astype(np.float32)
