@@ -9,12 +9,12 @@
 // before it: no move reads what another one writes.
 //
 // What bounds them.  The plan reads 8 bytes a slot and writes little: 36 layers x 64
-// rows x 8 heads of 2,049 .. 2,112 slots (312 MB, 47 us at the copy rate) take 109
-// us, 2.9 TB/s.  It is bound by instructions (two thirds of the issue slots, 30
-// a slot for key, range, count, list and mark together and as many again for what
-// a unit does once).  The moves are memory: half of 8 x 1,000 tokens in 36 layers
-// (609 MB) in 111 us, 5.5 TB/s, 82 % of the copy rate, rows of 256 bytes from
-// scattered pages.  Small ones: 3.1 and 3.6 us.
+// rows x 8 heads of 2,049 .. 2,112 slots (312 MB, 47 us at the copy rate) take 81
+// us, 3.9 TB/s.  It is bound by instructions (74 % of the issue slots, 59 % of the
+// integer pipe's; 26 for 32 slots in four passes, the rest what a unit does once).
+// The moves are memory: half of 8 x 1,000 tokens in 36 layers (609 MB) in 111 us, 5.5
+// TB/s, 82 % of the copy rate, rows of 256 bytes from scattered pages.  Small ones:
+// 2.9 and 3.6 us.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -188,15 +188,15 @@ __device__ __forceinline__ void plan_count(uint32_t bins, uint32_t x, uint32_t w
                  "r"(width), "r"(bins + ((x >> shift) << 2))
                  : "memory");
 }
-// Appends (key, ~slot) to the list, if x = key - from is in the open range.
-__device__ __forceinline__ void plan_append(uint32_t count, uint32_t list, uint32_t x, uint32_t width, uint32_t key, int i)
+// Appends (key, ~slot) to the list, if x = key - from is below `size`.
+__device__ __forceinline__ void plan_append(uint32_t count, uint32_t list, uint32_t x, uint32_t size, uint32_t key, int i)
 {
     asm volatile("{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
-                 "setp.le.u32 p, %0, %1;\n\t"
+                 "setp.lt.u32 p, %0, %1;\n\t"
                  "@p atom.shared.add.u32 n, [%2], 1;\n\t"
                  "@p mad.lo.u32 n, n, 8, %3;\n\t"
                  "@p st.shared.v2.u32 [n], {%4, %5};\n\t}" ::"r"(x),
-                 "r"(width), "r"(count), "r"(list), "r"(~(uint32_t)i), "r"(key)
+                 "r"(size), "r"(count), "r"(list), "r"(~(uint32_t)i), "r"(key)
                  : "memory");
 }
 
@@ -210,7 +210,7 @@ __device__ __forceinline__ void plan_append(uint32_t count, uint32_t list, uint3
 // Few threads with many keys each: what a warp does once (votes, scans, waits)
 // then weighs less.
 template <int THREADS, int KEYS>
-__global__ void __launch_bounds__(THREADS, (KEYS == 17 || KEYS == 0 ? 1024 : 1280) / THREADS)
+__global__ void __launch_bounds__(THREADS, (KEYS == 0 ? 1024 : 1280) / THREADS)
     evict_plan_kernel(const __grid_constant__ PlanParams p)
 {
     constexpr int kWarps = THREADS / 32;
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(THREADS, (KEYS == 17 || KEYS == 0 ? 1024 : 128
     __shared__ uint32_t s_lo, s_hi;
     __shared__ int s_safe, s_count, s_k, s_in;
     __shared__ uint32_t s_from;
-    __shared__ uint64_t s_least;
+    __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t unit = blockIdx.x;
     const int per_layer = p.batch * p.num_kv_heads;
@@ -357,34 +357,48 @@ __global__ void __launch_bounds__(THREADS, (KEYS == 17 || KEYS == 0 ? 1024 : 128
             __syncthreads();
         }
     }
-    // The last that stays: key `least`, and among equals slot `last`.
-    uint32_t least = among ? tie : from;
-    int last = among ? (int)~from : 0x7fffffff;
-    if (k < in) {
-        if (among)
+    // A bit for every slot that stays: those above the open range, and of those in
+    // it the k first, unless all do.
+    const bool all = k == in;
+    if (among) { // key `tie`: up to slot `last`
+        int last = (int)~from;
+        if (!all) {
             keys.each_rarely(tid, [&](int i, uint32_t key) {
                 if (key == tie && ~(uint32_t)i - from <= width)
-                    s_list[atomicAdd(&s_count, 1)] = (uint64_t)key << 32 | ~(uint32_t)i;
+                    s_list[atomicAdd(&s_count, 1)] = ~(uint32_t)i;
             });
-        else
-            keys.each(tid, [&](int i, uint32_t key) {
-                plan_append(smem_addr(&s_count), smem_addr(s_list), key - from, width, key, i);
-            });
-        __syncthreads();
-        if (tid < in) { // (at most 128)
-            const uint64_t x = s_list[tid];
-            int above = 0;
-            for (int j = 0; j < in; ++j)
-                above += s_list[j] > x ? 1 : 0;
-            if (above == k - 1)
-                s_least = x;
+            __syncthreads();
+            if (tid < in) {
+                const uint64_t x = s_list[tid];
+                int above = 0;
+                for (int j = 0; j < in; ++j)
+                    above += s_list[j] > x ? 1 : 0;
+                if (above == k - 1)
+                    s_last = (int)~(uint32_t)x;
+            }
+            __syncthreads();
+            last = s_last;
         }
-        __syncthreads();
-        least = (uint32_t)(s_least >> 32);
-        last = (int)~(uint32_t)s_least;
+        keys.mark(tid, bits, [&](int i, uint32_t key) { return (key > tie) | ((key == tie) & (i <= last)); });
+    } else {
+        const uint32_t size = all ? 0 : width + 1, stays = from + size;
+        keys.mark(tid, bits, [&](int i, uint32_t key) {
+            plan_append(smem_addr(&s_count), smem_addr(s_list), key - from, size, key, i);
+            return key >= stays;
+        });
+        if (!all) {
+            __syncthreads();
+            if (tid < in) { // (at most 128)
+                const uint64_t x = s_list[tid];
+                int above = 0;
+                for (int j = 0; j < in; ++j)
+                    above += s_list[j] > x ? 1 : 0;
+                const uint32_t i = ~(uint32_t)x;
+                if (above < k)
+                    atomicOr(&bits[i >> 5], 1u << (i & 31));
+            }
+        }
     }
-
-    keys.mark(tid, bits, [&](int i, uint32_t key) { return (key > least) | ((key == least) & (i <= last)); });
     __syncthreads();
 
     // Holes before the budget and slots that stay behind it, i-th to i-th: how many
@@ -398,11 +412,53 @@ __global__ void __launch_bounds__(THREADS, (KEYS == 17 || KEYS == 0 ? 1024 : 128
         const uint32_t word = bits[w] & (e >= 32 ? 0xffffffffu : (1u << e) - 1); // of the row's slots
         return n <= 0 ? word : n >= 32 ? 0u : word & ~((1u << n) - 1);
     };
-    constexpr int kHands = KEYS > 0 && KEYS * kWarps <= 128 ? 32 : THREADS; // up to four words a lane, one warp does
-    const int per_thread = (words + kHands - 1) / kHands;
-    const int a = min(words, tid * per_thread), z = min(words, a + per_thread);
-    int2 at = make_int2(0, 0);
-    if (tid < kHands) {
+    int2 *out = p.moves + unit * p.max_moves;
+    if (KEYS > 0) {
+        // A word a thread (there are fewer), its holes or what stays behind the budget;
+        // the word that the budget cuts has both, and its holes come last.  Both counts
+        // in one number; the list is put together where the masses were.
+        const int cut = keep >> 5, w = tid == words ? cut : tid;
+        const bool hole = tid < cut || tid == words;
+        const uint32_t word = tid > words ? 0 : hole ? holes_of(w) : extra_of(w);
+        const uint32_t bits_of = (uint32_t)__popc(word), mine = hole ? bits_of : bits_of << 16;
+        uint32_t upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, upto, d);
+            upto += lane >= d ? x : 0;
+        }
+        if (lane == 31)
+            s_scan[warp].x = (int)upto;
+        __syncthreads();
+        uint32_t before = upto - mine, total = 0;
+#pragma unroll
+        for (int i = 0; i < KEYS * kWarps / 32 + 1; ++i) { // warps that have words
+            before += i < warp ? (uint32_t)s_scan[i].x : 0;
+            total += (uint32_t)s_scan[i].x;
+        }
+        int *list = reinterpret_cast<int *>(s_dyn);
+        uint32_t at = hole ? 2 * (before & 0xffff) + 1 : 2 * (before >> 16);
+        // A few words of many bits the warp does together, one after the other.
+        uint32_t dense = __ballot_sync(0xffffffffu, bits_of > 4);
+        dense = __popc(dense) > 12 ? 0 : dense;
+        for (uint32_t m = dense; m != 0; m &= m - 1) {
+            const int from = __ffs(m) - 1;
+            const uint32_t of = __shfl_sync(0xffffffffu, word, from), to = __shfl_sync(0xffffffffu, at, from);
+            const int slot = __shfl_sync(0xffffffffu, w, from) * 32 + lane;
+            if ((of >> lane & 1) != 0)
+                list[to + 2 * __popc(of & ((1u << lane) - 1))] = slot;
+        }
+        for (uint32_t m = (dense >> lane & 1) != 0 ? 0 : word; m != 0; m &= m - 1, at += 2)
+            list[at] = w * 32 + __ffs(m) - 1;
+        __syncthreads();
+        const int n = (int)(total >> 16);
+        for (int i = tid; i < n; i += THREADS)
+            out[i] = reinterpret_cast<const int2 *>(list)[i];
+        if (tid == 0)
+            p.num_moves[unit] = n;
+    } else {
+        const int per_thread = (words + THREADS - 1) / THREADS;
+        const int a = min(words, tid * per_thread), z = min(words, a + per_thread);
         int2 mine = make_int2(0, 0);
         for (int w = a; w < z; ++w) {
             mine.x += __popc(extra_of(w));
@@ -415,56 +471,21 @@ __global__ void __launch_bounds__(THREADS, (KEYS == 17 || KEYS == 0 ? 1024 : 128
             upto.x += lane >= d ? x : 0;
             upto.y += lane >= d ? y : 0;
         }
-        if (kHands > 32 && lane == 31)
+        if (lane == 31)
             s_scan[warp] = upto;
-        at = make_int2(upto.x - mine.x, upto.y - mine.y);
-    }
-    if (kHands > 32) {
         __syncthreads();
+        int2 at = make_int2(upto.x - mine.x, upto.y - mine.y);
         for (int w = 0; w < warp; ++w) {
             at.x += s_scan[w].x;
             at.y += s_scan[w].y;
         }
-    }
-    int32_t *out = reinterpret_cast<int32_t *>(p.moves + unit * p.max_moves);
-    if (KEYS > 0) {
-        // A word has holes or slots that stay; the one that the budget cuts may have
-        // both, and its holes come last in the list.
-        __shared__ uint2 s_words[KEYS > 0 ? KEYS * kWarps + 1 : 1]; // (bits, how many before)
-        const int cut = keep >> 5;
-        if (tid < kHands) {
-            for (int w = a; w < z; ++w) {
-                const uint32_t extra = extra_of(w), holes = holes_of(w);
-                s_words[w] = w < cut ? make_uint2(holes, at.y) : make_uint2(extra, at.x);
-                if (w == cut)
-                    s_words[words] = make_uint2(holes, at.y);
-                at.x += __popc(extra);
-                at.y += __popc(holes);
-            }
-            if (tid == kHands - 1)
-                p.num_moves[unit] = at.x;
-        }
-        __syncthreads();
-        const uint32_t before = (1u << lane) - 1;
-        for (int i0 = warp; i0 <= words; i0 += 32 * kWarps) { // a word a lane, then those that have a bit
-            const int i = i0 + lane * kWarps;
-            const uint2 mine = i <= words ? s_words[i] : make_uint2(0, 0);
-            for (uint32_t m = __ballot_sync(0xffffffffu, mine.x != 0); m != 0; m &= m - 1) {
-                const int from = __ffs(m) - 1, w = i0 + from * kWarps;
-                const uint32_t word = __shfl_sync(0xffffffffu, mine.x, from), n = __shfl_sync(0xffffffffu, mine.y, from);
-                if ((word >> lane & 1) != 0)
-                    out[2 * (n + __popc(word & before)) + (w < cut || w == words ? 1 : 0)] =
-                        (w == words ? cut : w) * 32 + lane;
-            }
-        }
-    } else {
         for (int w = a; w < z; ++w) {
             for (uint32_t m = extra_of(w); m != 0; m &= m - 1)
-                out[2 * at.x++] = w * 32 + __ffs(m) - 1;
+                out[at.x++].x = w * 32 + __ffs(m) - 1;
             for (uint32_t m = holes_of(w); m != 0; m &= m - 1)
-                out[2 * at.y++ + 1] = w * 32 + __ffs(m) - 1;
+                out[at.y++].y = w * 32 + __ffs(m) - 1;
         }
-        if (tid == kHands - 1)
+        if (tid == THREADS - 1)
             p.num_moves[unit] = at.x;
     }
 }
@@ -585,7 +606,11 @@ bool aligned16(const void *p)
 
 constexpr int kPlanCached = 38912; // keys in shared memory at most; longer rows make theirs again
 
-// Keys in registers up to 17,408 slots, then in shared memory.
+// Keys in registers up to 17,408 slots, 17 a thread at most, then in shared memory.
+// 36 x 64 x 8 rows of 4,000 slots: 319 us with 32 keys in each of 128 threads, 305 with
+// 17 in 256; 36 x 16 x 8 of 8,192: 224 with keys in shared memory, 161 with 17 in 512;
+// 36 x 4 x 8 of 32,000: 832 with 128 threads, 266 with 1,024.  Rows of 1,100 slots:
+// 74 with nine keys a thread, 97 with 17 of which half are idle.
 struct PlanEntry {
     int slots, threads;
     const void *kernel;
