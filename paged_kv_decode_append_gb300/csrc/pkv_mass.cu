@@ -21,7 +21,7 @@
 // (tensor 43 %, exponentials 43 %, issue slots 51 % of the elapsed cycles): a pair
 // goes from the MMAs to the sums and back in 3,700 cycles, and TMEM holds four.
 // Of those the sums take 2,350 (four TMEM loads at 300, the rest arithmetic), the
-// MMAs 700 from first to last.  Two rows of 3,500 .. 4,095 queries: 169 us, 1.0 PFLOP/s; head_dim 256, whose
+// MMAs 700 from first to last.  Two rows of 3,500 .. 4,095 queries: 160 us, 1.1 PFLOP/s; head_dim 256, whose
 // pairs have twice the MMAs for the same sums: 107 us, 1.2 PFLOP/s (tensor 52 %).
 //
 // How (one persistent CTA per SM):
@@ -29,9 +29,13 @@
 //    for every block the steps through the query tiles that see it.  Every CTA
 //    takes an equal range; it finds it itself from the row arrays (no plan
 //    kernel, no host readback).  Rows whose queries fit one tile go by blocks of
-//    128 keys, as runs; others by 256, and from eight query tiles on by 512 (head_dim
-//    128 and 64): the query tiles then stream past two or four key tiles at once,
-//    which halves what they cost in L2 reads each time.
+//    128 keys, as runs; others by 256, so that the query tiles stream past two key
+//    tiles at once; and those with few query tiles over a long context by 512 (head_dim
+//    128 and 64), so that a block has steps enough: 8 rows of 64 queries on 8,192 tokens
+//    take 45 us by 512 and 49 by 256, of 256 queries 121 and 131, of 448 204 and 206
+//    (head_dim 64: 202 and 197).  Where the queries are the row 512 goes far past the
+//    causal limit: 64 prompts of 512 tokens take 164 us by 512 and 122 by 256, 2 of
+//    4,096 144 and 131.
 //  - A block cut between CTAs leaves partial sums in the workspace; the last
 //    CTA to arrive (a ticket for every 32 keys) adds them up in the order of the
 //    line, so results do not depend on timing.
@@ -57,7 +61,8 @@ namespace {
 constexpr int kMmKeysLog = 7;
 constexpr int kMmKeys = 128;     // keys of a tile: M of every MMA
 constexpr int kMmCols = 128;     // (query, head) columns of a query tile
-constexpr int kMmWide = 8;       // steps from which a block has four key tiles
+constexpr int kMmFewSteps = 12;  // up to here, and with this many cached tokens to a step, a block
+constexpr int kMmTokensPerStep = 256; // has four key tiles
 constexpr int kFixCost = 2;      // positions that a key tile costs before its first step
 constexpr int kMinRange = 6;     // positions that are worth a CTA of their own
 constexpr int kMmMaxCtas = 160;  // persistent CTAs the workspace has room for
@@ -229,7 +234,9 @@ __device__ __forceinline__ MmRow mm_row(const MmParams &p, const MmRaw &raw)
     }
     r.queries = (int)n;
     r.steps = r.queries <= p.q_tile ? 1 : (r.queries + p.q_tile - 1) / p.q_tile;
-    r.tiles = r.steps == 1 ? 1 : r.steps < kMmWide ? 2 : p.most_tiles;
+    r.tiles = r.steps == 1                                                             ? 1
+              : r.steps <= kMmFewSteps && r.len / r.steps >= kMmTokensPerStep ? p.most_tiles
+                                                                              : 2;
     const int shift = kMmKeysLog + (r.tiles >> 1); // log2 of a block's keys
     r.blocks = (int)((keys + (1 << shift) - 1) >> shift);
     r.full = (int)min((int64_t)r.blocks, (((int64_t)r.len + p.q_tile - 1) >> shift) + 1);

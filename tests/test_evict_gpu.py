@@ -313,6 +313,18 @@ def test_mass_of_prompts(D, Hq, Hkv, P, layout):
     check_mass(case, lse, run_mass(case, lse))
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,P,layout", [(128, 8, 2, 16, wl.NHD), (64, 2, 2, 64, wl.HND), (64, 16, 1, 8, wl.NHD)])
+def test_mass_of_few_queries_on_long_contexts(D, Hq, Hkv, P, layout):
+    """Blocks of four key tiles, and the rows next to where they begin."""
+    q = 128 // (Hq // Hkv)  # queries of a tile
+    counts, lens = [2 * q + 3, q + 1, 12 * q, 12 * q + 1, 2 * q], [3 * 256 + 7, 512, 12 * 256 + 1, 13 * 256, 511]
+    case, lse = mass_case(21, counts, lens, Hq, Hkv, D, P, layout)
+    check_mass(case, lse, run_mass(case, lse))
+    for b in (0, 2):  # alone: cut into more pieces
+        case, lse = mass_case(22 + b, counts[b:b + 1], lens[b:b + 1], Hq, Hkv, D, P, layout)
+        check_mass(case, lse, run_mass(case, lse))
+
+
 def test_mass_is_the_weight_of_the_attention():
     """With the lse that the attention calls write: every query and head gives
     one in all (a weight is as exact as the attention's lse, 1e-3 of it here)."""
