@@ -202,6 +202,23 @@ def test_rope_append_row_fates():
     check_append(case, got, fn, positions(case), rows=[2, 3, 4], turned=np.arange(38) >= 23)
 
 
+@pytest.mark.parametrize("P,n", [(8, 2043), (8, 2044), (1, 700)])
+def test_append_of_rows_of_many_pages(P, n):
+    """Hundreds of pages to a row: good rows, and a bad page anywhere."""
+    f, fn = freqs_of(64)
+    case = wl.mixed_step(31, [n, 3], [5, 9], 4, 2, 64, P, device=DEV)
+    got = run_append(case, f)
+    assert got[3] == 0
+    check_append(case, got, fn, positions(case))
+    table = case.block_table.copy()
+    for at, page in ((5 // P, 0), ((5 + n - 1) // P, -1), ((5 + n // 2) // P, case.num_pages)):
+        case.block_table = table.copy()
+        case.block_table[0, at] = page
+        got = run_append(case, f)
+        assert got[3] == pkv.api.ERR_PAGE
+        check_append(case, got, fn, positions(case), rows=[1])
+
+
 # ------------------------------------------------------------------- mass
 
 
