@@ -311,7 +311,8 @@ __global__ void __launch_bounds__(THREADS, (KEYS == 0 ? 1024 : 1280) / THREADS)
         k = keep;
         in = safe;
     }
-    while (in > kPlanList && k < in) {
+    // (A round leaves a 256th of the range: at most four of keys and four of slots.)
+    for (int round = 0; round < 8 && in > kPlanList && k < in; ++round) {
         if (!among && width == 0)
             ties(from);
         const int shift = max(0, 24 - __clz(width)); // 256 bins over the range
@@ -360,12 +361,20 @@ __global__ void __launch_bounds__(THREADS, (KEYS == 0 ? 1024 : 1280) / THREADS)
     // A bit for every slot that stays: those above the open range, and of those in
     // it the k first, unless all do.
     const bool all = k == in;
+    // (Keys that are made anew for every pass could change under a writer that does
+    // not belong there; nothing goes past its array even then.)
+    in = min(in, kPlanList);
+    auto list_late = [&](uint32_t key, int i) {
+        const int n = atomicAdd(&s_count, 1);
+        if (n < kPlanList)
+            s_list[n] = (uint64_t)key << 32 | ~(uint32_t)i;
+    };
     if (among) { // key `tie`: up to slot `last`
         int last = (int)~from;
         if (!all) {
             keys.each_rarely(tid, [&](int i, uint32_t key) {
                 if (key == tie && ~(uint32_t)i - from <= width)
-                    s_list[atomicAdd(&s_count, 1)] = ~(uint32_t)i;
+                    list_late(0, i);
             });
             __syncthreads();
             if (tid < in) {
@@ -383,7 +392,10 @@ __global__ void __launch_bounds__(THREADS, (KEYS == 0 ? 1024 : 1280) / THREADS)
     } else {
         const uint32_t size = all ? 0 : width + 1, stays = from + size;
         keys.mark(tid, bits, [&](int i, uint32_t key) {
-            plan_append(smem_addr(&s_count), smem_addr(s_list), key - from, size, key, i);
+            if (KEYS > 0)
+                plan_append(smem_addr(&s_count), smem_addr(s_list), key - from, size, key, i);
+            else if (key - from < size)
+                list_late(key, i);
             return key >= stays;
         });
         if (!all) {
@@ -394,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, (KEYS == 0 ? 1024 : 1280) / THREADS)
                 for (int j = 0; j < in; ++j)
                     above += s_list[j] > x ? 1 : 0;
                 const uint32_t i = ~(uint32_t)x;
-                if (above < k)
+                if (above < k && (KEYS > 0 || i < (uint32_t)L))
                     atomicOr(&bits[i >> 5], 1u << (i & 31));
             }
         }
@@ -482,13 +494,13 @@ __global__ void __launch_bounds__(THREADS, (KEYS == 0 ? 1024 : 1280) / THREADS)
             at.y += s_scan[w].y;
         }
         for (int w = a; w < z; ++w) {
-            for (uint32_t m = extra_of(w); m != 0; m &= m - 1)
+            for (uint32_t m = extra_of(w); m != 0 && at.x < p.max_moves; m &= m - 1)
                 out[at.x++].x = w * 32 + __ffs(m) - 1;
-            for (uint32_t m = holes_of(w); m != 0; m &= m - 1)
+            for (uint32_t m = holes_of(w); m != 0 && at.y < p.max_moves; m &= m - 1)
                 out[at.y++].y = w * 32 + __ffs(m) - 1;
         }
         if (tid == THREADS - 1)
-            p.num_moves[unit] = at.x;
+            p.num_moves[unit] = min(at.x, p.max_moves);
     }
 }
 
