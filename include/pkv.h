@@ -777,8 +777,8 @@ PKV_API pkv_status pkv_attn_mass(const pkv_cache_desc *desc, const void *k_cache
  * every layer and kv head, and the moves that bring them to the front.  A row
  * keeps n_b = min(L_b, budgets[b]) slots (all, with a negative budget): first
  * those whose position is among the row's newest `recent` ones (slot_pos >= L_b +
- * evicted[b] - recent) or below `sink`, then by mass (NaN below all); among
- * equals the lowest slot.
+ * evicted[b] - recent) or below `sink`, then the others; both by mass (NaN below
+ * all), and among equals the lowest slot.
  *  mass, slot_pos    device [num_layers, batch, num_kv_heads, slots], read only.
  *  cache_seqlens, evicted, budgets  device int32 [batch]; evicted may be NULL.
  *  moves             device int32 [num_layers, batch, num_kv_heads, max_moves,

@@ -76,10 +76,17 @@ template <int THREADS, int KEYS> struct PlanKeys {
     uint32_t *held; // KEYS > 0: the masses, then the positions
     int L, cached, sink;
     uint32_t open; // positions from sink on that are not protected
+    bool crowded;  // KEYS = 0: keys as in crowd
 
+    __device__ __forceinline__ bool safe(int position) const
+    {
+        return (uint32_t)position - (uint32_t)sink >= open;
+    }
     __device__ __forceinline__ uint32_t key(uint32_t rank, int position) const
     {
-        return (uint32_t)position - (uint32_t)sink >= open ? kSafeKey : rank;
+        if (KEYS == 0 && crowded)
+            return safe(position) ? rank + 1 : 0;
+        return safe(position) ? kSafeKey : rank;
     }
     __device__ __forceinline__ uint32_t at(int i) const
     {
@@ -108,9 +115,13 @@ template <int THREADS, int KEYS> struct PlanKeys {
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncthreads();
         } else {
-            for (int i = tid; i < min(L, cached); i += THREADS)
-                held[i] = key(plan_rank(__float_as_uint(mass[i])), pos[i]);
+            hold(tid);
         }
+    }
+    __device__ __forceinline__ void hold(int tid)
+    {
+        for (int i = tid; i < min(L, cached); i += THREADS)
+            held[i] = key(plan_rank(__float_as_uint(mass[i])), pos[i]);
     }
     // Keys into registers.  Masses are taken for their bits, which is right for 0 ..
     // +inf; if there are others their ranks are put in their place first.
@@ -129,6 +140,23 @@ template <int THREADS, int KEYS> struct PlanKeys {
 #pragma unroll 1
         for (int i = tid; i < L; i += THREADS)
             held[i] = plan_rank(held[i]);
+    }
+    // More slots are protected than stay: they alone are ranked, by mass, above the
+    // others, whose key becomes 0.
+    __device__ __forceinline__ void crowd(int tid, bool ranked)
+    {
+        if (KEYS > 0) {
+#pragma unroll 1
+            for (int i = tid; i < L; i += THREADS) {
+                const uint32_t rank = ranked ? held[i] : plan_rank(held[i]);
+                held[i] = safe((int)held[KEYS * THREADS + i]) ? rank + 1 : 0;
+                held[KEYS * THREADS + i] = (uint32_t)sink; // not protected any more
+            }
+            open = 1;
+        } else {
+            crowded = true;
+            hold(tid);
+        }
     }
     static __device__ __forceinline__ void copy16(void *to, const void *from)
     {
@@ -200,7 +228,8 @@ __device__ __forceinline__ void plan_append(uint32_t count, uint32_t list, uint3
                  : "memory");
 }
 
-// One CTA for each (layer, row, kv head).  Slots are ranked by key, equal keys
+// One CTA for each (layer, row, kv head).  Slots are ranked by key (protected ones
+// first; where those are too many, among themselves by mass), equal keys
 // by slot, the lowest first.  The key of the last slot that stays is found by
 // counting into 256 bins over the range that is still open, narrowed until a bin
 // is to be taken whole or has at most 128 slots, which are ranked against one
@@ -253,6 +282,7 @@ __global__ void __launch_bounds__(THREADS, (KEYS == 0 ? 1024 : 1280) / THREADS)
     keys.L = L;
     keys.cached = p.cached;
     keys.sink = p.sink;
+    keys.crowded = false;
     keys.open = (uint32_t)(max((int64_t)p.sink - 1, min((int64_t)INT32_MAX, oldest)) - p.sink + 1);
     keys.load(tid, p.slots);
     auto no_bins = [&] {
@@ -264,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, (KEYS == 0 ? 1024 : 1280) / THREADS)
 
     // Protected slots, and the range of the others' keys.
     int safe;
-    for (bool ranked = KEYS == 0;; ranked = true) {
+    for (bool ranked = KEYS == 0, crowded = false;;) {
         keys.take(tid);
         uint32_t lo = kSafeKey, hi = 0;
         safe = 0;
@@ -282,10 +312,18 @@ __global__ void __launch_bounds__(THREADS, (KEYS == 0 ? 1024 : 1280) / THREADS)
             atomicMax(&s_hi, hi);
         }
         __syncthreads();
-        if (ranked || s_hi <= kPlainMost + 1)
+        safe = s_safe - (KEYS > 0 ? KEYS * THREADS - L : 0);
+        const bool plain = ranked || s_hi <= kPlainMost + 1;
+        if (plain && (safe <= keep || crowded))
             break;
         __syncthreads();
-        keys.rank(tid); // negative masses, -0 or NaN
+        if (!plain) {
+            keys.rank(tid); // negative masses, -0 or NaN
+        } else {
+            keys.crowd(tid, ranked);
+            crowded = true;
+        }
+        ranked = true;
         if (tid == 0) {
             s_lo = kSafeKey;
             s_hi = 0;
@@ -293,13 +331,12 @@ __global__ void __launch_bounds__(THREADS, (KEYS == 0 ? 1024 : 1280) / THREADS)
         }
         __syncthreads();
     }
-    safe = s_safe - (KEYS > 0 ? KEYS * THREADS - L : 0);
 
     // The open range [from, from + width]: of keys, or (`among`) of ~slot among the
     // slots of key `tie`.
     uint32_t from = s_lo, width = s_hi - 1 - s_lo, tie = 0;
     int k = keep - safe, in = L - safe; // the k-th greatest of `in` slots there is looked for
-    bool among = keep <= safe;
+    bool among = keep == safe;
     auto ties = [&](uint32_t key) {
         among = true;
         tie = key;

@@ -88,8 +88,7 @@ def plan_row(mass, pos, L, gone, budget, sink, recent):
     m = mass[:L].astype(np.float64)
     safe = (pos[:L] < sink) | (pos[:L].astype(np.int64) >= L + gone - recent)
     nan = np.isnan(m)
-    order = sorted(range(L), key=lambda i: (not safe[i], False if safe[i] else nan[i],
-                                            0.0 if safe[i] or nan[i] else -m[i], i))
+    order = sorted(range(L), key=lambda i: (not safe[i], nan[i], 0.0 if nan[i] else -m[i], i))
     stay = np.zeros(L, bool)
     stay[order[:keep]] = True
     src = [i for i in range(keep, L) if stay[i]]

@@ -548,6 +548,9 @@ def test_plan_at_the_ends_of_its_variants(slots, low):
         mass[0, 1, 0, -1] = np.uint32(0xffffffff).view(np.float32)
     pos = np.tile(np.arange(slots), (1, 4, 1, 1))
     check_plan(mass, pos, lens, None, budgets, 3, 40, plan(mass, pos, lens, None, budgets, 3, 40))
+    # more protected slots than stay: some, all, and exactly as many
+    for sink, recent in ((3, slots // 2 + 9), (slots, 0), (0, 77), (0, 60)):
+        check_plan(mass, pos, lens, None, budgets, sink, recent, plan(mass, pos, lens, None, budgets, sink, recent))
 
 
 def test_plan_row_fates():
