@@ -642,6 +642,15 @@ __device__ __forceinline__ void mm_commit(uint64_t *bar)
                  : "memory");
 }
 
+// One arrival of the warp.
+__device__ __forceinline__ void mm_arrive(uint64_t *bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\t"
+                 "@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
 // Two warps issue, every other (key tile, step) pair each (`half`: which), and so
 // have two accumulators and every other key slot to themselves: what a pair costs
 // a warp besides its MMAs (waits, votes, descriptors: 500 cycles) then overlaps
@@ -692,10 +701,17 @@ __device__ void mm_mma(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
                 return slot;
             };
             if (!by_chunk) { // all chunks, then the key tiles (or the run's blocks) one by one
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c)
-                    next_chunk(c);
                 const int pairs = tiles == 1 ? blocks : tiles;
+                // For a single pair the other warp issues nothing, and the sums' arrival says
+                // nothing of its wait: without an arrival of its own a chunk could be loaded
+                // over, and its barrier two phases on, before this warp has looked.
+                const bool idle = pairs == 1 && ((half ^ seq) & 1) != 0;
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const uint32_t slot = next_chunk(c);
+                    if (idle)
+                        mm_arrive(&bars.q_empty[slot]);
+                }
 #pragma unroll 1
                 for (int j = (half ^ seq) & 1; j < pairs && going; j += 2) {
                     const uint32_t u = seq + j, x = tile0 + j;
@@ -898,8 +914,9 @@ __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
                 return;
             ++taken;
             // What the MMAs have read is free: the key tile after its last step, the
-            // query tile after the last pairs of the two issuing warps.  (Told from
-            // here: a commit for it would cost those warps more than an MMA does.)
+            // query tile after the last pairs of the two issuing warps (of a single pair
+            // the other warp tells itself).  (Told from here: a commit for it would cost
+            // those warps more than an MMA does.)
             const uint32_t tile = tile0 + (uint32_t)(tok - s.tok) / kMmKeys;
             if (quarter == 0 && lane == 0) {
                 if (now == s.step1 - 1)
@@ -908,8 +925,7 @@ __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
                 if ((C::kChunks <= 2 || s.tiles == 1) && pair >= pairs - 2)
 #pragma unroll
                     for (int c = 0; c < C::kChunks; ++c)
-                        mbar_arrive_cnt(&bars.q_empty[(q0 + (now - s.step0) * C::kChunks + c) % C::kQStages],
-                                        pairs == 1 ? 2 : 1);
+                        mbar_arrive(&bars.q_empty[(q0 + (now - s.step0) * C::kChunks + c) % C::kQStages]);
             }
             tc_fence_after();
             auto leave = [&] { // all of the accumulator is in registers
@@ -1032,7 +1048,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         }
         for (int i = 0; i < C::kQStages; ++i) {
             mbar_init(&bars.q_full[i], 1);
-            mbar_init(&bars.q_empty[i], 2); // once for each issuing warp's MMAs
+            mbar_init(&bars.q_empty[i], 2); // once for each issuing warp
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bars.s_full[i], 1);
