@@ -22,7 +22,8 @@
  *
  * Conventions shared by every entry point:
  *  - All tensors are dense, row major, in the shapes stated; "bf16" is the
- *    bfloat16 bit layout.  Device pointers must be 16-byte aligned.
+ *    bfloat16 bit layout.  Device pointers must be 16-byte aligned, where
+ *    nothing else is said.
  *  - The caller owns every buffer.  The library never allocates or frees
  *    device memory and never synchronises the host inside a device call, so
  *    every device call can be captured in a CUDA graph.  `stream` is a
@@ -719,6 +720,9 @@ PKV_API pkv_status pkv_rope_append(const pkv_cache_desc *desc, void *k_cache, vo
  * used by every call here; only causal masks among tokens of one call look at
  * slots, and those tokens are always the last.  A row that is cut down needs
  * pages of its own: a page that two block tables name would be moved in both.
+ * Layers and rows of larger tensors can be handed on as they lie: mass and
+ * slot_pos are 16-byte aligned where slots is a multiple of 4 and 4-byte aligned
+ * otherwise, lse 4-byte and moves 8-byte aligned.
  * Source: "flex_attention + paged KV + CUDA graphs vs vLLM", "What each option
  * did" (a page pool of fixed size reserved up front); "mini-infer系统实战-06 True
  * PagedAttention", section 8 (what a pool of pages holds).

@@ -654,6 +654,10 @@ bool aligned16(const void *p)
 {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
+bool aligned8(const void *p) // moves are read and written in pairs
+{
+    return (reinterpret_cast<uintptr_t>(p) & 7u) == 0;
+}
 
 constexpr int kPlanCached = 38912; // keys in shared memory at most; longer rows make theirs again
 
@@ -722,7 +726,8 @@ pkv_status pkv_evict_plan(const float *mass, const int32_t *slot_pos, int32_t nu
     if (batch == 0)
         return PKV_OK;
     if (mass == nullptr || slot_pos == nullptr || cache_seqlens == nullptr || budgets == nullptr || moves == nullptr ||
-        num_moves == nullptr || row_lens == nullptr || !aligned16(mass) || !aligned16(slot_pos) || !aligned16(moves))
+        num_moves == nullptr || row_lens == nullptr || !slots_aligned(mass, slots) || !slots_aligned(slot_pos, slots) ||
+        !aligned8(moves))
         return PKV_EINVAL;
     PlanParams p;
     p.mass = mass;
@@ -780,7 +785,7 @@ pkv_status pkv_evict_apply(const pkv_cache_desc *desc, int32_t num_layers, void 
     }
     if (batch == 0)
         return PKV_OK;
-    if (moves == nullptr || num_moves == nullptr || row_lens == nullptr || block_table == nullptr || !aligned16(moves) ||
+    if (moves == nullptr || num_moves == nullptr || row_lens == nullptr || block_table == nullptr || !aligned8(moves) ||
         (cache_seqlens == nullptr && evicted != nullptr))
         return PKV_EINVAL;
     p.moves = reinterpret_cast<const int2 *>(moves);

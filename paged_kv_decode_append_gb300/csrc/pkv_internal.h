@@ -279,6 +279,13 @@ constexpr int kEvictMaxSlots = 1 << 19; // slots of a row of scores
 constexpr int kMaxMassBatch = 1024;
 constexpr int kMassMaxKeys = 0x7ffff000; // keys of a row (token arithmetic is 32-bit)
 
+// Scores and positions: the layers and rows of a 16-byte aligned tensor begin on 16
+// bytes where slots is a multiple of 4, on 4 bytes otherwise.
+inline bool slots_aligned(const void *p, int slots)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (slots % 4 == 0 ? 15u : 3u)) == 0;
+}
+
 struct MassShape {
     int group;        // num_q_heads / num_kv_heads
     int q_tile;       // queries of a query tile

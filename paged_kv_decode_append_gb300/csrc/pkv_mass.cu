@@ -1187,8 +1187,8 @@ pkv_status pkv_attn_mass(const pkv_cache_desc *desc, const void *k_cache, const 
     if (batch == 0 || total_q == 0)
         return PKV_OK;
     if (k_cache == nullptr || q == nullptr || lse == nullptr || block_table == nullptr || cache_seqlens == nullptr ||
-        mass == nullptr || !aligned16(k_cache) || !aligned16(q) || !aligned16(lse) || !aligned16(mass) ||
-        !aligned16(slot_pos))
+        mass == nullptr || !aligned16(k_cache) || !aligned16(q) || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 ||
+        !slots_aligned(mass, slots) || !slots_aligned(slot_pos, slots))
         return PKV_EINVAL;
     if (workspace == nullptr || workspace_bytes < shape.bytes || !aligned16(workspace))
         return PKV_EWORKSPACE;

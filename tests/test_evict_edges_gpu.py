@@ -27,3 +27,52 @@ def test_mass_of_rows_of_one_tile(D, Hq, Hkv):
     for _ in range(50):
         again = base.run_mass(case, lse, ws=ws)
         assert again[3] == 0 and base.same_bits(again[1], first[1])
+
+
+def rows_state(layers, B, K, slots, seed):
+    """Scores and positions of all layers in one tensor each."""
+    g = torch.Generator().manual_seed(seed)
+    mass = torch.rand((layers, B, K, slots), generator=g).to(DEV)
+    pos = torch.arange(slots, dtype=torch.int32, device=DEV).expand(layers, B, K, slots).contiguous()
+    return mass, pos
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,slots", [(3, 2, 1, 2049), (1, 1, 1, 1001), (3, 6, 2, 203), (1, 2, 1, 510)])
+def test_layers_of_one_state(B, Hq, Hkv, slots):
+    """Layer by layer out of one state whose layers begin on 4 bytes: weights of
+    each layer, plan and moves of the last ones."""
+    layers = 3
+    rng = np.random.default_rng(slots)
+    lens = rng.integers(slots // 2, slots - 1, B)
+    case, lse = base.mass_case(slots, [1] * B, lens, Hq, Hkv, 64, 16)
+    mass, pos = rows_state(layers, B, Hkv, slots, 3)
+    start = mass.clone()
+    # lse of tokens out of the middle of a larger tensor
+    wide = torch.zeros(B + 3, Hq, device=DEV)
+    wide[3:] = lse.to(DEV)
+    assert any(mass[l].data_ptr() % 16 for l in range(layers)) and any(wide[i].data_ptr() % 16 for i in range(4))
+    table, old = base.i32(case.block_table), base.i32(case.cache_seqlens)
+    for l in range(layers):
+        pkv.pkv_attn_mass(case.k_cache, case.q, wide[3:], table, old, case.softmax_scale, mass[l], slot_pos=pos[l],
+                          layout=case.layout)
+        want = base.run_mass(case, lse, old=start[l].cpu())
+        assert base.same_bits(mass[l].cpu(), want[1])
+    c = base.Caches(layers, lens + 1, Hkv, 64, 16, base.wl.NHD, slots=slots, seed=4)
+    c.mass, c.pos = mass, pos
+    budgets = [int(x) // 2 for x in lens]
+    width = slots // 2 | 1
+    moves = torch.full((layers, B, Hkv, width, 2), -5, dtype=torch.int32, device=DEV)
+    num = torch.full((layers, B, Hkv), -5, dtype=torch.int32, device=DEV)
+    for part in (slice(0, 1), slice(1, layers)):
+        _, _, rows = pkv.pkv_evict_plan(mass[part], pos[part], base.i32(lens + 1), c.gone, base.i32(budgets), 2, 9,
+                                        moves=moves[part], num_moves=num[part])
+    got = [x.cpu().numpy() for x in (moves, num, rows)] + [0]
+    base.check_plan(mass.cpu().numpy(), pos.cpu().numpy(), lens + 1, c.gone.cpu().numpy(), budgets, 2, 9, got)
+    lists = [[[[tuple(m) for m in got[0][l, b, h, : got[1][l, b, h]].tolist()] for h in range(Hkv)] for b in range(B)]
+             for l in range(layers)]
+    before, length, gone, err = c.clone(), base.i32(lens + 1), c.gone.clone(), base.zero()
+    for part, last in ((slice(0, 1), False), (slice(1, layers), True)):
+        pkv.pkv_evict_apply(pkv.LayerCaches(c.k[part], c.v[part], c.layout), moves[part], num[part], rows, base.i32(c.table),
+                            length if last else None, gone if last else None, mass=mass[part], slot_pos=pos[part], err_flag=err)
+    assert int(err.item()) == 0 and length.tolist() == budgets
+    c.check(before, lists)
