@@ -47,7 +47,7 @@ __device__ __forceinline__ PlanRow plan_row(const PlanParams &p, int b)
     const int budget = p.budgets[b];
     r.err = 0;
     r.keep = r.L < 0 || budget < 0 ? r.L : min(budget, r.L);
-    if (r.keep < r.L && (r.L > p.slots || min(r.keep, r.L - r.keep) > p.max_moves)) {
+    if (r.L > p.slots || min(r.keep, r.L - r.keep) > p.max_moves) {
         r.err = PKV_ERR_OVERFLOW;
         r.keep = r.L;
     }

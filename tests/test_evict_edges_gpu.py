@@ -76,3 +76,13 @@ def test_layers_of_one_state(B, Hq, Hkv, slots):
                             length if last else None, gone if last else None, mass=mass[part], slot_pos=pos[part], err_flag=err)
     assert int(err.item()) == 0 and length.tolist() == budgets
     c.check(before, lists)
+
+
+@pytest.mark.parametrize("budget", [-1, 50, 101, 2 ** 31 - 1])
+def test_plan_of_a_row_without_scores_for_all_slots(budget):
+    """Its error is the row's own, whether its budget bites or not."""
+    mass, pos = (x.cpu().numpy() for x in rows_state(1, 2, 2, 100, 5))
+    for lens, err in (([101, 60], pkv.api.ERR_OVERFLOW), ([2 ** 31 - 1, 60], pkv.api.ERR_OVERFLOW), ([100, 60], 0), ([-1, 60], 0)):
+        got = base.plan(mass, pos, lens, None, [budget, 10], 2, 3)
+        assert got[3] == err
+        base.check_plan(mass, pos, lens, None, [budget, 10], 2, 3, got, failed=[0] if err else [])
