@@ -3,7 +3,7 @@
 // tensor cores (tcgen05, TMEM accumulators).
 //
 // What it computes.  mass[t] += sum over the (query, head) columns c that see
-// slot t of exp2(k_t . q_c scale log2(e) - lse_c log2(e)).  The lse is given, so
+// slot t of exp2((k_t . q_c scale - lse_c) log2(e)).  The lse is given, so
 // there is no running maximum and nothing to rescale: S^T = K Q^T with the keys
 // on the MMA's rows, so that a TMEM lane is a key and a thread adds up its own
 // key's columns in a register.  No value crosses threads, and what a NaN in one
@@ -44,10 +44,15 @@
 //    warp for all: 180 us for 106 at head_dim 256); 4-19 sum, four warps to a
 //    pair, each group with an accumulator of its own.  The sums tell the loaders
 //    what is free: as commits of the issuing warps that took 43 us for 41 (decode).
+//  - Scores are exact products summed in fp32.  The exponent is the difference
+//    d of score and lse, rounded once, and only then in base 2: what the
+//    conversion rounds goes with d and not with the score.  A weight is off by at
+//    most (3 |d| + 4) 2^-24 of itself at any size of score.  (Score and lse each
+//    in base 2 first, which saves a multiplication for two weights, took a
+//    rounding of the whole score into every weight: 3e-5 of it at scores of 200.)
 //  - Sums of a step's columns are plain fp32 (four runs of 32 terms); steps are
 //    added up with a compensation for what the addition drops, so thousands of
-//    queries lose nothing.  Scores are exact products summed in fp32, and
-//    exponentials fp32: against 64 bits the result is off by 1e-7 .. 8e-7.
+//    queries lose nothing.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -169,7 +174,7 @@ struct MmParams {
     int32_t *pos, *err_flag;
     int32_t *tickets; // [CTA][tile][quarter]: pieces of a block's 32 keys that are there
     float *parts;     // [CTA][begun before this CTA / in it][512 keys]
-    float q_scale;    // softmax_scale * log2(e)
+    float scale;      // softmax_scale
     int batch, num_q_heads, num_kv_heads, group, total_q, max_blocks;
     int page_shift, box_shift, num_pages, layout, slots;
     int q_tile;     // queries of a query tile
@@ -782,19 +787,19 @@ __device__ __forceinline__ void mm_ld(uint32_t taddr, uint32_t (&r)[16])
 }
 #undef PKV_O8
 
-// The sum of 2^(x scale + z) over N columns; z holds -lse log2(e).
+// The sum of e^(x scale + z) over N columns; z holds -lse.
 template <bool MASKED, int N>
 __device__ __forceinline__ void mm_sum_of(const uint32_t (&x)[N], const float *z, float scale, int from, int to,
                                           float2 &sum0, float2 &sum1)
 {
-    const float2 s2 = make_float2(scale, scale);
+    const float2 s2 = make_float2(scale, scale), log2e = make_float2(1.4426950408889634f, 1.4426950408889634f);
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
         const float4 z4 = *reinterpret_cast<const float4 *>(z + i);
-        const float2 a = ffma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), s2,
-                               make_float2(z4.x, z4.y));
-        const float2 c = ffma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), s2,
-                               make_float2(z4.z, z4.w));
+        const float2 a = fmul2(ffma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), s2,
+                                     make_float2(z4.x, z4.y)), log2e);
+        const float2 c = fmul2(ffma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), s2,
+                                     make_float2(z4.z, z4.w)), log2e);
         float2 w0 = make_float2(ex2_approx(a.x), ex2_approx(a.y));
         float2 w1 = make_float2(ex2_approx(c.x), ex2_approx(c.y));
         if (MASKED) {
@@ -863,7 +868,7 @@ __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
         };
         auto stage = [&](float z) {
             room = room == 256 ? 0 : room + 128;
-            lse[room + r] = z == -INFINITY ? z : z * -1.4426950408889634f;
+            lse[room + r] = z == -INFINITY ? z : -z;
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&bars.z_full[w]);
@@ -944,7 +949,7 @@ __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
                     mm_ld(acc + c, x);
                     if (c + 32 == kMmCols)
                         leave();
-                    mm_sum_of<false>(x, zs + c, p.q_scale, 0, 32, sum0, sum1);
+                    mm_sum_of<false>(x, zs + c, p.scale, 0, 32, sum0, sum1);
                 }
             } else {
                 // columns of queries before the key's own see nothing of it; of a tile
@@ -960,14 +965,14 @@ __device__ void mm_sum(const MmParams &p, uint8_t *smem, MmBars &bars, uint32_t 
                     mm_ld(acc + c, x);
                     if (c + 16 >= cols)
                         leave();
-                    mm_sum_of<false>(x, zs + c, p.q_scale, 0, 16, sum0, sum1);
+                    mm_sum_of<false>(x, zs + c, p.scale, 0, 16, sum0, sum1);
                 }
 #pragma unroll 1
                 for (int c = whole; c < cols; c += 16) {
                     mm_ld(acc + c, x);
                     if (c + 16 >= cols)
                         leave();
-                    mm_sum_of<true>(x, zs + c, p.q_scale, seen - c, cols - c, sum0, sum1);
+                    mm_sum_of<true>(x, zs + c, p.scale, seen - c, cols - c, sum0, sum1);
                 }
             }
             mm_add(sum, dropped, (sum0.x + sum1.x) + (sum0.y + sum1.y));
@@ -1210,7 +1215,7 @@ pkv_status pkv_attn_mass(const pkv_cache_desc *desc, const void *k_cache, const 
     p.err_flag = err_flag;
     p.tickets = reinterpret_cast<int32_t *>(ws);
     p.parts = reinterpret_cast<float *>(ws + shape.off_parts);
-    p.q_scale = softmax_scale * 1.4426950408889634f;
+    p.scale = softmax_scale;
     p.batch = batch;
     p.num_q_heads = num_q_heads;
     p.num_kv_heads = desc->num_kv_heads;

@@ -86,3 +86,41 @@ def test_plan_of_a_row_without_scores_for_all_slots(budget):
         got = base.plan(mass, pos, lens, None, [budget, 10], 2, 3)
         assert got[3] == err
         base.check_plan(mass, pos, lens, None, [budget, 10], 2, 3, got, failed=[0] if err else [])
+
+
+@pytest.mark.parametrize("counts,lens", [([1] * 5, [0, 100, 700, 1500, 129]), ([9, 40, 300], [50, 600, 0]), ([5, 700], [3000, 9])])
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 2, 2), (128, 2, 2), (128, 8, 2), (256, 6, 1)])
+def test_weights_of_large_scores(D, Hq, Hkv, counts, lens):
+    """Weights are as exact for scores of 200 as for small ones.
+
+    Queries and keys are small whole numbers, so that products and their sums are
+    exact in fp32 and what is off comes from the weight alone: with d = scale q.k -
+    lse, one rounding of d, one of log2(e) and one of their product (3 |d| 2^-24 of
+    the weight), exp2 (2^-22).  Sums: 32 terms to a run, then no more than ten
+    roundings (runs, steps, pieces, halves)."""
+    case, _ = base.mass_case(D + len(counts), counts, lens, Hq, Hkv, D, 16, sharp=1.0)
+    g = torch.Generator().manual_seed(D)
+    whole = torch.randint(-4, 5, case.k_cache.shape, generator=g).float()
+    whole[..., :8] = 4
+    case.k_cache.copy_(whole.to(DEV))
+    q = torch.randint(-4, 5, case.q.shape, generator=g).float()
+    q[..., :8] = round(6.25 * D ** 0.5)  # 200 of every score
+    case.q.copy_(q.to(DEV))
+    lse = base.lse_all(case)
+    assert float(lse.min()) > 150
+    fresh = [0] * len(lens)
+    got = base.run_mass(case, lse, fresh=fresh)
+    assert got[3] == 0
+    scale, G = float(np.float32(case.softmax_scale)), Hq // Hkv
+    for b, L in enumerate(lens):
+        lo, n = int(case.qo_indptr[b]), counts[b]
+        k = base.ref.row_keys(case, b, L + n)
+        seen = torch.arange(L + n) <= L + torch.arange(n)[:, None]
+        want, off = torch.zeros(Hkv, L + n, dtype=torch.float64), torch.zeros(Hkv, L + n, dtype=torch.float64)
+        for h in range(Hq):
+            d = case.q[lo:lo + n, h].double().cpu() @ k[:, h // G].T * scale - lse[lo:lo + n, h].double()[:, None]
+            w = torch.where(seen, d.exp(), 0.0)
+            want[h // G] += w.sum(0)
+            off[h // G] += (w * torch.expm1(2.0 ** -24 * (3 * d.abs() + 4))).sum(0)
+        off += 2.0 ** -24 * (42 if n * G > 1 else 0) * want + n * G * 2.0 ** -126
+        assert ((got[1][b, :, : L + n].double() - want).abs() <= off).all()
