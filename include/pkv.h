@@ -649,8 +649,8 @@ typedef enum {
  *   NTK     (base factor^(rot_dim / (rot_dim - 2)))^(-2 i / rot_dim)
  *   PARTS   g_i where a pair makes at least `high` turns over orig_len tokens,
  *           g_i / factor where at most `low`, a ramp over the pairs between
- *           (from floor of the first pair to ceil of the last); attn_factor is
- *           0.1 ln(factor) + 1
+ *           (from floor of the first pair, at least 0, to ceil of the last, at
+ *           most rot_dim - 1); attn_factor is 0.1 ln(factor) + 1
  *   TURNS   the same with a ramp over the number of turns, and attn_factor 1 */
 typedef enum {
     PKV_ROPE_PLAIN = 0,

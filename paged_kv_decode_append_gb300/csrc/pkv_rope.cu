@@ -299,6 +299,8 @@ pkv_status pkv_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double 
     if (scaling == PKV_ROPE_PARTS) {
         first = fmax(floor(pair_of(high)), 0.0);
         span = fmax(fmin(ceil(pair_of(low)), R - 1.0) - first, 1e-3);
+        if (pair_of(low) <= 0.0) // not even pair 0 makes more than `low` turns
+            first = -span;
     }
     for (int i = 0; i < rot_dim / 2; ++i) {
         double f = pow(base, -2.0 * i / R);
