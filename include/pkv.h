@@ -664,7 +664,9 @@ typedef enum {
  * pkv_rope_freqs -- the rot_dim / 2 frequencies f_i, on the host (the caller
  * copies them to the device once), and the factor a of the rotated part
  * (attn_factor, or NULL).  base > 1; factor >= 1 except for PLAIN; 0 < low < high
- * and orig_len > 0 for PARTS and TURNS (ignored otherwise).
+ * and orig_len > 0 for PARTS and TURNS (ignored otherwise).  Computed in 64-bit
+ * floats: PLAIN, LINEAR and NTK frequencies are off by at most 2^-53 turns per
+ * token, which is 2^-33 of a turn at position 10^6.
  */
 PKV_API pkv_status pkv_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, double low,
                                   double high, double orig_len, uint64_t *freqs, float *attn_factor);

@@ -4,11 +4,12 @@
 // What it computes.  Pair i of a head, (x, y), is turned by the angle 2 pi
 // frac(pos F_i / 2^64) and scaled: (a (x cos - y sin), a (y cos + x sin)).  F_i
 // is the pair's frequency in turns per token as a 64-bit fixed-point fraction,
-// so that pos F_i modulo 2^64 is the fraction of a turn itself, exact but for
-// the rounding of F_i (2^-65 pos turns): a product of 32-bit floats would have
-// lost the angle of position 10^6 altogether.  Its upper 32 bits are rounded
-// to 24 for the sine (an angle off by at most 2^-24); everything else is in 32
-// bits, rounded to bf16 once.
+// so that pos F_i modulo 2^64 is the fraction of a turn itself, exactly: a
+// product of 32-bit floats would have lost the angle of position 10^6
+// altogether.  (F_i as pkv_rope_freqs makes it, in 64-bit floats, is off by up to
+// 2^-53 turns per token: 2^-33 of a turn at position 10^6.)  Its upper 32 bits
+// are rounded to 24 for the sine, an angle off by at most 2^-25 of half a turn or
+// 2^-23.3 radians; everything else is in 32 bits, rounded to bf16 once.
 //
 // What bounds it: memory.  Every q, k and v is read once and written once; the
 // angles of a token are worked out once for all its heads.  16 prompts of 9,549

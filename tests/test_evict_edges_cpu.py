@@ -3,6 +3,7 @@ of larger tensors, frequencies, and how the library and its Python module are
 built."""
 import ctypes
 import math
+from decimal import Decimal, localcontext
 
 import numpy as np
 import pytest
@@ -56,3 +57,20 @@ def test_pairs_of_at_most_low_turns_are_stretched(rot, base, scaling):
         assert (np.abs(got - 1 / factor) <= off)[slow].all() and (np.abs(got - 1.0) <= off)[fast].all()
         assert (got >= 1 / factor - off).all() and (got <= 1 + off).all()
         assert length > 7 or slow.all()
+
+
+@pytest.mark.parametrize("rot,base", [(16, 150000000), (64, 10000), (128, 1000000), (256, 500000)])
+@pytest.mark.parametrize("scaling,factor", [("plain", 1), ("linear", 3), ("linear", 8), ("ntk", 4), ("ntk", 7)])
+def test_frequencies_against_60_digits(rot, base, scaling, factor):
+    """Within 2^-53 turns per token: with g radians, the power is off by two steps of
+    2^-53 and by the exponent's rounding, |ln g| of them, two pi, the two divisions
+    and a changed base by one each, in all (6 + |ln g|) g 2^-53 / (2 pi) at most,
+    which is largest at g = 1; and by half of 2^-64."""
+    f, _ = pkv.rope_freqs(rot, float(base), scaling=scaling, factor=float(factor), device="cpu")
+    with localcontext() as digits:
+        digits.prec = 60
+        turn = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+        b = base * (Decimal(factor) ** (Decimal(rot) / (rot - 2)) if scaling == "ntk" else 1)
+        for i, got in enumerate(f.numpy().view(np.uint64).tolist()):
+            want = b ** (Decimal(-2 * i) / rot) / turn / (factor if scaling == "linear" else 1)
+            assert abs(Decimal(got) / 2 ** 64 - want) <= Decimal(2) ** -53
