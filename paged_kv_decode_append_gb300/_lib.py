@@ -114,15 +114,14 @@ def load(build_if_missing: bool = True):
 
 def calls():
     """The module ``pkv_torch``: calls from torch tensors to the library, checked
-    in C++ (builds the library first if need be, as :func:`load`)."""
+    in C++.  Builds the library and the module first if need be, as :func:`load`;
+    raises if the module cannot be built for this torch and Python."""
     global _calls
     if _calls is None:
         load()
-        path = _build.TORCH_LIB_PATH
-        if not os.path.exists(path):
-            raise RuntimeError(f"Python module missing: {path} (run __graft_entry__.build())")
         with _lock:
             if _calls is None:
+                path = _build.build_module()
                 loader = importlib.machinery.ExtensionFileLoader("pkv_torch", path)
                 spec = importlib.util.spec_from_file_location("pkv_torch", path, loader=loader)
                 module = importlib.util.module_from_spec(spec)

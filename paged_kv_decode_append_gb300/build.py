@@ -2,8 +2,10 @@
 
 Translation units are compiled in parallel; the CUDA runtime is linked
 statically so the library loads on machines without a GPU driver (host-only
-entry points such as the page pool work there).  ``pkv_torch.so`` is a Python
+entry points such as the page pool work there).  ``pkv_torch`` is a Python
 module on top of it that checks tensors in C++ (g++, with torch's headers).
+The library does not need it: where it cannot be built, the library is, and the
+calls that go through the module say why.
 """
 from __future__ import annotations
 
@@ -20,7 +22,6 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libpkv.so")
-TORCH_LIB_PATH = os.path.join(HERE, "pkv_torch.so")
 
 CUDA_SOURCES = ["pkv_decode.cu", "pkv_prefill.cu", "pkv_append.cu", "pkv_api.cu", "pkv_static.cu",
                 "pkv_table.cu", "pkv_tree.cu", "pkv_tree_attn.cu", "pkv_rope.cu", "pkv_mass.cu", "pkv_evict.cu"]
@@ -37,27 +38,52 @@ def _nvcc() -> str:
 
 
 def _sources():
-    return [os.path.join(CSRC, s) for s in CUDA_SOURCES + CXX_SOURCES + [TORCH_SOURCE]] + \
+    return [os.path.join(CSRC, s) for s in CUDA_SOURCES + CXX_SOURCES] + \
         [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))] + \
         [os.path.join(INCLUDE, "pkv.h")]
 
 
+def _newer(path: str, sources) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(s) <= os.path.getmtime(path) for s in sources)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(TORCH_LIB_PATH):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(TORCH_LIB_PATH))
-    return all(os.path.getmtime(s) <= t for s in _sources())
+    return _newer(LIB_PATH, _sources())
 
 
-def _torch_job():
-    """Compile command of the Python module, its object and how it is linked."""
+def module_path() -> str:
+    """Where the Python module lies, under a name of its own for every torch and
+    Python: one that was built for others is not loaded."""
+    import torch
+
+    return os.path.join(HERE, f"pkv_torch-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def module_up_to_date() -> bool:
+    return _newer(module_path(), [os.path.join(CSRC, TORCH_SOURCE), os.path.join(INCLUDE, "pkv.h")])
+
+
+def _run(cmd):
+    return cmd, subprocess.run(cmd, capture_output=True, text=True)
+
+
+def _good(step: str, result, verbose: bool = False) -> None:
+    cmd, r = result
+    if r.returncode != 0:
+        raise RuntimeError(f"{step} failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    if verbose and (r.stdout or r.stderr):
+        sys.stderr.write(r.stdout + r.stderr)
+
+
+def _module_job():
+    """Compile command of the Python module and how its object is linked."""
     import torch
 
     root = os.path.dirname(torch.__file__)
     obj = os.path.join(BUILD_DIR, "pkv_torch.o")
     cxx = shutil.which("g++") or "g++"
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
-    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
                 "-isystem", os.path.join(root, "include"),
                 "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
@@ -69,8 +95,28 @@ def _torch_job():
     return compile_, link
 
 
+def _link_module(link, verbose: bool) -> None:
+    path = module_path()
+    tmp = path + f".tmp{os.getpid()}"
+    link[link.index(None)] = tmp
+    _good("link", _run(link), verbose)
+    os.replace(tmp, path)
+
+
+def build_module(force: bool = False, verbose: bool = False) -> str:
+    """Compile and link the Python module alone (the library is there); returns its
+    path, or raises with what the compiler says."""
+    if force or not module_up_to_date():
+        os.makedirs(BUILD_DIR, exist_ok=True)
+        compile_, link = _module_job()
+        _good("compile", _run(compile_), verbose)
+        _link_module(link, verbose)
+    return module_path()
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link; returns the library path."""
+    """Compile and link the library, and the Python module if that can be built;
+    returns the library path."""
     if not force and up_to_date():
         return LIB_PATH
     nvcc = _nvcc()
@@ -85,33 +131,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
         obj = os.path.join(BUILD_DIR, s.replace(".cc", ".o"))
         jobs.append([nvcc, *common, "-x", "c++", "-c", os.path.join(CSRC, s), "-o", obj])
 
-    torch_compile, torch_link = _torch_job()
-    jobs.append(torch_compile)
-
-    def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        return cmd, r
+    objs = [j[-1] for j in jobs]
+    failure = None  # of the module
+    try:
+        module_compile, module_link = _module_job()
+        jobs.append(module_compile)
+    except Exception as e:  # (no torch, or one of another kind)
+        failure = e
 
     with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-        results = list(ex.map(run, jobs))
-    for cmd, r in results:
-        if r.returncode != 0:
-            raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
-            sys.stderr.write(r.stdout + r.stderr)
-    objs = [j[-1] for j in jobs[:-1]]
+        results = list(ex.map(_run, jobs))
+    for result in results[:len(objs)]:
+        _good("compile", result, verbose)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    link = [nvcc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "-soname=libpkv.so", "-o", tmp, *objs]
-    r = subprocess.run(link, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed: {' '.join(link)}\n{r.stdout}\n{r.stderr}")
+    _good("link", _run([nvcc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "-soname=libpkv.so", "-o", tmp, *objs]))
     os.replace(tmp, LIB_PATH)
-    tmp = TORCH_LIB_PATH + f".tmp{os.getpid()}"
-    torch_link[torch_link.index(None)] = tmp
-    r = subprocess.run(torch_link, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed: {' '.join(torch_link)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, TORCH_LIB_PATH)
+    if failure is None:
+        try:
+            _good("compile", results[-1], verbose)
+            _link_module(module_link, verbose)
+        except Exception as e:
+            failure = e
+    if failure is not None:
+        sys.stderr.write(f"pkv_torch was not built: {failure}\n")
     return LIB_PATH
 
 

@@ -3,6 +3,7 @@ of larger tensors, frequencies, and how the library and its Python module are
 built."""
 import ctypes
 import math
+import os
 from decimal import Decimal, localcontext
 
 import numpy as np
@@ -10,6 +11,7 @@ import pytest
 
 import paged_kv_decode_append_gb300 as pkv
 from paged_kv_decode_append_gb300 import _lib
+from paged_kv_decode_append_gb300 import build as pkv_build
 from paged_kv_decode_append_gb300.api import CacheDesc
 
 FAKE = 0x10000  # aligned, never dereferenced on these paths
@@ -74,3 +76,40 @@ def test_frequencies_against_60_digits(rot, base, scaling, factor):
         for i, got in enumerate(f.numpy().view(np.uint64).tolist()):
             want = b ** (Decimal(-2 * i) / rot) / turn / (factor if scaling == "linear" else 1)
             assert abs(Decimal(got) / 2 ** 64 - want) <= Decimal(2) ** -53
+
+
+def fail():
+    raise ImportError("no torch with CUDA here")
+
+
+@pytest.mark.parametrize("job", ["missing", "compile", "link"])
+def test_the_library_is_built_where_its_python_module_cannot_be(tmp_path, monkeypatch, capfd, job):
+    here = str(tmp_path)
+    for name, value in (("HERE", here), ("BUILD_DIR", os.path.join(here, "_build")), ("LIB_PATH", os.path.join(here, "libpkv.so")),
+                        ("CUDA_SOURCES", []), ("CXX_SOURCES", ["pkv_pool.cc"])):
+        monkeypatch.setattr(pkv_build, name, value)
+    ok, no = ["true", "-o", None], ["false", "-o", None]
+    monkeypatch.setattr(pkv_build, "_module_job",
+                        {"missing": fail, "compile": lambda: (no[:1], list(ok)), "link": lambda: (ok[:1], list(no))}[job])
+    assert not pkv_build.up_to_date()
+    assert pkv_build.build() == pkv_build.LIB_PATH and os.path.getsize(pkv_build.LIB_PATH) > 0 and pkv_build.up_to_date()
+    assert "pkv_torch was not built" in capfd.readouterr().err and not os.path.exists(pkv_build.module_path())
+    with pytest.raises((ImportError, RuntimeError)):  # asked for by name: why not
+        pkv_build.build_module()
+
+
+def test_a_module_of_another_torch_or_python_is_not_taken(monkeypatch):
+    import sysconfig
+
+    import torch
+
+    pkv_build.build()
+    path = pkv_build.build_module()
+    assert pkv_build.module_up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.1")
+        assert pkv_build.module_path() != path and not pkv_build.module_up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name: ".other.so")
+        assert pkv_build.module_path() != path and not pkv_build.module_up_to_date()
+    assert _lib.calls().__file__ == path
