@@ -722,6 +722,13 @@ PKV_API pkv_status pkv_rope_append(const pkv_cache_desc *desc, void *k_cache, vo
  * used by every call here; only causal masks among tokens of one call look at
  * slots, and those tokens are always the last.  A row that is cut down needs
  * pages of its own: a page that two block tables name would be moved in both.
+ * Lengths: pkv_rope_append and pkv_attn_mass take them without the step's
+ * tokens, as an attention that appends them does; an attention of what is cached
+ * already (no k_new) takes them with these tokens, and the plan those that the
+ * caller has advanced.  So a captured step with pkv_rope_append keeps two arrays.
+ * A decode call right behind pkv_rope_append goes without PKV_DECODE_EARLY_KV,
+ * and one right behind pkv_evict_apply without PKV_DECODE_OVERLAP_PROLOGUE: those
+ * write what it would read early.
  * Layers and rows of larger tensors can be handed on as they lie: mass and
  * slot_pos are 16-byte aligned where slots is a multiple of 4 and 4-byte aligned
  * otherwise, lse 4-byte and moves 8-byte aligned.

@@ -541,7 +541,8 @@ def pkv_rope_append(k_cache, v_cache, q, k_new, v_new, block_table, cache_seqlen
     """:func:`pkv_append` of rotated ``k_new`` and the rotation of the same
     tokens' ``q`` (or None), in one pass.  Token i of row b is at position
     ``cache_seqlens[b] + i + evicted[b]`` unless ``positions`` ``[T]`` says
-    otherwise.  Returns ``q_out``, which may be ``q``."""
+    otherwise.  An attention behind it (without ``k_new``) takes the lengths with
+    the new tokens.  Returns ``q_out``, which may be ``q``."""
     if q is not None and q_out is None:
         q_out = torch.empty_like(q)
     st = _lib.calls().rope_append(k_cache, v_cache, q, k_new, v_new, block_table, cache_seqlens, freqs, pairing, attn_factor,

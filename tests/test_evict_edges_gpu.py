@@ -124,3 +124,154 @@ def test_weights_of_large_scores(D, Hq, Hkv, counts, lens):
             off[h // G] += (w * torch.expm1(2.0 ** -24 * (3 * d.abs() + 4))).sum(0)
         off += 2.0 ** -24 * (42 if n * G > 1 else 0) * want + n * G * 2.0 ** -126
         assert ((got[1][b, :, : L + n].double() - want).abs() <= off).all()
+
+
+class Decoder:
+    """A decoder's steps of one token a row inside a budget of slots, next to the
+    decode attention: rotation, attention, weights in every layer, then plan, moves
+    and tables.  One row is padding.  `way`: how keys get into the cache."""
+
+    layers, B, slots, steps = 3, 5, 80, 8
+
+    def __init__(self, way, D, Hq, Hkv, P, layout):
+        self.way, self.D, self.G, self.P, self.layout, self.scale = way, D, Hq // Hkv, P, layout, D ** -0.5
+        g = torch.Generator().manual_seed(D + P)
+        pages, K, B = 150, Hkv, self.B
+        shape = (pages, P, K, D) if layout == base.wl.NHD else (pages, K, P, D)
+        self.ks, self.vs = ([torch.randn(shape, generator=g).bfloat16().to(DEV) for _ in range(self.layers)] for _ in range(2))
+        self.caches = pkv.LayerCaches(self.ks, self.vs, layout)
+        self.pool, self.held, self.gone = pkv.device_pool(pages), base.i32([0] * B), base.i32([0, 7, 100, 0, 3])
+        self.table = torch.zeros(B, -(-self.slots // P), dtype=torch.int32, device=DEV)
+        self.lens, self.one, self.err = base.i32([39, 24, 5, -1, 60]), base.i32([1] * B), base.zero()
+        self.budgets = base.i32([30, 24, 24, 24, -1])
+        pkv.pkv_table_update(self.pool, self.table, self.held, self.lens, None, P)
+        self.mass = torch.rand((self.layers, B, K, self.slots), generator=g).to(DEV)
+        self.pos = (torch.arange(self.slots, device=DEV) + self.gone[:, None, None]).int().expand(self.mass.shape).contiguous()
+        self.inputs = [[torch.randn((self.layers, B, h, D), generator=g).bfloat16().to(DEV) for h in (Hq, K, K)]
+                       for _ in range(self.steps)]
+        self.now = [torch.empty_like(x) for x in self.inputs[0]]  # this step's q, k, v
+        self.turned = [torch.empty_like(x) for x in self.now[:2]]
+        self.out, self.lse = torch.empty_like(self.now[0]), torch.empty(self.layers, B, Hq, device=DEV)
+        self.freqs, _ = pkv.rope_freqs(D)
+        desc = pkv.cache_desc(self.ks[0], layout)
+        self.ws = pkv.decode_workspace(B, self.table.shape[1], Hq, desc, DEV)
+        self.mass_ws = pkv.mass_workspace(B, B, self.table.shape[1], Hq, desc, DEV)
+        self.work = (torch.zeros(self.layers, B, K, self.slots // 2, 2, dtype=torch.int32, device=DEV),
+                     torch.zeros(self.layers, B, K, dtype=torch.int32, device=DEV), torch.zeros(B, 2, dtype=torch.int32, device=DEV))
+        if way == "step":
+            self.graph = pkv.DecodeStep(self.ks, self.vs, list(self.turned[0]), list(self.turned[1]), list(self.now[2]),
+                                        self.table, self.lens, self.scale, list(self.out), list(self.lse), self.ws, self.err,
+                                        layout, pkv.api.DECODE_USE_PLAN | pkv.api.DECODE_OVERLAP_PROLOGUE)
+
+    def attend(self, l, after, positions):
+        q, k, v = (x[l] for x in self.now)
+        if self.way == "append":  # rotated and appended, then attended with the lengths after
+            pkv.pkv_rope_append(self.ks[l], self.vs[l], q, k, v, self.table, self.lens, self.freqs, evicted=self.gone,
+                                q_out=self.turned[0][l], err_flag=self.err, layout=self.layout)
+            pkv.pkv_decode_attn(self.ks[l], self.vs[l], self.turned[0][l], None, None, self.table, after, self.scale,
+                                out=self.out[l], lse=self.lse[l], workspace=self.ws, err_flag=self.err, layout=self.layout)
+            return
+        pkv.pkv_rope(q, k, positions, self.freqs, q_out=self.turned[0][l], k_out=self.turned[1][l])
+        if self.way == "step":
+            return
+        api = pkv.api
+        flags = 0 if self.way == "fused" else api.DECODE_MAKE_PLAN if l == 0 else \
+            api.DECODE_USE_PLAN | api.DECODE_OVERLAP_PROLOGUE | api.DECODE_EARLY_KV
+        pkv.pkv_decode_attn(self.ks[l], self.vs[l], self.turned[0][l], self.turned[1][l], v, self.table, self.lens, self.scale,
+                            out=self.out[l], lse=self.lse[l], workspace=self.ws, err_flag=self.err, layout=self.layout,
+                            flags=flags)
+
+    def step(self, look=None):
+        pkv.pkv_table_update(self.pool, self.table, self.held, self.lens, self.one, self.P, err_flag=self.err)
+        after = self.lens + (self.lens >= 0).int()
+        positions = self.lens + self.gone
+        for l in range(self.layers):
+            self.attend(l, after, positions)
+        if self.way == "step":
+            self.graph.launch()
+        for l in range(self.layers):
+            if look is not None:
+                look(self, l)
+            pkv.pkv_attn_mass(self.ks[l], self.turned[0][l], self.lse[l], self.table, self.lens, self.scale, self.mass[l],
+                              evicted=self.gone, slot_pos=self.pos[l], workspace=self.mass_ws, err_flag=self.err,
+                              layout=self.layout)
+            if look is not None:
+                look(self, l, done=True)
+        self.lens.copy_(after)
+        pkv.pkv_evict_plan(self.mass, self.pos, self.lens, self.gone, self.budgets, 2, 5, *self.work, err_flag=self.err)
+        pkv.pkv_evict_apply(self.caches, *self.work, self.table, self.lens, self.gone, mass=self.mass, slot_pos=self.pos,
+                            err_flag=self.err)
+        pkv.pkv_table_update(self.pool, self.table, self.held, self.lens, None, self.P, err_flag=self.err)
+
+    def state(self):
+        return [*self.ks, *self.vs, self.mass, self.pos, self.lens, self.gone, self.table, self.held, self.pool, self.out, self.lse,
+                self.err]
+
+    def run(self, how):
+        for x in self.inputs:
+            for to, new in zip(self.now, x):
+                to.copy_(new)
+            how()
+        torch.cuda.synchronize()
+        return [x.clone() for x in self.state()]
+
+
+def look(s, l, done=False):
+    """A step's attention and weights against 64 bits over what is cached."""
+    from types import SimpleNamespace
+
+    table, lens = s.table.cpu().numpy(), s.lens.tolist()
+    if not done:
+        s.was = s.mass[l].double().cpu()
+        return
+    K = s.mass.shape[2]
+    for b, L in enumerate(lens):
+        if L < 0:
+            assert base.same_bits(s.mass[l, b].double().cpu(), s.was[b]) and not s.out[l, b].any()
+            continue
+        k, v = (base.ref.row_keys(SimpleNamespace(k_cache=x, block_table=table, page_size=s.P, layout=s.layout, num_kv_heads=K,
+                                                  head_dim=s.D), b, L + 1) for x in (s.ks[l], s.vs[l]))
+        assert torch.equal(v[L], s.now[2][l, b].double().cpu())
+        if s.way != "append":
+            assert torch.equal(k[L], s.turned[1][l, b].double().cpu())
+        q = s.turned[0][l, b].double().cpu()
+        want = s.was[b].clone()
+        want[:, L] = 0.0
+        for h in range(K * s.G):
+            w = torch.softmax(k[:, h // s.G] @ q[h] * s.scale, 0)
+            out = w @ v[:, h // s.G]
+            assert ((s.out[l, b, h].double().cpu() - out).abs() <= 1e-2 + 1e-2 * out.abs()).all()  # the attention's bound
+            want[h // s.G, : L + 1] += w
+        # a weight is as exact as the attention's lse, 1e-3 of it here
+        assert ((s.mass[l, b].double().cpu() - want).abs() <= 1e-3 * want).all()
+        assert s.pos[l, b, :, L].tolist() == [L + int(s.gone[b])] * K
+
+
+WAYS = ["fused", "plan", "append", "step"]
+SHAPES = [(128, 8, 2, 16, base.wl.NHD), (64, 4, 4, 8, base.wl.HND), (256, 8, 1, 64, base.wl.NHD)]
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,P,layout", SHAPES)
+@pytest.mark.parametrize("way", WAYS)
+def test_steps_next_to_the_decode_attention(way, D, Hq, Hkv, P, layout):
+    """With the fused append (and a plan shared by the layers, and a captured step of
+    all layers), and with rotated keys appended before an attention alone."""
+    s = Decoder(way, D, Hq, Hkv, P, layout)
+    s.run(lambda: s.step(look))
+    assert int(s.err.item()) == 0 and s.lens.tolist() == [30, 24, 13, -1, 68]
+    assert s.gone.tolist() == [17, 15, 100, 0, 3] and s.held.tolist() == [-(-n // P) for n in (30, 24, 13, 0, 68)]
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,P,layout", SHAPES)
+@pytest.mark.parametrize("way", WAYS[:3])
+def test_whole_steps_in_a_graph(way, D, Hq, Hkv, P, layout):
+    """Tables, rotation, attention, weights, plan and moves captured once and replayed
+    step after step: as eagerly, bit for bit."""
+    s = Decoder(way, D, Hq, Hkv, P, layout)
+    eager = s.run(s.step)
+    s = Decoder(way, D, Hq, Hkv, P, layout)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.step()
+    replayed = s.run(graph.replay)
+    assert all(base.same_bits(a, b) for a, b in zip(eager, replayed)) and int(s.err.item()) == 0
