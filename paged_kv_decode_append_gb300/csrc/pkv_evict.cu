@@ -488,8 +488,9 @@ __global__ void __launch_bounds__(THREADS, (KEYS == 0 ? 1024 : 1280) / THREADS)
         int *list = reinterpret_cast<int *>(s_dyn);
         uint32_t at = hole ? 2 * (before & 0xffff) + 1 : 2 * (before >> 16);
         // A few words of many bits the warp does together, one after the other: rows of
-        // 2,112 slots that keep 2,048 take 92 us with every word a thread's, 83 so; where
-        // most words have many bits (1,056 kept) it is 122 and 146.
+        // 2,112 slots that keep 2,048 take 86 us with every word a thread's, 80 so; where
+        // most words have many bits (1,056 kept) all of them so take 137, none 115, and up
+        // to twelve of a warp 111.
         uint32_t dense = __ballot_sync(0xffffffffu, bits_of > 4);
         dense = __popc(dense) > 12 ? 0 : dense;
         for (uint32_t m = dense; m != 0; m &= m - 1) {
@@ -662,10 +663,13 @@ bool aligned8(const void *p) // moves are read and written in pairs
 constexpr int kPlanCached = 38912; // keys in shared memory at most; longer rows make theirs again
 
 // Keys in registers up to 17,408 slots, 17 a thread at most, then in shared memory.
-// 36 x 64 x 8 rows of 4,000 slots: 319 us with 32 keys in each of 128 threads, 305 with
-// 17 in 256; 36 x 16 x 8 of 8,192: 224 with keys in shared memory, 161 with 17 in 512;
-// 36 x 4 x 8 of 32,000: 832 with 128 threads, 266 with 1,024.  Rows of 1,100 slots:
-// 74 with nine keys a thread, 97 with 17 of which half are idle.
+// As few threads as that allows: 36 x 64 x 8 rows of 1,100 slots take 62 us with nine
+// keys in each of 128 threads, 81 with 17 of which half are idle, 116 with nine in 256;
+// of 2,112 slots 81 with 17 in 128, 113 with nine in 256; of 3,900 218 with 17 in 256
+// (31 in 128, which registers still hold, 215).  36 x 16 x 8 of 8,192: 134 with 17 in
+// 512, 233 with keys in shared memory; 36 x 8 x 8 of 16,384: 169 with 17 in 1,024, 288
+// with keys in shared memory.  Longer ones: 36 x 4 x 8 of 32,000 246 with 1,024
+// threads, 305 with 512, 756 with 128.
 struct PlanEntry {
     int slots, threads;
     const void *kernel;

@@ -14,15 +14,16 @@
 // x 16: memory.  64 uneven rows of 95,000 tokens in all, one of 32,768, take 39
 // us, 5.1 TB/s; while it streams it runs at 93 % of the copy rate, and the first
 // MMA comes 6.6 us after a CTA has begun (5.0 until its range and pages are known
-// and the first copy leaves, 1.6 until its data is there).  One token over 64: 7.4 us.
+// and the first copy leaves, 1.6 until its data is there).  One token over 64: 7.5 us.
 // With many queries 128 keys x 128 columns (a pair) are 8 MMAs of 128 x 128 x 16,
 // 512 cycles at the tensor pipe's nominal rate, and 16,384 exponentials, 512
-// cycles at the 32 a cycle measured; a pair takes about 940.  No unit is full
-// (tensor 43 %, exponentials 43 %, issue slots 51 % of the elapsed cycles): a pair
-// goes from the MMAs to the sums and back in 3,700 cycles, and TMEM holds four.
-// Of those the sums take 2,350 (four TMEM loads at 300, the rest arithmetic), the
-// MMAs 700 from first to last.  Two rows of 3,500 .. 4,095 queries: 160 us, 1.1 PFLOP/s; head_dim 256, whose
-// pairs have twice the MMAs for the same sums: 107 us, 1.2 PFLOP/s (tensor 52 %).
+// cycles at the 32 a cycle measured; a pair takes about 990.  No unit is full
+// (tensor 43 %, exponentials 43 %, issue slots 57 % of the elapsed cycles): a pair
+// goes from the MMAs to the sums and back in 3,990 cycles, and TMEM holds four.
+// Of those the sums take 2,580 (four TMEM loads at 300, the rest arithmetic), the
+// MMAs 670 from first to last.  Two rows of 3,500 .. 4,095 queries: 168 us, 1.0
+// PFLOP/s; head_dim 256, whose pairs have twice the MMAs for the same sums: 111 us,
+// 1.2 PFLOP/s (tensor 52 %).
 //
 // How (one persistent CTA per SM):
 //  - Work is laid out along a line: for every (row, kv head) its blocks of keys,
@@ -32,24 +33,29 @@
 //    128 keys, as runs; others by 256, so that the query tiles stream past two key
 //    tiles at once; and those with few query tiles over a long context by 512 (head_dim
 //    128 and 64), so that a block has steps enough: 8 rows of 64 queries on 8,192 tokens
-//    take 45 us by 512 and 49 by 256, of 256 queries 121 and 131, of 448 204 and 206
-//    (head_dim 64: 202 and 197).  Where the queries are the row 512 goes far past the
-//    causal limit: 64 prompts of 512 tokens take 164 us by 512 and 122 by 256, 2 of
-//    4,096 144 and 131.
+//    take 48 us by 512 and 50 by 256, of 256 queries 129 and 137; past twelve steps
+//    the two are even (448 queries 219 and 220, head_dim 64 211 and 209).  Where the
+//    queries are the row 512 goes far past the causal limit: 64 prompts of 512 tokens
+//    take 172 us by 512 and 127 by 256, 2 of 4,096 152 and 139.
 //  - A block cut between CTAs leaves partial sums in the workspace; the last
 //    CTA to arrive (a ticket for every 32 keys) adds them up in the order of the
 //    line, so results do not depend on timing.
 //  - Warps: 0 loads K; 2 cuts the range into runs, hands them out through a ring
 //    and loads the query tiles; 1 and 3 issue the MMAs, every other pair each (one
-//    warp for all: 180 us for 106 at head_dim 256); 4-19 sum, four warps to a
+//    warp for all took 180 us where two took 106, head_dim 256); 4-19 sum, four warps to a
 //    pair, each group with an accumulator of its own.  The sums tell the loaders
 //    what is free: as commits of the issuing warps that took 43 us for 41 (decode).
-//  - Scores are exact products summed in fp32.  The exponent is the difference
-//    d of score and lse, rounded once, and only then in base 2: what the
-//    conversion rounds goes with d and not with the score.  A weight is off by at
-//    most (3 |d| + 4) 2^-24 of itself at any size of score.  (Score and lse each
-//    in base 2 first, which saves a multiplication for two weights, took a
-//    rounding of the whole score into every weight: 3e-5 of it at scores of 200.)
+//  - The exponent is the difference d of score and lse, rounded once, and only
+//    then in base 2: what the conversion rounds goes with d and not with the
+//    score.  From the score on a weight is off by at most (3 |d| + 4) 2^-24 of
+//    itself.  (Score and lse each in base 2 first, which saves a multiplication for
+//    two weights and 3 to 5 % of the time of prompts, took a rounding of the whole
+//    score into every weight: 3e-5 of it at scores of 200.)
+//  - The score itself is the sum of exact products that the tensor cores make in
+//    fp32: 16 at a time are added to what is there, and what does not fit is cut
+//    off.  It falls short by 1.4e-7 of itself at head_dim 64, 2e-7 at 128 and 6e-7
+//    at 256 (measured, scores near 20), and a weight by that much of the score:
+//    3e-6, 4e-6 and 1.1e-5.  Scores around 0 leave weights within 3e-7 .. 6e-7.
 //  - Sums of a step's columns are plain fp32 (four runs of 32 terms); steps are
 //    added up with a compensation for what the addition drops, so thousands of
 //    queries lose nothing.
