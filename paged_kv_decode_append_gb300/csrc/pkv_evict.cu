@@ -655,6 +655,10 @@ bool aligned16(const void *p)
 {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
+bool aligned4(const void *p)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
+}
 bool aligned8(const void *p) // moves are read and written in pairs
 {
     return (reinterpret_cast<uintptr_t>(p) & 7u) == 0;
@@ -790,7 +794,7 @@ pkv_status pkv_evict_apply(const pkv_cache_desc *desc, int32_t num_layers, void 
     if (batch == 0)
         return PKV_OK;
     if (moves == nullptr || num_moves == nullptr || row_lens == nullptr || block_table == nullptr || !aligned8(moves) ||
-        (cache_seqlens == nullptr && evicted != nullptr))
+        (cache_seqlens == nullptr && evicted != nullptr) || !aligned4(mass) || !aligned4(slot_pos))
         return PKV_EINVAL;
     p.moves = reinterpret_cast<const int2 *>(moves);
     p.num_moves = num_moves;

@@ -35,6 +35,19 @@ def test_alignment_of_slices():
     assert mass(pos=None) == EWORKSPACE
 
 
+def test_apply_refuses_scores_between_words():
+    """Scores and positions off a 4-byte boundary, which no load may take."""
+    one = (ctypes.c_void_p * 1)(FAKE)
+
+    def apply(mass=FAKE, pos=FAKE, slots=65):
+        return _lib.load().pkv_evict_apply(ctypes.byref(CacheDesc(64, 16, 1, 128, 1)), 1, one, one, FAKE, 4, FAKE, FAKE, FAKE, 4,
+                                           mass, pos, slots, FAKE, FAKE, 2, None, None)
+
+    for at in (1, 2, 3):
+        for slots in (64, 65):
+            assert apply(mass=FAKE + at, slots=slots) == apply(pos=FAKE + at, slots=slots) == EINVAL
+
+
 def turns_of(*args, **kw):
     """Frequencies in turns per token of 64-bit floats."""
     f, _ = pkv.rope_freqs(*args, device="cpu", **kw)
