@@ -275,3 +275,50 @@ def test_whole_steps_in_a_graph(way, D, Hq, Hkv, P, layout):
         s.step()
     replayed = s.run(graph.replay)
     assert all(base.same_bits(a, b) for a, b in zip(eager, replayed)) and int(s.err.item()) == 0
+
+
+def test_pools_past_32_bits():
+    """Pages behind the 2^31-th element of their pools: as in small ones."""
+    D, K, P, counts, lens = 128, 1, 16, [1, 40, 1], [100, 33, 300]
+    case = base.wl.mixed_step(41, counts, lens, 4, K, D, P, device=DEV)
+    f, _ = base.freqs_of(D)
+    far = 2 ** 31 // (P * K * D)
+    got = []
+    for shift in (0, far):
+        kc, vc = (torch.empty((case.num_pages + shift, P, K, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        kc[shift:], vc[shift:] = case.k_cache, case.v_cache
+        table = base.i32(np.where(case.block_table > 0, case.block_table + shift, 0))
+        old, ptr, err = base.i32(lens), base.i32(case.qo_indptr), base.zero()
+        slots = case.max_blocks * P
+        mass, pos = torch.ones(1, 3, K, slots, device=DEV), torch.zeros(1, 3, K, slots, dtype=torch.int32, device=DEV)
+        q = pkv.pkv_rope_append(kc, vc, case.q, case.k_new, case.v_new, table, old, f, append_indptr=ptr, err_flag=err)
+        pkv.pkv_attn_mass(kc, q, torch.full((42, 4), 6.0, device=DEV), table, old, case.softmax_scale, mass[0], qo_indptr=ptr,
+                          slot_pos=pos[0], err_flag=err)
+        now, gone = base.i32(np.array(lens) + counts), base.i32([0, 0, 0])
+        moves, num, rows = pkv.pkv_evict_plan(mass, pos, now, gone, base.i32([40, 20, 100]), 1, 4, err_flag=err)
+        pkv.pkv_evict_apply(pkv.LayerCaches([kc], [vc]), moves, num, rows, table, now, gone, mass=mass, slot_pos=pos, err_flag=err)
+        assert int(err.item()) == 0 and now.tolist() == [40, 20, 100] and int(num.max()) > 0
+        got.append([q, kc[shift:].clone(), vc[shift:].clone(), mass, pos])
+        del kc, vc
+    assert all(base.same_bits(a, b) for a, b in zip(*got))
+
+
+def test_weights_on_two_streams_at_once():
+    """With a workspace each, and a third call behind both."""
+    cases = [base.mass_case(s, c, n, 8, 2, 128, 16) for s, c, n in ((42, [600, 1], [100, 900]), (43, [1] * 40, list(range(0, 1600, 40))))]
+    want = [base.run_mass(c, z)[1] for c, z in cases]
+    calls, streams = [], [torch.cuda.Stream() for _ in cases]
+    for (case, z), w in zip(cases, want):
+        args = [z.to(DEV), base.i32(case.block_table), base.i32(case.cache_seqlens), base.i32(case.qo_indptr)]
+        ws = pkv.mass_workspace(case.batch, case.q.shape[0], case.max_blocks, 8, pkv.cache_desc(case.k_cache), DEV)
+        start = torch.rand(w.shape, generator=torch.Generator().manual_seed(1)).to(DEV)
+        calls.append((case, args, ws, [start.clone() for _ in range(20)]))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for (case, (z, table, lens, ptr), ws, out), stream in zip(calls, streams):
+            with torch.cuda.stream(stream):
+                pkv.pkv_attn_mass(case.k_cache, case.q, z, table, lens, case.softmax_scale, out[i], qo_indptr=ptr, workspace=ws,
+                                  layout=case.layout)
+    torch.cuda.synchronize()
+    for (_, _, _, out), w in zip(calls, want):
+        assert all(base.same_bits(x.cpu(), w) for x in out)
